@@ -83,7 +83,7 @@ typedef struct {
 #define MOE_ERR_UNSUPPORTED    2 /* shape the kernels do not take (d or f not a multiple of 8, E > 1024) */
 #define MOE_ERR_CAPACITY       3 /* R_cap < T*k + E*(align-1) */
 #define MOE_ERR_CUDA           4 /* a CUDA runtime / driver call failed */
-#define MOE_ERR_DEVICE_INDEX   5 /* device: an expert id outside [0, E) in a caller-supplied index */
+#define MOE_ERR_DEVICE_INDEX   5 /* device: an index out of range in caller-supplied device data (expert id, cache page, length) */
 #define MOE_ERR_DEVICE_TIMEOUT 6 /* device: a bounded wait inside a kernel gave up */
 
 /* ------------------------------------------------------------------------
@@ -369,6 +369,134 @@ int moe_decode_fwd(const moe_bf16* x, const float* w_router, const float* bias,
 size_t moe_decode_workspace_size(int64_t T, int d, int f, int E, int k);
 
 /* ------------------------------------------------------------------------
+ * The attention in front of the layer: rotary positions, a paged cache of
+ * keys and values, the append to it and the attention of new tokens over it.
+ * (No counterpart on the source pages: what a user who serves a model of
+ * these layers needs next to them. The formulas below are the definition.)
+ *
+ * Conventions of these four calls, beside those at the top:
+ *   - The structs are passed as HOST pointers; the arrays inside are device
+ *     arrays. Nothing of a struct is kept after the call returns.
+ *   - q, k, v, out are [T, H, D] views: heads packed (D elements apart), tokens
+ *     a stride of their own apart (in elements, a multiple of 8, >= H*D), so
+ *     slices of one projection's output need no copy.
+ *   - D: head dimension, a multiple of 8, 8 .. 128. Pointers are 16-byte
+ *     aligned.
+ *   - Hq = G * Hkv query heads: query head h reads key/value head h / G.
+ * ------------------------------------------------------------------------ */
+
+/* A cache of n_pages pages, each page_size token slots of Hkv heads: the key
+ * of (page, head, slot) is the D elements at k + page * page_stride +
+ * head * head_stride + slot * token_stride, values alike (elements, multiples
+ * of 8; 64-bit offsets). [pages, heads, slots, D] keeps a head's page in one
+ * piece; [pages, slots, heads, D] works as well. page_size: any >= 1 (the
+ * chunk kernel on the tensor cores' own path takes multiples of 8, others run
+ * the general kernel). */
+typedef struct {
+  moe_bf16* k;
+  moe_bf16* v;
+  int64_t n_pages;
+  int64_t page_stride, head_stride, token_stride;
+  int32_t page_size;
+  int32_t Hkv;
+  int32_t D;
+} moe_kv_cache;
+
+/* A ragged batch of B sequences: sequence b's new tokens are rows
+ * cu_q[b] .. cu_q[b+1] - 1 of the [T, ...] arrays and the last ones of its
+ * kv_len[b] tokens in the cache (so its token i sits at cache position
+ * kv_len[b] - n_q + i); position c lies in page page_table[b * table_stride +
+ * c / page_size], slot c % page_size. Sequences may be empty; rows at or past
+ * cu_q[B] belong to none. Table entries past a sequence's last page are not
+ * read. max_q: the largest number of new tokens of a sequence, a hint the
+ * kernel is chosen by; a wrong one costs time only. */
+typedef struct {
+  const int32_t* cu_q;        /* [B + 1], ascending, cu_q[0] = 0 */
+  const int32_t* kv_len;      /* [B], new tokens included */
+  const int32_t* page_table;  /* [B, table_stride], max_pages entries used */
+  int64_t table_stride;
+  int64_t T;
+  int32_t B;
+  int32_t max_pages;          /* max_pages * page_size <= 2^30 */
+  int32_t max_q;
+} moe_kv_batch;
+
+/* Rotary positions: pairs i = 0 .. rd/2 - 1 of a head's first rd elements
+ * (i and i + rd/2, or 2i and 2i + 1 when interleaved) turn by the angle
+ * pos[axis[i]][t] * w_i, and are multiplied by `scale`; elements >= rd stay.
+ * turns[i] is w_i / 2 pi (turns a position) as a 64-bit binary fraction,
+ * round(2^64 w_i / 2 pi) mod 2^64: position times it, mod 2^64, is the angle,
+ * so far positions lose nothing. axis NULL: every pair follows axis 0.
+ * Several axes (time, height, width) are the rotation of image and video
+ * tokens; any assignment of pairs to axes works. */
+typedef struct {
+  const uint64_t* turns;      /* [rd / 2] */
+  const int32_t* axis;        /* [rd / 2] in [0, n_axes), or NULL */
+  int32_t rd;                 /* even, 2 .. D */
+  int32_t n_axes;             /* 1 .. 8 */
+  int32_t interleaved;
+  float scale;                /* 1 unless the frequencies' scheme has one */
+} moe_rotary;
+
+/* ------------------------------------------------------------------------
+ * moe_rope — q_out = R q (and k_out = R k unless k is NULL), R the rotation
+ * of the token's positions; transpose != 0: R^T, the backward pass (dq from
+ * the gradient of q_out). fp32 from the bf16 values, rounded once. In place
+ * (q_out == q with equal strides) is fine; other overlaps are not.
+ *  pos [n_axes, T] int32 (any sign);  q, q_out [T, Hq, D];  k, k_out [T, Hk, D]
+ * An axis outside [0, n_axes) raises MOE_ERR_DEVICE_INDEX (axis 0 is used).
+ * ------------------------------------------------------------------------ */
+int moe_rope(const moe_rotary* rot, const int32_t* pos, int64_t T, int D, int transpose,
+             const moe_bf16* q, int64_t q_stride, int Hq, moe_bf16* q_out, int64_t qo_stride,
+             const moe_bf16* k, int64_t k_stride, int Hk, moe_bf16* k_out, int64_t ko_stride,
+             moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_kv_append — the new tokens' keys (rotated when rot is given) and values
+ * into the cache, and their rotated queries into q_out in the same pass.
+ *  k, v [T, Hkv, D];  q [T, Hq, D] and q_out, or q NULL (Hq = 0)
+ *  rot NULL: keys and queries are copied;  pos [n_axes, T] int32, or NULL: a
+ *  token's cache position on every axis (0 for a row of no sequence)
+ * A token whose cache position or page (not in [0, n_pages)) is outside the
+ * cache raises MOE_ERR_DEVICE_INDEX and is not written. Pages that several
+ * sequences share must not be written by more than one of them. In place for
+ * q as in moe_rope.
+ * ------------------------------------------------------------------------ */
+int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_rotary* rot,
+                  const int32_t* pos, const moe_bf16* k, int64_t k_stride, const moe_bf16* v,
+                  int64_t v_stride, const moe_bf16* q, int64_t q_stride, int Hq, moe_bf16* q_out,
+                  int64_t qo_stride, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_attn_paged — attention of the batch's new tokens over the cache (their
+ * own keys and values included: append first).
+ *   s_j = scale <q[t, h], k_j> over the keys j row (t, h) sees: j < kv_len,
+ *   causal: j <= c (c the token's cache position), window > 0: j > c - window;
+ *   out[t, h] = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sinks[h]));
+ *   lse[t, h] = log of that denominator.
+ * A row that sees no key gives out = 0 (lse = sinks[h], or -inf). What lies in
+ * the cache outside a row's keys does not reach it, be it infinite or NaN.
+ * Scores, maxima and sums are fp32; the weights exp(s_j - max) are rounded to
+ * bf16 for the product with V (the sum takes them unrounded); out is rounded
+ * once. Results of two calls are bitwise equal on one GPU model.
+ *  q, out [T, Hq, D] (out may not overlap q);  sinks [Hq] fp32 or NULL;
+ *  lse [T, Hq] fp32 packed, or NULL;  scale finite and > 0
+ *  ws: moe_attn_paged_workspace_size(Hq, Hkv, D) bytes, 256-byte aligned (its size
+ *  depends on the current device); one call at a time per buffer.
+ * A kv_len outside [0, max_pages * page_size], a page outside [0, n_pages) or
+ * a cu_q that runs out of [0, T] or backwards raises MOE_ERR_DEVICE_INDEX;
+ * nothing out of bounds is read or written, and that sequence's rows are
+ * unspecified. Rows of no sequence are not written.
+ * Limits: T * Hq < 2^31, T < 2^30.
+ * ------------------------------------------------------------------------ */
+int moe_attn_paged(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_bf16* q,
+                   int64_t q_stride, int Hq, float scale, int causal, int window,
+                   const float* sinks, moe_bf16* out, int64_t out_stride, float* lse, void* ws,
+                   size_t ws_bytes, moe_stream_t stream);
+/* 0 for arguments the call rejects. */
+size_t moe_attn_paged_workspace_size(int Hq, int Hkv, int D);
+
+/* ------------------------------------------------------------------------
  * Workspace sizes (bytes) for the calls that take `ws`. Any 256-byte-aligned
  * device buffer of at least this size works; its contents need no
  * initialisation and are scratch after the call.
@@ -411,6 +539,9 @@ const char* moe_status_str(int code);
 #define MOE_KERNEL_ROUTE_BWD     12
 #define MOE_KERNEL_DECODE        13
 #define MOE_KERNEL_FUSED_FWD     14
+#define MOE_KERNEL_ROPE          15
+#define MOE_KERNEL_ATTN          16
+#define MOE_KERNEL_ATTN_COMBINE  17
 int moe_timer_start(int kernel, int max_launches);
 int moe_timer_read(float* total_ms, int* launches);
 

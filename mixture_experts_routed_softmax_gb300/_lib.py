@@ -14,6 +14,7 @@ _P = ctypes.c_void_p      # device / host pointer as an integer
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 SIGNATURES = {
     "moe_route": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
@@ -35,6 +36,10 @@ SIGNATURES = {
     "moe_decode_fwd": (_I, [_P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _P, _P,
                             _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_decode_workspace_size": (_SZ, [_I64, _I, _I, _I, _I]),
+    "moe_rope": (_I, [_P, _P, _I64, _I, _I, _P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I64, _P]),
+    "moe_kv_append": (_I, [_P, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I, _P, _I64, _P]),
+    "moe_attn_paged": (_I, [_P, _P, _P, _I64, _I, _F, _I, _I, _P, _P, _I64, _P, _P, _SZ, _P]),
+    "moe_attn_paged_workspace_size": (_SZ, [_I, _I, _I]),
     "moe_workspace_size": (_SZ, [_I, _I64, _I, _I, _I, _I]),
     "moe_row_capacity": (_I64, [_I64, _I, _I, _I]),
     "moe_status": (_I, [_P]),
@@ -59,6 +64,26 @@ class Swiglu(ctypes.Structure):
                 ("up_offset", ctypes.c_float)]
 
 
+class KVCache(ctypes.Structure):
+    """moe_kv_cache: a paged cache of keys and values (strides in elements)."""
+    _fields_ = [("k", _P), ("v", _P), ("n_pages", _I64), ("page_stride", _I64),
+                ("head_stride", _I64), ("token_stride", _I64), ("page_size", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
+class KVBatchArgs(ctypes.Structure):
+    """moe_kv_batch: a ragged batch of new tokens and their pages."""
+    _fields_ = [("cu_q", _P), ("kv_len", _P), ("page_table", _P), ("table_stride", _I64),
+                ("T", _I64), ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_q", ctypes.c_int32)]
+
+
+class Rotary(ctypes.Structure):
+    """moe_rotary: frequencies in turns a position, the axis of each pair."""
+    _fields_ = [("turns", _P), ("axis", _P), ("rd", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 MOE_WS_PERMUTE = 1
 MOE_WS_ROUTE_BWD = 2
 MOE_WS_ROUTE = 3
@@ -67,7 +92,7 @@ KERNELS = {
     "router_logits": 1, "topk": 2, "permute": 3, "gateup_fwd": 4, "down_fwd": 5,
     "combine": 6, "combine_bwd": 7, "down_dgrad": 8, "gateup_dgrad": 9,
     "wgrad_down": 10, "wgrad_gateup": 11, "route_bwd": 12,
-    "decode": 13, "fused_fwd": 14,
+    "decode": 13, "fused_fwd": 14, "rope": 15, "attn": 16, "attn_combine": 17,
 }
 
 _lib = None

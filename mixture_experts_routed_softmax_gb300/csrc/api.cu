@@ -114,7 +114,7 @@ const char* moe_status_str(int code) {
     case MOE_ERR_UNSUPPORTED: return "MOE_ERR_UNSUPPORTED: shape not supported by the kernels";
     case MOE_ERR_CAPACITY: return "MOE_ERR_CAPACITY: R_cap below T*k + E*(align-1)";
     case MOE_ERR_CUDA: return "MOE_ERR_CUDA: a CUDA call failed";
-    case MOE_ERR_DEVICE_INDEX: return "MOE_ERR_DEVICE_INDEX: expert id outside [0, E)";
+    case MOE_ERR_DEVICE_INDEX: return "MOE_ERR_DEVICE_INDEX: an expert id, cache page or length out of range";
     case MOE_ERR_DEVICE_TIMEOUT: return "MOE_ERR_DEVICE_TIMEOUT: a bounded wait in a kernel gave up";
     default: return "unknown moe status code";
   }
@@ -136,7 +136,7 @@ int moe_status(moe_stream_t stream) {
 }
 
 int moe_timer_start(int kernel, int max_launches) {
-  if (kernel < MOE_KERNEL_ROUTER_LOGITS || kernel > MOE_KERNEL_FUSED_FWD || max_launches <= 0)
+  if (kernel < MOE_KERNEL_ROUTER_LOGITS || kernel > MOE_KERNEL_ATTN_COMBINE || max_launches <= 0)
     return MOE_ERR_ARG;
   std::lock_guard<std::mutex> lock(g_timer.mu);
   if (g_timer.kernel != 0) return MOE_ERR_ARG;

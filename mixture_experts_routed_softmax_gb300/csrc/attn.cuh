@@ -1,0 +1,334 @@
+// attn.cuh — what the attention kernels share: the batch, the mask as a key
+// range per row, and the schedule that cuts the batch's work evenly.
+//
+// Work units. The G query heads of one key/value head and the n_q new tokens
+// of a sequence are n_q * G rows over the same keys: row r is token r / G,
+// head h * G + r % G. A unit is (sequence b, head h, row tile m of TM rows);
+// its keys are one range (the union of its rows' masks), cut into tiles of TN.
+// Units in the order (b, h, m) laid end to end, one tile a step (an empty unit
+// counts one: its rows are still to be written), make a line of `total` steps;
+// CTA c of n takes steps [total * c / n, total * (c + 1) / n). Every CTA so
+// has the same number of tiles whatever the lengths, and writes at most two
+// partial results: the unit it enters in the middle (slot 0) and the unit it
+// begins and does not end (slot 1). A second launch joins the parts of each
+// cut unit in order, so results do not depend on timing.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+constexpr int kAttnMaxD = 128;
+constexpr int kAttnMaxKeys = 1 << 30;
+
+struct AttnBatch {
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t table_stride;
+  int64_t n_pages, page_stride, token_stride;
+  int T, B, max_pages, page_size;
+};
+
+inline AttnBatch attn_batch(const moe_kv_cache& c, const moe_kv_batch& b) {
+  return AttnBatch{b.cu_q, b.kv_len, b.page_table, b.table_stride, c.n_pages, c.page_stride,
+                   c.token_stride, (int)b.T, b.B, b.max_pages, c.page_size};
+}
+
+struct AttnArgs {
+  AttnBatch bt;
+  const moe_bf16* k;
+  const moe_bf16* v;
+  int64_t head_stride;
+  const moe_bf16* q;
+  moe_bf16* out;
+  int64_t q_stride, out_stride;
+  const float* sinks;
+  float* lse;
+  int Hq, Hkv, G, D;
+  float scale_log2;      // scale * log2(e): scores and maxima are kept in powers of two
+  int causal, window;    // window 0: none
+  float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
+  float2* part_ml;       // [2 * CTAs][TM] their (max, sum)
+  int* status;
+};
+
+// ------------------------------------------------------------- the batch --
+// The sequence row t belongs to: the number of sequences that end at or
+// before t. Called by a whole warp; 32 ends are looked at a step. -1: none.
+__device__ __forceinline__ int find_sequence(const int32_t* cu_q, int B, int t, int lane) {
+  int lo = 0, end = B;      // the answer lies in [lo, end]
+  while (lo < end) {
+    const int step = (end - lo + 31) >> 5;
+    const int64_t last = (int64_t)lo + (int64_t)(lane + 1) * step - 1;
+    const bool past = last < end && cu_q[last + 1] <= t;
+    const int full = __popc(__ballot_sync(0xFFFFFFFFu, past));
+    lo += full * step;
+    // the first group not wholly past: its last sequence is known to end later
+    if (full < 32 && lo + step - 1 < end) end = lo + step - 1;
+    if (step == 1) break;
+  }
+  return lo < B ? lo : -1;
+}
+
+struct Seq {
+  int q0, nq, n;     // first row, new tokens, keys
+};
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
+  const int s = a.bt.cu_q[b], e = a.bt.cu_q[b + 1];
+  int n = a.bt.kv_len[b];
+  const int cap = a.bt.max_pages * a.bt.page_size;
+  Seq q{s, e - s, n};
+  if (s < 0 || e < s || e > a.bt.T || n < 0 || n > cap) {
+    raise_status(a.status, MOE_ERR_DEVICE_INDEX);
+    q.n = n < 0 ? 0 : n > cap ? cap : n;
+    if (s < 0 || e < s || e > a.bt.T) q = Seq{0, 0, q.n};
+  }
+  return q;
+}
+
+// ---------------------------------------------------------------- the mask --
+// Token i of a sequence sees keys [key_lo, key_hi).
+__device__ __forceinline__ int key_hi(const AttnArgs& a, const Seq& s, int i) {
+  if (!a.causal) return s.n;
+  const int c = s.n - s.nq + i;
+  return c < 0 ? 0 : c + 1;       // c < n always
+}
+__device__ __forceinline__ int key_lo(const AttnArgs& a, const Seq& s, int i) {
+  if (a.window == 0) return 0;
+  const int c = s.n - s.nq + i - a.window + 1;
+  return c < 0 ? 0 : c;
+}
+
+template <int TM, int TN>
+struct Tiling {
+  static __device__ __forceinline__ int row_tiles(const AttnArgs& a, const Seq& s) {
+    return (s.nq * a.G + TM - 1) / TM;
+  }
+  // key range and tiles of row tile m
+  struct Span {
+    int lo, hi, t0, nt;
+  };
+  static __device__ __forceinline__ Span span(const AttnArgs& a, const Seq& s, int m) {
+    const int rows = s.nq * a.G;
+    const int r0 = m * TM;
+    const int r1 = min(r0 + TM, rows) - 1;
+    Span p;
+    p.lo = key_lo(a, s, r0 / a.G);
+    p.hi = key_hi(a, s, r1 / a.G);
+    if (p.hi <= p.lo) {
+      p.lo = p.hi = p.t0 = p.nt = 0;
+    } else {
+      p.t0 = p.lo / TN;
+      p.nt = (p.hi + TN - 1) / TN - p.t0;
+    }
+    return p;
+  }
+  static __device__ __forceinline__ int weight(const AttnArgs& a, const Seq& s, int m) {
+    const int nt = span(a, s, m).nt;
+    return nt > 0 ? nt : 1;
+  }
+};
+
+// ------------------------------------------------------------ the schedule --
+struct Place {              // of a step of the line, in shared memory
+  long long total;          // steps of the line
+  int b, h, m;
+  int off;                  // steps into the unit
+  long long warp_sum[32];
+  long long rem, head_w;
+};
+
+__device__ __forceinline__ long long cta_start(long long total, int cta, int n) {
+  return total * cta / n;
+}
+
+// Steps of one head of the sequence of each lane (0 for nq = 0). A lane with
+// many row tiles gets its warp's help.
+template <int TM, int TN>
+__device__ __forceinline__ long long head_weight(const AttnArgs& a, const Seq& s) {
+  using TL = Tiling<TM, TN>;
+  const int lane = threadIdx.x & 31;
+  const int nm = s.nq > 0 ? TL::row_tiles(a, s) : 0;
+  long long w = 0;
+  if (nm <= 4)
+    for (int m = 0; m < nm; ++m) w += TL::weight(a, s, m);
+  uint32_t big = __ballot_sync(0xFFFFFFFFu, nm > 4);
+  while (big) {
+    const int src = __ffs(big) - 1;
+    big &= big - 1;
+    Seq t;
+    t.q0 = 0;
+    t.nq = __shfl_sync(0xFFFFFFFFu, s.nq, src);
+    t.n = __shfl_sync(0xFFFFFFFFu, s.n, src);
+    const int tm = __shfl_sync(0xFFFFFFFFu, nm, src);
+    long long part = 0;
+    for (int m = lane; m < tm; m += 32) part += TL::weight(a, t, m);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+    if (lane == src) w = part;
+  }
+  return w;
+}
+
+// Where CTA `cta` of `n` begins, into `pl` (by the whole block of NT threads,
+// ends with a barrier). False when the line has no steps.
+template <int TM, int TN, int NT>
+__device__ bool locate(const AttnArgs& a, int cta, int n, Place& pl) {
+  constexpr int NW = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = a.bt.B;
+  long long base = 0, total = 0, x0 = 0;
+  // first pass: the line's length; second: the sequence that holds step x0
+  for (int pass = 0; pass < 2; ++pass) {
+    base = 0;
+    for (int b0 = 0; b0 < B; b0 += NT) {
+      const int b = b0 + tid;
+      Seq s{0, 0, 0};
+      if (b < B) s = load_seq(a, b);
+      const long long hw = head_weight<TM, TN>(a, s);
+      const long long w = hw * a.Hkv;
+      long long inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      if (lane == 31) pl.warp_sum[warp] = inc;
+      __syncthreads();
+      long long before = 0, all = 0;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const long long v = pl.warp_sum[i];
+        if (i < warp) before += v;
+        all += v;
+      }
+      if (pass == 1) {
+        const long long lo = base + before + inc - w;
+        if (x0 >= lo && x0 < lo + w) {
+          pl.b = b;
+          pl.rem = x0 - lo;
+          pl.head_w = hw;
+        }
+      }
+      base += all;
+      __syncthreads();
+    }
+    if (pass == 0) {
+      total = base;
+      if (total == 0) return false;
+      x0 = cta_start(total, cta, n);
+    }
+  }
+  if (warp == 0) {
+    const Seq s = load_seq(a, pl.b);
+    const int h = (int)(pl.rem / pl.head_w);
+    long long rem = pl.rem - h * pl.head_w;
+    const int nm = Tiling<TM, TN>::row_tiles(a, s);
+    for (int m0 = 0; m0 < nm; m0 += 32) {
+      const int m = m0 + lane;
+      const int w = m < nm ? Tiling<TM, TN>::weight(a, s, m) : 0;
+      long long inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      const bool here = rem >= inc - w && rem < inc;
+      if (here) {
+        pl.m = m;
+        pl.off = (int)(rem - (inc - w));
+      }
+      if (__any_sync(0xFFFFFFFFu, here)) break;
+      rem -= __shfl_sync(0xFFFFFFFFu, inc, 31);
+    }
+    if (lane == 0) {
+      pl.h = h;
+      pl.total = total;
+    }
+  }
+  __syncthreads();
+  return true;
+}
+
+// The units of a CTA's stretch, one after the other.
+template <int TM, int TN>
+struct Walk {
+  using TL = Tiling<TM, TN>;
+  const AttnArgs& a;
+  Seq s;
+  int b, h, m, nm, off;
+  long long left;      // steps of the stretch still to do, this unit's included
+  typename TL::Span sp;
+  int w, take;         // the unit's steps, and those of this CTA
+
+  __device__ __forceinline__ Walk(const AttnArgs& a_, const Place& pl, int cta, int n)
+      : a(a_), b(pl.b), h(pl.h), m(pl.m), off(pl.off) {
+    left = cta_start(pl.total, cta + 1, n) - cta_start(pl.total, cta, n);
+    s = load_seq(a, b);
+    nm = TL::row_tiles(a, s);
+    unit();
+  }
+  __device__ __forceinline__ void unit() {
+    sp = TL::span(a, s, m);
+    w = sp.nt > 0 ? sp.nt : 1;
+    take = (long long)(w - off) < left ? w - off : (int)left;
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool whole() const { return off == 0 && take == w; }
+  __device__ __forceinline__ int slot() const { return off > 0 ? 0 : 1; }
+  __device__ __forceinline__ void next() {
+    left -= take;
+    if (left <= 0) return;
+    off = 0;
+    if (++m == nm) {
+      m = 0;
+      if (++h == a.Hkv) {
+        h = 0;
+        nm = 0;
+        while (nm == 0 && ++b < a.bt.B) {
+          s = load_seq(a, b);
+          nm = TL::row_tiles(a, s);
+        }
+        if (nm == 0) {      // lengths that changed under the kernel
+          left = 0;
+          return;
+        }
+      }
+    }
+    unit();
+  }
+};
+
+// ------------------------------------------------------------- arithmetic --
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float neg_inf() { return __int_as_float((int)0xFF800000); }
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// A row's (max, sum) with its sink joined, the factor its accumulator takes and
+// its log-sum-exp. A row without keys (l = 0) gets factor 0.
+struct RowEnd {
+  float factor, lse;
+};
+__device__ __forceinline__ RowEnd row_end(float m, float l, const float* sinks, int head) {
+  float f = 1.f;
+  if (sinks) {
+    const float s2 = sinks[head] * kLog2e;
+    const float mt = fmaxf(m, s2);
+    const float ref = mt == neg_inf() ? 0.f : mt;
+    f = ex2(m - ref);
+    l = l * f + ex2(s2 - ref);
+    m = mt;
+  }
+  RowEnd e;
+  e.factor = l == 0.f ? 0.f : f / l;
+  e.lse = l == 0.f ? neg_inf() : m * kLn2 + logf(l);
+  return e;
+}
+
+}  // namespace moe

@@ -117,4 +117,23 @@ cudaError_t launch_wgrad_gateup(const GroupedDims& g, const moe_bf16* xp, const 
                                 const moe_bf16* dU, moe_bf16* dw_gate, moe_bf16* dw_up,
                                 int* status, cudaStream_t s);
 
+
+// rope.cu
+cudaError_t launch_rope(const moe_rotary* rot, const int32_t* pos, int64_t T, int D,
+                        int transpose, const moe_bf16* q, int64_t q_stride, int Hq,
+                        moe_bf16* q_out, int64_t qo_stride, const moe_bf16* k, int64_t k_stride,
+                        int Hk, moe_bf16* k_out, int64_t ko_stride, int* status, cudaStream_t s);
+cudaError_t launch_kv_append(const moe_kv_cache& c, const moe_kv_batch& b, const moe_rotary* rot,
+                             const int32_t* pos, const moe_bf16* k, int64_t k_stride,
+                             const moe_bf16* v, int64_t v_stride, const moe_bf16* q,
+                             int64_t q_stride, int Hq, moe_bf16* q_out, int64_t qo_stride,
+                             int* status, cudaStream_t s);
+
+// attn_rows.cu
+size_t attn_ws_bytes(int D);
+cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_bf16* q,
+                        int64_t q_stride, int Hq, float scale, int causal, int window,
+                        const float* sinks, moe_bf16* out, int64_t out_stride, float* lse,
+                        void* ws, int* status, cudaStream_t s);
+
 }  // namespace moe
