@@ -262,8 +262,11 @@ struct Walk {
   typename TL::Span sp;
   int w, take;         // the unit's steps, and those of this CTA
 
-  __device__ __forceinline__ Walk(const AttnArgs& a_, const Place& pl, int cta, int n)
-      : a(a_), b(pl.b), h(pl.h), m(pl.m), off(pl.off) {
+  // work: locate's answer; false: a walk of nothing
+  __device__ __forceinline__ Walk(const AttnArgs& a_, const Place& pl, int cta, int n,
+                                  bool work = true)
+      : a(a_), b(pl.b), h(pl.h), m(pl.m), off(pl.off), left(0) {
+    if (!work) return;
     left = cta_start(pl.total, cta + 1, n) - cta_start(pl.total, cta, n);
     s = load_seq(a, b);
     nm = TL::row_tiles(a, s);
@@ -330,5 +333,10 @@ __device__ __forceinline__ RowEnd row_end(float m, float l, const float* sinks, 
   e.lse = l == 0.f ? neg_inf() : m * kLn2 + logf(l);
   return e;
 }
+
+// attn_chunk.cu
+bool attn_chunk_takes(int page_size);
+size_t attn_chunk_ws_bytes(int D);
+cudaError_t launch_attn_chunk(const AttnArgs& a, const moe_kv_cache& c, void* ws, cudaStream_t s);
 
 }  // namespace moe

@@ -50,6 +50,7 @@
 // an expert with no rows gets a zero tile.
 #include "common.cuh"
 #include "internal.h"
+#include "tmap.h"
 
 #include <mutex>
 
@@ -1441,6 +1442,20 @@ static bool map3d_out(CUtensorMap* m, const void* ptr, uint64_t N, uint64_t M, u
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_kv(CUtensorMap* m, const void* ptr, const moe_kv_cache& c, int slots) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.page_size, (cuuint64_t)c.Hkv,
+                        (cuuint64_t)c.n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * 2, (cuuint64_t)c.head_stride * 2,
+                           (cuuint64_t)c.page_stride * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)slots, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // tiles_upper: an upper bound on the kernel's tiles (pair tiles for PAIR). A
