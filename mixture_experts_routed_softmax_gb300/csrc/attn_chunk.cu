@@ -46,14 +46,55 @@ struct ChunkGeo {
   static constexpr uint32_t o_col0 = 256;                // O of half h: 256 + h * DP
 };
 
-// O[tmem] (+)= P[tmem] * V[smem]
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// The product-issuing warp runs as one: every value an instruction takes is the
+// same in all lanes (uniform registers), and one elected lane issues. A single
+// lane running ahead alone costs about 90 cycles an instruction in moves to
+// uniform registers, more than the 32 to 64 the product itself takes.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e;
+}
+// A descriptor from its two halves: only the address in the low one varies.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  return ((uint64_t)hi << 32) | lo;
+}
+// S[tmem] (+)= Q[smem] * K[smem]^T, by the elected lane
+__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d_tmem, uint64_t adesc,
+                                        uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+// O[tmem] (+)= P[tmem] * V[smem]
+__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                        uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(
+          bar),
+      "r"(leader)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -81,6 +122,11 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float* r) {
         "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ void tmem_st32f(uint32_t taddr, const float* r) {
   uint32_t u[32];
@@ -301,84 +347,95 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     } else if (work && warp == kMmaWarp) {
       // ----------------------------------------------------------- products --
-      if (lane == 0) {
-        constexpr uint32_t kIdQK = idesc_bf16(128, kChunkTN, 0, 0);
-        constexpr uint32_t kIdPV = idesc_bf16(128, DP, 0, 1);
-        int kslot = 0;                    // ring slot of the next K tile
-        uint32_t kphase = 0;
-        uint32_t units[2] = {0, 0}, tiles[2] = {0, 0};
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          ok = ok && mbar_wait_bounded(smem_u32(bar), parity, abort, a.status);
-          return ok;
-        };
-        auto qk = [&](int h, int slot) {
+      constexpr uint32_t kIdQK = idesc_bf16(128, kChunkTN, 0, 0);
+      constexpr uint32_t kIdPV = idesc_bf16(128, DP, 0, 1);
+      const uint32_t leader = elect_one();
+      const uint32_t td = uniform(tmem);
+      const uint64_t qd0 = sdesc_sw128(s_q, 16, 1024);
+      const uint64_t kd0 = sdesc_sw128(s_kv, 16, 1024);
+      const uint64_t vd0 = sdesc_sw128(s_kv, kChunkTN * 128, 1024);
+      int kslot = 0;                    // ring slot of the next K tile
+      uint32_t kphase = 0;
+      uint32_t units[2] = {0, 0}, tiles[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && mbar_wait_bounded(smem_u32(bar), parity, abort, a.status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        return ok;
+      };
+      auto commit = [&](uint64_t* bar) { umma_commit_by(leader, smem_u32(bar)); };
+      auto qk = [&](int h, int slot) {
+        const uint32_t q = uniform((uint32_t)qd0 + h * (G::q_half >> 4));
+        const uint32_t k = uniform((uint32_t)kd0 + slot * (G::tile >> 4));
+        const uint32_t hi = uniform((uint32_t)(kd0 >> 32));
+        const uint32_t d = uniform(td + G::s_col0 + h * 128);
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          constexpr int kBlock = (128 * 128) >> 4;
+          const int at = (kk >> 2) * kBlock + (kk & 3) * 2;
+          umma_ss(leader, d, desc_of(q + at, hi), desc_of(k + at, hi), kIdQK, kk > 0);
+        }
+        commit(&sh.s_full[h]);
+      };
+      auto pv = [&](int h, int slot, bool first) {
+        const uint32_t v = uniform((uint32_t)vd0 + slot * (G::tile >> 4));
+        const uint32_t hi = uniform((uint32_t)(vd0 >> 32));
+        const uint32_t d = uniform(td + G::o_col0 + h * DP);
+        const uint32_t p = uniform(td + G::s_col0 + h * 128);
+        const uint32_t add = uniform(first ? 0u : 1u);
+#pragma unroll
+        for (int kk = 0; kk < kChunkTN / 16; ++kk)
+          umma_ts(leader, d, p + kk * 8, desc_of(v + kk * (2048 >> 4), hi), kIdPV,
+                  kk > 0 ? 1u : add);
+      };
+      for (Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x); wk.more() && ok;
+           wk.next()) {
+        const int nt = wk.sp.nt > 0 ? wk.take : 0;
+        if (nt == 0) continue;
+        const int nh = wk.s.nq * a.G - wk.m * kChunkTM > 128 ? 2 : 1;
+        auto step = [&]() { if (++kslot == G::slots) { kslot = 0; kphase ^= 1u; } };
+        // the first tile's scores
+        if (!wait(&sh.kv_full[kslot], kphase)) break;
+        for (int h = 0; h < nh; ++h) {
+          if (!wait(&sh.q_ready[h], units[h] & 1)) break;
+          ++units[h];
           tc_fence_after();
-          const uint32_t sq = s_q + h * G::q_half, sk = s_kv + slot * G::tile;
-#pragma unroll
-          for (int kk = 0; kk < DP / 16; ++kk) {
-            const uint32_t at = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-            umma_bf16(tmem + G::s_col0 + h * 128, sdesc_sw128(sq + at, 16, 1024),
-                      sdesc_sw128(sk + at, 16, 1024), kIdQK, kk > 0);
-          }
-          umma_commit(smem_u32(&sh.s_full[h]));
-        };
-        auto pv = [&](int h, int slot, bool first) {
-          const uint32_t sv = s_kv + slot * G::tile;
-#pragma unroll
-          for (int kk = 0; kk < kChunkTN / 16; ++kk)
-            umma_bf16_ts(tmem + G::o_col0 + h * DP, tmem + G::s_col0 + h * 128 + kk * 8,
-                         sdesc_sw128(sv + kk * 2048, kChunkTN * 128, 1024), kIdPV,
-                         !(first && kk == 0));
-        };
-        for (Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x); wk.more() && ok;
-             wk.next()) {
-          const int nt = wk.sp.nt > 0 ? wk.take : 0;
-          if (nt == 0) continue;
-          const int nh = wk.s.nq * a.G - wk.m * kChunkTM > 128 ? 2 : 1;
-          auto step = [&]() { if (++kslot == G::slots) { kslot = 0; kphase ^= 1u; } };
-          // the first tile's scores
-          if (!wait(&sh.kv_full[kslot], kphase)) break;
+          qk(h, kslot);
+        }
+        if (!ok) break;
+        commit(&sh.kv_empty[kslot]);
+        step();
+        for (int j = 0; j < nt; ++j) {
+          const int vslot = kslot;
+          if (!wait(&sh.kv_full[vslot], kphase)) break;
+          step();
+          const bool more = j + 1 < nt;
+          const int nkslot = kslot;
+          if (more && !wait(&sh.kv_full[nkslot], kphase)) break;
           for (int h = 0; h < nh; ++h) {
-            if (!wait(&sh.q_ready[h], units[h] & 1)) break;
-            ++units[h];
-            qk(h, kslot);
+            if (!wait(&sh.p_ready[h], tiles[h] & 1)) break;
+            ++tiles[h];
+            tc_fence_after();
+            // products of one thread run in the order of issue: the next scores
+            // overwrite P's columns after this product has read them
+            const bool skip = *(volatile int*)&sh.by_hand[h];
+            if (!__any_sync(0xFFFFFFFFu, skip)) pv(h, vslot, j == 0);
+            if (more) qk(h, nkslot);
+            else commit(&sh.o_done[h]);
           }
           if (!ok) break;
-          umma_commit(smem_u32(&sh.kv_empty[kslot]));
-          step();
-          for (int j = 0; j < nt; ++j) {
-            const int vslot = kslot;
-            if (!wait(&sh.kv_full[vslot], kphase)) break;
+          commit(&sh.kv_empty[vslot]);
+          if (more) {
+            commit(&sh.kv_empty[nkslot]);
             step();
-            const bool more = j + 1 < nt;
-            const int nkslot = kslot;
-            for (int h = 0; h < nh; ++h) {
-              if (!wait(&sh.p_ready[h], tiles[h] & 1)) break;
-              ++tiles[h];
-              tc_fence_after();
-              // products of one thread run in the order of issue: the next scores
-              // overwrite P's columns after this product has read them
-              if (!*(volatile int*)&sh.by_hand[h]) pv(h, vslot, j == 0);
-              if (!more) umma_commit(smem_u32(&sh.o_done[h]));
-              if (more) {
-                if (h == 0 && !wait(&sh.kv_full[nkslot], kphase)) break;
-                qk(h, nkslot);
-              }
-            }
-            if (!ok) break;
-            umma_commit(smem_u32(&sh.kv_empty[vslot]));
-            if (more) {
-              umma_commit(smem_u32(&sh.kv_empty[nkslot]));
-              step();
-            }
           }
         }
-        // every product has finished before tensor memory is freed
-        umma_commit(smem_u32(&sh.drain));
-        volatile int never = 0;
-        mbar_wait_bounded(smem_u32(&sh.drain), 0, &never, a.status);
       }
+      // every product has finished before tensor memory is freed
+      commit(&sh.drain);
+      volatile int never = 0;
+      mbar_wait_bounded(smem_u32(&sh.drain), 0, &never, a.status);
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ softmax --
@@ -454,9 +511,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           float mx[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = sc[i];
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
 #pragma unroll
-          for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], sc[c]);
+          for (int c = 8; c < 128; c += 2)
+            mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], sc[c], sc[c + 1]);
           const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
           const bool grew = m2 > m_ref + kRescaleAt;      // true for the first key a row sees
           if (__any_sync(0xFFFFFFFFu, grew)) {
