@@ -28,11 +28,24 @@ struct AttnBatch {
   int64_t table_stride;
   int64_t n_pages, page_stride, token_stride;
   int T, B, max_pages, page_size;
+  int page_shift;        // log2 of page_size, or -1
 };
+
+inline int shift_of(int v) {
+  if (v & (v - 1)) return -1;
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+// Divisions by sizes known at run time take some hundred cycles where powers
+// of two, the common case, take a shift.
+__device__ __forceinline__ int page_of(const AttnBatch& b, int key) {
+  return b.page_shift >= 0 ? key >> b.page_shift : key / b.page_size;
+}
 
 inline AttnBatch attn_batch(const moe_kv_cache& c, const moe_kv_batch& b) {
   return AttnBatch{b.cu_q, b.kv_len, b.page_table, b.table_stride, c.n_pages, c.page_stride,
-                   c.token_stride, (int)b.T, b.B, b.max_pages, c.page_size};
+                   c.token_stride, (int)b.T, b.B, b.max_pages, c.page_size, shift_of(c.page_size)};
 }
 
 struct AttnArgs {
@@ -46,12 +59,17 @@ struct AttnArgs {
   const float* sinks;
   float* lse;
   int Hq, Hkv, G, D;
+  int g_shift;           // log2 of G, or -1
   float scale_log2;      // scale * log2(e): scores and maxima are kept in powers of two
   int causal, window;    // window 0: none
   float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
   float2* part_ml;       // [2 * CTAs][TM] their (max, sum)
   int* status;
 };
+
+__device__ __forceinline__ int div_group(const AttnArgs& a, int row) {
+  return a.g_shift >= 0 ? row >> a.g_shift : row / a.G;
+}
 
 // ------------------------------------------------------------- the batch --
 // The sequence row t belongs to: the number of sequences that end at or
@@ -114,8 +132,8 @@ struct Tiling {
     const int r0 = m * TM;
     const int r1 = min(r0 + TM, rows) - 1;
     Span p;
-    p.lo = key_lo(a, s, r0 / a.G);
-    p.hi = key_hi(a, s, r1 / a.G);
+    p.lo = key_lo(a, s, div_group(a, r0));
+    p.hi = key_hi(a, s, div_group(a, r1));
     if (p.hi <= p.lo) {
       p.lo = p.hi = p.t0 = p.nt = 0;
     } else {
@@ -261,6 +279,7 @@ struct Walk {
   long long left;      // steps of the stretch still to do, this unit's included
   typename TL::Span sp;
   int w, take;         // the unit's steps, and those of this CTA
+  int all_lo, all_hi;  // the keys every row of the unit sees
 
   // work: locate's answer; false: a walk of nothing
   __device__ __forceinline__ Walk(const AttnArgs& a_, const Place& pl, int cta, int n,
@@ -276,6 +295,15 @@ struct Walk {
     sp = TL::span(a, s, m);
     w = sp.nt > 0 ? sp.nt : 1;
     take = (long long)(w - off) < left ? w - off : (int)left;
+    const int rows = s.nq * a.G;
+    all_lo = key_lo(a, s, div_group(a, min(m * TM + TM, rows) - 1));
+    all_hi = key_hi(a, s, div_group(a, m * TM));
+  }
+  // the CTA's tile j of the unit; an edge tile is one that some row sees in part
+  __device__ __forceinline__ int first_key(int j) const { return (sp.t0 + off + j) * TN; }
+  __device__ __forceinline__ bool edge(int j) const {
+    const int k0 = first_key(j);
+    return k0 < all_lo || k0 + TN > all_hi;
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ bool whole() const { return off == 0 && take == w; }
@@ -302,6 +330,20 @@ struct Walk {
     unit();
   }
 };
+
+// ---------------------------------------------------- asynchronous copies --
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
+  const int n = full ? 16 : 0;       // 0: the destination is filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // ------------------------------------------------------------- arithmetic --
 __device__ __forceinline__ float ex2(float x) {

@@ -17,22 +17,28 @@
 // half's products run.
 //   warps 0-3, 4-7   softmax of half 0 and 1: one row per thread (the row's
 //                    maximum and sum need no shuffles), the accumulator's
-//                    rescale, the epilogue, and loading the half's queries
-//   warp 8           issues the products (one thread); owns tensor memory
+//                    rescale, the epilogue
+//   warp 8           issues the products; owns tensor memory
 //   warp 9           loads K and V tiles by TMA through a ring, one box per
 //                    stretch of keys that neither a page nor a tile cuts
+//   warps 10, 11     the queries of half 0 and 1, as soon as the unit before
+//                    has had its last scores; the values of tiles that some
+//                    row sees in part: out-of-range rows become zeros, and
+//                    infinities and NaN are looked for
 #include "attn.cuh"
 #include "attn_join.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "tmap.h"
 
+#include <type_traits>
+
 namespace moe {
 
 constexpr int kChunkTM = 256;
 constexpr int kChunkTN = 128;
-constexpr int kChunkThreads = 384;    // warps 10 and 11 only give up their registers
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kChunkThreads = 384;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
 constexpr float kRescaleAt = 8.f;
 
 template <int DP>
@@ -42,8 +48,11 @@ struct ChunkGeo {
   static constexpr int q_half = 128 * DP * 2;
   static constexpr int slots = DP == 128 ? 5 : 8;        // K and V tiles alternate
   static constexpr int smem = 2 * q_half + slots * tile + 1024;
-  static constexpr uint32_t s_col0 = 0;                  // S (and P) of half h: h * 128
-  static constexpr uint32_t o_col0 = 256;                // O of half h: 256 + h * DP
+  // Tensor memory, 512 columns: O of the two halves, and scores (the weights in
+  // their place) of as many items as are left: 2 for D = 128, 3 for 64, where
+  // a half's next scores so wait for it while it works on the present ones.
+  static constexpr int bufs = (512 - 2 * DP) / 128;
+  static constexpr uint32_t o_col0 = bufs * 128;
 };
 
 // The product-issuing warp runs as one: every value an instruction takes is the
@@ -53,49 +62,33 @@ struct ChunkGeo {
 __device__ __forceinline__ uint32_t uniform(uint32_t v) {
   return __shfl_sync(0xFFFFFFFFu, v, 0);
 }
-__device__ __forceinline__ uint32_t elect_one() {
+__device__ __forceinline__ bool elect_one() {
   uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "elect.sync _|p, 0xFFFFFFFF;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(e));
-  return e;
+  return e != 0;
 }
 // A descriptor from its two halves: only the address in the low one varies.
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
   return ((uint64_t)hi << 32) | lo;
 }
-// S[tmem] (+)= Q[smem] * K[smem]^T, by the elected lane
-__device__ __forceinline__ void umma_ss(uint32_t leader, uint32_t d_tmem, uint64_t adesc,
-                                        uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
-      : "memory");
-}
 // O[tmem] (+)= P[tmem] * V[smem]
-__device__ __forceinline__ void umma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
-                                        uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(leader)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "setp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(
-          bar),
-      "r"(leader)
-      : "memory");
+// The product warp's wait when the first try has not succeeded.
+__device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                         int* status) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -174,14 +167,11 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return o;
 }
 
-// no infinity or NaN among eight bf16 values
-__device__ __forceinline__ bool finite8(const uint4& v) {
-  bool bad = false;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    bad = bad || (w[i] & 0x7F800000u) == 0x7F800000u || (w[i] & 0x7F80u) == 0x7F80u;
-  return !bad;
+// nonzero: an infinity or NaN among eight bf16 values (an exponent of all ones)
+__device__ __forceinline__ uint32_t not_finite8(const uint4& v) {
+  constexpr uint32_t e = 0x7F807F80u;
+  return __vcmpeq2(v.x & e, e) | __vcmpeq2(v.y & e, e) | __vcmpeq2(v.z & e, e) |
+         __vcmpeq2(v.w & e, e);
 }
 
 // O += P V of one tile by a warp for its 32 rows (one a lane), over the keys
@@ -235,21 +225,44 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Waits until a count in shared memory has reached `need`; gives up like
+// mbar_wait_bounded.
+__device__ __forceinline__ bool count_wait_bounded(const int* count, int need,
+                                                   volatile int* abort_flag, int* status) {
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1; *(const volatile int*)count < need; ++i) {
+    __nanosleep(20);
+    if ((i & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > (uint64_t)kWaitLimitNs) {
+        *abort_flag = 1;
+        raise_status(status, MOE_ERR_DEVICE_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
 struct ChunkShared {
   Place pl;
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t v_seen[8];   // an edge tile's values have been looked through
+  uint64_t q_ready[2], q_free[2], o_done[2], drain;
+  uint64_t s_full[2][3];   // of a half, its items in turn (each half waits for every one of its
+                           // own, so that no phase is taken for the one after the next)
+  uint64_t p_ready[3];     // of a buffer
   uint32_t tmem;
   int abort;
-  uint64_t looked[2];   // the half's warps have looked through a tile's values
-  int bad[2][2][4];     // what each of them found (two tiles in turn)
-  int by_hand[2];       // they have added this tile's P V themselves
+  int issued;           // tiles whose loads have been issued
+  int bad[8][2];        // per slot: an infinity or NaN among them (each helper's half)
 };
 
 template <int DP>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-    attn_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mapK,
-                      const __grid_constant__ CUtensorMap mapV, int box) {
+    attn_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mapQ,
+                      const __grid_constant__ CUtensorMap mapK,
+                      const __grid_constant__ CUtensorMap mapV, int box, int q_by_tma) {
   using G = ChunkGeo<DP>;
   using TL = Tiling<kChunkTM, kChunkTN>;
   extern __shared__ uint8_t smem_raw[];
@@ -266,16 +279,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int i = 0; i < G::slots; ++i) {
       mbar_init(smem_u32(&sh.kv_full[i]), 1);
       mbar_init(smem_u32(&sh.kv_empty[i]), 1);
+      mbar_init(smem_u32(&sh.v_seen[i]), 2);
     }
     for (int h = 0; h < 2; ++h) {
-      mbar_init(smem_u32(&sh.q_ready[h]), 4);
-      mbar_init(smem_u32(&sh.s_full[h]), 1);
-      mbar_init(smem_u32(&sh.p_ready[h]), 4);
+      mbar_init(smem_u32(&sh.q_ready[h]), 1);
+      mbar_init(smem_u32(&sh.q_free[h]), 1);
       mbar_init(smem_u32(&sh.o_done[h]), 1);
-      mbar_init(smem_u32(&sh.looked[h]), 4);
+    }
+    for (int i = 0; i < G::bufs; ++i) {
+      mbar_init(smem_u32(&sh.s_full[0][i]), 1);
+      mbar_init(smem_u32(&sh.s_full[1][i]), 1);
+      mbar_init(smem_u32(&sh.p_ready[i]), 4);
     }
     mbar_init(smem_u32(&sh.drain), 1);
     sh.abort = 0;
+    sh.issued = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -306,7 +324,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const bool mine = lane < nbox && key < wk.sp.hi && key + box > wk.sp.lo;
           int page = 0, pslot = 0;
           if (mine) {
-            const int pg = key / a.bt.page_size;
+            const int pg = page_of(a.bt, key);
             page = a.bt.table[(int64_t)wk.b * a.bt.table_stride + pg];
             pslot = key - pg * a.bt.page_size;
             if (page < 0 || page >= a.bt.n_pages) {
@@ -332,6 +350,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                             bar, c * 64, pslot, wk.h, page);
             }
             ++fills;
+            if (kv == 1 && lane == 0) *(volatile int*)&sh.issued = fills >> 1;
             if (++slot == G::slots) { slot = 0; phase ^= 1u; }
           }
         }
@@ -349,86 +368,166 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // ----------------------------------------------------------- products --
       constexpr uint32_t kIdQK = idesc_bf16(128, kChunkTN, 0, 0);
       constexpr uint32_t kIdPV = idesc_bf16(128, DP, 0, 1);
-      const uint32_t leader = elect_one();
+      const bool leader = elect_one();
       const uint32_t td = uniform(tmem);
       const uint64_t qd0 = sdesc_sw128(s_q, 16, 1024);
       const uint64_t kd0 = sdesc_sw128(s_kv, 16, 1024);
       const uint64_t vd0 = sdesc_sw128(s_kv, kChunkTN * 128, 1024);
-      int kslot = 0;                    // ring slot of the next K tile
-      uint32_t kphase = 0;
-      uint32_t units[2] = {0, 0}, tiles[2] = {0, 0};
+      // Items: the (tile, half) pairs of a unit in turn; item number n of the CTA
+      // has score buffer n % bufs. Scores run `bufs` items ahead of the weights.
+      // This warp's own instructions are on the critical path of every item: what
+      // it loops over goes through a shuffle once a unit, so that positions,
+      // descriptors and branches stay in uniform registers, and positions are
+      // counters that wrap.
+      struct Ring {
+        int at;
+        uint32_t phase;
+        __device__ __forceinline__ void step(int by, int n) {
+          at += by;
+          if (at >= n) { at -= n; phase ^= 1u; }
+        }
+      };
+      Ring k{0, 0}, v{1, 0};            // ring slots of the next K and V tile
+      Ring pb{0, 0}, sb{0, 0};          // buffers of the next weights, the next scores
+      int given0 = 0, given1 = 0;       // per half: the scores' next barrier
+      uint32_t units0 = 0, units1 = 0;
+      uint32_t seen = 0;                // a bit per slot: the parity of its next v_seen
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && mbar_wait_bounded(smem_u32(bar), parity, abort, a.status);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        return ok;
+        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(bar), parity)))
+          ok = wait_slowly(smem_u32(bar), parity, abort, a.status) && ok;
       };
-      auto commit = [&](uint64_t* bar) { umma_commit_by(leader, smem_u32(bar)); };
-      auto qk = [&](int h, int slot) {
-        const uint32_t q = uniform((uint32_t)qd0 + h * (G::q_half >> 4));
-        const uint32_t k = uniform((uint32_t)kd0 + slot * (G::tile >> 4));
-        const uint32_t hi = uniform((uint32_t)(kd0 >> 32));
-        const uint32_t d = uniform(td + G::s_col0 + h * 128);
+      auto commit = [&](uint64_t* bar) {
+        if (leader) umma_commit(smem_u32(bar));
+      };
+      const uint32_t q_lo = uniform((uint32_t)qd0), q_hi = uniform((uint32_t)(qd0 >> 32));
+      const uint32_t k_lo = uniform((uint32_t)kd0), v_lo = uniform((uint32_t)vd0);
+      const uint32_t v_hi = uniform((uint32_t)(vd0 >> 32));
+
+      // the scores of the next tile for half H (compile-time); last: of the unit
+      auto scores = [&](auto H, bool first, bool last, bool k_done) {
+        constexpr int h = decltype(H)::value;
+        const uint32_t q = q_lo + h * (G::q_half >> 4);
+        const uint32_t k0 = k_lo + k.at * (G::tile >> 4);
+        const uint32_t d = td + sb.at * 128;
+        if (first) wait(&sh.q_ready[h], (h ? units1++ : units0++) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) {
-          constexpr int kBlock = (128 * 128) >> 4;
-          const int at = (kk >> 2) * kBlock + (kk & 3) * 2;
-          umma_ss(leader, d, desc_of(q + at, hi), desc_of(k + at, hi), kIdQK, kk > 0);
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            constexpr int kBlock = (128 * 128) >> 4;
+            const int at = (kk >> 2) * kBlock + (kk & 3) * 2;
+            umma_bf16(d, desc_of(q + at, q_hi), desc_of(k0 + at, q_hi), kIdQK, kk > 0);
+          }
         }
-        commit(&sh.s_full[h]);
+        int& given = h ? given1 : given0;
+        commit(&sh.s_full[h][given]);
+        if (++given == G::bufs) given = 0;
+        if (last) commit(&sh.q_free[h]);
+        sb.step(1, G::bufs);
+        if (k_done) {
+          commit(&sh.kv_empty[k.at]);
+          k.step(2, G::slots);
+        }
       };
-      auto pv = [&](int h, int slot, bool first) {
-        const uint32_t v = uniform((uint32_t)vd0 + slot * (G::tile >> 4));
-        const uint32_t hi = uniform((uint32_t)(vd0 >> 32));
-        const uint32_t d = uniform(td + G::o_col0 + h * DP);
-        const uint32_t p = uniform(td + G::s_col0 + h * 128);
-        const uint32_t add = uniform(first ? 0u : 1u);
+      // O of half H (+)= P V over the 16-key steps [s0, s1) of the tile
+      auto product = [&](auto H, bool add, bool skip, int s0, int s1) {
+        constexpr int h = decltype(H)::value;
+        const uint32_t vv = v_lo + v.at * (G::tile >> 4);
+        const uint32_t d = td + G::o_col0 + h * DP;
+        const uint32_t p = td + pb.at * 128;
+        const uint32_t ad = add ? 1u : 0u;
+        wait(&sh.p_ready[pb.at], pb.phase);
+        if (!ok) return;
+        tc_fence_after();
+        if (s1 - s0 == kChunkTN / 16) {
+          if (leader && !skip) {
 #pragma unroll
-        for (int kk = 0; kk < kChunkTN / 16; ++kk)
-          umma_ts(leader, d, p + kk * 8, desc_of(v + kk * (2048 >> 4), hi), kIdPV,
-                  kk > 0 ? 1u : add);
+            for (int kk = 0; kk < kChunkTN / 16; ++kk)
+              umma_ts(d, p + kk * 8, desc_of(vv + kk * (2048 >> 4), v_hi), kIdPV,
+                      kk > 0 ? 1u : ad);
+          }
+        } else if (!skip) {
+#pragma unroll 1
+          for (int kk = s0; kk < s1; ++kk) {
+            const uint32_t pk = uniform(p + kk * 8), vk = uniform(vv + kk * (2048 >> 4));
+            const uint32_t ak = uniform(kk > s0 ? 1u : ad);
+            if (leader) umma_ts(d, pk, desc_of(vk, v_hi), kIdPV, ak);
+          }
+        }
+        commit(&sh.o_done[h]);
+        pb.step(1, G::bufs);
       };
-      for (Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x); wk.more() && ok;
-           wk.next()) {
-        const int nt = wk.sp.nt > 0 ? wk.take : 0;
+      using H0 = std::integral_constant<int, 0>;
+      using H1 = std::integral_constant<int, 1>;
+
+      Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x);
+      for (; uniform(wk.more() ? 1u : 0u) && ok; wk.next()) {
+        const int nt = (int)uniform(wk.sp.nt > 0 ? wk.take : 0);
         if (nt == 0) continue;
-        const int nh = wk.s.nq * a.G - wk.m * kChunkTM > 128 ? 2 : 1;
-        auto step = [&]() { if (++kslot == G::slots) { kslot = 0; kphase ^= 1u; } };
-        // the first tile's scores
-        if (!wait(&sh.kv_full[kslot], kphase)) break;
-        for (int h = 0; h < nh; ++h) {
-          if (!wait(&sh.q_ready[h], units[h] & 1)) break;
-          ++units[h];
-          tc_fence_after();
-          qk(h, kslot);
+        const bool two = uniform(wk.s.nq * a.G - wk.m * kChunkTM > 128 ? 1u : 0u) != 0;
+        // tiles [0, e0) and [e1, nt) are edge tiles
+        int e0 = 0, e1 = nt;
+        while (e0 < nt && wk.edge(e0)) ++e0;
+        while (e1 > e0 && wk.edge(e1 - 1)) --e1;
+        e0 = (int)uniform(e0);
+        e1 = (int)uniform(e1);
+        int sj = 0;                     // scores: the tile of the next item
+        // the first items' scores
+        auto first_scores = [&](auto H, bool k_done) {
+          if (H.value == 0) wait(&sh.kv_full[k.at], k.phase);
+          if (ok) scores(H, sj == 0, sj + 1 == nt, k_done);
+          if (k_done) ++sj;
+        };
+        if (two) {
+          first_scores(H0{}, false);
+          first_scores(H1{}, true);
+          if (G::bufs == 3 && nt > 1 && ok) first_scores(H0{}, false);
+        } else {
+          for (int i = 0; i < G::bufs && i < nt && ok; ++i) first_scores(H0{}, true);
         }
-        if (!ok) break;
-        commit(&sh.kv_empty[kslot]);
-        step();
-        for (int j = 0; j < nt; ++j) {
-          const int vslot = kslot;
-          if (!wait(&sh.kv_full[vslot], kphase)) break;
-          step();
-          const bool more = j + 1 < nt;
-          const int nkslot = kslot;
-          if (more && !wait(&sh.kv_full[nkslot], kphase)) break;
-          for (int h = 0; h < nh; ++h) {
-            if (!wait(&sh.p_ready[h], tiles[h] & 1)) break;
-            ++tiles[h];
-            tc_fence_after();
-            // products of one thread run in the order of issue: the next scores
-            // overwrite P's columns after this product has read them
-            const bool skip = *(volatile int*)&sh.by_hand[h];
-            if (!__any_sync(0xFFFFFFFFu, skip)) pv(h, vslot, j == 0);
-            if (more) qk(h, nkslot);
-            else commit(&sh.o_done[h]);
+        for (int j = 0; j < nt && ok; ++j) {
+          wait(&sh.kv_full[v.at], v.phase);
+          bool skip = false;
+          int s0 = 0, s1 = kChunkTN / 16;
+          // 16-key steps [s0, s1) of an edge tile hold the unit's keys; in the
+          // others V is whatever the ring held before
+          if ((j < e0 || j >= e1) && ok) {
+            const int k0 = wk.first_key(j);
+            s0 = (int)uniform(max(wk.sp.lo - k0, 0) >> 4);
+            s1 = (int)uniform((min(wk.sp.hi - k0, kChunkTN) + 15) >> 4);
+            wait(&sh.v_seen[v.at], seen >> v.at & 1);
+            seen ^= 1u << v.at;
+            skip = uniform(sh.bad[v.at][0] | sh.bad[v.at][1]) != 0;
           }
-          if (!ok) break;
-          commit(&sh.kv_empty[vslot]);
-          if (more) {
-            commit(&sh.kv_empty[nkslot]);
-            step();
+          // products of one thread run in the order of issue: the new scores take
+          // the buffer's place after the product has read the weights
+          if (two) {
+            if (G::bufs == 2) {
+              // the scores after an item are its own half's, one tile on
+              const bool more = j + 1 < nt, last = j + 2 == nt;
+              if (more && ok) wait(&sh.kv_full[k.at], k.phase);
+              if (ok) product(H0{}, j > 0, skip, s0, s1);
+              if (more && ok) scores(H0{}, false, last, false);
+              if (ok) product(H1{}, j > 0, skip, s0, s1);
+              if (more && ok) scores(H1{}, false, last, true);
+            } else {
+              // half 1's one tile on, then half 0's two tiles on
+              if (ok) product(H0{}, j > 0, skip, s0, s1);
+              if (j + 1 < nt && ok) scores(H1{}, false, j + 2 == nt, true);
+              if (j + 2 < nt && ok) wait(&sh.kv_full[k.at], k.phase);
+              if (ok) product(H1{}, j > 0, skip, s0, s1);
+              if (j + 2 < nt && ok) scores(H0{}, false, j + 3 == nt, false);
+            }
+          } else {
+            const bool more = j + G::bufs < nt;
+            if (more && ok) wait(&sh.kv_full[k.at], k.phase);
+            if (ok) product(H0{}, j > 0, skip, s0, s1);
+            if (more && ok) scores(H0{}, false, j + G::bufs + 1 == nt, true);
           }
+          if (ok) commit(&sh.kv_empty[v.at]);
+          v.step(2, G::slots);
         }
       }
       // every product has finished before tensor memory is freed
@@ -436,6 +535,100 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       volatile int never = 0;
       mbar_wait_bounded(smem_u32(&sh.drain), 0, &never, a.status);
       __syncwarp();
+    } else if (work && warp >= kHelpWarp) {
+      // ------------------------------------------------ queries, edge values --
+      const int half = warp - kHelpWarp;
+      constexpr int NC = DP / 8;            // 16-byte pieces of a row
+      int vslot = 1, gone = 0;              // gone: tiles gone by
+      uint32_t vphase = 0, units = 0;
+      bool ok = true;
+      for (Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x); wk.more() && ok;
+           wk.next()) {
+        const int nt = wk.sp.nt > 0 ? wk.take : 0;
+        if (nt == 0) continue;
+        const int r0 = wk.m * kChunkTM + half * 128;
+        const int nrows = wk.s.nq * a.G - r0;
+        if (nrows > 0) {
+          if (units > 0)
+            ok = mbar_wait_bounded(smem_u32(&sh.q_free[half]), (units - 1) & 1, abort, a.status);
+          if (!__all_sync(0xFFFFFFFFu, ok)) break;
+          ++units;
+          const uint32_t bar = smem_u32(&sh.q_ready[half]);
+          const uint32_t dst = s_q + half * G::q_half;
+          if (q_by_tma) {
+            // G heads x 128 / G tokens; rows past the sequence are other tokens'
+            // queries or zeros, and what comes of them is dropped
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar, G::q_half);
+#pragma unroll
+              for (int c = 0; c < G::halves; ++c)
+                tma_load_3d(dst + c * (128 * 128), &mapQ, bar, c * 64, wk.h * a.G,
+                            wk.s.q0 + div_group(a, r0));
+            }
+            __syncwarp();
+          } else {
+            // four rows a lane
+#pragma unroll 1
+            for (int r = lane; r < 128; r += 32) {
+              const int rr = r0 + min(r, nrows - 1);
+              const int tok = div_group(a, rr), g = rr - tok * a.G;
+              const moe_bf16* src = a.q + (int64_t)(wk.s.q0 + tok) * a.q_stride +
+                                    (int64_t)(wk.h * a.G + g) * a.D;
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                const bool in = c * 8 < a.D;
+                cp_async16(dst + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                           src + (in ? c * 8 : 0), in);
+              }
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+          }
+        }
+        for (int j = 0; j < nt; ++j) {
+          if (wk.edge(j)) {
+            // the tiles between are not waited for, so first the loads must have
+            // come to this one: a barrier's parity tells one round of the ring
+            // from the next, not from the one after
+            ok = count_wait_bounded(&sh.issued, gone + 1, abort, a.status) &&
+                 mbar_wait_bounded(smem_u32(&sh.kv_full[vslot]), vphase, abort, a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+            const int k0 = wk.first_key(j);
+            uint8_t* const vt = kv_mem + vslot * G::tile;
+            // Zeros: the rows out of range in the first and last 16-key step that
+            // the product takes. Looked through: the rows that only some see.
+            const int v0 = max(wk.sp.lo - k0, 0), v1 = min(wk.sp.hi - k0, kChunkTN);
+            const int f0 = min(max(wk.all_lo - k0, v0), v1), f1 = max(min(wk.all_hi - k0, v1), f0);
+            auto piece = [&](int i) {      // piece i % NC of key row i / NC
+              const int row = i / NC, c = i - row * NC;
+              return reinterpret_cast<uint4*>(vt + (c >> 3) * (128 * 128) + row * 128 +
+                                              (((c ^ row) & 7) << 4));
+            };
+            const int t = half * 32 + lane;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = (v0 & ~15) * NC + t; i < v0 * NC; i += 64) *piece(i) = zero;
+            for (int i = v1 * NC + t; i < ((v1 + 15) & ~15) * NC; i += 64) *piece(i) = zero;
+            uint32_t bad = 0;
+#pragma unroll 4
+            for (int i = v0 * NC + t; i < f0 * NC; i += 64) bad |= not_finite8(*piece(i));
+#pragma unroll 4
+            for (int i = f1 * NC + t; i < v1 * NC; i += 64) bad |= not_finite8(*piece(i));
+            fence_async_smem();
+            const int any = __any_sync(0xFFFFFFFFu, bad != 0);
+            if (lane == 0) {
+              sh.bad[vslot][half] = any;
+              mbar_arrive(smem_u32(&sh.v_seen[vslot]));
+            }
+            __syncwarp();
+          }
+          ++gone;
+          vslot += 2;
+          if (vslot >= G::slots) { vslot -= G::slots; vphase ^= 1u; }
+        }
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax --
@@ -443,176 +636,162 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int half = warp >> 2;
     const int row = (warp & 3) * 32 + lane;             // of the half
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t t_s = t_lane + G::s_col0 + half * 128;
     const uint32_t t_o = t_lane + G::o_col0 + half * DP;
-    uint8_t* const q_mem = smem + half * G::q_half;
-    int vslot = 1;                    // ring slot of the tile's V (K's is the one before)
-    uint32_t vphase = 0;
-    uint32_t tiles = 0, ends = 0, looks = 0;
+    uint32_t item0 = 0;               // as the product warp counts
+    int tile0 = 0;
+    uint32_t mine = 0;                // this half's items so far
+    uint32_t seen = 0;
     bool ok = true;
-    auto vstep = [&]() {
-      vslot += 2;
-      if (vslot >= G::slots) { vslot -= G::slots; vphase ^= 1u; }
-    };
     Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x, work);
     for (; wk.more() && ok; wk.next()) {
       const Seq s = wk.s;
       const int r0 = wk.m * kChunkTM + half * 128;
-      const int nrows = min(128, s.nq * a.G - r0);
+      const int left = s.nq * a.G - wk.m * kChunkTM;
+      const int nh = left > 128 ? 2 : 1;
+      const int nrows = min(128, left - half * 128);
       const int nt = wk.sp.nt > 0 ? wk.take : 0;
+      const uint32_t first_item = item0 + half;
+      const int first_tile = tile0;
+      item0 += nt * nh;
+      tile0 += nt;
       if (nrows <= 0) {               // the half has no rows: its tiles go by
-        for (int j = 0; j < nt; ++j) vstep();
+        for (int j = 0; j < nt; ++j)
+          if (wk.edge(j)) seen ^= 1u << ((2 * (first_tile + j) + 1) % G::slots);
         continue;
       }
       const int r = r0 + min(row, nrows - 1);
-      const int tok = r / a.G, head = wk.h * a.G + (r - tok * a.G);
+      const int tok = div_group(a, r), head = wk.h * a.G + (r - tok * a.G);
       const int64_t grow = s.q0 + tok;
       const bool real = row < nrows;
       float m_ref = neg_inf(), l = 0.f;
       if (nt > 0) {
-        // ---- queries: one row per thread, in the 128-byte swizzle ------------
-        const uint4* src =
-            reinterpret_cast<const uint4*>(a.q + grow * a.q_stride + (int64_t)head * a.D);
-#pragma unroll
-        for (int c = 0; c < DP / 8; ++c) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (real && c * 8 < a.D) v = src[c];
-          *reinterpret_cast<uint4*>(q_mem + (c >> 3) * (128 * 128) + row * 128 +
-                                    (((c & 7) ^ (row & 7)) << 4)) = v;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.q_ready[half]));
-
         const int lo = key_lo(a, s, tok), hi = real ? key_hi(a, s, tok) : 0;
-        // keys every row of the half sees: [all_lo, all_hi); of the warp alike
-        const int all_lo = key_lo(a, s, (r0 + nrows - 1) / a.G), all_hi = key_hi(a, s, r0 / a.G);
+        // keys every row of the warp sees: [warp_lo, warp_hi)
         const int w0 = r0 + min((warp & 3) * 32, nrows - 1);
         const int w1 = r0 + min((warp & 3) * 32 + 31, nrows - 1);
-        const int warp_lo = key_lo(a, s, w1 / a.G), warp_hi = key_hi(a, s, w0 / a.G);
+        const int warp_lo = key_lo(a, s, div_group(a, w1)),
+                  warp_hi = key_hi(a, s, div_group(a, w0));
 
         for (int j = 0; j < nt; ++j) {
-          const int k0 = (wk.sp.t0 + wk.off + j) * kChunkTN;
-          ok = ok && mbar_wait_bounded(smem_u32(&sh.s_full[half]), tiles & 1, abort, a.status);
+          const int k0 = wk.first_key(j);
+          const uint32_t n = first_item + j * nh;
+          const int buf = n % G::bufs;
+          const uint32_t t_s = t_lane + buf * 128;
+          ok = ok && mbar_wait_bounded(smem_u32(&sh.s_full[half][mine % G::bufs]),
+                                       (mine / G::bufs) & 1, abort, a.status);
           if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-          ++tiles;
           tc_fence_after();
-          float sc[128];
-          tmem_ld32f(t_s, sc);
-          tmem_ld32f(t_s + 32, sc + 32);
-          tmem_ld32f(t_s + 64, sc + 64);
-          tmem_ld32f(t_s + 96, sc + 96);
-          tmem_ld_wait();
-          if (k0 < warp_lo || k0 + kChunkTN > warp_hi) {
+          // the half's product before this one, for who is to change O
+          auto o_is_done = [&]() {
+            ok = ok && mbar_wait_bounded(smem_u32(&sh.o_done[half]), (mine - 1) & 1, abort,
+                                         a.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+          };
+          // The weights are taken against the maximum so far while the tile's own
+          // is still being found; only when a row's has grown by more than 2^8
+          // (always in a unit's first tile, where it is found first) the scores
+          // are read again. Stored weights replace them only afterwards.
+          bool find_first = j == 0;
+          uint32_t pk[64];
+          float2 acc[2];
+          for (;;) {
+            float sc[128];
+            tmem_ld32f(t_s, sc);
+            tmem_ld32f(t_s + 32, sc + 32);
+            tmem_ld32f(t_s + 64, sc + 64);
+            tmem_ld32f(t_s + 96, sc + 96);
+            tmem_ld_wait();
             // masked by selection: a masked score's value, NaN or not, is dropped
+            if (k0 + kChunkTN > warp_hi) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              sc[c] = (k0 + c >= lo && k0 + c < hi) ? sc[c] : neg_inf();
-          }
-          float mx[4];
+              for (int c = 0; c < 128; ++c) sc[c] = c < hi - k0 ? sc[c] : neg_inf();
+            }
+            if (k0 < warp_lo) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
+              for (int c = 0; c < 128; ++c) sc[c] = c >= lo - k0 ? sc[c] : neg_inf();
+            }
+            if (find_first) {
+              float mx[4];
 #pragma unroll
-          for (int c = 8; c < 128; c += 2)
-            mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], sc[c], sc[c + 1]);
-          const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-          const bool grew = m2 > m_ref + kRescaleAt;      // true for the first key a row sees
-          if (__any_sync(0xFFFFFFFFu, grew)) {
-            const float nm = grew ? m2 : m_ref;
-            const float f = nm == neg_inf() ? 1.f : ex2(m_ref - nm);
-            m_ref = nm;
-            l *= f;
-            if (j > 0) {
-              // the scores' barrier stands for every product issued before them
+              for (int i = 0; i < 4; ++i) mx[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
+#pragma unroll
+              for (int c = 8; c < 128; c += 2)
+                mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], sc[c], sc[c + 1]);
+              const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+              const float nm = m2 > m_ref + kRescaleAt ? m2 : m_ref;
+              const float f = nm == neg_inf() ? 1.f : ex2(m_ref - nm);
+              m_ref = nm;
+              l *= f;
+              if (j > 0) {
+                o_is_done();
 #pragma unroll 1
-              for (int c = 0; c < DP; c += 32) {
-                float o[32];
-                tmem_ld32f(t_o + c, o);
-                tmem_ld_wait();
+                for (int c = 0; c < DP; c += 32) {
+                  float o[32];
+                  tmem_ld32f(t_o + c, o);
+                  tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= f;
-                tmem_st32f(t_o + c, o);
+                  for (int i = 0; i < 32; ++i) o[i] *= f;
+                  tmem_st32f(t_o + c, o);
+                }
               }
             }
-          }
-          const float ref = m_ref == neg_inf() ? 0.f : m_ref;
-          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                           make_float2(0.f, 0.f)};
+            const float ref = m_ref == neg_inf() ? 0.f : m_ref;
+            float mx[2] = {neg_inf(), neg_inf()};
+            acc[0] = acc[1] = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c0 = 0; c0 < 128; c0 += 64) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              float2 t = fma2(make_float2(sc[c0 + c], sc[c0 + c + 1]), a.scale_log2, -ref);
+            for (int c = 0; c < 128; c += 2) {
+              float2 t = fma2(make_float2(sc[c], sc[c + 1]), a.scale_log2, -ref);
+              mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], sc[c], sc[c + 1]);
               t = make_float2(ex2(t.x), ex2(t.y));
-              acc[(c >> 1) & 3] = add2(acc[(c >> 1) & 3], t);
+              acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], t);
               pk[c / 2] = pack_bf16(t.x, t.y);
             }
-            tmem_st32(t_s + c0 / 2, pk);
+            const bool grew = fmaxf(mx[0], mx[1]) * a.scale_log2 > m_ref + kRescaleAt;
+            if (find_first || !__any_sync(0xFFFFFFFFu, grew)) break;
+            find_first = true;
           }
-          acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+          // every product is waited for in turn: a barrier's parity tells only the
+          // latest phase from the one before (it has mostly ended long ago)
+          if (j > 0) o_is_done();
+          tmem_st32(t_s, pk);
+          tmem_st32(t_s + 32, pk + 32);
+          acc[0] = add2(acc[0], acc[1]);
           l += acc[0].x + acc[0].y;
-          // A zero weight does not keep an infinite or NaN value out of the product.
-          // V rows outside the unit's keys hold whatever the cache holds there:
-          // they become zeros. In a tile that some of the half's rows see only in
-          // part, the values are looked through; should one not be finite, the
-          // half's warps add the tile's P V to O themselves, key by key over the
-          // rows that see it, and the product is not issued.
-          const bool ragged = k0 < wk.sp.lo || k0 + kChunkTN > wk.sp.hi;
-          const bool differ = max(k0, wk.sp.lo) < all_lo || min(k0 + kChunkTN, wk.sp.hi) > all_hi;
-          bool by_hand = false;
-          if (ragged || differ) {
-            ok = ok && mbar_wait_bounded(smem_u32(&sh.kv_full[vslot]), vphase, abort, a.status);
-            uint8_t* const vt = kv_mem + vslot * G::tile;
-            // one key row per thread, its 16-byte pieces in an order of its own
-            // (no two of 8 lanes on the same banks)
-            const bool in = k0 + row >= wk.sp.lo && k0 + row < wk.sp.hi;
-            bool bad = false;
-#pragma unroll
-            for (int c = 0; c < DP / 8; ++c) {
-              uint4* p = reinterpret_cast<uint4*>(vt + (c >> 3) * (128 * 128) + row * 128 +
-                                                  (((c + row) & 7) << 4));
-              if (!in) *p = make_uint4(0u, 0u, 0u, 0u);
-              else if (differ) bad = bad || !finite8(*p);
-            }
-            fence_async_smem();
-            if (differ) {
-              const int at = looks & 1;
-              sh.bad[half][at][warp & 3] = __any_sync(0xFFFFFFFFu, bad);
+          tmem_st_wait();
+          if (wk.edge(j)) {
+            // A zero weight does not keep an infinite or NaN value out of the
+            // product: a tile that some row sees in part and that holds one is not
+            // multiplied; its P V is added here, key by key over the rows that see it.
+            const int t = first_tile + j, vslot = (2 * t + 1) % G::slots;
+            ok = ok && mbar_wait_bounded(smem_u32(&sh.v_seen[vslot]), seen >> vslot & 1, abort,
+                                         a.status);
+            seen ^= 1u << vslot;
+            const bool by_hand = ok && (sh.bad[vslot][0] | sh.bad[vslot][1]) != 0;
+            if (__any_sync(0xFFFFFFFFu, by_hand)) {
+              ok = ok && mbar_wait_bounded(smem_u32(&sh.kv_full[vslot]),
+                                           ((2 * t + 1) / G::slots) & 1, abort, a.status);
               __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&sh.looked[half]));
-              ok = ok && mbar_wait_bounded(smem_u32(&sh.looked[half]), looks & 1, abort, a.status);
-              ++looks;
-              const volatile int* f = sh.bad[half][at];
-              by_hand = (f[0] | f[1] | f[2] | f[3]) != 0;
-              __syncwarp();
-            }
-            if (by_hand) {
+              add_by_hand<DP>(t_s, t_o, kv_mem + vslot * G::tile, k0, lo, hi, j > 0);
               tmem_st_wait();
-              add_by_hand<DP>(t_s, t_o, vt, k0, lo, hi, j > 0);
             }
           }
-          tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            *(volatile int*)&sh.by_hand[half] = by_hand;
-            mbar_arrive(smem_u32(&sh.p_ready[half]));
-          }
-          vstep();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[buf]));
+          ++mine;
         }
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        ok = mbar_wait_bounded(smem_u32(&sh.o_done[half]), ends & 1, abort, a.status);
-        ++ends;
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        ok = ok && mbar_wait_bounded(smem_u32(&sh.o_done[half]), (mine - 1) & 1, abort, a.status);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
         tc_fence_after();
       }
       // ---- the unit's rows: final, or this CTA's part ------------------------
       const bool whole = wk.whole();
       RowEnd e{1.f, 0.f};
       if (whole) e = row_end(m_ref, l, a.sinks, head);
-      moe_bf16* const dst = a.out + grow * a.out_stride + (int64_t)head * a.D;
       const int64_t prow = ((int64_t)blockIdx.x * 2 + wk.slot()) * kChunkTM + half * 128 + row;
+      moe_bf16* const dst = a.out + grow * a.out_stride + (int64_t)head * a.D;
+      float* const part = a.part_o + prow * DP;
 #pragma unroll 1
       for (int c = 0; c < DP; c += 32) {
         float o[32];
@@ -634,7 +813,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         } else if (real) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(a.part_o + prow * DP + c + i * 4) =
+            *reinterpret_cast<float4*>(part + c + i * 4) =
                 make_float4(o[i * 4], o[i * 4 + 1], o[i * 4 + 2], o[i * 4 + 3]);
         }
         __syncwarp();      // the next load is the whole warp's
@@ -672,6 +851,11 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
   CUtensorMap mk, mv;
   const int box = kv_box(c.page_size);
   if (!map_kv(&mk, c.k, c, box) || !map_kv(&mv, c.v, c, box)) return cudaErrorInvalidValue;
+  // a half's 128 rows are whole tokens when G divides 128
+  const int by_tma = 128 % a.G == 0 ? 1 : 0;
+  CUtensorMap mq = mk;
+  if (by_tma && !map_heads(&mq, a.q, a.D, a.Hq, a.bt.T, a.q_stride, a.G, 128 / a.G))
+    return cudaErrorInvalidValue;
   auto kern = attn_chunk_kernel<DP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
   if (e != cudaSuccess) return e;
@@ -679,7 +863,8 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
   a.part_ml = static_cast<float2*>(ws);
   a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * kChunkTM);
   timer_before(MOE_KERNEL_ATTN, s);
-  e = launch_pdl(true, kern, dim3(n), dim3(kChunkThreads), G::smem, s, a, mk, mv, box);
+  e = launch_pdl(true, kern, dim3(n), dim3(kChunkThreads), G::smem, s, a, mq, mk, mv, box,
+                 by_tma);
   timer_after(MOE_KERNEL_ATTN, s);
   if (e != cudaSuccess) return e;
   timer_before(MOE_KERNEL_ATTN_COMBINE, s);

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
       t.x = t.x * f + v.x * g; t.y = t.y * f + v.y * g;
       t.z = t.z * f + v.z * g; t.w = t.w * f + v.w * g;
     }
-    const int tok = (r0 + r) / a.G, head = pl.h * a.G + (r0 + r) - tok * a.G;
+    const int tok = div_group(a, r0 + r), head = pl.h * a.G + (r0 + r) - tok * a.G;
     const RowEnd e = row_end(m, l, a.sinks, head);
     if (c4 * 4 < a.D)
       *reinterpret_cast<uint2*>(a.out + (int64_t)(s.q0 + tok) * a.out_stride +

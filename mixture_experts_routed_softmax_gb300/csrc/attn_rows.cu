@@ -35,18 +35,6 @@ struct RowsGeo {
   static constexpr int smem = (ring > merge ? ring : merge) + q_bytes;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
-  const int n = full ? 16 : 0;       // 0: the destination is filled with zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -94,7 +82,7 @@ __device__ __forceinline__ bool chunk_finite(uint32_t sv) {
 // -1: outside [lo, hi), or a page outside the cache.
 __device__ __forceinline__ int64_t key_at(const AttnArgs& a, int b, int key, int lo, int hi) {
   if (key < lo || key >= hi) return -1;
-  const int pg = key / a.bt.page_size;
+  const int pg = page_of(a.bt, key);
   const int page = a.bt.table[(int64_t)b * a.bt.table_stride + pg];
   if (page < 0 || page >= a.bt.n_pages) {
     raise_status(a.status, MOE_ERR_DEVICE_INDEX);
@@ -134,7 +122,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const AttnArgs 
       const int r = i / NC, c = i - r * NC;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (r < nrows && c * 8 < a.D) {
-        const int tok = (r0 + r) / a.G, g = (r0 + r) - tok * a.G;
+        const int tok = div_group(a, r0 + r), g = (r0 + r) - tok * a.G;
         v = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.q0 + tok) * a.q_stride +
                                             (int64_t)(h * a.G + g) * a.D + c * 8);
       }
@@ -147,12 +135,12 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const AttnArgs 
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = mb * 16 + lr + 8 * e;
-        const int tok = (r0 + min(r, nrows - 1)) / a.G;
+        const int tok = div_group(a, r0 + min(r, nrows - 1));
         lo[mb][e] = key_lo(a, s, tok);
         hi[mb][e] = r < nrows ? key_hi(a, s, tok) : 0;
       }
-    const int all_lo = key_lo(a, s, (r0 + nrows - 1) / a.G);
-    const int all_hi = key_hi(a, s, r0 / a.G);
+    const int all_lo = wk.all_lo;
+    const int all_hi = wk.all_hi;
     const bool rows_differ = all_lo > wk.sp.lo || all_hi < wk.sp.hi;
 
     float o[MB][ND][4];
@@ -365,7 +353,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const AttnArgs 
         t.x += f * v.x; t.y += f * v.y; t.z += f * v.z; t.w += f * v.w;
       }
       if (whole) {
-        const int tok = (r0 + r) / a.G, head = h * a.G + (r0 + r) - tok * a.G;
+        const int tok = div_group(a, r0 + r), head = h * a.G + (r0 + r) - tok * a.G;
         const RowEnd e = row_end(m, l, a.sinks, head);
         if (c4 * 4 < a.D) {
           uint2 w2 = make_uint2(pack_bf16(t.x * e.factor, t.y * e.factor),
@@ -435,6 +423,7 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   a.q = q; a.q_stride = q_stride; a.out = out; a.out_stride = out_stride;
   a.sinks = sinks; a.lse = lse;
   a.Hq = Hq; a.Hkv = c.Hkv; a.G = Hq / c.Hkv; a.D = c.D;
+  a.g_shift = shift_of(a.G);
   a.scale_log2 = scale * kLog2e;
   a.causal = causal ? 1 : 0;
   // a window of the whole cache or more masks nothing
