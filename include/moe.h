@@ -487,7 +487,7 @@ int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const mo
  * a cu_q that runs out of [0, T] or backwards raises MOE_ERR_DEVICE_INDEX;
  * nothing out of bounds is read or written, and that sequence's rows are
  * unspecified. Rows of no sequence are not written.
- * Limits: T * Hq < 2^31, T < 2^30.
+ * Limits: T * Hq <= 2^30.
  * ------------------------------------------------------------------------ */
 int moe_attn_paged(const moe_kv_cache* cache, const moe_kv_batch* batch, const moe_bf16* q,
                    int64_t q_stride, int Hq, float scale, int causal, int window,

@@ -22,7 +22,7 @@ static int check_head_dim(int D) {
 }
 static int check_tokens(int64_t T, int64_t H) {
   if (T < 0 || H <= 0) return MOE_ERR_ARG;
-  if (T >= ((int64_t)1 << 30) || H > 65536 || T * H >= ((int64_t)1 << 31))
+  if (T >= ((int64_t)1 << 30) || H > 65536 || T * H > ((int64_t)1 << 30))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -7,8 +7,8 @@
 // its keys are one range (the union of its rows' masks), cut into tiles of TN.
 // Units in the order (b, h, m) laid end to end, one tile a step (an empty unit
 // counts one: its rows are still to be written), make a line of `total` steps;
-// CTA c of n takes steps [total * c / n, total * (c + 1) / n). Every CTA so
-// has the same number of tiles whatever the lengths, and writes at most two
+// each of n CTAs takes total / n steps in a row (the first ones one more). Every
+// CTA so has the same number of tiles whatever the lengths, and writes at most two
 // partial results: the unit it enters in the middle (slot 0) and the unit it
 // begins and does not end (slot 1). A second launch joins the parts of each
 // cut unit in order, so results do not depend on timing.
@@ -28,24 +28,26 @@ struct AttnBatch {
   int64_t table_stride;
   int64_t n_pages, page_stride, token_stride;
   int T, B, max_pages, page_size;
-  int page_shift;        // log2 of page_size, or -1
+  uint32_t page_recip;
 };
 
-inline int shift_of(int v) {
-  if (v & (v - 1)) return -1;
-  int s = 0;
-  while ((1 << s) < v) ++s;
-  return s;
+// Divisions by sizes known at run time: the product with ceil(2^32 / d), whose
+// high half is the quotient or one more for any 32-bit dividend below 2^31.
+// recip 0 stands for d = 1.
+inline uint32_t recip_of(int d) {
+  return d == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + d - 1) / d);
 }
-// Divisions by sizes known at run time take some hundred cycles where powers
-// of two, the common case, take a shift.
+__device__ __forceinline__ int divide_by(int n, int d, uint32_t recip) {
+  const uint32_t q = __umulhi((uint32_t)n, recip);
+  return recip == 0 ? n : (int)(q * (uint32_t)d > (uint32_t)n ? q - 1 : q);
+}
 __device__ __forceinline__ int page_of(const AttnBatch& b, int key) {
-  return b.page_shift >= 0 ? key >> b.page_shift : key / b.page_size;
+  return divide_by(key, b.page_size, b.page_recip);
 }
 
 inline AttnBatch attn_batch(const moe_kv_cache& c, const moe_kv_batch& b) {
   return AttnBatch{b.cu_q, b.kv_len, b.page_table, b.table_stride, c.n_pages, c.page_stride,
-                   c.token_stride, (int)b.T, b.B, b.max_pages, c.page_size, shift_of(c.page_size)};
+                   c.token_stride, (int)b.T, b.B, b.max_pages, c.page_size, recip_of(c.page_size)};
 }
 
 struct AttnArgs {
@@ -59,7 +61,7 @@ struct AttnArgs {
   const float* sinks;
   float* lse;
   int Hq, Hkv, G, D;
-  int g_shift;           // log2 of G, or -1
+  uint32_t g_recip;
   float scale_log2;      // scale * log2(e): scores and maxima are kept in powers of two
   int causal, window;    // window 0: none
   float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
@@ -68,7 +70,7 @@ struct AttnArgs {
 };
 
 __device__ __forceinline__ int div_group(const AttnArgs& a, int row) {
-  return a.g_shift >= 0 ? row >> a.g_shift : row / a.G;
+  return divide_by(row, a.G, a.g_recip);
 }
 
 // ------------------------------------------------------------- the batch --
@@ -149,16 +151,27 @@ struct Tiling {
 };
 
 // ------------------------------------------------------------ the schedule --
-struct Place {              // of a step of the line, in shared memory
-  long long total;          // steps of the line
+// All of it runs once a unit or less and is kept out of line: what a warp's
+// steady state executes has to fit the instruction cache.
+struct Line {               // the line of steps, cut for n CTAs
+  long long total, per;     // per = total / n; the first `rem` CTAs take one more
+  int rem;
+  __device__ __forceinline__ long long start(int cta) const {
+    return per * cta + (cta < rem ? cta : rem);
+  }
+};
+struct Place {              // of a CTA's first step, in shared memory
+  Line line;
+  long long warp_sum[32];
+  long long in_seq, head_w;
   int b, h, m;
   int off;                  // steps into the unit
-  long long warp_sum[32];
-  long long rem, head_w;
 };
 
-__device__ __forceinline__ long long cta_start(long long total, int cta, int n) {
-  return total * cta / n;
+// a / b of values that nearly always fit 32 bits
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
 }
 
 // Steps of one head of the sequence of each lane (0 for nq = 0). A lane with
@@ -169,9 +182,8 @@ __device__ __forceinline__ long long head_weight(const AttnArgs& a, const Seq& s
   const int lane = threadIdx.x & 31;
   const int nm = s.nq > 0 ? TL::row_tiles(a, s) : 0;
   long long w = 0;
-  if (nm <= 4)
-    for (int m = 0; m < nm; ++m) w += TL::weight(a, s, m);
-  uint32_t big = __ballot_sync(0xFFFFFFFFu, nm > 4);
+  if (nm == 1) w = TL::weight(a, s, 0);
+  uint32_t big = __ballot_sync(0xFFFFFFFFu, nm > 1);
   while (big) {
     const int src = __ffs(big) - 1;
     big &= big - 1;
@@ -190,146 +202,167 @@ __device__ __forceinline__ long long head_weight(const AttnArgs& a, const Seq& s
 }
 
 // Where CTA `cta` of `n` begins, into `pl` (by the whole block of NT threads,
-// ends with a barrier). False when the line has no steps.
+// ends with a barrier). False when no step of the line begins there: the CTA
+// has none, and no unit is cut in front of it.
 template <int TM, int TN, int NT>
-__device__ bool locate(const AttnArgs& a, int cta, int n, Place& pl) {
+__device__ __noinline__ bool locate(const AttnArgs& a, int cta, int n, Place& pl) {
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.bt.B;
-  long long base = 0, total = 0, x0 = 0;
-  // first pass: the line's length; second: the sequence that holds step x0
+  // The line's length, then the sequence that holds the CTA's first step. Up to
+  // NT sequences, one a thread, the second pass looks at what the first has.
+  long long total = 0, x0 = 0, hw = 0, inc = 0, before = 0;
+#pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    base = 0;
+    long long base = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < B; b0 += NT) {
       const int b = b0 + tid;
-      Seq s{0, 0, 0};
-      if (b < B) s = load_seq(a, b);
-      const long long hw = head_weight<TM, TN>(a, s);
-      const long long w = hw * a.Hkv;
-      long long inc = w;
+      if (pass == 0 || B > NT) {
+        Seq s{0, 0, 0};
+        if (b < B) s = load_seq(a, b);
+        hw = head_weight<TM, TN>(a, s);
+        inc = hw * a.Hkv;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += up;
-      }
-      if (lane == 31) pl.warp_sum[warp] = inc;
-      __syncthreads();
-      long long before = 0, all = 0;
-#pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        const long long v = pl.warp_sum[i];
-        if (i < warp) before += v;
-        all += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+          if (lane >= o) inc += up;
+        }
+        __syncthreads();
+        if (lane == 31) pl.warp_sum[warp] = inc;
+        __syncthreads();
+        before = 0;
+        long long all = 0;
+#pragma unroll 1
+        for (int i = 0; i < NW; ++i) {
+          const long long v = pl.warp_sum[i];
+          if (i < warp) before += v;
+          all += v;
+        }
+        total = base + all;
       }
       if (pass == 1) {
-        const long long lo = base + before + inc - w;
-        if (x0 >= lo && x0 < lo + w) {
+        const long long hi = base + before + inc, lo = hi - hw * a.Hkv;
+        if (x0 >= lo && x0 < hi) {
           pl.b = b;
-          pl.rem = x0 - lo;
+          pl.in_seq = x0 - lo;
           pl.head_w = hw;
         }
       }
-      base += all;
-      __syncthreads();
+      base = total;
     }
     if (pass == 0) {
-      total = base;
       if (total == 0) return false;
-      x0 = cta_start(total, cta, n);
+      Line ln;
+      ln.total = total;
+      ln.per = divide(total, n);
+      ln.rem = (int)(total - ln.per * n);
+      x0 = ln.start(cta);
+      if (x0 >= total) return false;      // fewer steps than CTAs: none for this one
+      if (tid == 0) pl.line = ln;
     }
   }
+  __syncthreads();
   if (warp == 0) {
     const Seq s = load_seq(a, pl.b);
-    const int h = (int)(pl.rem / pl.head_w);
-    long long rem = pl.rem - h * pl.head_w;
+    const int h = (int)divide(pl.in_seq, pl.head_w);
+    long long rem = pl.in_seq - h * pl.head_w;
     const int nm = Tiling<TM, TN>::row_tiles(a, s);
+#pragma unroll 1
     for (int m0 = 0; m0 < nm; m0 += 32) {
       const int m = m0 + lane;
       const int w = m < nm ? Tiling<TM, TN>::weight(a, s, m) : 0;
-      long long inc = w;
+      long long run = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += up;
+        const long long up = __shfl_up_sync(0xFFFFFFFFu, run, o);
+        if (lane >= o) run += up;
       }
-      const bool here = rem >= inc - w && rem < inc;
+      const bool here = rem >= run - w && rem < run;
       if (here) {
         pl.m = m;
-        pl.off = (int)(rem - (inc - w));
+        pl.off = (int)(rem - (run - w));
       }
       if (__any_sync(0xFFFFFFFFu, here)) break;
-      rem -= __shfl_sync(0xFFFFFFFFu, inc, 31);
+      rem -= __shfl_sync(0xFFFFFFFFu, run, 31);
     }
-    if (lane == 0) {
-      pl.h = h;
-      pl.total = total;
-    }
+    if (lane == 0) pl.h = h;
   }
   __syncthreads();
   return true;
 }
 
-// The units of a CTA's stretch, one after the other.
-template <int TM, int TN>
-struct Walk {
-  using TL = Tiling<TM, TN>;
-  const AttnArgs& a;
-  Seq s;
-  int b, h, m, nm, off;
+// A unit of a CTA's stretch, in shared memory: written by one thread, read by
+// those that work on it.
+struct Unit {
   long long left;      // steps of the stretch still to do, this unit's included
-  typename TL::Span sp;
+  Seq s;
+  int b, h, m, nm;
+  int off;             // the unit's steps that others do before
   int w, take;         // the unit's steps, and those of this CTA
-  int all_lo, all_hi;  // the keys every row of the unit sees
+  int lo, hi;          // the keys of its rows
+  int all_lo, all_hi;  // those every row sees
+  int t0, nt;          // tiles: the first, and this CTA's number of them
 
-  // work: locate's answer; false: a walk of nothing
-  __device__ __forceinline__ Walk(const AttnArgs& a_, const Place& pl, int cta, int n,
-                                  bool work = true)
-      : a(a_), b(pl.b), h(pl.h), m(pl.m), off(pl.off), left(0) {
-    if (!work) return;
-    left = cta_start(pl.total, cta + 1, n) - cta_start(pl.total, cta, n);
-    s = load_seq(a, b);
-    nm = TL::row_tiles(a, s);
-    unit();
-  }
-  __device__ __forceinline__ void unit() {
-    sp = TL::span(a, s, m);
-    w = sp.nt > 0 ? sp.nt : 1;
-    take = (long long)(w - off) < left ? w - off : (int)left;
-    const int rows = s.nq * a.G;
-    all_lo = key_lo(a, s, div_group(a, min(m * TM + TM, rows) - 1));
-    all_hi = key_hi(a, s, div_group(a, m * TM));
-  }
-  // the CTA's tile j of the unit; an edge tile is one that some row sees in part
-  __device__ __forceinline__ int first_key(int j) const { return (sp.t0 + off + j) * TN; }
-  __device__ __forceinline__ bool edge(int j) const {
-    const int k0 = first_key(j);
-    return k0 < all_lo || k0 + TN > all_hi;
-  }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ bool whole() const { return off == 0 && take == w; }
   __device__ __forceinline__ int slot() const { return off > 0 ? 0 : 1; }
-  __device__ __forceinline__ void next() {
-    left -= take;
-    if (left <= 0) return;
-    off = 0;
-    if (++m == nm) {
-      m = 0;
-      if (++h == a.Hkv) {
-        h = 0;
-        nm = 0;
-        while (nm == 0 && ++b < a.bt.B) {
-          s = load_seq(a, b);
-          nm = TL::row_tiles(a, s);
-        }
-        if (nm == 0) {      // lengths that changed under the kernel
-          left = 0;
-          return;
-        }
-      }
-    }
-    unit();
-  }
 };
+
+template <int TM, int TN>
+__device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
+  const typename Tiling<TM, TN>::Span sp = Tiling<TM, TN>::span(a, u.s, u.m);
+  u.w = sp.nt > 0 ? sp.nt : 1;
+  u.take = (long long)(u.w - u.off) < u.left ? u.w - u.off : (int)u.left;
+  u.lo = sp.lo;
+  u.hi = sp.hi;
+  const int rows = u.s.nq * a.G;
+  u.all_lo = key_lo(a, u.s, div_group(a, min(u.m * TM + TM, rows) - 1));
+  u.all_hi = key_hi(a, u.s, div_group(a, u.m * TM));
+  u.t0 = sp.t0 + u.off;
+  u.nt = sp.nt > 0 ? u.take : 0;
+}
+// The first unit of CTA `cta`'s stretch (work: locate's answer; false: none).
+template <int TM, int TN>
+__device__ __noinline__ void unit_first(const AttnArgs& a, const Place& pl, int cta, bool work,
+                                        Unit& u) {
+  u.left = 0;
+  if (!work) return;
+  u.left = pl.line.start(cta + 1) - pl.line.start(cta);
+  u.b = pl.b;
+  u.h = pl.h;
+  u.m = pl.m;
+  u.off = pl.off;
+  u.s = load_seq(a, u.b);
+  u.nm = Tiling<TM, TN>::row_tiles(a, u.s);
+  unit_set<TM, TN>(a, u);
+}
+template <int TM, int TN>
+__device__ __noinline__ void unit_next(const AttnArgs& a, Unit& u) {
+  u.left -= u.take;
+  if (u.left <= 0) return;
+  u.off = 0;
+  if (++u.m == u.nm) {
+    u.m = 0;
+    if (++u.h == a.Hkv) {
+      u.h = 0;
+      int nm = 0, b = u.b;
+      Seq s{0, 0, 0};
+      while (nm == 0 && ++b < a.bt.B) {
+        s = load_seq(a, b);
+        nm = Tiling<TM, TN>::row_tiles(a, s);
+      }
+      if (nm == 0) {      // lengths that changed under the kernel
+        u.left = 0;
+        return;
+      }
+      u.b = b;
+      u.s = s;
+      u.nm = nm;
+    }
+  }
+  unit_set<TM, TN>(a, u);
+}
 
 // ---------------------------------------------------- asynchronous copies --
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {

@@ -21,10 +21,13 @@
 //   warp 8           issues the products; owns tensor memory
 //   warp 9           loads K and V tiles by TMA through a ring, one box per
 //                    stretch of keys that neither a page nor a tile cuts
-//   warps 10, 11     the queries of half 0 and 1, as soon as the unit before
-//                    has had its last scores; the values of tiles that some
-//                    row sees in part: out-of-range rows become zeros, and
-//                    infinities and NaN are looked for
+//   warp 10          the queries of a half, as soon as the unit before has had
+//                    its last scores; the values of tiles that some row sees in
+//                    part: out-of-range rows become zeros, and infinities and
+//                    NaN are looked for
+//   warp 11          D <= 64: issues S = Q K^T, warp 8 only O += P V. There an
+//                    item's products take 512 cycles, less than one warp takes
+//                    to issue both beside two busy softmax warps on its scheduler
 #include "attn.cuh"
 #include "attn_join.cuh"
 #include "common.cuh"
@@ -38,7 +41,7 @@ namespace moe {
 constexpr int kChunkTM = 256;
 constexpr int kChunkTN = 128;
 constexpr int kChunkThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10, kScoreWarp = 11;
 constexpr float kRescaleAt = 8.f;
 
 template <int DP>
@@ -53,6 +56,9 @@ struct ChunkGeo {
   // a half's next scores so wait for it while it works on the present ones.
   static constexpr int bufs = (512 - 2 * DP) / 128;
   static constexpr uint32_t o_col0 = bufs * 128;
+  // With a buffer to spare the scores need not follow the product that frees
+  // theirs in one warp's order of issue: a second warp waits for its end.
+  static constexpr bool split = bufs == 3;
 };
 
 // The product-issuing warp runs as one: every value an instruction takes is the
@@ -85,10 +91,21 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The product warp's wait when the first try has not succeeded.
+// A bounded wait whose loop is out of line: the roles' steady state has to stay
+// small, or the SM spends its time fetching instructions (measured: with every
+// path inline 2.5 of 7.5 cycles between a warp's instructions were fetches).
 __device__ __noinline__ bool wait_slowly(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* status) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status));
+  return mbar_wait_bounded(bar, parity, abort_flag, status);
+}
+// For a whole warp: true in all lanes, or (given up) false in all. CALL: the loop
+// by a call (the softmax warps, whose registers a call would need, keep it here).
+template <bool CALL>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          int* status) {
+  if (__builtin_expect(__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)), 1)) return true;
+  return __all_sync(0xFFFFFFFFu, CALL ? wait_slowly(bar, parity, abort_flag, status)
+                                      : mbar_wait_bounded(bar, parity, abort_flag, status));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -231,8 +248,8 @@ __device__ __forceinline__ bool count_wait_bounded(const int* count, int need,
                                                    volatile int* abort_flag, int* status) {
   const uint64_t t0 = global_ns();
   for (uint32_t i = 1; *(const volatile int*)count < need; ++i) {
-    __nanosleep(20);
-    if ((i & 63u) == 0) {
+    __nanosleep(200);
+    if ((i & 15u) == 0) {
       if (*abort_flag) return false;
       if (global_ns() - t0 > (uint64_t)kWaitLimitNs) {
         *abort_flag = 1;
@@ -244,23 +261,119 @@ __device__ __forceinline__ bool count_wait_bounded(const int* count, int need,
   return true;
 }
 
+// mbar_wait_bounded for a warp that has time: it sleeps between its looks, so
+// that it takes no issue slots from the warps it shares a scheduler with.
+__device__ __forceinline__ bool mbar_doze_bounded(uint32_t bar, uint32_t parity, uint32_t ns,
+                                                  volatile int* abort_flag, int* status) {
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    __nanosleep(ns);
+    if ((i & 15u) == 0) {
+      if (*abort_flag) return false;
+      if (global_ns() - t0 > (uint64_t)kWaitLimitNs) {
+        *abort_flag = 1;
+        raise_status(status, MOE_ERR_DEVICE_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// One tile's row of scores as a thread sees it: keys k0 .. k0 + 127, of which
+// the row sees [lo, hi). Masked by selection: a masked score's value, NaN or
+// not, is dropped.
+struct RowMask {
+  int k0, lo, hi;
+  __device__ __forceinline__ float operator()(float s, int c) const {
+    return k0 + c >= lo && k0 + c < hi ? s : neg_inf();
+  }
+};
+// the row's largest score (of the tile that opens a unit, or outgrows the maximum)
+__device__ __forceinline__ float tile_max(uint32_t t_s, RowMask mask) {
+  float m = neg_inf();
+#pragma unroll 1
+  for (int c0 = 0; c0 < 128; c0 += 32) {
+    float sc[32];
+    tmem_ld32f(t_s + c0, sc);
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) m = fmaxf(m, mask(sc[c], c0 + c));
+  }
+  return m;
+}
+// O of the warp's rows times a factor each
+template <int DP>
+__device__ __forceinline__ void scale_rows(uint32_t t_o, float f) {
+#pragma unroll 1
+  for (int c = 0; c < DP; c += 32) {
+    float o[32];
+    tmem_ld32f(t_o + c, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] *= f;
+    tmem_st32f(t_o + c, o);
+  }
+}
+// The row's weights exp2(s * scale - ref) as bf16 pairs, their sum (unrounded)
+// and the largest score.
+template <bool MASKED>
+__device__ __forceinline__ void tile_weights(uint32_t t_s, float scale, float ref, RowMask mask,
+                                             uint32_t* pk, float& sum, float& top) {
+  float sc[128];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) tmem_ld32f(t_s + g * 32, sc + g * 32);
+  tmem_ld_wait();
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int c = 0; c < 128; ++c) sc[c] = mask(sc[c], c);
+  }
+  float mx[2] = {neg_inf(), neg_inf()};
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int c = 0; c < 128; c += 2) {
+    float2 t = fma2(make_float2(sc[c], sc[c + 1]), scale, -ref);
+    mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], sc[c], sc[c + 1]);
+    t = make_float2(ex2(t.x), ex2(t.y));
+    acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], t);
+    pk[c / 2] = pack_bf16(t.x, t.y);
+  }
+  acc[0] = add2(acc[0], acc[1]);
+  sum = acc[0].x + acc[0].y;
+  top = fmaxf(mx[0], mx[1]);
+}
+
+// Tiles [0, e0) and [e1, nt) of a unit are edge tiles: some row sees them in part.
+__device__ __forceinline__ void edges(const Unit& u, int& e0, int& e1) {
+  // the first tile that begins at or after all_lo, the tiles that end by all_hi
+  e0 = (u.all_lo + kChunkTN - 1) / kChunkTN - u.t0;
+  e0 = min(max(e0, 0), u.nt);
+  e1 = u.all_hi / kChunkTN - u.t0;
+  e1 = min(max(e1, e0), u.nt);
+}
+
 struct ChunkShared {
   Place pl;
+  Unit unit[4];         // the CTA's units, handed on by the load warp
+  uint64_t unit_full[4], unit_empty[4];
   uint64_t kv_full[8], kv_empty[8];
   uint64_t v_seen[8];   // an edge tile's values have been looked through
-  uint64_t q_ready[2], q_free[2], o_done[2], drain;
+  uint64_t q_ready[2], q_free[2], drain[2];
+  uint64_t o_done[2][2];   // of a half, its products in turn
+  uint64_t buf_free[3];    // split: the product that read the buffer has ended
   uint64_t s_full[2][3];   // of a half, its items in turn (each half waits for every one of its
                            // own, so that no phase is taken for the one after the next)
   uint64_t p_ready[3];     // of a buffer
   uint32_t tmem;
   int abort;
   int issued;           // tiles whose loads have been issued
-  int bad[8][2];        // per slot: an infinity or NaN among them (each helper's half)
+  int bad[8];           // per slot: an infinity or NaN among them
 };
 
 template <int DP>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-    attn_chunk_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap mapQ,
+    attn_chunk_kernel(const __grid_constant__ AttnArgs a,
+                      const __grid_constant__ CUtensorMap mapQ,
                       const __grid_constant__ CUtensorMap mapK,
                       const __grid_constant__ CUtensorMap mapV, int box, int q_by_tma) {
   using G = ChunkGeo<DP>;
@@ -279,19 +392,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int i = 0; i < G::slots; ++i) {
       mbar_init(smem_u32(&sh.kv_full[i]), 1);
       mbar_init(smem_u32(&sh.kv_empty[i]), 1);
-      mbar_init(smem_u32(&sh.v_seen[i]), 2);
+      mbar_init(smem_u32(&sh.v_seen[i]), 1);
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(smem_u32(&sh.q_ready[h]), 1);
       mbar_init(smem_u32(&sh.q_free[h]), 1);
-      mbar_init(smem_u32(&sh.o_done[h]), 1);
+      mbar_init(smem_u32(&sh.o_done[h][0]), 1);
+      mbar_init(smem_u32(&sh.o_done[h][1]), 1);
+      mbar_init(smem_u32(&sh.drain[h]), 1);
     }
     for (int i = 0; i < G::bufs; ++i) {
       mbar_init(smem_u32(&sh.s_full[0][i]), 1);
       mbar_init(smem_u32(&sh.s_full[1][i]), 1);
       mbar_init(smem_u32(&sh.p_ready[i]), 4);
+      mbar_init(smem_u32(&sh.buf_free[i]), 1);
     }
-    mbar_init(smem_u32(&sh.drain), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sh.unit_full[i]), 1);
+      mbar_init(smem_u32(&sh.unit_empty[i]), G::split ? 11 : 10);
+    }
     sh.abort = 0;
     sh.issued = 0;
     fence_mbar_init();
@@ -305,9 +424,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // The warp's next unit is there (false: the end, or given up); it has read it.
+  auto take_unit = [&](auto call, int u, bool& ok) {
+    ok = ok && wait_warp<decltype(call)::value>(smem_u32(&sh.unit_full[u & 3]), (u >> 2) & 1, abort,
+                                                a.status);
+    return ok && sh.unit[u & 3].more();
+  };
+  auto give_unit = [&](int u) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.unit_empty[u & 3]));
+  };
+  using Call = std::true_type;
+  using Inline = std::false_type;
   if (warp >= 8) {
     regs_down<88>();
-    if (work && warp == kLoadWarp) {
+    if (warp == kLoadWarp) {
       // -------------------------------------------------------------- loads --
       // lane i < nbox: the box of keys [tile + i * box, + box)
       const int nbox = kChunkTN / box;
@@ -316,12 +447,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       uint32_t phase = 0;
       int fills = 0;
       bool ok = true;
-      for (Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x); wk.more() && ok;
-           wk.next()) {
-        const int nt = wk.sp.nt > 0 ? wk.take : 0;
+      for (int u = 0;; ++u) {
+        // the next unit (or the end, a unit without steps) for every role
+        Unit& un = sh.unit[u & 3];
+        ok = wait_warp<true>(smem_u32(&sh.unit_empty[u & 3]), ((u >> 2) & 1) ^ 1, abort, a.status);
+        if (!ok) break;
+        if (lane == 0) {
+          if (u == 0) {
+            unit_first<kChunkTM, kChunkTN>(a, sh.pl, blockIdx.x, work, un);
+          } else {
+            un = sh.unit[(u - 1) & 3];
+            unit_next<kChunkTM, kChunkTN>(a, un);
+          }
+          mbar_arrive(smem_u32(&sh.unit_full[u & 3]));
+        }
+        __syncwarp();
+        const Unit wk = un;
+        if (!wk.more()) break;
+        const int nt = wk.nt;
         for (int j = 0; j < nt && ok; ++j) {
-          const int key = (wk.sp.t0 + wk.off + j) * kChunkTN + lane * box;
-          const bool mine = lane < nbox && key < wk.sp.hi && key + box > wk.sp.lo;
+          const int key = (wk.t0 + j) * kChunkTN + lane * box;
+          const bool mine = lane < nbox && key < wk.hi && key + box > wk.lo;
           int page = 0, pslot = 0;
           if (mine) {
             const int pg = page_of(a.bt, key);
@@ -336,7 +482,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes * (uint32_t)G::halves;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            ok = ok && mbar_wait_bounded(smem_u32(&sh.kv_empty[slot]), phase ^ 1u, abort, a.status);
+            ok = ok && mbar_doze_bounded(smem_u32(&sh.kv_empty[slot]), phase ^ 1u, 100, abort,
+                                         a.status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             const uint32_t bar = smem_u32(&sh.kv_full[slot]);
@@ -364,7 +511,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           mbar_wait_bounded(smem_u32(&sh.kv_full[slot]), phase, &never, a.status);
         }
       }
-    } else if (work && warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || (G::split && warp == kScoreWarp)) {
       // ----------------------------------------------------------- products --
       constexpr uint32_t kIdQK = idesc_bf16(128, kChunkTN, 0, 0);
       constexpr uint32_t kIdPV = idesc_bf16(128, DP, 0, 1);
@@ -390,12 +537,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       Ring k{0, 0}, v{1, 0};            // ring slots of the next K and V tile
       Ring pb{0, 0}, sb{0, 0};          // buffers of the next weights, the next scores
       int given0 = 0, given1 = 0;       // per half: the scores' next barrier
+      uint32_t done0 = 0, done1 = 0;    // per half: the product's next barrier
+      uint32_t uses = 0;                // split: a bit per buffer, set once it has been used
       uint32_t units0 = 0, units1 = 0;
       uint32_t seen = 0;                // a bit per slot: the parity of its next v_seen
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(smem_u32(bar), parity)))
-          ok = wait_slowly(smem_u32(bar), parity, abort, a.status) && ok;
+        ok = wait_warp<true>(smem_u32(bar), parity, abort, a.status) && ok;
       };
       auto commit = [&](uint64_t* bar) {
         if (leader) umma_commit(smem_u32(bar));
@@ -411,6 +559,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t k0 = k_lo + k.at * (G::tile >> 4);
         const uint32_t d = td + sb.at * 128;
         if (first) wait(&sh.q_ready[h], (h ? units1++ : units0++) & 1);
+        if constexpr (G::split) {
+          // the buffer's product before: none for its first use
+          if (uses >> sb.at & 1) wait(&sh.buf_free[sb.at], sb.phase ^ 1u);
+          uses |= 1u << sb.at;
+        }
         if (!ok) return;
         tc_fence_after();
         if (leader) {
@@ -456,36 +609,44 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (leader) umma_ts(d, pk, desc_of(vk, v_hi), kIdPV, ak);
           }
         }
-        commit(&sh.o_done[h]);
+        uint32_t& done = h ? done1 : done0;
+        commit(&sh.o_done[h][done]);
+        done ^= 1u;
+        if constexpr (G::split) commit(&sh.buf_free[pb.at]);
         pb.step(1, G::bufs);
       };
       using H0 = std::integral_constant<int, 0>;
       using H1 = std::integral_constant<int, 1>;
 
-      Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x);
-      for (; uniform(wk.more() ? 1u : 0u) && ok; wk.next()) {
-        const int nt = (int)uniform(wk.sp.nt > 0 ? wk.take : 0);
+      for (int u = 0; uniform(take_unit(Call{}, u, ok) ? 1u : 0u); ++u) {
+        const Unit wk = sh.unit[u & 3];
+        give_unit(u);
+        const int nt = (int)uniform(wk.nt);
         if (nt == 0) continue;
         const bool two = uniform(wk.s.nq * a.G - wk.m * kChunkTM > 128 ? 1u : 0u) != 0;
         // tiles [0, e0) and [e1, nt) are edge tiles
         int e0 = 0, e1 = nt;
-        while (e0 < nt && wk.edge(e0)) ++e0;
-        while (e1 > e0 && wk.edge(e1 - 1)) --e1;
+        edges(wk, e0, e1);
         e0 = (int)uniform(e0);
         e1 = (int)uniform(e1);
-        int sj = 0;                     // scores: the tile of the next item
-        // the first items' scores
-        auto first_scores = [&](auto H, bool k_done) {
-          if (H.value == 0) wait(&sh.kv_full[k.at], k.phase);
-          if (ok) scores(H, sj == 0, sj + 1 == nt, k_done);
-          if (k_done) ++sj;
-        };
-        if (two) {
-          first_scores(H0{}, false);
-          first_scores(H1{}, true);
-          if (G::bufs == 3 && nt > 1 && ok) first_scores(H0{}, false);
-        } else {
-          for (int i = 0; i < G::bufs && i < nt && ok; ++i) first_scores(H0{}, true);
+        if (G::split && warp == kScoreWarp) {
+          for (int j = 0; j < nt && ok; ++j) {
+            wait(&sh.kv_full[k.at], k.phase);
+            if (ok) scores(H0{}, j == 0, j + 1 == nt, !two);
+            if (two && ok) scores(H1{}, j == 0, j + 1 == nt, true);
+          }
+          continue;
+        }
+        // one warp for all: the scores of the unit's first items
+        if (!G::split) {
+          wait(&sh.kv_full[k.at], k.phase);
+          if (ok) scores(H0{}, true, nt == 1, !two);
+          if (two) {
+            if (ok) scores(H1{}, true, nt == 1, true);
+          } else if (nt > 1) {
+            wait(&sh.kv_full[k.at], k.phase);
+            if (ok) scores(H0{}, false, nt == 2, true);
+          }
         }
         for (int j = 0; j < nt && ok; ++j) {
           wait(&sh.kv_full[v.at], v.phase);
@@ -494,65 +655,59 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           // 16-key steps [s0, s1) of an edge tile hold the unit's keys; in the
           // others V is whatever the ring held before
           if ((j < e0 || j >= e1) && ok) {
-            const int k0 = wk.first_key(j);
-            s0 = (int)uniform(max(wk.sp.lo - k0, 0) >> 4);
-            s1 = (int)uniform((min(wk.sp.hi - k0, kChunkTN) + 15) >> 4);
+            const int k0 = (wk.t0 + j) * kChunkTN;
+            s0 = (int)uniform(max(wk.lo - k0, 0) >> 4);
+            s1 = (int)uniform((min(wk.hi - k0, kChunkTN) + 15) >> 4);
             wait(&sh.v_seen[v.at], seen >> v.at & 1);
             seen ^= 1u << v.at;
-            skip = uniform(sh.bad[v.at][0] | sh.bad[v.at][1]) != 0;
+            skip = uniform(sh.bad[v.at]) != 0;
           }
-          // products of one thread run in the order of issue: the new scores take
-          // the buffer's place after the product has read the weights
+          // Products of one thread run in the order of issue: the new scores take
+          // the buffer's place after the product has read the weights. After an
+          // item: its own half's next tile; with one half, two tiles on.
+          const int dj = two ? 1 : 2;
+          const bool more = !G::split && j + dj < nt, last = j + dj + 1 == nt;
+          if (more && ok) wait(&sh.kv_full[k.at], k.phase);
+          if (ok) product(H0{}, j > 0, skip, s0, s1);
+          if (more && ok) scores(H0{}, false, last, !two);
           if (two) {
-            if (G::bufs == 2) {
-              // the scores after an item are its own half's, one tile on
-              const bool more = j + 1 < nt, last = j + 2 == nt;
-              if (more && ok) wait(&sh.kv_full[k.at], k.phase);
-              if (ok) product(H0{}, j > 0, skip, s0, s1);
-              if (more && ok) scores(H0{}, false, last, false);
-              if (ok) product(H1{}, j > 0, skip, s0, s1);
-              if (more && ok) scores(H1{}, false, last, true);
-            } else {
-              // half 1's one tile on, then half 0's two tiles on
-              if (ok) product(H0{}, j > 0, skip, s0, s1);
-              if (j + 1 < nt && ok) scores(H1{}, false, j + 2 == nt, true);
-              if (j + 2 < nt && ok) wait(&sh.kv_full[k.at], k.phase);
-              if (ok) product(H1{}, j > 0, skip, s0, s1);
-              if (j + 2 < nt && ok) scores(H0{}, false, j + 3 == nt, false);
-            }
-          } else {
-            const bool more = j + G::bufs < nt;
-            if (more && ok) wait(&sh.kv_full[k.at], k.phase);
-            if (ok) product(H0{}, j > 0, skip, s0, s1);
-            if (more && ok) scores(H0{}, false, j + G::bufs + 1 == nt, true);
+            if (ok) product(H1{}, j > 0, skip, s0, s1);
+            if (more && ok) scores(H1{}, false, last, true);
           }
           if (ok) commit(&sh.kv_empty[v.at]);
           v.step(2, G::slots);
         }
       }
       // every product has finished before tensor memory is freed
-      commit(&sh.drain);
+      uint64_t* const drain = &sh.drain[warp == kMmaWarp ? 0 : 1];
+      commit(drain);
       volatile int never = 0;
-      mbar_wait_bounded(smem_u32(&sh.drain), 0, &never, a.status);
+      mbar_wait_bounded(smem_u32(drain), 0, &never, a.status);
       __syncwarp();
-    } else if (work && warp >= kHelpWarp) {
+    } else if (warp == kHelpWarp) {
       // ------------------------------------------------ queries, edge values --
-      const int half = warp - kHelpWarp;
       constexpr int NC = DP / 8;            // 16-byte pieces of a row
       int vslot = 1, gone = 0;              // gone: tiles gone by
-      uint32_t vphase = 0, units = 0;
+      uint32_t vphase = 0, units[2] = {0, 0};
       bool ok = true;
-      for (Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x); wk.more() && ok;
-           wk.next()) {
-        const int nt = wk.sp.nt > 0 ? wk.take : 0;
+      for (int u = 0; take_unit(Call{}, u, ok); ++u) {
+        const Unit wk = sh.unit[u & 3];
+        give_unit(u);
+        const int nt = wk.nt;
         if (nt == 0) continue;
-        const int r0 = wk.m * kChunkTM + half * 128;
-        const int nrows = wk.s.nq * a.G - r0;
-        if (nrows > 0) {
-          if (units > 0)
-            ok = mbar_wait_bounded(smem_u32(&sh.q_free[half]), (units - 1) & 1, abort, a.status);
-          if (!__all_sync(0xFFFFFFFFu, ok)) break;
-          ++units;
+        int e0, e1;
+        edges(wk, e0, e1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r0 = wk.m * kChunkTM + half * 128;
+          const int nrows = wk.s.nq * a.G - r0;
+          if (nrows <= 0) break;
+          if (units[half] > 0)
+            ok = ok && mbar_doze_bounded(smem_u32(&sh.q_free[half]), (units[half] - 1) & 1, 200,
+                                         abort, a.status);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          ++units[half];
           const uint32_t bar = smem_u32(&sh.q_ready[half]);
           const uint32_t dst = s_q + half * G::q_half;
           if (q_by_tma) {
@@ -589,37 +744,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
         for (int j = 0; j < nt; ++j) {
-          if (wk.edge(j)) {
+          if (j < e0 || j >= e1) {
             // the tiles between are not waited for, so first the loads must have
             // come to this one: a barrier's parity tells one round of the ring
             // from the next, not from the one after
             ok = count_wait_bounded(&sh.issued, gone + 1, abort, a.status) &&
                  mbar_wait_bounded(smem_u32(&sh.kv_full[vslot]), vphase, abort, a.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-            const int k0 = wk.first_key(j);
+            const int k0 = (wk.t0 + j) * kChunkTN;
             uint8_t* const vt = kv_mem + vslot * G::tile;
             // Zeros: the rows out of range in the first and last 16-key step that
             // the product takes. Looked through: the rows that only some see.
-            const int v0 = max(wk.sp.lo - k0, 0), v1 = min(wk.sp.hi - k0, kChunkTN);
+            const int v0 = max(wk.lo - k0, 0), v1 = min(wk.hi - k0, kChunkTN);
             const int f0 = min(max(wk.all_lo - k0, v0), v1), f1 = max(min(wk.all_hi - k0, v1), f0);
             auto piece = [&](int i) {      // piece i % NC of key row i / NC
               const int row = i / NC, c = i - row * NC;
               return reinterpret_cast<uint4*>(vt + (c >> 3) * (128 * 128) + row * 128 +
                                               (((c ^ row) & 7) << 4));
             };
-            const int t = half * 32 + lane;
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            for (int i = (v0 & ~15) * NC + t; i < v0 * NC; i += 64) *piece(i) = zero;
-            for (int i = v1 * NC + t; i < ((v1 + 15) & ~15) * NC; i += 64) *piece(i) = zero;
+            for (int i = (v0 & ~15) * NC + lane; i < v0 * NC; i += 32) *piece(i) = zero;
+            for (int i = v1 * NC + lane; i < ((v1 + 15) & ~15) * NC; i += 32) *piece(i) = zero;
             uint32_t bad = 0;
-#pragma unroll 4
-            for (int i = v0 * NC + t; i < f0 * NC; i += 64) bad |= not_finite8(*piece(i));
-#pragma unroll 4
-            for (int i = f1 * NC + t; i < v1 * NC; i += 64) bad |= not_finite8(*piece(i));
+#pragma unroll 8
+            for (int i = v0 * NC + lane; i < f0 * NC; i += 32) bad |= not_finite8(*piece(i));
+#pragma unroll 8
+            for (int i = f1 * NC + lane; i < v1 * NC; i += 32) bad |= not_finite8(*piece(i));
             fence_async_smem();
             const int any = __any_sync(0xFFFFFFFFu, bad != 0);
             if (lane == 0) {
-              sh.bad[vslot][half] = any;
+              sh.bad[vslot] = any;
               mbar_arrive(smem_u32(&sh.v_seen[vslot]));
             }
             __syncwarp();
@@ -642,21 +796,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint32_t mine = 0;                // this half's items so far
     uint32_t seen = 0;
     bool ok = true;
-    Walk<kChunkTM, kChunkTN> wk(a, sh.pl, blockIdx.x, gridDim.x, work);
-    for (; wk.more() && ok; wk.next()) {
+    for (int u = 0; take_unit(Inline{}, u, ok); ++u) {
+      const Unit wk = sh.unit[u & 3];
+      give_unit(u);
       const Seq s = wk.s;
       const int r0 = wk.m * kChunkTM + half * 128;
       const int left = s.nq * a.G - wk.m * kChunkTM;
       const int nh = left > 128 ? 2 : 1;
       const int nrows = min(128, left - half * 128);
-      const int nt = wk.sp.nt > 0 ? wk.take : 0;
+      const int nt = wk.nt, t0 = wk.t0;
+      int e0, e1;
+      edges(wk, e0, e1);
       const uint32_t first_item = item0 + half;
       const int first_tile = tile0;
       item0 += nt * nh;
       tile0 += nt;
       if (nrows <= 0) {               // the half has no rows: its tiles go by
         for (int j = 0; j < nt; ++j)
-          if (wk.edge(j)) seen ^= 1u << ((2 * (first_tile + j) + 1) % G::slots);
+          if (j < e0 || j >= e1) seen ^= 1u << ((2 * (first_tile + j) + 1) % G::slots);
         continue;
       }
       const int r = r0 + min(row, nrows - 1);
@@ -673,104 +830,67 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                   warp_hi = key_hi(a, s, div_group(a, w0));
 
         for (int j = 0; j < nt; ++j) {
-          const int k0 = wk.first_key(j);
+          const int k0 = (t0 + j) * kChunkTN;
           const uint32_t n = first_item + j * nh;
           const int buf = n % G::bufs;
           const uint32_t t_s = t_lane + buf * 128;
-          ok = ok && mbar_wait_bounded(smem_u32(&sh.s_full[half][mine % G::bufs]),
-                                       (mine / G::bufs) & 1, abort, a.status);
-          if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+          ok = ok && wait_warp<false>(smem_u32(&sh.s_full[half][mine % G::bufs]), (mine / G::bufs) & 1,
+                               abort, a.status);
+          if (!ok) break;
           tc_fence_after();
-          // the half's product before this one, for who is to change O
+          // the half's product before this one has ended, for who is to change O
+          // (the two before it have: their buffers hold later scores)
           auto o_is_done = [&]() {
-            ok = ok && mbar_wait_bounded(smem_u32(&sh.o_done[half]), (mine - 1) & 1, abort,
-                                         a.status);
-            ok = __all_sync(0xFFFFFFFFu, ok);
+            ok = ok && wait_warp<false>(smem_u32(&sh.o_done[half][(mine - 1) & 1]),
+                                 ((mine - 1) >> 1) & 1, abort, a.status);
             tc_fence_after();
           };
           // The weights are taken against the maximum so far while the tile's own
           // is still being found; only when a row's has grown by more than 2^8
-          // (always in a unit's first tile, where it is found first) the scores
-          // are read again. Stored weights replace them only afterwards.
-          bool find_first = j == 0;
+          // (taken as so in a unit's first tile) the maximum is found first, O
+          // rescaled and the scores read again. The weights replace them only then.
+          const RowMask mask{k0, lo, hi};
+          const bool masked = k0 + kChunkTN > warp_hi || k0 < warp_lo;
           uint32_t pk[64];
-          float2 acc[2];
-          for (;;) {
-            float sc[128];
-            tmem_ld32f(t_s, sc);
-            tmem_ld32f(t_s + 32, sc + 32);
-            tmem_ld32f(t_s + 64, sc + 64);
-            tmem_ld32f(t_s + 96, sc + 96);
-            tmem_ld_wait();
-            // masked by selection: a masked score's value, NaN or not, is dropped
-            if (k0 + kChunkTN > warp_hi) {
-#pragma unroll
-              for (int c = 0; c < 128; ++c) sc[c] = c < hi - k0 ? sc[c] : neg_inf();
-            }
-            if (k0 < warp_lo) {
-#pragma unroll
-              for (int c = 0; c < 128; ++c) sc[c] = c >= lo - k0 ? sc[c] : neg_inf();
-            }
-            if (find_first) {
-              float mx[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mx[i] = fmaxf(sc[2 * i], sc[2 * i + 1]);
-#pragma unroll
-              for (int c = 8; c < 128; c += 2)
-                mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], sc[c], sc[c + 1]);
-              const float m2 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+          float sum, top;
+          bool grew = j == 0;
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            if (__builtin_expect(__any_sync(0xFFFFFFFFu, grew), 0)) {
+              const float m2 = tile_max(t_s, mask) * a.scale_log2;
               const float nm = m2 > m_ref + kRescaleAt ? m2 : m_ref;
               const float f = nm == neg_inf() ? 1.f : ex2(m_ref - nm);
               m_ref = nm;
               l *= f;
               if (j > 0) {
                 o_is_done();
-#pragma unroll 1
-                for (int c = 0; c < DP; c += 32) {
-                  float o[32];
-                  tmem_ld32f(t_o + c, o);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] *= f;
-                  tmem_st32f(t_o + c, o);
-                }
+                scale_rows<DP>(t_o, f);
               }
             }
             const float ref = m_ref == neg_inf() ? 0.f : m_ref;
-            float mx[2] = {neg_inf(), neg_inf()};
-            acc[0] = acc[1] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 128; c += 2) {
-              float2 t = fma2(make_float2(sc[c], sc[c + 1]), a.scale_log2, -ref);
-              mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], sc[c], sc[c + 1]);
-              t = make_float2(ex2(t.x), ex2(t.y));
-              acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], t);
-              pk[c / 2] = pack_bf16(t.x, t.y);
-            }
-            const bool grew = fmaxf(mx[0], mx[1]) * a.scale_log2 > m_ref + kRescaleAt;
-            if (find_first || !__any_sync(0xFFFFFFFFu, grew)) break;
-            find_first = true;
+            if (__builtin_expect(masked, 0))
+              tile_weights<true>(t_s, a.scale_log2, ref, mask, pk, sum, top);
+            else
+              tile_weights<false>(t_s, a.scale_log2, ref, mask, pk, sum, top);
+            grew = real && top * a.scale_log2 > m_ref + kRescaleAt;
+            if (__builtin_expect(!__any_sync(0xFFFFFFFFu, grew), 1)) break;
           }
-          // every product is waited for in turn: a barrier's parity tells only the
-          // latest phase from the one before (it has mostly ended long ago)
-          if (j > 0) o_is_done();
           tmem_st32(t_s, pk);
           tmem_st32(t_s + 32, pk + 32);
-          acc[0] = add2(acc[0], acc[1]);
-          l += acc[0].x + acc[0].y;
+          l += sum;
           tmem_st_wait();
-          if (wk.edge(j)) {
+          if (__builtin_expect(j < e0 || j >= e1, 0)) {
             // A zero weight does not keep an infinite or NaN value out of the
             // product: a tile that some row sees in part and that holds one is not
             // multiplied; its P V is added here, key by key over the rows that see it.
             const int t = first_tile + j, vslot = (2 * t + 1) % G::slots;
-            ok = ok && mbar_wait_bounded(smem_u32(&sh.v_seen[vslot]), seen >> vslot & 1, abort,
-                                         a.status);
+            ok = ok && wait_warp<false>(smem_u32(&sh.v_seen[vslot]), seen >> vslot & 1, abort, a.status);
             seen ^= 1u << vslot;
-            const bool by_hand = ok && (sh.bad[vslot][0] | sh.bad[vslot][1]) != 0;
+            const bool by_hand = ok && sh.bad[vslot] != 0;
             if (__any_sync(0xFFFFFFFFu, by_hand)) {
-              ok = ok && mbar_wait_bounded(smem_u32(&sh.kv_full[vslot]),
-                                           ((2 * t + 1) / G::slots) & 1, abort, a.status);
+              ok = ok && wait_warp<false>(smem_u32(&sh.kv_full[vslot]), ((2 * t + 1) / G::slots) & 1,
+                                   abort, a.status);
+              if (j > 0) o_is_done();
               __syncwarp();
               add_by_hand<DP>(t_s, t_o, kv_mem + vslot * G::tile, k0, lo, hi, j > 0);
               tmem_st_wait();
@@ -781,8 +901,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[buf]));
           ++mine;
         }
-        ok = ok && mbar_wait_bounded(smem_u32(&sh.o_done[half]), (mine - 1) & 1, abort, a.status);
-        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+        // the last two products in turn: a parity tells a barrier's latest phase
+        // only from the one before
+        for (uint32_t i = mine > 1 ? mine - 2 : 0; i < mine && ok; ++i)
+          ok = wait_warp<false>(smem_u32(&sh.o_done[half][i & 1]), (i >> 1) & 1, abort, a.status);
+        if (!ok) break;
         tc_fence_after();
       }
       // ---- the unit's rows: final, or this CTA's part ------------------------

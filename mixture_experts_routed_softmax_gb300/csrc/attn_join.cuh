@@ -12,18 +12,18 @@ namespace moe {
 constexpr int kJoinThreads = 256;
 
 template <int TM, int TN, int DP>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a, int n) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a, int n) {
   __shared__ Place pl;
   pdl_enter();
   const int cta = blockIdx.x + 1;
   if (!locate<TM, TN, kJoinThreads>(a, cta, n, pl)) return;
-  const long long total = pl.total;
-  const long long unit0 = cta_start(total, cta, n) - pl.off;
-  if (pl.off == 0 || cta_start(total, cta - 1, n) > unit0) return;
+  const Line line = pl.line;
+  const long long unit0 = line.start(cta) - pl.off;
+  if (pl.off == 0 || line.start(cta - 1) > unit0) return;
   const Seq s = load_seq(a, pl.b);
   const long long unit1 = unit0 + Tiling<TM, TN>::weight(a, s, pl.m);
   int last = cta;             // the parts are those of CTAs cta - 1 .. last - 1
-  while (last < n && cta_start(total, last, n) < unit1) ++last;
+  while (last < n && line.start(last) < unit1) ++last;
   const int r0 = pl.m * TM;
   const int nrows = min(TM, s.nq * a.G - r0);
   const int stripes = gridDim.y;
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p = cta - 1; p < last; ++p) {
       // a CTA without steps left no part
-      if (cta_start(total, p + 1, n) == cta_start(total, p, n)) continue;
+      if (line.start(p + 1) == line.start(p)) continue;
       const int64_t slot = (int64_t)p * 2 + (p == cta - 1 ? 1 : 0);
       const float2 ml = a.part_ml[slot * TM + r];
       const float4 v = *reinterpret_cast<const float4*>(a.part_o + (slot * TM + r) * DP + c4 * 4);

@@ -93,25 +93,28 @@ __device__ __forceinline__ int64_t key_at(const AttnArgs& a, int b, int key, int
 }
 
 template <int DP, int MB>
-__global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
   using G = RowsGeo<DP, MB>;
   constexpr int TM = G::TM, TN = kRowsTN, S = G::stages;
   constexpr int ND = DP / 8;               // 8-wide column tiles of the accumulator
   constexpr int NC = DP / 8;               // 16-byte pieces of a row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Place pl;
+  __shared__ Unit un;
   __shared__ float2 s_ml[kRowsWarps][TM];
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (!locate<TM, TN, kRowsThreads>(a, blockIdx.x, gridDim.x, pl)) return;
-  Walk<TM, TN> wk(a, pl, blockIdx.x, gridDim.x);
+  if (tid == 0) unit_first<TM, TN>(a, pl, blockIdx.x, true, un);
+  __syncthreads();
 
   const uint32_t s_ring = smem_u32(smem) + warp * S * G::stage;
   const uint32_t s_q = smem_u32(smem) + (uint32_t)(G::smem - G::q_bytes);
   float* const merge = reinterpret_cast<float*>(smem);
   const int lr = lane >> 2, lc = lane & 3;      // accumulator row and column pair
 
-  for (; wk.more(); wk.next()) {
+  while (un.more()) {
+    const Unit wk = un;
     const Seq s = wk.s;
     const int rows = s.nq * a.G;
     const int r0 = wk.m * TM;
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const AttnArgs 
       }
     const int all_lo = wk.all_lo;
     const int all_hi = wk.all_hi;
-    const bool rows_differ = all_lo > wk.sp.lo || all_hi < wk.sp.hi;
+    const bool rows_differ = all_lo > wk.lo || all_hi < wk.hi;
 
     float o[MB][ND][4];
     float mx[MB][2], sum[MB][2];
@@ -152,8 +155,8 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const AttnArgs 
       mx[mb][0] = mx[mb][1] = neg_inf();
       sum[mb][0] = sum[mb][1] = 0.f;
     }
-    const int ntile = wk.sp.nt > 0 ? wk.take : 0;
-    const int tile0 = wk.sp.t0 + wk.off;
+    const int ntile = wk.nt;
+    const int tile0 = wk.t0;
     const moe_bf16* kh = a.k + (int64_t)h * a.head_stride;
     const moe_bf16* vh = a.v + (int64_t)h * a.head_stride;
 
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const AttnArgs 
     auto first_key = [&](int j) { return (tile0 + j) * TN + warp * kChunk; };
     auto lookup = [&](int j) -> int64_t {
       if (j >= ntile) return -1;
-      return key_at(a, wk.b, first_key(j) + (lane & 15), wk.sp.lo, wk.sp.hi);
+      return key_at(a, wk.b, first_key(j) + (lane & 15), wk.lo, wk.hi);
     };
     auto issue = [&](int j, int64_t at) {
       if (j < ntile) {
@@ -367,6 +370,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const AttnArgs 
         if (c4 == 0) a.part_ml[pslot * TM + r] = make_float2(m, l);
       }
     }
+    if (tid == 0) unit_next<TM, TN>(a, un);
     __syncthreads();          // the merge buffer is the ring again
   }
 }
@@ -423,7 +427,7 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   a.q = q; a.q_stride = q_stride; a.out = out; a.out_stride = out_stride;
   a.sinks = sinks; a.lse = lse;
   a.Hq = Hq; a.Hkv = c.Hkv; a.G = Hq / c.Hkv; a.D = c.D;
-  a.g_shift = shift_of(a.G);
+  a.g_recip = recip_of(a.G);
   a.scale_log2 = scale * kLog2e;
   a.causal = causal ? 1 : 0;
   // a window of the whole cache or more masks nothing
