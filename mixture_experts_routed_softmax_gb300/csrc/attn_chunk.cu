@@ -6,10 +6,11 @@
 //   S = Q K^T      tcgen05.mma, both operands in shared memory, S in tensor memory
 //   P = exp2(S * scale - max), rounded to bf16 over S's own columns
 //   O += P V       tcgen05.mma with P read from tensor memory
-// One pass with a running maximum: a row's reference maximum is only moved
-// (and O rescaled in tensor memory) when it grew by more than 2^8, so the
-// accumulator is touched a few times a unit instead of once a tile; weights of
-// up to 2^8 cost no precision, in bf16 or in the fp32 sums.
+// One pass with a running reference for the exponent: a row's is the maximum of
+// its first 32 keys, and is only moved (O, the sum and the tile's stored weights
+// rescaled) when a score exceeds it by more than 16 in powers of two. Weights of
+// up to 2^16 cost no precision, in bf16 or in the fp32 sums, and the accumulator
+// is next to never touched between products.
 //
 // The tensor cores and the exponentials are the two resources of like cost
 // (for D = 128 four 128x128x128 products and 32 Ki exponentials a tile), so
@@ -42,7 +43,7 @@ constexpr int kChunkTM = 256;
 constexpr int kChunkTN = 128;
 constexpr int kChunkThreads = 384;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10, kScoreWarp = 11;
-constexpr float kRescaleAt = 8.f;
+constexpr float kRescaleAt = 16.f;
 
 template <int DP>
 struct ChunkGeo {
@@ -118,6 +119,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
       "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float* r) {
@@ -284,63 +293,52 @@ __device__ __forceinline__ bool mbar_doze_bounded(uint32_t bar, uint32_t parity,
 // the row sees [lo, hi). Masked by selection: a masked score's value, NaN or
 // not, is dropped.
 struct RowMask {
-  int k0, lo, hi;
+  int lo, hi;      // less k0
   __device__ __forceinline__ float operator()(float s, int c) const {
-    return k0 + c >= lo && k0 + c < hi ? s : neg_inf();
+    return c >= lo && c < hi ? s : neg_inf();
   }
 };
-// the row's largest score (of the tile that opens a unit, or outgrows the maximum)
-__device__ __forceinline__ float tile_max(uint32_t t_s, RowMask mask) {
-  float m = neg_inf();
-#pragma unroll 1
-  for (int c0 = 0; c0 < 128; c0 += 32) {
-    float sc[32];
-    tmem_ld32f(t_s + c0, sc);
-    tmem_ld_wait();
-#pragma unroll
-    for (int c = 0; c < 32; ++c) m = fmaxf(m, mask(sc[c], c0 + c));
-  }
-  return m;
-}
 // O of the warp's rows times a factor each
 template <int DP>
 __device__ __forceinline__ void scale_rows(uint32_t t_o, float f) {
 #pragma unroll 1
-  for (int c = 0; c < DP; c += 32) {
-    float o[32];
-    tmem_ld32f(t_o + c, o);
+  for (int c = 0; c < DP; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(t_o + c, o);
     tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] *= f;
-    tmem_st32f(t_o + c, o);
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+    tmem_st16(t_o + c, o);
+  }
+  tmem_st_wait();
+}
+// the first n columns of stored weights (bf16 pairs) times a factor each
+__device__ __forceinline__ void scale_weights(uint32_t t_p, int n, float f) {
+  tmem_st_wait();
+#pragma unroll 1
+  for (int c = 0; c < n; c += 16) {
+    uint32_t w[16];
+    tmem_ld16(t_p + c, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
+    tmem_st16(t_p + c, w);
   }
 }
-// The row's weights exp2(s * scale - ref) as bf16 pairs, their sum (unrounded)
-// and the largest score.
-template <bool MASKED>
-__device__ __forceinline__ void tile_weights(uint32_t t_s, float scale, float ref, RowMask mask,
-                                             uint32_t* pk, float& sum, float& top) {
-  float sc[128];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) tmem_ld32f(t_s + g * 32, sc + g * 32);
-  tmem_ld_wait();
-  if constexpr (MASKED) {
-#pragma unroll
-    for (int c = 0; c < 128; ++c) sc[c] = mask(sc[c], c);
-  }
+// 32 scores to weights exp2(s * scale - ref), as bf16 pairs; their sum
+// (unrounded) is added to acc; the largest score.
+__device__ __forceinline__ float group_weights(const float* x, float scale, float ref,
+                                               uint32_t* pk, float2* acc) {
   float mx[2] = {neg_inf(), neg_inf()};
-  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-  for (int c = 0; c < 128; c += 2) {
-    float2 t = fma2(make_float2(sc[c], sc[c + 1]), scale, -ref);
-    mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], sc[c], sc[c + 1]);
+  for (int c = 0; c < 32; c += 2) {
+    float2 t = fma2(make_float2(x[c], x[c + 1]), scale, -ref);
+    mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], x[c], x[c + 1]);
     t = make_float2(ex2(t.x), ex2(t.y));
     acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], t);
     pk[c / 2] = pack_bf16(t.x, t.y);
   }
-  acc[0] = add2(acc[0], acc[1]);
-  sum = acc[0].x + acc[0].y;
-  top = fmaxf(mx[0], mx[1]);
+  return fmaxf(mx[0], mx[1]);
 }
 
 // Tiles [0, e0) and [e1, nt) of a unit are edge tiles: some row sees them in part.
@@ -845,39 +843,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                  ((mine - 1) >> 1) & 1, abort, a.status);
             tc_fence_after();
           };
-          // The weights are taken against the maximum so far while the tile's own
-          // is still being found; only when a row's has grown by more than 2^8
-          // (taken as so in a unit's first tile) the maximum is found first, O
-          // rescaled and the scores read again. The weights replace them only then.
-          const RowMask mask{k0, lo, hi};
-          const bool masked = k0 + kChunkTN > warp_hi || k0 < warp_lo;
-          uint32_t pk[64];
-          float sum, top;
-          bool grew = j == 0;
-#pragma unroll 1
-          for (int pass = 0; pass < 2; ++pass) {
+          // In groups of 32 keys, the next one loaded while one is worked on; a
+          // group's weights take the place of scores already read. The loop is
+          // kept rolled (two groups a turn) for the instruction cache.
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto group = [&](const float* x, int g) {
+            uint32_t pk[16];
+            const float2 was[2] = {acc[0], acc[1]};
+            float top = group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk, acc);
+            const bool grew = real && top * a.scale_log2 > m_ref + kRescaleAt;
             if (__builtin_expect(__any_sync(0xFFFFFFFFu, grew), 0)) {
-              const float m2 = tile_max(t_s, mask) * a.scale_log2;
-              const float nm = m2 > m_ref + kRescaleAt ? m2 : m_ref;
+              const float nm = grew ? top * a.scale_log2 : m_ref;
               const float f = nm == neg_inf() ? 1.f : ex2(m_ref - nm);
               m_ref = nm;
               l *= f;
+              acc[0] = make_float2(was[0].x * f, was[0].y * f);
+              acc[1] = make_float2(was[1].x * f, was[1].y * f);
+              scale_weights(t_s, g * 16, f);
               if (j > 0) {
                 o_is_done();
                 scale_rows<DP>(t_o, f);
               }
+              group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk, acc);
             }
-            const float ref = m_ref == neg_inf() ? 0.f : m_ref;
-            if (__builtin_expect(masked, 0))
-              tile_weights<true>(t_s, a.scale_log2, ref, mask, pk, sum, top);
-            else
-              tile_weights<false>(t_s, a.scale_log2, ref, mask, pk, sum, top);
-            grew = real && top * a.scale_log2 > m_ref + kRescaleAt;
-            if (__builtin_expect(!__any_sync(0xFFFFFFFFu, grew), 1)) break;
+            tmem_st16(t_s + g * 16, pk);
+          };
+          const bool masked = k0 + kChunkTN > warp_hi || k0 < warp_lo;
+          const RowMask mask{lo - k0, hi - k0};
+          float x0[32], x1[32];
+          tmem_ld32f(t_s, x0);
+#pragma unroll 1
+          for (int g = 0; g < 4; g += 2) {
+            tmem_ld_wait();
+            tmem_ld32f(t_s + g * 32 + 32, x1);
+            if (__builtin_expect(masked, 0)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x0[c] = mask(x0[c], g * 32 + c);
+            }
+            group(x0, g);
+            tmem_ld_wait();
+            if (g == 0) tmem_ld32f(t_s + 64, x0);
+            if (__builtin_expect(masked, 0)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x1[c] = mask(x1[c], g * 32 + 32 + c);
+            }
+            group(x1, g + 1);
           }
-          tmem_st32(t_s, pk);
-          tmem_st32(t_s + 32, pk + 32);
-          l += sum;
+          acc[0] = add2(acc[0], acc[1]);
+          l += acc[0].x + acc[0].y;
           tmem_st_wait();
           if (__builtin_expect(j < e0 || j >= e1, 0)) {
             // A zero weight does not keep an infinite or NaN value out of the
