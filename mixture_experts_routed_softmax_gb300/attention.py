@@ -17,21 +17,35 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from .layer import _p, _stream
 
 BF16 = torch.bfloat16
 _ref = _lib.ctypes.addressof
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _view(name: str, t: torch.Tensor, T: int, H: int, D: int) -> int:
-    """Check a [T, H, D] bf16 view with packed heads; its token stride."""
-    if t.dtype != BF16 or t.device.type != "cuda":
+    """Check a [T, H, D] bf16 view with packed heads; its token stride. (These
+    checks are a good part of a one-token call's host time: the usual case,
+    tokens of packed heads, is looked at first.)"""
+    if t.dtype is not BF16 or not t.is_cuda:
         raise ValueError(f"{name}: a bf16 CUDA tensor is needed")
-    if tuple(t.shape) != (T, H, D):
+    if t.shape != (T, H, D):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, H, D)}")
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    st, sh, sd = t.stride()
+    if sd == 1 and sh == D:
+        return st if T > 1 else H * D
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"{name}: heads must be packed (strides {t.stride()})")
-    return t.stride(0) if T > 1 else H * D
+    return st if T > 1 else H * D
+
+
+def _check(fn: str, code: int) -> None:
+    if code:
+        raise _lib.MoEError(fn, code)
 
 
 def _int32(name: str, t: torch.Tensor, shape) -> torch.Tensor:
@@ -75,6 +89,9 @@ class Rope:
                      else torch.tensor(list(axis), dtype=torch.int32, device=device))
         self.args = _lib.Rotary(_p(self.turns), _p(self.axis), self.rd, n_axes, int(interleaved),
                                 float(scale))
+        self._ref = _ref(self.args)
+        self._call = self.lib.moe_rope
+        self._dev = self.turns.device.index
 
     @classmethod
     def from_base(cls, rd: int, base: float, **kw) -> "Rope":
@@ -84,8 +101,9 @@ class Rope:
     def _pos(self, pos: torch.Tensor, T: int) -> torch.Tensor:
         if pos.dim() == 1:
             pos = pos[None]
-        _int32("pos", pos, (self.n_axes, T))
-        if self.n_axes > 1 and T > 0 and pos.stride(0) != T:
+        if pos.dtype is not torch.int32 or not pos.is_cuda or pos.shape != (self.n_axes, T):
+            raise ValueError(f"pos: an int32 CUDA tensor of shape {(self.n_axes, T)} is needed")
+        if not pos.is_contiguous():
             raise ValueError("pos: its rows must be packed")
         return pos
 
@@ -97,10 +115,16 @@ class Rope:
         Hk = 0 if k is None else int(k.shape[1])
         if (k is None) != (k_out is None):
             raise ValueError("k and k_out go together")
-        _lib.call("moe_rope", _ref(self.args), _p(pos), T, D, int(transpose),
-                  _p(q), _view("q", q, T, H, D), H, _p(q_out), _view("q_out", q_out, T, H, D),
-                  _p(k), 0 if k is None else _view("k", k, T, Hk, D), Hk, _p(k_out),
-                  0 if k is None else _view("k_out", k_out, T, Hk, D), _stream(stream))
+        ks = kos = 0
+        kp = kop = None
+        if k is not None:
+            ks, kos = _view("k", k, T, Hk, D), _view("k_out", k_out, T, Hk, D)
+            kp, kop = k.data_ptr(), k_out.data_ptr()
+        _check("moe_rope", self._call(
+            self._ref, pos.data_ptr(), T, D, int(transpose), q.data_ptr(),
+            _view("q", q, T, H, D), H, q_out.data_ptr(), _view("q_out", q_out, T, H, D),
+            kp, ks, Hk, kop, kos,
+            _current_stream(self._dev) if stream is None else stream.cuda_stream))
         return q_out
 
 
@@ -119,6 +143,7 @@ class KVBatch:
         stride = self.page_table.stride(0) if B > 1 else pages
         self.args = _lib.KVBatchArgs(_p(self.cu_q), _p(self.kv_len), _p(self.page_table), stride,
                                      self.T, B, pages, self.T if max_q is None else int(max_q))
+        self._ref = _ref(self.args)
 
 
 @dataclass
@@ -168,6 +193,11 @@ class PagedAttention:
         st = k_cache.stride()
         self.cache = _lib.KVCache(_p(k_cache), _p(v_cache), self.n_pages, st[0], st[ha], st[sa],
                                   self.page_size, self.Hkv, self.D)
+        self._ref = _ref(self.cache)
+        self._rope = None if rope is None else _ref(rope.args)
+        self._sinks = _p(self.sinks)
+        self._call_append, self._call_attend = self.lib.moe_kv_append, self.lib.moe_attn_paged
+        self._dev = self.device.index
 
     def buffers(self, T: int, lse: bool = False) -> AttnBuffers:
         kw = dict(device=self.device)
@@ -189,11 +219,17 @@ class PagedAttention:
             if self.rope is None:
                 raise ValueError("positions without a rotation")
             pos = self.rope._pos(pos, T)
-        _lib.call("moe_kv_append", _ref(self.cache), _ref(batch.args),
-                  None if self.rope is None else _ref(self.rope.args), _p(pos),
-                  _p(k), _view("k", k, T, Hkv, D), _p(v), _view("v", v, T, Hkv, D),
-                  _p(q), 0 if q is None else _view("q", q, T, Hq, D), Hq, _p(q_out),
-                  0 if q is None else _view("q_out", q_out, T, Hq, D), _stream(stream))
+        qs = qos = 0
+        qp = qop = pp = None
+        if q is not None:
+            qs, qos = _view("q", q, T, Hq, D), _view("q_out", q_out, T, Hq, D)
+            qp, qop = q.data_ptr(), q_out.data_ptr()
+        if pos is not None:
+            pp = pos.data_ptr()
+        _check("moe_kv_append", self._call_append(
+            self._ref, batch._ref, self._rope, pp, k.data_ptr(), _view("k", k, T, Hkv, D),
+            v.data_ptr(), _view("v", v, T, Hkv, D), qp, qs, Hq, qop, qos,
+            _current_stream(self._dev) if stream is None else stream.cuda_stream))
         return q_out
 
     def attend(self, q, batch: KVBatch, b: AttnBuffers, out=None, stream=None):
@@ -201,12 +237,14 @@ class PagedAttention:
         b.lse, when there, takes the log-sum-exp of every row."""
         out = b.out if out is None else out
         T, Hq, D = batch.T, self.Hq, self.D
-        if b.lse is not None and (tuple(b.lse.shape) != (T, Hq) or not b.lse.is_contiguous()):
-            raise ValueError(f"lse: shape {tuple(b.lse.shape)}, expected {(T, Hq)}")
-        _lib.call("moe_attn_paged", _ref(self.cache), _ref(batch.args), _p(q),
-                  _view("q", q, T, Hq, D), Hq, self.scale, int(self.causal), self.window,
-                  _p(self.sinks), _p(out), _view("out", out, T, Hq, D), _p(b.lse), _p(b.ws),
-                  b.ws.numel(), _stream(stream))
+        lse, ws = b.lse, b.ws
+        if lse is not None and (lse.shape != (T, Hq) or not lse.is_contiguous()):
+            raise ValueError(f"lse: shape {tuple(lse.shape)}, expected {(T, Hq)}")
+        _check("moe_attn_paged", self._call_attend(
+            self._ref, batch._ref, q.data_ptr(), _view("q", q, T, Hq, D), Hq, self.scale,
+            self.causal, self.window, self._sinks, out.data_ptr(), _view("out", out, T, Hq, D),
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+            _current_stream(self._dev) if stream is None else stream.cuda_stream))
         return out
 
     def forward(self, q, k, v, batch: KVBatch, b: AttnBuffers, pos=None, stream=None):
@@ -216,4 +254,5 @@ class PagedAttention:
 
     def status(self, stream=None) -> int:
         """Synchronise and read (and clear) the device status word."""
-        return int(self.lib.moe_status(_stream(stream)))
+        return int(self.lib.moe_status(
+            _current_stream(self._dev) if stream is None else stream.cuda_stream))

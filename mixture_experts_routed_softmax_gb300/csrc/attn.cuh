@@ -14,6 +14,8 @@
 // cut unit in order, so results do not depend on timing.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace moe {
@@ -377,6 +379,21 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+
+// ------------------------------------------------------------------ host --
+// Raises a kernel's shared-memory limit on the current device, once per device.
+struct SmemOnce {
+  std::atomic<uint64_t> done{0};
+  cudaError_t set(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+    return e;
+  }
+};
 
 // ------------------------------------------------------------- arithmetic --
 __device__ __forceinline__ float ex2(float x) {

@@ -993,7 +993,8 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
   if (by_tma && !map_heads(&mq, a.q, a.D, a.Hq, a.bt.T, a.q_stride, a.G, 128 / a.G))
     return cudaErrorInvalidValue;
   auto kern = attn_chunk_kernel<DP>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
+  static SmemOnce once;
+  cudaError_t e = once.set((const void*)kern, G::smem);
   if (e != cudaSuccess) return e;
   const int n = num_sms();
   a.part_ml = static_cast<float2*>(ws);

@@ -387,7 +387,8 @@ template <int DP, int MB>
 static cudaError_t launch_rows(AttnArgs a, void* ws, cudaStream_t s) {
   using G = RowsGeo<DP, MB>;
   auto kern = attn_rows_kernel<DP, MB>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::smem);
+  static SmemOnce once;
+  cudaError_t e = once.set((const void*)kern, G::smem);
   if (e != cudaSuccess) return e;
   const int n = rows_ctas<DP, MB>();
   a.part_ml = static_cast<float2*>(ws);
