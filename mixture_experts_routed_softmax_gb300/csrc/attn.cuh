@@ -66,6 +66,8 @@ struct AttnArgs {
   uint32_t g_recip;
   float scale_log2;      // scale * log2(e): scores and maxima are kept in powers of two
   int causal, window;    // window 0: none
+  int rows_over, rows_upto;   // sequences with rows in (rows_over, rows_upto] take part
+  int whole;             // units are not cut: a CTA takes those that begin in its stretch
   float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
   float2* part_ml;       // [2 * CTAs][TM] their (max, sum)
   int* status;
@@ -106,6 +108,8 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
     q.n = n < 0 ? 0 : n > cap ? cap : n;
     if (s < 0 || e < s || e > a.bt.T) q = Seq{0, 0, q.n};
   }
+  const int rows = q.nq * a.G;
+  if (rows <= a.rows_over || rows > a.rows_upto) q.nq = 0;
   return q;
 }
 
@@ -315,7 +319,7 @@ template <int TM, int TN>
 __device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
   const typename Tiling<TM, TN>::Span sp = Tiling<TM, TN>::span(a, u.s, u.m);
   u.w = sp.nt > 0 ? sp.nt : 1;
-  u.take = (long long)(u.w - u.off) < u.left ? u.w - u.off : (int)u.left;
+  u.take = a.whole || (long long)(u.w - u.off) < u.left ? u.w - u.off : (int)u.left;
   u.lo = sp.lo;
   u.hi = sp.hi;
   const int rows = u.s.nq * a.G;
@@ -323,21 +327,6 @@ __device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
   u.all_hi = key_hi(a, u.s, div_group(a, u.m * TM));
   u.t0 = sp.t0 + u.off;
   u.nt = sp.nt > 0 ? u.take : 0;
-}
-// The first unit of CTA `cta`'s stretch (work: locate's answer; false: none).
-template <int TM, int TN>
-__device__ __noinline__ void unit_first(const AttnArgs& a, const Place& pl, int cta, bool work,
-                                        Unit& u) {
-  u.left = 0;
-  if (!work) return;
-  u.left = pl.line.start(cta + 1) - pl.line.start(cta);
-  u.b = pl.b;
-  u.h = pl.h;
-  u.m = pl.m;
-  u.off = pl.off;
-  u.s = load_seq(a, u.b);
-  u.nm = Tiling<TM, TN>::row_tiles(a, u.s);
-  unit_set<TM, TN>(a, u);
 }
 template <int TM, int TN>
 __device__ __noinline__ void unit_next(const AttnArgs& a, Unit& u) {
@@ -365,8 +354,33 @@ __device__ __noinline__ void unit_next(const AttnArgs& a, Unit& u) {
   }
   unit_set<TM, TN>(a, u);
 }
+// The first unit of CTA `cta`'s stretch (work: locate's answer; false: none).
+template <int TM, int TN>
+__device__ __noinline__ void unit_first(const AttnArgs& a, const Place& pl, int cta, bool work,
+                                        Unit& u) {
+  u.left = 0;
+  if (!work) return;
+  u.left = pl.line.start(cta + 1) - pl.line.start(cta);
+  u.b = pl.b;
+  u.h = pl.h;
+  u.m = pl.m;
+  u.off = pl.off;
+  u.s = load_seq(a, u.b);
+  u.nm = Tiling<TM, TN>::row_tiles(a, u.s);
+  unit_set<TM, TN>(a, u);
+  // a unit that begins in the stretch before is that CTA's
+  if (a.whole && u.off > 0) unit_next<TM, TN>(a, u);
+}
 
 // ---------------------------------------------------- asynchronous copies --
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint32_t bar, int c0,
+                                            int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool full) {
   const int n = full ? 16 : 0;       // 0: the destination is filled with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)

@@ -1,34 +1,43 @@
 // attn_rows.cu — attention over the paged cache for few rows per key/value
 // head (decode, draft verification), and for page sizes the chunk kernel does
-// not take; the launch that joins cut units.
+// not take; the choice between the two.
 //
-// out = sum_j p_j v_j / sum_j p_j with p_j = exp(s_j - max): one pass over the
-// keys with a running maximum and sum. With R rows over the keys the work is
+// out = sum_j p_j v_j / sum_j p_j with p_j = exp(s_j - ref): one pass over the
+// keys with a running reference and sum. With R rows over the keys the work is
 // 4 R D operations for 4 D bytes of a key and value, so up to a few dozen rows
 // the bound is reading the cache once. Hence: warps that never wait for each
-// other, each with its own keys (16 of a 64-key tile), its own ring of 16-byte
-// asynchronous copies, its own maxima, sums and accumulator, joined through
+// other, each with its own keys (a quarter of a tile), its own ring of 16-byte
+// asynchronous copies, its own references, sums and accumulator, joined through
 // shared memory once per unit. The products run on mma.sync (m16n8k16): its
 // rate is far above what the copies feed, and it takes 16 rows where tcgen05
 // takes 128.
+//
+// A warp's step is 8 KiB of keys and values; what it costs beside the copies is
+// instructions, so a row's reference is held (the maximum of its first step)
+// until a score exceeds it by more than 16 in powers of two: no shuffles and no
+// rescaling in the usual step; and pages of a multiple of 16 keys come by TMA, a
+// box of keys an instruction of one lane, others by 16-byte copies with an
+// address a key (444 instead of some 230 instructions a step).
 #include "attn.cuh"
 #include "attn_join.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "tmap.h"
 
 namespace moe {
 
 constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = 32 * kRowsWarps;
-constexpr int kChunk = 16;                        // keys of a warp's step
-constexpr int kRowsTN = kChunk * kRowsWarps;
+constexpr float kRowsRescaleAt = 16.f;
 
 template <int DP, int MB>
 struct RowsGeo {
   static constexpr int TM = 16 * MB;
+  static constexpr int chunk = DP == 128 ? 16 : 32;              // keys of a warp's step
+  static constexpr int TN = chunk * kRowsWarps;
   static constexpr int row_bytes = DP * 2;
-  static constexpr int stage = 2 * kChunk * row_bytes;           // K and V
-  static constexpr int stages = DP == 128 ? 3 : 4;
+  static constexpr int stage = 2 * chunk * row_bytes;            // K and V: 8 KiB
+  static constexpr int stages = 3;
   static constexpr int ring = kRowsWarps * stages * stage;
   static constexpr int merge = kRowsWarps * TM * DP * 4;         // reuses the ring
   static constexpr int q_bytes = TM * row_bytes;
@@ -54,11 +63,12 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// byte offset of 16-byte piece c of row r; the pieces of 8 rows are permuted so
-// that ldmatrix reads 8 rows of one piece from 8 different banks groups
-template <int DP>
+// Byte offset of 16-byte piece c of row r of a tile of ROWS rows: 64-element
+// column blocks, each in the 128-byte swizzle TMA writes (the pieces of 8 rows
+// permuted, so that ldmatrix reads 8 rows of one piece without conflicts).
+template <int ROWS>
 __device__ __forceinline__ uint32_t tile_at(int r, int c) {
-  return (uint32_t)(r * DP * 2 + ((c ^ (r & 7)) << 4));
+  return (uint32_t)((c >> 3) * (ROWS * 128) + r * 128 + (((c ^ r) & 7) << 4));
 }
 
 __device__ __forceinline__ uint32_t ld_shared32(uint32_t addr) {
@@ -67,43 +77,57 @@ __device__ __forceinline__ uint32_t ld_shared32(uint32_t addr) {
   return v;
 }
 // No infinity or NaN among the chunk's values (by the whole warp).
-template <int DP>
-__device__ __forceinline__ bool chunk_finite(uint32_t sv) {
+template <int DP, int KEYS>
+__device__ __noinline__ bool chunk_finite(uint32_t sv) {
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kChunk * DP / 64; ++i) {
+#pragma unroll 4
+  for (int i = 0; i < KEYS * DP / 64; ++i) {
     const uint32_t v = ld_shared32(sv + (i * 32 + (threadIdx.x & 31)) * 4);
     bad = bad || (v & 0x7F800000u) == 0x7F800000u || (v & 0x7F80u) == 0x7F80u;
   }
   return !__any_sync(0xFFFFFFFFu, bad);
 }
 
-// The offset of key `key`'s slot in the cache (elements, before the head), or
-// -1: outside [lo, hi), or a page outside the cache.
-__device__ __forceinline__ int64_t key_at(const AttnArgs& a, int b, int key, int lo, int hi) {
-  if (key < lo || key >= hi) return -1;
+// The page and slot of key `key` of the sequence whose table row begins at
+// `table_at`; -1 for a page outside the cache.
+__device__ __forceinline__ int slot_of(const AttnArgs& a, int64_t table_at, int key, int& slot) {
   const int pg = page_of(a.bt, key);
-  const int page = a.bt.table[(int64_t)b * a.bt.table_stride + pg];
-  if (page < 0 || page >= a.bt.n_pages) {
-    raise_status(a.status, MOE_ERR_DEVICE_INDEX);
-    return -1;
-  }
-  return (int64_t)page * a.bt.page_stride +
-         (int64_t)(key - pg * a.bt.page_size) * a.bt.token_stride;
+  const int page = a.bt.table[table_at + pg];
+  slot = key - pg * a.bt.page_size;
+  if (page >= 0 && page < a.bt.n_pages) return page;
+  raise_status(a.status, MOE_ERR_DEVICE_INDEX);
+  return -1;
+}
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 
-template <int DP, int MB>
-__global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_constant__ AttnArgs a) {
+// PAGE16: pages of a multiple of 16 keys; a step's keys come in boxes of `box`
+// (16, or the whole step), each in one page.
+template <int DP, int MB, bool PAGE16>
+__global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
+    const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mapK,
+    const __grid_constant__ CUtensorMap mapV, int box) {
   using G = RowsGeo<DP, MB>;
-  constexpr int TM = G::TM, TN = kRowsTN, S = G::stages;
+  constexpr int TM = G::TM, TN = G::TN, S = G::stages, KC = G::chunk;
   constexpr int ND = DP / 8;               // 8-wide column tiles of the accumulator
   constexpr int NC = DP / 8;               // 16-byte pieces of a row
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int NK = KC / 8;               // 8-key tiles of a step's scores
+  constexpr int NG = KC / 16;              // 16-key groups
+  constexpr int NH = DP / 64;              // column blocks
+  extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Place pl;
   __shared__ Unit un;
   __shared__ float2 s_ml[kRowsWarps][TM];
-  pdl_enter();
+  __shared__ uint64_t full[kRowsWarps][S];
+  __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (PAGE16 && tid == 0) {
+    for (int i = 0; i < kRowsWarps * S; ++i) mbar_init(smem_u32(&full[0][0] + i), 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  pdl_enter();
   if (!locate<TM, TN, kRowsThreads>(a, blockIdx.x, gridDim.x, pl)) return;
   if (tid == 0) unit_first<TM, TN>(a, pl, blockIdx.x, true, un);
   __syncthreads();
@@ -113,6 +137,8 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
   float* const merge = reinterpret_cast<float*>(smem);
   const int lr = lane >> 2, lc = lane & 3;      // accumulator row and column pair
 
+  volatile int never = 0;
+  int used = 0, done = 0;      // ring slots filled and worked on by this warp so far
   while (un.more()) {
     const Unit wk = un;
     const Seq s = wk.s;
@@ -120,6 +146,68 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
     const int r0 = wk.m * TM;
     const int nrows = min(TM, rows - r0);
     const int h = wk.h;
+    const int ntile = wk.nt;
+    const int64_t head_at = (int64_t)h * a.head_stride;
+    const int64_t table_at = (int64_t)wk.b * a.bt.table_stride;
+
+    // step j of this warp: keys [first_key(j), + KC)
+    auto first_key = [&](int j) { return (wk.t0 + j) * TN + warp * KC; };
+    // Where a step's keys are: lane g, its box of keys (PAGE16), or lane r, its
+    // key: page and slot; page -1: nothing to load.
+    struct Spot {
+      int page, slot;
+    };
+    auto lookup = [&](int j) {
+      Spot p{-1, 0};
+      const int span = PAGE16 ? box : 1;
+      const int key = first_key(j) + lane * span;
+      if (j < ntile && lane * span < KC && key + span > wk.lo && key < wk.hi)
+        p.page = slot_of(a, table_at, key, p.slot);
+      return p;
+    };
+    auto issue = [&](int j, Spot at) {
+      if constexpr (PAGE16) {
+        if (j >= ntile) return;
+        const uint32_t dst = s_ring + (used % S) * G::stage;
+        const uint32_t bar = smem_u32(&full[warp][used % S]);
+        const uint32_t bytes = (uint32_t)box * 128u * (2 * NH);
+        const uint32_t all = __popc(__ballot_sync(0xFFFFFFFFu, at.page >= 0)) * bytes;
+        if (lane == 0) mbar_arrive_expect_tx(bar, all);
+        __syncwarp();
+        if (at.page >= 0) {
+#pragma unroll
+          for (int c = 0; c < NH; ++c) {
+            const uint32_t d = dst + c * (KC * 128) + lane * box * 128;
+            tma_load_4d(d, &mapK, bar, c * 64, at.slot, h, at.page);
+            tma_load_4d(d + KC * G::row_bytes, &mapV, bar, c * 64, at.slot, h, at.page);
+          }
+        }
+        ++used;
+      } else {
+        if (j < ntile) {
+          constexpr int kRowsPer = 32 / NC;           // rows covered by one warp-wide copy
+          const uint32_t dst = s_ring + (used % S) * G::stage;
+          const int pc = lane % NC, pr = lane / NC;
+          const int64_t mine = (int64_t)at.page * a.bt.page_stride +
+                               (int64_t)at.slot * a.bt.token_stride;
+          const int64_t off = at.page >= 0 ? mine : -1;
+#pragma unroll
+          for (int i = 0; i < KC / kRowsPer; ++i) {
+            const int r = i * kRowsPer + pr;
+            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, r);
+            const bool in = o >= 0 && pc * 8 < a.D;
+            const int64_t e = in ? o + head_at + pc * 8 : 0;
+            cp_async16(dst + tile_at<KC>(r, pc), a.k + e, in);
+            cp_async16(dst + KC * G::row_bytes + tile_at<KC>(r, pc), a.v + e, in);
+          }
+          ++used;
+        }
+        cp_async_commit();
+      }
+    };
+    for (int j = 0; j < S - 1; ++j) issue(j, lookup(j));
+    Spot ahead = lookup(S - 1);         // the next step's, looked up a step early
+
     // ---- the rows' queries into shared memory (rows past the unit: zeros) --
     for (int i = tid; i < TM * NC; i += kRowsThreads) {
       const int r = i / NC, c = i - r * NC;
@@ -129,7 +217,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
         v = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.q0 + tok) * a.q_stride +
                                             (int64_t)(h * a.G + g) * a.D + c * 8);
       }
-      *reinterpret_cast<uint4*>(smem + (G::smem - G::q_bytes) + tile_at<DP>(r, c)) = v;
+      *reinterpret_cast<uint4*>(smem + (G::smem - G::q_bytes) + tile_at<TM>(r, c)) = v;
     }
     // ---- each row's keys; the range every row sees needs no mask -----------
     int lo[MB][2], hi[MB][2];
@@ -142,9 +230,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
         lo[mb][e] = key_lo(a, s, tok);
         hi[mb][e] = r < nrows ? key_hi(a, s, tok) : 0;
       }
-    const int all_lo = wk.all_lo;
-    const int all_hi = wk.all_hi;
-    const bool rows_differ = all_lo > wk.lo || all_hi < wk.hi;
+    const bool rows_differ = wk.all_lo > wk.lo || wk.all_hi < wk.hi;
 
     float o[MB][ND][4];
     float mx[MB][2], sum[MB][2];
@@ -155,86 +241,79 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
       mx[mb][0] = mx[mb][1] = neg_inf();
       sum[mb][0] = sum[mb][1] = 0.f;
     }
-    const int ntile = wk.nt;
-    const int tile0 = wk.t0;
-    const moe_bf16* kh = a.k + (int64_t)h * a.head_stride;
-    const moe_bf16* vh = a.v + (int64_t)h * a.head_stride;
-
-    // chunk j of this warp: keys [first_key(j), + 16)
-    auto first_key = [&](int j) { return (tile0 + j) * TN + warp * kChunk; };
-    auto lookup = [&](int j) -> int64_t {
-      if (j >= ntile) return -1;
-      return key_at(a, wk.b, first_key(j) + (lane & 15), wk.lo, wk.hi);
-    };
-    auto issue = [&](int j, int64_t at) {
-      if (j < ntile) {
-        const uint32_t dst = s_ring + (j % S) * G::stage;
-        constexpr int kRowsPer = 32 / NC;           // rows covered by one warp-wide copy
-        const int c = lane % NC;
-#pragma unroll
-        for (int i = 0; i < kChunk / kRowsPer; ++i) {
-          const int r = i * kRowsPer + lane / NC;
-          const int64_t off = __shfl_sync(0xFFFFFFFFu, at, r);
-          const bool ok = off >= 0 && c * 8 < a.D;
-          const int64_t e = ok ? off + c * 8 : 0;
-          cp_async16(dst + tile_at<DP>(r, c), kh + e, ok);
-          cp_async16(dst + kChunk * G::row_bytes + tile_at<DP>(r, c), vh + e, ok);
-        }
-      }
-      cp_async_commit();
-    };
-    int64_t ahead = -1;      // the next chunk's slots, looked up a step early
-    for (int j = 0; j < S - 1; ++j) issue(j, lookup(j));
-    ahead = lookup(S - 1);
     __syncthreads();         // the queries are in shared memory
 
     uint32_t qf[MB == 1 ? DP / 16 : 1][4];
     if constexpr (MB == 1) {
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk)
-        ldmatrix4(s_q + tile_at<DP>(lane & 15, kk * 2 + (lane >> 4)), qf[kk]);
+        ldmatrix4(s_q + tile_at<TM>(lane & 15, kk * 2 + (lane >> 4)), qf[kk]);
     }
 
+#pragma unroll 1
     for (int j = 0; j < ntile; ++j) {
       issue(j + S - 1, ahead);
       ahead = lookup(j + S);
-      cp_async_wait<S - 1>();
-      __syncwarp();
-      const uint32_t sk = s_ring + (j % S) * G::stage;
-      const uint32_t sv = sk + kChunk * G::row_bytes;
-      float c[MB][2][4];
+      const uint32_t sk = s_ring + (done % S) * G::stage;
+      const uint32_t sv = sk + KC * G::row_bytes;
+      const int k0 = first_key(j);
+      if constexpr (PAGE16) {
+        const bool ok = mbar_wait_bounded(smem_u32(&full[warp][done % S]), (done / S) & 1, &s_abort,
+                                          a.status);
+        __syncwarp();
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;      // given up: reported, results void
+        // values of keys out of range are what the cache or an older step left:
+        // zeros, so that their zero weights give zeros
+        if (k0 < wk.lo || k0 + KC > wk.hi) {
+          for (int i = lane; i < KC * NC; i += 32) {
+            const int key = k0 + i / NC;
+            if (key < wk.lo || key >= wk.hi)
+              st_shared_zero16(sv + tile_at<KC>(i / NC, i % NC));
+          }
+          fence_async_smem();
+          __syncwarp();
+        }
+      } else {
+        cp_async_wait<S - 1>();
+        __syncwarp();
+      }
+      ++done;
+      float c[MB][NK][4];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) c[mb][n][0] = c[mb][n][1] = c[mb][n][2] = c[mb][n][3] = 0.f;
+        for (int n = 0; n < NK; ++n) c[mb][n][0] = c[mb][n][1] = c[mb][n][2] = c[mb][n][3] = 0.f;
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
-        // B of two 8-key tiles: (keys 0-7, d lo), (0-7, d hi), (8-15, d lo), (8-15, d hi)
-        uint32_t kf[4];
-        ldmatrix4(sk + tile_at<DP>((lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)),
-                  kf);
+        uint32_t q4[MB][4];
+        if constexpr (MB > 1) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          if constexpr (MB == 1) {
-            mma16816(c[mb][0], qf[kk], kf[0], kf[1]);
-            mma16816(c[mb][1], qf[kk], kf[2], kf[3]);
-          } else {
-            uint32_t q4[4];
-            ldmatrix4(s_q + tile_at<DP>(mb * 16 + (lane & 15), kk * 2 + (lane >> 4)), q4);
-            mma16816(c[mb][0], q4, kf[0], kf[1]);
-            mma16816(c[mb][1], q4, kf[2], kf[3]);
+          for (int mb = 0; mb < MB; ++mb)
+            ldmatrix4(s_q + tile_at<TM>(mb * 16 + (lane & 15), kk * 2 + (lane >> 4)), q4[mb]);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          // B of two 8-key tiles: (keys 0-7, d lo), (0-7, d hi), (8-15, d lo), (8-15, d hi)
+          uint32_t kf[4];
+          ldmatrix4(sk + tile_at<KC>(g * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                     kk * 2 + ((lane >> 3) & 1)),
+                    kf);
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
+            const uint32_t* qa = MB == 1 ? qf[kk] : q4[mb];
+            mma16816(c[mb][2 * g], qa, kf[0], kf[1]);
+            mma16816(c[mb][2 * g + 1], qa, kf[2], kf[3]);
           }
         }
       }
-      const int k0 = first_key(j);
-      const bool masked = k0 < all_lo || k0 + kChunk > all_hi;
-      uint32_t pf[MB][4];
+      const bool masked = k0 < wk.all_lo || k0 + KC > wk.all_hi;
+      uint32_t pf[MB][NG][4];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb) {
         if (masked) {
           // masked by selection: a masked score's value, NaN or not, is dropped
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < NK; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = k0 + n * 8 + lc * 2 + (e & 1);
@@ -242,24 +321,26 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
               c[mb][n][e] = see ? c[mb][n][e] : neg_inf();
             }
         }
-        float nm[2], ref[2];
+        float top[2];
         bool grew = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(fmaxf(c[mb][0][2 * e], c[mb][0][2 * e + 1]),
-                          fmaxf(c[mb][1][2 * e], c[mb][1][2 * e + 1]));
-          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
-          t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
-          nm[e] = fmaxf(mx[mb][e], t * a.scale_log2);
-          ref[e] = nm[e] == neg_inf() ? 0.f : nm[e];
-          grew = grew || nm[e] > mx[mb][e];
+          top[e] = fmaxf(c[mb][0][2 * e], c[mb][0][2 * e + 1]);
+#pragma unroll
+          for (int n = 1; n < NK; ++n)
+            top[e] = fmaxf(top[e], fmaxf(c[mb][n][2 * e], c[mb][n][2 * e + 1]));
+          grew = grew || top[e] * a.scale_log2 > mx[mb][e] + kRowsRescaleAt;
         }
-        if (__any_sync(0xFFFFFFFFu, grew)) {
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, grew), 0)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = ex2(mx[mb][e] - ref[e]);
+            float t = top[e];
+            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
+            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2)) * a.scale_log2;
+            const float nm = t > mx[mb][e] + kRowsRescaleAt ? t : mx[mb][e];
+            const float f = nm == neg_inf() ? 1.f : ex2(mx[mb][e] - nm);
+            mx[mb][e] = nm;
             sum[mb][e] *= f;
-            mx[mb][e] = nm[e];
 #pragma unroll
             for (int n = 0; n < ND; ++n) {
               o[mb][n][2 * e] *= f;
@@ -267,39 +348,50 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
             }
           }
         }
+        const float ref[2] = {mx[mb][0] == neg_inf() ? 0.f : mx[mb][0],
+                              mx[mb][1] == neg_inf() ? 0.f : mx[mb][1]};
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NK; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             c[mb][n][e] = ex2(fmaf(c[mb][n][e], a.scale_log2, -ref[e >> 1]));
             sum[mb][e >> 1] += c[mb][n][e];
           }
-        pf[mb][0] = pack_bf16(c[mb][0][0], c[mb][0][1]);
-        pf[mb][1] = pack_bf16(c[mb][0][2], c[mb][0][3]);
-        pf[mb][2] = pack_bf16(c[mb][1][0], c[mb][1][1]);
-        pf[mb][3] = pack_bf16(c[mb][1][2], c[mb][1][3]);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          pf[mb][g][0] = pack_bf16(c[mb][2 * g][0], c[mb][2 * g][1]);
+          pf[mb][g][1] = pack_bf16(c[mb][2 * g][2], c[mb][2 * g][3]);
+          pf[mb][g][2] = pack_bf16(c[mb][2 * g + 1][0], c[mb][2 * g + 1][1]);
+          pf[mb][g][3] = pack_bf16(c[mb][2 * g + 1][2], c[mb][2 * g + 1][3]);
+        }
       }
       // A zero weight does not keep an infinite or NaN value out of the product.
       // Keys outside the unit's range are zeros in the ring; keys that some of
-      // the rows see are looked through, and a chunk that holds such a value is
+      // the rows see are looked through, and a step that holds such a value is
       // summed without the matrix unit, key by key over the rows that see it.
-      if (masked && rows_differ && !chunk_finite<DP>(sv)) {
+      if (__builtin_expect(masked && rows_differ, 0) && !chunk_finite<DP, KC>(sv)) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-          for (int k = 0; k < kChunk; ++k)
+          for (int g = 0; g < NG; ++g)
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+              // the weight of (row, key) is with lane lc = key % 8 / 2 of the row
+              const int src = lr * 4 + ((k & 7) >> 1);
+              const uint32_t w4[2][2] = {{pf[mb][g][0], pf[mb][g][1]}, {pf[mb][g][2], pf[mb][g][3]}};
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t w2 = __shfl_sync(0xFFFFFFFFu, pf[mb][(k >> 3) * 2 + e],
-                                              lr * 4 + ((k & 7) >> 1));
-              const float w = (k & 1) ? bf16_hi(w2) : bf16_lo(w2);
-              const int key = k0 + k;
-              if (key >= lo[mb][e] && key < hi[mb][e]) {
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t w2 = __shfl_sync(0xFFFFFFFFu, k < 8 ? w4[0][e] : w4[1][e], src);
+                const float w = (k & 1) ? bf16_hi(w2) : bf16_lo(w2);
+                const int key = k0 + g * 16 + k;
+                const bool see = key >= lo[mb][e] && key < hi[mb][e];
 #pragma unroll
                 for (int n = 0; n < ND; ++n) {
-                  const uint32_t v2 = ld_shared32(sv + tile_at<DP>(k, n) + lc * 4);
-                  o[mb][n][2 * e] = fmaf(w, bf16_lo(v2), o[mb][n][2 * e]);
-                  o[mb][n][2 * e + 1] = fmaf(w, bf16_hi(v2), o[mb][n][2 * e + 1]);
+                  const uint32_t v2 = ld_shared32(sv + tile_at<KC>(g * 16 + k, n) + lc * 4);
+                  const float x = fmaf(w, bf16_lo(v2), o[mb][n][2 * e]);
+                  const float y = fmaf(w, bf16_hi(v2), o[mb][n][2 * e + 1]);
+                  o[mb][n][2 * e] = see ? x : o[mb][n][2 * e];
+                  o[mb][n][2 * e + 1] = see ? y : o[mb][n][2 * e + 1];
                 }
               }
             }
@@ -307,19 +399,28 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
         continue;
       }
 #pragma unroll
-      for (int n2 = 0; n2 < ND / 2; ++n2) {
-        // B of two 8-column tiles: (keys 0-7, d lo), (8-15, d lo), (0-7, d hi), (8-15, d hi)
-        uint32_t vf[4];
-        ldmatrix4_trans(sv + tile_at<DP>(lane & 15, n2 * 2 + (lane >> 4)), vf);
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-          mma16816(o[mb][2 * n2], pf[mb], vf[0], vf[1]);
-          mma16816(o[mb][2 * n2 + 1], pf[mb], vf[2], vf[3]);
+        for (int n2 = 0; n2 < ND / 2; ++n2) {
+          // B of two 8-column tiles: (keys 0-7, d lo), (8-15, d lo), (0-7, d hi), (8-15, d hi)
+          uint32_t vf[4];
+          ldmatrix4_trans(sv + tile_at<KC>(g * 16 + (lane & 15), n2 * 2 + (lane >> 4)), vf);
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) {
+            mma16816(o[mb][2 * n2], pf[mb][g], vf[0], vf[1]);
+            mma16816(o[mb][2 * n2 + 1], pf[mb][g], vf[2], vf[3]);
+          }
         }
-      }
       __syncwarp();
     }
-    cp_async_wait<0>();
+    if constexpr (PAGE16) {
+      // after giving up: copies in flight land before the ring is used again
+      for (; done < used; ++done)
+        mbar_wait_bounded(smem_u32(&full[warp][done % S]), (done / S) & 1, &never, a.status);
+      __syncwarp();
+    } else {
+      cp_async_wait<0>();
+    }
 
     // ---- join the warps ----------------------------------------------------
     __syncthreads();          // every warp is done with the ring
@@ -371,11 +472,19 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(const __grid_co
       }
     }
     if (tid == 0) unit_next<TM, TN>(a, un);
+    if constexpr (PAGE16) fence_async_smem();
     __syncthreads();          // the merge buffer is the ring again
   }
 }
 
 // ------------------------------------------------------------------ host --
+// Up to so many rows (tokens x query heads of a key head) a sequence is worked on
+// by the kernel above; more go to the chunk kernel where its pages allow.
+constexpr int kFewRows = 64;
+// Units of at most so many keys are not cut: the second launch costs more than
+// an even load is worth.
+constexpr int kWholeKeys = 1024;
+
 template <int DP, int MB>
 static int rows_ctas() {
   // CTAs an SM holds by shared memory (227 KiB, 1 KiB reserved a CTA)
@@ -383,26 +492,39 @@ static int rows_ctas() {
   return num_sms() * (per < 4 ? per : 4);
 }
 
-template <int DP, int MB>
-static cudaError_t launch_rows(AttnArgs a, void* ws, cudaStream_t s) {
+template <int DP, int MB, bool PAGE16>
+static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cudaStream_t s) {
   using G = RowsGeo<DP, MB>;
-  auto kern = attn_rows_kernel<DP, MB>;
+  auto kern = attn_rows_kernel<DP, MB, PAGE16>;
   static SmemOnce once;
   cudaError_t e = once.set((const void*)kern, G::smem);
   if (e != cudaSuccess) return e;
+  CUtensorMap mk = {}, mv = {};
+  const int box = c.page_size % G::chunk == 0 ? G::chunk : 16;
+  if (PAGE16 && (!map_kv(&mk, c.k, c, box) || !map_kv(&mv, c.v, c, box)))
+    return cudaErrorInvalidValue;
   const int n = rows_ctas<DP, MB>();
   a.part_ml = static_cast<float2*>(ws);
   a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * G::TM);
   timer_before(MOE_KERNEL_ATTN, s);
-  e = launch_pdl(true, kern, dim3(n), dim3(kRowsThreads), G::smem, s, a);
+  e = launch_pdl(true, kern, dim3(n), dim3(kRowsThreads), G::smem, s, a, mk, mv, box);
   timer_after(MOE_KERNEL_ATTN, s);
-  if (e != cudaSuccess) return e;
+  note_launches(1);
+  if (e != cudaSuccess || a.whole) return e;
   timer_before(MOE_KERNEL_ATTN_COMBINE, s);
-  e = launch_pdl(true, attn_join_kernel<G::TM, kRowsTN, DP>, dim3(n - 1), dim3(kJoinThreads), 0, s,
+  e = launch_pdl(true, attn_join_kernel<G::TM, G::TN, DP>, dim3(n - 1), dim3(kJoinThreads), 0, s,
                  a, n);
   timer_after(MOE_KERNEL_ATTN_COMBINE, s);
-  note_launches(2);
+  note_launches(1);
   return e;
+}
+
+template <int DP>
+static cudaError_t launch_rows(const AttnArgs& a, const moe_kv_cache& c, int64_t rows,
+                               bool page16, void* ws, cudaStream_t s) {
+  if (rows <= 16)
+    return page16 ? launch_rows<DP, 1, true>(a, c, ws, s) : launch_rows<DP, 1, false>(a, c, ws, s);
+  return page16 ? launch_rows<DP, 2, true>(a, c, ws, s) : launch_rows<DP, 2, false>(a, c, ws, s);
 }
 
 template <int DP, int MB>
@@ -432,13 +554,33 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   a.scale_log2 = scale * kLog2e;
   a.causal = causal ? 1 : 0;
   // a window of the whole cache or more masks nothing
-  a.window = window >= b.max_pages * c.page_size ? 0 : window;
+  const int64_t cap = (int64_t)b.max_pages * c.page_size;
+  a.window = window >= cap ? 0 : window;
   a.status = status;
+  a.rows_over = 0;
+  a.rows_upto = 1 << 30;
+  const bool page16 = c.page_size % 16 == 0;
   const int64_t rows = (int64_t)b.max_q * a.G;
-  if (rows > 32 && attn_chunk_takes(c.page_size)) return launch_attn_chunk(a, c, ws, s);
-  const bool small = rows <= 16;
-  if (c.D <= 64) return small ? launch_rows<64, 1>(a, ws, s) : launch_rows<64, 2>(a, ws, s);
-  return small ? launch_rows<128, 1>(a, ws, s) : launch_rows<128, 2>(a, ws, s);
+  const bool chunks = rows > kFewRows && attn_chunk_takes(c.page_size);
+  // Both kernels where sequences may be of both kinds: not when all have max_q
+  // tokens, nor when one is all there is.
+  const bool both = chunks && b.B > 1 && b.T != (int64_t)b.B * b.max_q;
+  cudaError_t e = cudaSuccess;
+  if (!chunks || both) {
+    AttnArgs r = a;
+    if (both) r.rows_upto = kFewRows;
+    const int64_t seen = (int64_t)a.window + b.max_q;
+    const int64_t keys = a.window && seen < cap ? seen : cap;
+    r.whole = keys <= kWholeKeys ? 1 : 0;
+    const int64_t most = both ? kFewRows : rows;
+    e = c.D <= 64 ? launch_rows<64>(r, c, most, page16, ws, s)
+                  : launch_rows<128>(r, c, most, page16, ws, s);
+  }
+  if (e == cudaSuccess && chunks) {
+    if (both) a.rows_over = kFewRows;
+    e = launch_attn_chunk(a, c, ws, s);
+  }
+  return e;
 }
 
 }  // namespace moe
