@@ -5,13 +5,14 @@
 // of a sequence are n_q * G rows over the same keys: row r is token r / G,
 // head h * G + r % G. A unit is (sequence b, head h, row tile m of TM rows);
 // its keys are one range (the union of its rows' masks), cut into tiles of TN.
-// Units in the order (b, h, m) laid end to end, one tile a step (an empty unit
-// counts one: its rows are still to be written), make a line of `total` steps;
-// each of n CTAs takes total / n steps in a row (the first ones one more). Every
-// CTA so has the same number of tiles whatever the lengths, and writes at most two
-// partial results: the unit it enters in the middle (slot 0) and the unit it
-// begins and does not end (slot 1). A second launch joins the parts of each
-// cut unit in order, so results do not depend on timing.
+// Units in the order (b, h, m) laid end to end, one step a tile and kUnitCost
+// steps more a unit (beginning and ending one takes about that long), make a
+// line; each of n CTAs takes an n-th of it. Every CTA so has the same work
+// whatever the lengths, and writes at most two partial results: the unit it
+// enters in the middle (slot 0) and the unit it begins and does not end (slot
+// 1). A boundary within kUnitCost of a unit's beginning or end moves there. A
+// second launch joins the parts of each cut unit in order, so results do not
+// depend on timing.
 #pragma once
 
 #include <atomic>
@@ -22,6 +23,7 @@ namespace moe {
 
 constexpr int kAttnMaxD = 128;
 constexpr int kAttnMaxKeys = 1 << 30;
+constexpr int kUnitCost = 2;
 
 struct AttnBatch {
   const int32_t* cu_q;
@@ -68,6 +70,7 @@ struct AttnArgs {
   int causal, window;    // window 0: none
   int rows_over, rows_upto;   // sequences with rows in (rows_over, rows_upto] take part
   int whole;             // units are not cut: a CTA takes those that begin in its stretch
+  struct Cut* cuts;      // [CTAs] the cut in front of each
   float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
   float2* part_ml;       // [2 * CTAs][TM] their (max, sum)
   int* status;
@@ -151,8 +154,7 @@ struct Tiling {
     return p;
   }
   static __device__ __forceinline__ int weight(const AttnArgs& a, const Seq& s, int m) {
-    const int nt = span(a, s, m).nt;
-    return nt > 0 ? nt : 1;
+    return span(a, s, m).nt + kUnitCost;
   }
 };
 
@@ -166,12 +168,31 @@ struct Line {               // the line of steps, cut for n CTAs
     return per * cta + (cta < rem ? cta : rem);
   }
 };
-struct Place {              // of a CTA's first step, in shared memory
-  Line line;
+struct Place {              // locate's, in shared memory
   long long warp_sum[32];
-  long long in_seq, head_w;
-  int b, h, m;
-  int off;                  // steps into the unit
+  long long in_seq, head_w, x0, x1, prev, per;
+  int rem, tall;            // tall: the sequence found has several row tiles
+};
+// What a join block needs of the cut in front of a CTA: a unit's rows and the
+// CTAs first .. last - 1 that have parts of it. first < 0: no cut to join there.
+struct alignas(32) Cut {
+  int q0, r0, nrows, h, first, last, pad[2];
+};
+
+// A unit of a CTA's stretch, in shared memory: written by one thread, read by
+// those that work on it.
+struct Unit {
+  long long to_end;    // steps from the unit's first to the end of the stretch
+  Seq s;
+  int more;            // 0: the stretch has no further unit
+  int b, h, m, nm;
+  int w, off, stop;    // the unit's steps; this CTA has [off, stop) of them
+  int lo, hi;          // the keys of its rows
+  int all_lo, all_hi;  // those every row sees
+  int t0, nt;          // tiles: the first, and this CTA's number of them
+
+  __device__ __forceinline__ bool whole() const { return off == 0 && stop == w; }
+  __device__ __forceinline__ int slot() const { return off > 0 ? 0 : 1; }
 };
 
 // a / b of values that nearly always fit 32 bits
@@ -207,17 +228,100 @@ __device__ __forceinline__ long long head_weight(const AttnArgs& a, const Seq& s
   return w;
 }
 
-// Where CTA `cta` of `n` begins, into `pl` (by the whole block of NT threads,
-// ends with a barrier). False when no step of the line begins there: the CTA
-// has none, and no unit is cut in front of it.
+// The unit (u.s, u.h, u.m) from step u.off on, for as far as the stretch goes.
+template <int TM, int TN>
+__device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
+  const typename Tiling<TM, TN>::Span sp = Tiling<TM, TN>::span(a, u.s, u.m);
+  u.w = sp.nt + kUnitCost;
+  u.stop = u.w;
+  if (!a.whole && u.to_end < u.w) {
+    const int e = (int)u.to_end;
+    if (e <= kUnitCost) {
+      u.more = 0;
+      return;
+    }
+    if (u.w - e > kUnitCost) u.stop = e;
+  }
+  u.more = 1;
+  u.lo = sp.lo;
+  u.hi = sp.hi;
+  const int rows = u.s.nq * a.G;
+  u.all_lo = key_lo(a, u.s, div_group(a, min(u.m * TM + TM, rows) - 1));
+  u.all_hi = key_hi(a, u.s, div_group(a, u.m * TM));
+  const int begin = max(u.off - kUnitCost, 0);
+  u.t0 = sp.t0 + begin;
+  u.nt = max(u.stop - kUnitCost, 0) - begin;
+}
+template <int TM, int TN>
+__device__ __noinline__ void unit_next(const AttnArgs& a, Unit& u) {
+  u.to_end -= u.w;
+  u.more = 0;
+  if (u.stop < u.w || u.to_end <= 0) return;
+  u.off = 0;
+  if (++u.m == u.nm) {
+    u.m = 0;
+    if (++u.h == a.Hkv) {
+      u.h = 0;
+      int nm = 0, b = u.b;
+      Seq s{0, 0, 0};
+      while (nm == 0 && ++b < a.bt.B) {
+        s = load_seq(a, b);
+        nm = Tiling<TM, TN>::row_tiles(a, s);
+      }
+      if (nm == 0) return;      // lengths that changed under the kernel
+      u.b = b;
+      u.s = s;
+      u.nm = nm;
+    }
+  }
+  unit_set<TM, TN>(a, u);
+}
+// The stretch's first unit, from the unit (u.s, b, h, m, nm) its first step x0
+// lies in, `off` steps into it; and the cut in front of the stretch.
+template <int TM, int TN>
+__device__ __noinline__ void unit_first(const AttnArgs& a, const Place& pl, int cta, int off,
+                                        Unit& u) {
+  Cut c{0, 0, 0, 0, -1, 0, {0, 0}};
+  const long long unit0 = pl.x0 - off;
+  u.to_end = pl.x1 - unit0;
+  u.w = u.stop = Tiling<TM, TN>::weight(a, u.s, u.m);
+  const bool at_begin = a.whole ? off == 0 : off <= kUnitCost;
+  const bool at_end = a.whole || u.w - off <= kUnitCost;
+  if (at_begin) {
+    u.off = 0;
+    unit_set<TM, TN>(a, u);
+  } else if (at_end) {
+    unit_next<TM, TN>(a, u);
+  } else {
+    u.off = off;
+    if (pl.prev - unit0 <= kUnitCost) {
+      // the first cut of its unit; the last part is that of the CTA that has the
+      // step the end's boundary is measured from
+      const long long y = unit0 + u.w - kUnitCost - 1, big = (long long)pl.rem * (pl.per + 1);
+      c.first = cta - 1;
+      c.last = 1 + (int)(y < big ? divide(y, pl.per + 1) : pl.rem + divide(y - big, pl.per));
+      c.q0 = u.s.q0;
+      c.h = u.h;
+      c.r0 = u.m * TM;
+      c.nrows = min(TM, u.s.nq * a.G - c.r0);
+    }
+    unit_set<TM, TN>(a, u);
+  }
+  if (a.cuts) a.cuts[cta] = c;
+}
+
+// CTA `cta` of `n`: its stretch's first unit into `u` and the cut in front of it
+// into a.cuts. By the whole block of NT threads; ends with a barrier.
 template <int TM, int TN, int NT>
-__device__ __noinline__ bool locate(const AttnArgs& a, int cta, int n, Place& pl) {
+__device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl, Unit& u) {
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.bt.B;
   // The line's length, then the sequence that holds the CTA's first step. Up to
-  // NT sequences, one a thread, the second pass looks at what the first has.
-  long long total = 0, x0 = 0, hw = 0, inc = 0, before = 0;
+  // NT sequences, one a thread, the second pass looks at what the first has; the
+  // thread that finds a sequence of one row tile has all the unit takes.
+  Seq s{0, 0, 0};
+  long long total = 0, x0 = 0, x1 = 0, hw = 0, inc = 0, before = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     long long base = 0;
@@ -225,7 +329,7 @@ __device__ __noinline__ bool locate(const AttnArgs& a, int cta, int n, Place& pl
     for (int b0 = 0; b0 < B; b0 += NT) {
       const int b = b0 + tid;
       if (pass == 0 || B > NT) {
-        Seq s{0, 0, 0};
+        s = Seq{0, 0, 0};
         if (b < B) s = load_seq(a, b);
         hw = head_weight<TM, TN>(a, s);
         inc = hw * a.Hkv;
@@ -250,34 +354,58 @@ __device__ __noinline__ bool locate(const AttnArgs& a, int cta, int n, Place& pl
       if (pass == 1) {
         const long long hi = base + before + inc, lo = hi - hw * a.Hkv;
         if (x0 >= lo && x0 < hi) {
-          pl.b = b;
-          pl.in_seq = x0 - lo;
-          pl.head_w = hw;
+          const long long in_seq = x0 - lo;
+          u.s = s;
+          u.b = b;
+          u.nm = Tiling<TM, TN>::row_tiles(a, s);
+          u.h = (int)divide(in_seq, hw);
+          pl.in_seq = in_seq - u.h * hw;
+          pl.tall = u.nm > 1;
+          if (u.nm == 1) {
+            u.m = 0;
+            unit_first<TM, TN>(a, pl, cta, (int)pl.in_seq, u);
+          }
         }
       }
       base = total;
     }
     if (pass == 0) {
-      if (total == 0) return false;
       Line ln;
       ln.total = total;
       ln.per = divide(total, n);
       ln.rem = (int)(total - ln.per * n);
       x0 = ln.start(cta);
-      if (x0 >= total) return false;      // fewer steps than CTAs: none for this one
-      if (tid == 0) pl.line = ln;
+      x1 = ln.start(cta + 1);
+      if (tid == 0) {
+        pl.x0 = x0;
+        pl.x1 = x1;
+        pl.prev = cta > 0 ? ln.start(cta - 1) : 0;
+        pl.per = ln.per;
+        pl.rem = ln.rem;
+        u.more = pl.tall = 0;
+      }
+      if (x0 >= total) {        // no steps, or fewer than CTAs: none for this one
+        if (tid == 0) {
+          u.more = 0;
+          if (a.cuts) a.cuts[cta] = Cut{0, 0, 0, 0, -1, 0, {0, 0}};
+        }
+        __syncthreads();
+        return;
+      }
+      __syncthreads();
     }
   }
   __syncthreads();
+  if (!pl.tall) return;
   if (warp == 0) {
-    const Seq s = load_seq(a, pl.b);
-    const int h = (int)divide(pl.in_seq, pl.head_w);
-    long long rem = pl.in_seq - h * pl.head_w;
-    const int nm = Tiling<TM, TN>::row_tiles(a, s);
+    // which of the sequence's row tiles
+    const Seq t = u.s;
+    const int nm = u.nm;
+    long long rem = pl.in_seq;
 #pragma unroll 1
     for (int m0 = 0; m0 < nm; m0 += 32) {
       const int m = m0 + lane;
-      const int w = m < nm ? Tiling<TM, TN>::weight(a, s, m) : 0;
+      const int w = m < nm ? Tiling<TM, TN>::weight(a, t, m) : 0;
       long long run = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -286,90 +414,14 @@ __device__ __noinline__ bool locate(const AttnArgs& a, int cta, int n, Place& pl
       }
       const bool here = rem >= run - w && rem < run;
       if (here) {
-        pl.m = m;
-        pl.off = (int)(rem - (run - w));
+        u.m = m;
+        unit_first<TM, TN>(a, pl, cta, (int)(rem - (run - w)), u);
       }
       if (__any_sync(0xFFFFFFFFu, here)) break;
       rem -= __shfl_sync(0xFFFFFFFFu, run, 31);
     }
-    if (lane == 0) pl.h = h;
   }
   __syncthreads();
-  return true;
-}
-
-// A unit of a CTA's stretch, in shared memory: written by one thread, read by
-// those that work on it.
-struct Unit {
-  long long left;      // steps of the stretch still to do, this unit's included
-  Seq s;
-  int b, h, m, nm;
-  int off;             // the unit's steps that others do before
-  int w, take;         // the unit's steps, and those of this CTA
-  int lo, hi;          // the keys of its rows
-  int all_lo, all_hi;  // those every row sees
-  int t0, nt;          // tiles: the first, and this CTA's number of them
-
-  __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ bool whole() const { return off == 0 && take == w; }
-  __device__ __forceinline__ int slot() const { return off > 0 ? 0 : 1; }
-};
-
-template <int TM, int TN>
-__device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
-  const typename Tiling<TM, TN>::Span sp = Tiling<TM, TN>::span(a, u.s, u.m);
-  u.w = sp.nt > 0 ? sp.nt : 1;
-  u.take = a.whole || (long long)(u.w - u.off) < u.left ? u.w - u.off : (int)u.left;
-  u.lo = sp.lo;
-  u.hi = sp.hi;
-  const int rows = u.s.nq * a.G;
-  u.all_lo = key_lo(a, u.s, div_group(a, min(u.m * TM + TM, rows) - 1));
-  u.all_hi = key_hi(a, u.s, div_group(a, u.m * TM));
-  u.t0 = sp.t0 + u.off;
-  u.nt = sp.nt > 0 ? u.take : 0;
-}
-template <int TM, int TN>
-__device__ __noinline__ void unit_next(const AttnArgs& a, Unit& u) {
-  u.left -= u.take;
-  if (u.left <= 0) return;
-  u.off = 0;
-  if (++u.m == u.nm) {
-    u.m = 0;
-    if (++u.h == a.Hkv) {
-      u.h = 0;
-      int nm = 0, b = u.b;
-      Seq s{0, 0, 0};
-      while (nm == 0 && ++b < a.bt.B) {
-        s = load_seq(a, b);
-        nm = Tiling<TM, TN>::row_tiles(a, s);
-      }
-      if (nm == 0) {      // lengths that changed under the kernel
-        u.left = 0;
-        return;
-      }
-      u.b = b;
-      u.s = s;
-      u.nm = nm;
-    }
-  }
-  unit_set<TM, TN>(a, u);
-}
-// The first unit of CTA `cta`'s stretch (work: locate's answer; false: none).
-template <int TM, int TN>
-__device__ __noinline__ void unit_first(const AttnArgs& a, const Place& pl, int cta, bool work,
-                                        Unit& u) {
-  u.left = 0;
-  if (!work) return;
-  u.left = pl.line.start(cta + 1) - pl.line.start(cta);
-  u.b = pl.b;
-  u.h = pl.h;
-  u.m = pl.m;
-  u.off = pl.off;
-  u.s = load_seq(a, u.b);
-  u.nm = Tiling<TM, TN>::row_tiles(a, u.s);
-  unit_set<TM, TN>(a, u);
-  // a unit that begins in the stretch before is that CTA's
-  if (a.whole && u.off > 0) unit_next<TM, TN>(a, u);
 }
 
 // ---------------------------------------------------- asynchronous copies --

@@ -231,18 +231,6 @@ __device__ __noinline__ void add_by_hand(uint32_t t_p, uint32_t t_o, const uint8
   }
 }
 
-// A warpgroup's registers a thread. 384 threads start with 168 each (64512);
-// the softmax warpgroups hold 128 scores and their packed weights at once:
-// 2 x 128 x 200 + 128 x 88 = 62464.
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // Waits until a count in shared memory has reached `need`; gives up like
 // mbar_wait_bounded.
 __device__ __forceinline__ bool count_wait_bounded(const int* count, int need,
@@ -410,15 +398,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const bool work = locate<kChunkTM, kChunkTN, kChunkThreads>(a, blockIdx.x, gridDim.x, sh.pl);
-  __syncthreads();
+  locate<kChunkTM, kChunkTN, kChunkThreads>(a, blockIdx.x, gridDim.x, sh.pl, sh.unit[0]);
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   // The warp's next unit is there (false: the end, or given up); it has read it.
   auto take_unit = [&](auto call, int u, bool& ok) {
     ok = ok && wait_warp<decltype(call)::value>(smem_u32(&sh.unit_full[u & 3]), (u >> 2) & 1, abort,
                                                 a.status);
-    return ok && sh.unit[u & 3].more();
+    return ok && sh.unit[u & 3].more != 0;
   };
   auto give_unit = [&](int u) {
     __syncwarp();
@@ -427,7 +414,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   using Call = std::true_type;
   using Inline = std::false_type;
   if (warp >= 8) {
-    regs_down<88>();
     if (warp == kLoadWarp) {
       // -------------------------------------------------------------- loads --
       // lane i < nbox: the box of keys [tile + i * box, + box)
@@ -438,14 +424,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       int fills = 0;
       bool ok = true;
       for (int u = 0;; ++u) {
-        // the next unit (or the end, a unit without steps) for every role
+        // the next unit (or that there is none) for every role
         Unit& un = sh.unit[u & 3];
         ok = wait_warp<true>(smem_u32(&sh.unit_empty[u & 3]), ((u >> 2) & 1) ^ 1, abort, a.status);
         if (!ok) break;
         if (lane == 0) {
-          if (u == 0) {
-            unit_first<kChunkTM, kChunkTN>(a, sh.pl, blockIdx.x, work, un);
-          } else {
+          if (u > 0) {
             un = sh.unit[(u - 1) & 3];
             unit_next<kChunkTM, kChunkTN>(a, un);
           }
@@ -453,7 +437,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         __syncwarp();
         const Unit wk = un;
-        if (!wk.more()) break;
+        if (!wk.more) break;
         const int nt = wk.nt;
         for (int j = 0; j < nt && ok; ++j) {
           const int key = (wk.t0 + j) * kChunkTN + lane * box;
@@ -776,7 +760,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax --
-    regs_up<200>();
     const int half = warp >> 2;
     const int row = (warp & 3) * 32 + lane;             // of the half
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -970,7 +953,7 @@ bool attn_chunk_takes(int page_size) { return page_size % 8 == 0; }
 
 size_t attn_chunk_ws_bytes(int D) {
   const int DP = D <= 64 ? 64 : 128;
-  return (size_t)2 * num_sms() * kChunkTM * (DP + 2) * sizeof(float);
+  return (size_t)num_sms() * (sizeof(Cut) + 2 * kChunkTM * (DP + 2) * sizeof(float));
 }
 
 template <int DP>
@@ -989,7 +972,8 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
   cudaError_t e = once.set((const void*)kern, G::smem);
   if (e != cudaSuccess) return e;
   const int n = num_sms();
-  a.part_ml = static_cast<float2*>(ws);
+  a.cuts = static_cast<Cut*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(a.cuts + n);
   a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * kChunkTM);
   timer_before(MOE_KERNEL_ATTN, s);
   e = launch_pdl(true, kern, dim3(n), dim3(kChunkThreads), G::smem, s, a, mq, mk, mv, box,
@@ -997,8 +981,8 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
   timer_after(MOE_KERNEL_ATTN, s);
   if (e != cudaSuccess) return e;
   timer_before(MOE_KERNEL_ATTN_COMBINE, s);
-  e = launch_pdl(true, attn_join_kernel<kChunkTM, kChunkTN, DP>, dim3(n - 1, 8),
-                 dim3(kJoinThreads), 0, s, a, n);
+  e = launch_pdl(true, attn_join_kernel<kChunkTM, DP>, dim3(n - 1, 8), dim3(kJoinThreads), 0, s,
+                 a);
   timer_after(MOE_KERNEL_ATTN_COMBINE, s);
   note_launches(2);
   return e;

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
   constexpr int NH = DP / 64;              // column blocks
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Place pl;
-  __shared__ Unit un;
+  __shared__ Unit un[2];
   __shared__ float2 s_ml[kRowsWarps][TM];
   __shared__ uint64_t full[kRowsWarps][S];
   __shared__ int s_abort;
@@ -128,9 +128,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     fence_mbar_init();
   }
   pdl_enter();
-  if (!locate<TM, TN, kRowsThreads>(a, blockIdx.x, gridDim.x, pl)) return;
-  if (tid == 0) unit_first<TM, TN>(a, pl, blockIdx.x, true, un);
-  __syncthreads();
+  locate<TM, TN, kRowsThreads>(a, blockIdx.x, gridDim.x, pl, un[0]);
 
   const uint32_t s_ring = smem_u32(smem) + warp * S * G::stage;
   const uint32_t s_q = smem_u32(smem) + (uint32_t)(G::smem - G::q_bytes);
@@ -139,8 +137,51 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 
   volatile int never = 0;
   int used = 0, done = 0;      // ring slots filled and worked on by this warp so far
-  while (un.more()) {
-    const Unit wk = un;
+  // Where a step's keys are: lane g, its box of keys (PAGE16), or lane r, its
+  // key: page and slot; page -1: nothing to load.
+  struct Spot {
+    int page, slot;
+  };
+  auto lookup = [&](const Unit& w, int j) {
+    Spot p{-1, 0};
+    const int span = PAGE16 ? box : 1;
+    const int key = (w.t0 + j) * TN + warp * KC + lane * span;
+    if (j < w.nt && lane * span < KC && key + span > w.lo && key < w.hi)
+      p.page = slot_of(a, (int64_t)w.b * a.bt.table_stride, key, p.slot);
+    return p;
+  };
+  // a thread's pieces of a unit's queries (rows past the unit: zeros)
+  constexpr int QP = TM * NC / kRowsThreads > 0 ? TM * NC / kRowsThreads : 1;
+  struct Pieces {
+    uint4 v[QP];
+  };
+  auto load_q = [&](const Unit& w) {
+    Pieces q;
+    const int r0 = w.m * TM, nrows = min(TM, w.s.nq * a.G - r0);
+#pragma unroll
+    for (int i = 0; i < QP; ++i) {
+      const int at = i * kRowsThreads + tid, r = at / NC, c = at - r * NC;
+      q.v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < nrows && c * 8 < a.D) {
+        const int tok = div_group(a, r0 + r), g = (r0 + r) - tok * a.G;
+        q.v[i] = *reinterpret_cast<const uint4*>(a.q + (int64_t)(w.s.q0 + tok) * a.q_stride +
+                                                 (int64_t)(w.h * a.G + g) * a.D + c * 8);
+      }
+    }
+    return q;
+  };
+
+  Spot spot[S];                // of the unit's first steps
+  Pieces qp;
+  auto unit_loads = [&](const Unit& w) {
+#pragma unroll
+    for (int j = 0; j < S; ++j) spot[j] = lookup(w, j);
+    qp = load_q(w);
+  };
+  int cur = 0;
+  if (un[0].more) unit_loads(un[0]);
+  while (un[cur].more) {
+    const Unit wk = un[cur];
     const Seq s = wk.s;
     const int rows = s.nq * a.G;
     const int r0 = wk.m * TM;
@@ -148,23 +189,9 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     const int h = wk.h;
     const int ntile = wk.nt;
     const int64_t head_at = (int64_t)h * a.head_stride;
-    const int64_t table_at = (int64_t)wk.b * a.bt.table_stride;
 
     // step j of this warp: keys [first_key(j), + KC)
     auto first_key = [&](int j) { return (wk.t0 + j) * TN + warp * KC; };
-    // Where a step's keys are: lane g, its box of keys (PAGE16), or lane r, its
-    // key: page and slot; page -1: nothing to load.
-    struct Spot {
-      int page, slot;
-    };
-    auto lookup = [&](int j) {
-      Spot p{-1, 0};
-      const int span = PAGE16 ? box : 1;
-      const int key = first_key(j) + lane * span;
-      if (j < ntile && lane * span < KC && key + span > wk.lo && key < wk.hi)
-        p.page = slot_of(a, table_at, key, p.slot);
-      return p;
-    };
     auto issue = [&](int j, Spot at) {
       if constexpr (PAGE16) {
         if (j >= ntile) return;
@@ -205,19 +232,18 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
         cp_async_commit();
       }
     };
-    for (int j = 0; j < S - 1; ++j) issue(j, lookup(j));
-    Spot ahead = lookup(S - 1);         // the next step's, looked up a step early
-
-    // ---- the rows' queries into shared memory (rows past the unit: zeros) --
-    for (int i = tid; i < TM * NC; i += kRowsThreads) {
-      const int r = i / NC, c = i - r * NC;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (r < nrows && c * 8 < a.D) {
-        const int tok = div_group(a, r0 + r), g = (r0 + r) - tok * a.G;
-        v = *reinterpret_cast<const uint4*>(a.q + (int64_t)(s.q0 + tok) * a.q_stride +
-                                            (int64_t)(h * a.G + g) * a.D + c * 8);
-      }
-      *reinterpret_cast<uint4*>(smem + (G::smem - G::q_bytes) + tile_at<TM>(r, c)) = v;
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j) issue(j, spot[j]);
+    Spot ahead = spot[S - 1];           // the next step's, looked up a step early
+#pragma unroll
+    for (int i = 0; i < QP; ++i) {
+      const int at = i * kRowsThreads + tid, r = at / NC, c = at - r * NC;
+      *reinterpret_cast<uint4*>(smem + (G::smem - G::q_bytes) + tile_at<TM>(r, c)) = qp.v[i];
+    }
+    // the next unit, found by a thread whose warp's first copies are on their way
+    if (tid == kRowsThreads - 32) {
+      un[cur ^ 1] = wk;
+      unit_next<TM, TN>(a, un[cur ^ 1]);
     }
     // ---- each row's keys; the range every row sees needs no mask -----------
     int lo[MB][2], hi[MB][2];
@@ -253,7 +279,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 #pragma unroll 1
     for (int j = 0; j < ntile; ++j) {
       issue(j + S - 1, ahead);
-      ahead = lookup(j + S);
+      ahead = lookup(wk, j + S);
       const uint32_t sk = s_ring + (done % S) * G::stage;
       const uint32_t sv = sk + KC * G::row_bytes;
       const int k0 = first_key(j);
@@ -423,7 +449,9 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     }
 
     // ---- join the warps ----------------------------------------------------
-    __syncthreads();          // every warp is done with the ring
+    __syncthreads();          // every warp is done with the ring, the next unit is known
+    cur ^= 1;
+    if (un[cur].more) unit_loads(un[cur]);
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -471,7 +499,6 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
         if (c4 == 0) a.part_ml[pslot * TM + r] = make_float2(m, l);
       }
     }
-    if (tid == 0) unit_next<TM, TN>(a, un);
     if constexpr (PAGE16) fence_async_smem();
     __syncthreads();          // the merge buffer is the ring again
   }
@@ -504,7 +531,8 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cuda
   if (PAGE16 && (!map_kv(&mk, c.k, c, box) || !map_kv(&mv, c.v, c, box)))
     return cudaErrorInvalidValue;
   const int n = rows_ctas<DP, MB>();
-  a.part_ml = static_cast<float2*>(ws);
+  if (!a.whole) a.cuts = static_cast<Cut*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<Cut*>(ws) + n);
   a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * G::TM);
   timer_before(MOE_KERNEL_ATTN, s);
   e = launch_pdl(true, kern, dim3(n), dim3(kRowsThreads), G::smem, s, a, mk, mv, box);
@@ -512,8 +540,7 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cuda
   note_launches(1);
   if (e != cudaSuccess || a.whole) return e;
   timer_before(MOE_KERNEL_ATTN_COMBINE, s);
-  e = launch_pdl(true, attn_join_kernel<G::TM, G::TN, DP>, dim3(n - 1), dim3(kJoinThreads), 0, s,
-                 a, n);
+  e = launch_pdl(true, attn_join_kernel<G::TM, DP>, dim3(n - 1), dim3(kJoinThreads), 0, s, a);
   timer_after(MOE_KERNEL_ATTN_COMBINE, s);
   note_launches(1);
   return e;
@@ -529,7 +556,8 @@ static cudaError_t launch_rows(const AttnArgs& a, const moe_kv_cache& c, int64_t
 
 template <int DP, int MB>
 static size_t rows_ws() {
-  return (size_t)2 * rows_ctas<DP, MB>() * RowsGeo<DP, MB>::TM * (DP + 2) * sizeof(float);
+  return (size_t)rows_ctas<DP, MB>() *
+         (sizeof(Cut) + 2 * RowsGeo<DP, MB>::TM * (DP + 2) * sizeof(float));
 }
 
 size_t attn_ws_bytes(int D) {
