@@ -70,6 +70,7 @@ struct AttnArgs {
   int causal, window;    // window 0: none
   int rows_over, rows_upto;   // sequences with rows in (rows_over, rows_upto] take part
   int whole;             // units are not cut: a CTA takes those that begin in its stretch
+  int least;             // a stretch has at least so many steps
   struct Cut* cuts;      // [CTAs] the cut in front of each
   float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
   float2* part_ml;       // [2 * CTAs][TM] their (max, sum)
@@ -106,11 +107,10 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   int n = a.bt.kv_len[b];
   const int cap = a.bt.max_pages * a.bt.page_size;
   Seq q{s, e - s, n};
-  if (s < 0 || e < s || e > a.bt.T || n < 0 || n > cap) {
-    raise_status(a.status, MOE_ERR_DEVICE_INDEX);
-    q.n = n < 0 ? 0 : n > cap ? cap : n;
-    if (s < 0 || e < s || e > a.bt.T) q = Seq{0, 0, q.n};
-  }
+  const bool bad_rows = s < 0 || e < s || e > a.bt.T;
+  if (bad_rows || n < 0 || n > cap) raise_status(a.status, MOE_ERR_DEVICE_INDEX);
+  q.n = min(max(n, 0), cap);
+  if (bad_rows) q.nq = 0;
   const int rows = q.nq * a.G;
   if (rows <= a.rows_over || rows > a.rows_upto) q.nq = 0;
   return q;
@@ -161,11 +161,25 @@ struct Tiling {
 // ------------------------------------------------------------ the schedule --
 // All of it runs once a unit or less and is kept out of line: what a warp's
 // steady state executes has to fit the instruction cache.
-struct Line {               // the line of steps, cut for n CTAs
+// a / b of values that nearly always fit 32 bits
+static __device__ __noinline__ long long divide_long(long long a, long long b) { return a / b; }
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (__builtin_expect(((a | b) >> 32) == 0, 1)) return (long long)((uint32_t)a / (uint32_t)b);
+  return divide_long(a, b);
+}
+struct Line {               // the line of steps, cut for n CTAs (or fewer, of a least length)
   long long total, per;     // per = total / n; the first `rem` CTAs take one more
-  int rem;
+  int n, rem;
+  __device__ __forceinline__ Line(long long total_, int ctas, int least)
+      : total(total_), per(divide(total_, ctas)), n(ctas) {
+    if (per < least) {
+      n = max(1, (int)divide(total, least));
+      per = divide(total, n);
+    }
+    rem = (int)(total - per * n);
+  }
   __device__ __forceinline__ long long start(int cta) const {
-    return per * cta + (cta < rem ? cta : rem);
+    return cta >= n ? total : per * cta + (cta < rem ? cta : rem);
   }
 };
 struct Place {              // locate's, in shared memory
@@ -194,12 +208,6 @@ struct Unit {
   __device__ __forceinline__ bool whole() const { return off == 0 && stop == w; }
   __device__ __forceinline__ int slot() const { return off > 0 ? 0 : 1; }
 };
-
-// a / b of values that nearly always fit 32 bits
-__device__ __forceinline__ long long divide(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
-  return a / b;
-}
 
 // Steps of one head of the sequence of each lane (0 for nq = 0). A lane with
 // many row tiles gets its warp's help.
@@ -370,10 +378,7 @@ __device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl
       base = total;
     }
     if (pass == 0) {
-      Line ln;
-      ln.total = total;
-      ln.per = divide(total, n);
-      ln.rem = (int)(total - ln.per * n);
+      const Line ln(total, n, a.least);
       x0 = ln.start(cta);
       x1 = ln.start(cta + 1);
       if (tid == 0) {
@@ -384,7 +389,7 @@ __device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl
         pl.rem = ln.rem;
         u.more = pl.tall = 0;
       }
-      if (x0 >= total) {        // no steps, or fewer than CTAs: none for this one
+      if (x0 >= total) {        // none for this CTA
         if (tid == 0) {
           u.more = 0;
           if (a.cuts) a.cuts[cta] = Cut{0, 0, 0, 0, -1, 0, {0, 0}};

@@ -129,6 +129,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -155,6 +161,9 @@ __device__ __forceinline__ void tmem_st32f(uint32_t taddr, const float* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -206,14 +215,14 @@ __device__ __noinline__ void add_by_hand(uint32_t t_p, uint32_t t_o, const uint8
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = add ? o[i] : 0.f;
 #pragma unroll 1
-    for (int k = 0; k < kChunkTN; k += 16) {
-      uint32_t p[8];
-      tmem_ld8(t_p + k / 2, p);
+    for (int k = 0; k < kChunkTN; k += 2) {
+      uint32_t p;
+      tmem_ld1(t_p + k / 2, p);
       tmem_ld_wait();
 #pragma unroll
-      for (int kk = 0; kk < 16; ++kk) {
+      for (int kk = 0; kk < 2; ++kk) {
         const int key = k + kk;
-        const float w = (kk & 1) ? bf16_hi(p[kk >> 1]) : bf16_lo(p[kk >> 1]);
+        const float w = kk ? bf16_hi(p) : bf16_lo(p);
         const bool see = k0 + key >= lo && k0 + key < hi;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -662,7 +671,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // ------------------------------------------------ queries, edge values --
       constexpr int NC = DP / 8;            // 16-byte pieces of a row
       int vslot = 1, gone = 0;              // gone: tiles gone by
-      uint32_t vphase = 0, units[2] = {0, 0};
+      uint32_t vphase = 0, units = 0;     // units: two bits a half
       bool ok = true;
       for (int u = 0; take_unit(Call{}, u, ok); ++u) {
         const Unit wk = sh.unit[u & 3];
@@ -671,17 +680,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (nt == 0) continue;
         int e0, e1;
         edges(wk, e0, e1);
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int r0 = wk.m * kChunkTM + half * 128;
           const int nrows = wk.s.nq * a.G - r0;
           if (nrows <= 0) break;
-          if (units[half] > 0)
-            ok = ok && mbar_doze_bounded(smem_u32(&sh.q_free[half]), (units[half] - 1) & 1, 200,
-                                         abort, a.status);
+          // 0: no unit of the half so far; else 2 + the parity of the last one's end
+          const uint32_t had = units >> (2 * half) & 3;
+          if (had)
+            ok = ok && mbar_doze_bounded(smem_u32(&sh.q_free[half]), had & 1, 200, abort, a.status);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
-          ++units[half];
+          units = (units & ~(3u << (2 * half))) | ((had == 2 ? 3u : 2u) << (2 * half));
           const uint32_t bar = smem_u32(&sh.q_ready[half]);
           const uint32_t dst = s_q + half * G::q_half;
           if (q_by_tma) {
@@ -737,12 +747,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                               (((c ^ row) & 7) << 4));
             };
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
             for (int i = (v0 & ~15) * NC + lane; i < v0 * NC; i += 32) *piece(i) = zero;
+#pragma unroll 1
             for (int i = v1 * NC + lane; i < ((v1 + 15) & ~15) * NC; i += 32) *piece(i) = zero;
             uint32_t bad = 0;
-#pragma unroll 8
+#pragma unroll 4
             for (int i = v0 * NC + lane; i < f0 * NC; i += 32) bad |= not_finite8(*piece(i));
-#pragma unroll 8
+#pragma unroll 4
             for (int i = f1 * NC + lane; i < v1 * NC; i += 32) bad |= not_finite8(*piece(i));
             fence_async_smem();
             const int any = __any_sync(0xFFFFFFFFu, bad != 0);
@@ -900,9 +912,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const bool whole = wk.whole();
       RowEnd e{1.f, 0.f};
       if (whole) e = row_end(m_ref, l, a.sinks, head);
-      const int64_t prow = ((int64_t)blockIdx.x * 2 + wk.slot()) * kChunkTM + half * 128 + row;
+      const int64_t pslot = (int64_t)blockIdx.x * 2 + wk.slot();
       moe_bf16* const dst = a.out + grow * a.out_stride + (int64_t)head * a.D;
-      float* const part = a.part_o + prow * DP;
 #pragma unroll 1
       for (int c = 0; c < DP; c += 32) {
         float o[32];
@@ -924,13 +935,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         } else if (real) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(part + c + i * 4) =
+            *reinterpret_cast<float4*>(
+                a.part_o + part_at<kChunkTM, DP>(pslot, half * 128 + row, c / 4 + i)) =
                 make_float4(o[i * 4], o[i * 4 + 1], o[i * 4 + 2], o[i * 4 + 3]);
         }
         __syncwarp();      // the next load is the whole warp's
       }
       if (real) {
-        if (!whole) a.part_ml[prow] = make_float2(m_ref, l);
+        if (!whole) a.part_ml[pslot * kChunkTM + half * 128 + row] = make_float2(m_ref, l);
         else if (a.lse) a.lse[grow * a.Hq + head] = e.lse;
       }
       tc_fence_before();
@@ -981,7 +993,7 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
   timer_after(MOE_KERNEL_ATTN, s);
   if (e != cudaSuccess) return e;
   timer_before(MOE_KERNEL_ATTN_COMBINE, s);
-  e = launch_pdl(true, attn_join_kernel<kChunkTM, DP>, dim3(n - 1, 8), dim3(kJoinThreads), 0, s,
+  e = launch_pdl(true, attn_join_kernel<kChunkTM, DP>, dim3(n - 1, 16), dim3(kJoinThreads), 0, s,
                  a);
   timer_after(MOE_KERNEL_ATTN_COMBINE, s);
   note_launches(2);

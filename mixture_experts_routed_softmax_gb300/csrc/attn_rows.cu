@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
         }
         if (a.lse && c4 == 0) a.lse[(int64_t)(s.q0 + tok) * a.Hq + head] = e.lse;
       } else {
-        *reinterpret_cast<float4*>(a.part_o + (pslot * TM + r) * DP + c4 * 4) = t;
+        *reinterpret_cast<float4*>(a.part_o + part_at<TM, DP>(pslot, r, c4)) = t;
         if (c4 == 0) a.part_ml[pslot * TM + r] = make_float2(m, l);
       }
     }
@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 // ------------------------------------------------------------------ host --
 // Up to so many rows (tokens x query heads of a key head) a sequence is worked on
 // by the kernel above; more go to the chunk kernel where its pages allow.
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 32;
 // Units of at most so many keys are not cut: the second launch costs more than
 // an even load is worth.
 constexpr int kWholeKeys = 1024;
@@ -540,7 +540,7 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cuda
   note_launches(1);
   if (e != cudaSuccess || a.whole) return e;
   timer_before(MOE_KERNEL_ATTN_COMBINE, s);
-  e = launch_pdl(true, attn_join_kernel<G::TM, DP>, dim3(n - 1), dim3(kJoinThreads), 0, s, a);
+  e = launch_pdl(true, attn_join_kernel<G::TM, DP>, dim3(n - 1, 4), dim3(kJoinThreads), 0, s, a);
   timer_after(MOE_KERNEL_ATTN_COMBINE, s);
   note_launches(1);
   return e;
@@ -600,12 +600,14 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
     const int64_t seen = (int64_t)a.window + b.max_q;
     const int64_t keys = a.window && seen < cap ? seen : cap;
     r.whole = keys <= kWholeKeys ? 1 : 0;
+    r.least = r.whole ? 1 : kUnitCost + 2;
     const int64_t most = both ? kFewRows : rows;
     e = c.D <= 64 ? launch_rows<64>(r, c, most, page16, ws, s)
                   : launch_rows<128>(r, c, most, page16, ws, s);
   }
   if (e == cudaSuccess && chunks) {
     if (both) a.rows_over = kFewRows;
+    a.least = kUnitCost + 4;
     e = launch_attn_chunk(a, c, ws, s);
   }
   return e;
