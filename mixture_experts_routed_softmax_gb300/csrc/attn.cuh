@@ -261,7 +261,7 @@ __device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
   u.nt = max(u.stop - kUnitCost, 0) - begin;
 }
 template <int TM, int TN>
-__device__ __noinline__ void unit_next(const AttnArgs& a, Unit& u) {
+__device__ __forceinline__ void unit_next(const AttnArgs& a, Unit& u) {
   u.to_end -= u.w;
   u.more = 0;
   if (u.stop < u.w || u.to_end <= 0) return;

@@ -7,7 +7,7 @@
 //   P = exp2(S * scale - max), rounded to bf16 over S's own columns
 //   O += P V       tcgen05.mma with P read from tensor memory
 // One pass with a running reference for the exponent: a row's is the maximum of
-// its first 32 keys, and is only moved (O, the sum and the tile's stored weights
+// its first 64 keys, and is only moved (O, the sum and the tile's stored weights
 // rescaled) when a score exceeds it by more than 16 in powers of two. Weights of
 // up to 2^16 cost no precision, in bf16 or in the fp32 sums, and the accumulator
 // is next to never touched between products.
@@ -16,19 +16,22 @@
 // (for D = 128 four 128x128x128 products and 32 Ki exponentials a tile), so
 // the halves alternate: while one half's scores are exponentiated, the other
 // half's products run.
-//   warps 0-3, 4-7   softmax of half 0 and 1: one row per thread (the row's
-//                    maximum and sum need no shuffles), the accumulator's
-//                    rescale, the epilogue
-//   warp 8           issues the products; owns tensor memory
-//   warp 9           loads K and V tiles by TMA through a ring, one box per
-//                    stretch of keys that neither a page nor a tile cuts
-//   warp 10          the queries of a half, as soon as the unit before has had
+//   warp 0           issues the products; owns tensor memory
+//   warp 1           loads K and V tiles by TMA through a ring, one box per
+//                    stretch of keys that neither a page nor a tile cuts; walks
+//                    the CTA's units and hands them on to the others
+//   warp 2           the queries of a half, as soon as the unit before has had
 //                    its last scores; the values of tiles that some row sees in
 //                    part: out-of-range rows become zeros, and infinities and
 //                    NaN are looked for
-//   warp 11          D <= 64: issues S = Q K^T, warp 8 only O += P V. There an
+//   warp 3           D <= 64: issues S = Q K^T, warp 0 only O += P V. There an
 //                    item's products take 512 cycles, less than one warp takes
-//                    to issue both beside two busy softmax warps on its scheduler
+//                    to issue both beside busy softmax warps on its scheduler
+//   warps 4-7, 8-11  softmax of half 0 and 1: one row per thread (the row's
+//                    maximum and sum need no shuffles), the accumulator's
+//                    rescale, the epilogue. (Two threads a row, 64 keys each, and
+//                    so four softmax warps a scheduler: 692 and 881 us for the
+//                    two shapes below.)
 #include "attn.cuh"
 #include "attn_join.cuh"
 #include "common.cuh"
@@ -42,7 +45,7 @@ namespace moe {
 constexpr int kChunkTM = 256;
 constexpr int kChunkTN = 128;
 constexpr int kChunkThreads = 384;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10, kScoreWarp = 11;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kHelpWarp = 2, kScoreWarp = 3;
 constexpr float kRescaleAt = 16.f;
 
 template <int DP>
@@ -314,13 +317,13 @@ __device__ __forceinline__ void scale_weights(uint32_t t_p, int n, float f) {
     tmem_st16(t_p + c, w);
   }
 }
-// 32 scores to weights exp2(s * scale - ref), as bf16 pairs; their sum
+// 64 scores to weights exp2(s * scale - ref), as bf16 pairs; their sum
 // (unrounded) is added to acc; the largest score.
 __device__ __forceinline__ float group_weights(const float* x, float scale, float ref,
                                                uint32_t* pk, float2* acc) {
   float mx[2] = {neg_inf(), neg_inf()};
 #pragma unroll
-  for (int c = 0; c < 32; c += 2) {
+  for (int c = 0; c < 64; c += 2) {
     float2 t = fma2(make_float2(x[c], x[c + 1]), scale, -ref);
     mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], x[c], x[c + 1]);
     t = make_float2(ex2(t.x), ex2(t.y));
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   };
   using Call = std::true_type;
   using Inline = std::false_type;
-  if (warp >= 8) {
+  if (warp < 4) {
     if (warp == kLoadWarp) {
       // -------------------------------------------------------------- loads --
       // lane i < nbox: the box of keys [tile + i * box, + box)
@@ -772,7 +775,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax --
-    const int half = warp >> 2;
+    const int half = (warp - 4) >> 2;
     const int row = (warp & 3) * 32 + lane;             // of the half
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_o = t_lane + G::o_col0 + half * DP;
@@ -830,12 +833,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                                  ((mine - 1) >> 1) & 1, abort, a.status);
             tc_fence_after();
           };
-          // In groups of 32 keys, the next one loaded while one is worked on; a
-          // group's weights take the place of scores already read. The loop is
-          // kept rolled (two groups a turn) for the instruction cache.
+          // In groups of 64 keys; a group's weights take the place of scores already
+          // read. The loop is kept rolled for the instruction cache (all 128 keys in
+          // line: 640 instead of 634 us a 2048-token chunk at D = 128, 790 instead
+          // of 675 us a 4 x 4096-token prefill at D = 64; groups of 32 with the next
+          // one loaded ahead: 716 and 700).
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           auto group = [&](const float* x, int g) {
-            uint32_t pk[16];
+            uint32_t pk[32];
             const float2 was[2] = {acc[0], acc[1]};
             float top = group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk, acc);
             const bool grew = real && top * a.scale_log2 > m_ref + kRescaleAt;
@@ -853,28 +858,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               }
               group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk, acc);
             }
-            tmem_st16(t_s + g * 16, pk);
+            tmem_st32(t_s + g * 16, pk);
           };
           const bool masked = k0 + kChunkTN > warp_hi || k0 < warp_lo;
           const RowMask mask{lo - k0, hi - k0};
-          float x0[32], x1[32];
-          tmem_ld32f(t_s, x0);
 #pragma unroll 1
-          for (int g = 0; g < 4; g += 2) {
+          for (int g = 0; g < 4; g += 2) {       // g: in 32 keys
+            float x[64];
+            tmem_ld32f(t_s + g * 32, x);
+            tmem_ld32f(t_s + g * 32 + 32, x + 32);
             tmem_ld_wait();
-            tmem_ld32f(t_s + g * 32 + 32, x1);
             if (__builtin_expect(masked, 0)) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) x0[c] = mask(x0[c], g * 32 + c);
+              for (int c = 0; c < 64; ++c) x[c] = mask(x[c], g * 32 + c);
             }
-            group(x0, g);
-            tmem_ld_wait();
-            if (g == 0) tmem_ld32f(t_s + 64, x0);
-            if (__builtin_expect(masked, 0)) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) x1[c] = mask(x1[c], g * 32 + 32 + c);
-            }
-            group(x1, g + 1);
+            group(x, g);
           }
           acc[0] = add2(acc[0], acc[1]);
           l += acc[0].x + acc[0].y;
