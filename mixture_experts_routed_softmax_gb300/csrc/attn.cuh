@@ -184,8 +184,10 @@ struct Line {               // the line of steps, cut for n CTAs (or fewer, of a
 };
 struct Place {              // locate's, in shared memory
   long long warp_sum[32];
-  long long in_seq, head_w, x0, x1, prev, per;
-  int rem, tall;            // tall: the sequence found has several row tiles
+  struct {
+    long long in_seq, x0, x1, prev, per;
+    int rem, tall;          // tall: the sequence found has several row tiles
+  } at[4];                  // of each stretch of the block
 };
 // What a join block needs of the cut in front of a CTA: a unit's rows and the
 // CTAs first .. last - 1 that have parts of it. first < 0: no cut to join there.
@@ -287,8 +289,9 @@ __device__ __forceinline__ void unit_next(const AttnArgs& a, Unit& u) {
 // The stretch's first unit, from the unit (u.s, b, h, m, nm) its first step x0
 // lies in, `off` steps into it; and the cut in front of the stretch.
 template <int TM, int TN>
-__device__ __noinline__ void unit_first(const AttnArgs& a, const Place& pl, int cta, int off,
-                                        Unit& u) {
+__device__ __noinline__ void unit_first(const AttnArgs& a, const Place& place, int k, int cta,
+                                        int off, Unit& u) {
+  const auto& pl = place.at[k];
   Cut c{0, 0, 0, 0, -1, 0, {0, 0}};
   const long long unit0 = pl.x0 - off;
   u.to_end = pl.x1 - unit0;
@@ -318,10 +321,12 @@ __device__ __noinline__ void unit_first(const AttnArgs& a, const Place& pl, int 
   if (a.cuts) a.cuts[cta] = c;
 }
 
-// CTA `cta` of `n`: its stretch's first unit into `u` and the cut in front of it
+// Stretches cta .. cta + K - 1 of `n` (one a CTA, or one a warp of its own units):
+// the first unit of stretch cta + k into u[k * pitch], and the cut in front of it
 // into a.cuts. By the whole block of NT threads; ends with a barrier.
-template <int TM, int TN, int NT>
-__device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl, Unit& u) {
+template <int TM, int TN, int NT, int K = 1>
+__device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl, Unit* us,
+                                    int pitch) {
   constexpr int NW = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.bt.B;
@@ -329,7 +334,7 @@ __device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl
   // NT sequences, one a thread, the second pass looks at what the first has; the
   // thread that finds a sequence of one row tile has all the unit takes.
   Seq s{0, 0, 0};
-  long long total = 0, x0 = 0, x1 = 0, hw = 0, inc = 0, before = 0;
+  long long total = 0, hw = 0, inc = 0, before = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     long long base = 0;
@@ -361,17 +366,20 @@ __device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl
       }
       if (pass == 1) {
         const long long hi = base + before + inc, lo = hi - hw * a.Hkv;
-        if (x0 >= lo && x0 < hi) {
-          const long long in_seq = x0 - lo;
+#pragma unroll 1
+        for (int k = 0; k < K; ++k) {
+          const long long x0 = pl.at[k].x0;
+          if (x0 < lo || x0 >= hi) continue;
+          Unit& u = us[k * pitch];
           u.s = s;
           u.b = b;
           u.nm = Tiling<TM, TN>::row_tiles(a, s);
-          u.h = (int)divide(in_seq, hw);
-          pl.in_seq = in_seq - u.h * hw;
-          pl.tall = u.nm > 1;
+          u.h = (int)divide(x0 - lo, hw);
+          pl.at[k].in_seq = x0 - lo - u.h * hw;
+          pl.at[k].tall = u.nm > 1;
           if (u.nm == 1) {
             u.m = 0;
-            unit_first<TM, TN>(a, pl, cta, (int)pl.in_seq, u);
+            unit_first<TM, TN>(a, pl, k, cta + k, (int)pl.at[k].in_seq, u);
           }
         }
       }
@@ -379,54 +387,54 @@ __device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl
     }
     if (pass == 0) {
       const Line ln(total, n, a.least);
-      x0 = ln.start(cta);
-      x1 = ln.start(cta + 1);
-      if (tid == 0) {
-        pl.x0 = x0;
-        pl.x1 = x1;
-        pl.prev = cta > 0 ? ln.start(cta - 1) : 0;
-        pl.per = ln.per;
-        pl.rem = ln.rem;
-        u.more = pl.tall = 0;
-      }
-      if (x0 >= total) {        // none for this CTA
-        if (tid == 0) {
-          u.more = 0;
-          if (a.cuts) a.cuts[cta] = Cut{0, 0, 0, 0, -1, 0, {0, 0}};
-        }
-        __syncthreads();
-        return;
+      if (tid < K) {
+        auto& at = pl.at[tid];
+        const int c = cta + tid;
+        at.x0 = ln.start(c);
+        at.x1 = ln.start(c + 1);
+        at.prev = c > 0 ? ln.start(c - 1) : 0;
+        at.per = ln.per;
+        at.rem = ln.rem;
+        at.tall = 0;
+        us[tid * pitch].more = 0;
+        // a start at the line's end: no steps
+        if (at.x0 >= total && a.cuts) a.cuts[c] = Cut{0, 0, 0, 0, -1, 0, {0, 0}};
       }
       __syncthreads();
+      if (pl.at[0].x0 >= total) return;      // nor for the stretches after it
     }
   }
   __syncthreads();
-  if (!pl.tall) return;
-  if (warp == 0) {
-    // which of the sequence's row tiles
-    const Seq t = u.s;
-    const int nm = u.nm;
-    long long rem = pl.in_seq;
 #pragma unroll 1
-    for (int m0 = 0; m0 < nm; m0 += 32) {
-      const int m = m0 + lane;
-      const int w = m < nm ? Tiling<TM, TN>::weight(a, t, m) : 0;
-      long long run = w;
+  for (int k = 0; k < K; ++k) {
+    if (!pl.at[k].tall) continue;
+    if (warp == 0) {
+      // which of the sequence's row tiles
+      Unit& u = us[k * pitch];
+      const Seq t = u.s;
+      const int nm = u.nm;
+      long long rem = pl.at[k].in_seq;
+#pragma unroll 1
+      for (int m0 = 0; m0 < nm; m0 += 32) {
+        const int m = m0 + lane;
+        const int w = m < nm ? Tiling<TM, TN>::weight(a, t, m) : 0;
+        long long run = w;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, run, o);
-        if (lane >= o) run += up;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long up = __shfl_up_sync(0xFFFFFFFFu, run, o);
+          if (lane >= o) run += up;
+        }
+        const bool here = rem >= run - w && rem < run;
+        if (here) {
+          u.m = m;
+          unit_first<TM, TN>(a, pl, k, cta + k, (int)(rem - (run - w)), u);
+        }
+        if (__any_sync(0xFFFFFFFFu, here)) break;
+        rem -= __shfl_sync(0xFFFFFFFFu, run, 31);
       }
-      const bool here = rem >= run - w && rem < run;
-      if (here) {
-        u.m = m;
-        unit_first<TM, TN>(a, pl, cta, (int)(rem - (run - w)), u);
-      }
-      if (__any_sync(0xFFFFFFFFu, here)) break;
-      rem -= __shfl_sync(0xFFFFFFFFu, run, 31);
     }
+    __syncthreads();
   }
-  __syncthreads();
 }
 
 // ---------------------------------------------------- asynchronous copies --

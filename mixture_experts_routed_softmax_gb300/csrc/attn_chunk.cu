@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  locate<kChunkTM, kChunkTN, kChunkThreads>(a, blockIdx.x, gridDim.x, sh.pl, sh.unit[0]);
+  locate<kChunkTM, kChunkTN, kChunkThreads>(a, blockIdx.x, gridDim.x, sh.pl, sh.unit, 1);
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   // The warp's next unit is there (false: the end, or given up); it has read it.

@@ -26,22 +26,24 @@
 
 namespace moe {
 
-constexpr int kRowsWarps = 4;
-constexpr int kRowsThreads = 32 * kRowsWarps;
 constexpr float kRowsRescaleAt = 16.f;
 
-template <int DP, int MB>
+constexpr int kRowsThreads = 128;
+
+// W: warps that work on a unit, 4 or 1; a block has 4 / W such groups.
+template <int DP, int MB, int W>
 struct RowsGeo {
+  static constexpr int groups = 4 / W;
   static constexpr int TM = 16 * MB;
   static constexpr int chunk = DP == 128 ? 16 : 32;              // keys of a warp's step
-  static constexpr int TN = chunk * kRowsWarps;
+  static constexpr int TN = chunk * W;
   static constexpr int row_bytes = DP * 2;
   static constexpr int stage = 2 * chunk * row_bytes;            // K and V: 8 KiB
   static constexpr int stages = 3;
-  static constexpr int ring = kRowsWarps * stages * stage;
-  static constexpr int merge = kRowsWarps * TM * DP * 4;         // reuses the ring
+  static constexpr int ring = 4 * stages * stage;
   static constexpr int q_bytes = TM * row_bytes;
-  static constexpr int smem = (ring > merge ? ring : merge) + q_bytes;
+  static constexpr int smem = ring + groups * q_bytes;
+  static_assert(TM * DP * 4 <= stages * stage, "a warp's part is joined through its ring");
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t* r) {
@@ -104,12 +106,12 @@ __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
 
 // PAGE16: pages of a multiple of 16 keys; a step's keys come in boxes of `box`
 // (16, or the whole step), each in one page.
-template <int DP, int MB, bool PAGE16>
+template <int DP, int MB, int W, bool PAGE16>
 __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mapK,
     const __grid_constant__ CUtensorMap mapV, int box) {
-  using G = RowsGeo<DP, MB>;
-  constexpr int TM = G::TM, TN = G::TN, S = G::stages, KC = G::chunk;
+  using G = RowsGeo<DP, MB, W>;
+  constexpr int TM = G::TM, TN = G::TN, S = G::stages, KC = G::chunk, NT = 32 * W;
   constexpr int ND = DP / 8;               // 8-wide column tiles of the accumulator
   constexpr int NC = DP / 8;               // 16-byte pieces of a row
   constexpr int NK = KC / 8;               // 8-key tiles of a step's scores
@@ -117,22 +119,34 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
   constexpr int NH = DP / 64;              // column blocks
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Place pl;
-  __shared__ Unit un[2];
-  __shared__ float2 s_ml[kRowsWarps][TM];
-  __shared__ uint64_t full[kRowsWarps][S];
+  __shared__ Unit units[G::groups][2];
+  __shared__ float2 s_mls[4][TM];
+  __shared__ uint64_t full[4][S];
   __shared__ int s_abort;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (PAGE16 && tid == 0) {
-    for (int i = 0; i < kRowsWarps * S; ++i) mbar_init(smem_u32(&full[0][0] + i), 1);
+  const int lane = threadIdx.x & 31, bwarp = threadIdx.x >> 5;
+  // within the group of warps that share a unit
+  const int group = bwarp / W, warp = bwarp % W, tid = threadIdx.x % NT;
+  if (PAGE16 && threadIdx.x == 0) {
+    for (int i = 0; i < 4 * S; ++i) mbar_init(smem_u32(&full[0][0] + i), 1);
     s_abort = 0;
     fence_mbar_init();
   }
   pdl_enter();
-  locate<TM, TN, kRowsThreads>(a, blockIdx.x, gridDim.x, pl, un[0]);
+  locate<TM, TN, kRowsThreads, G::groups>(a, blockIdx.x * G::groups, gridDim.x * G::groups, pl,
+                                          &units[0][0], 2);
+  Unit* const un = units[group];
+  float2(*const s_ml)[TM] = s_mls + group * W;
+  auto group_sync = [&]() {
+    if (W == 4) __syncthreads();
+    else __syncwarp();
+  };
 
-  const uint32_t s_ring = smem_u32(smem) + warp * S * G::stage;
-  const uint32_t s_q = smem_u32(smem) + (uint32_t)(G::smem - G::q_bytes);
-  float* const merge = reinterpret_cast<float*>(smem);
+  const uint32_t s_ring = smem_u32(smem) + bwarp * S * G::stage;
+  uint8_t* const q_mem = smem + G::ring + group * G::q_bytes;
+  const uint32_t s_q = smem_u32(q_mem);
+  // a warp's part of the unit: in its own ring
+  constexpr int kPartFloats = S * G::stage / 4;
+  float* const merge = reinterpret_cast<float*>(smem + group * W * S * G::stage);
   const int lr = lane >> 2, lc = lane & 3;      // accumulator row and column pair
 
   volatile int never = 0;
@@ -151,7 +165,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     return p;
   };
   // a thread's pieces of a unit's queries (rows past the unit: zeros)
-  constexpr int QP = TM * NC / kRowsThreads > 0 ? TM * NC / kRowsThreads : 1;
+  constexpr int QP = TM * NC / NT > 0 ? TM * NC / NT : 1;
   struct Pieces {
     uint4 v[QP];
   };
@@ -160,7 +174,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     const int r0 = w.m * TM, nrows = min(TM, w.s.nq * a.G - r0);
 #pragma unroll
     for (int i = 0; i < QP; ++i) {
-      const int at = i * kRowsThreads + tid, r = at / NC, c = at - r * NC;
+      const int at = i * NT + tid, r = at / NC, c = at - r * NC;
       q.v[i] = make_uint4(0u, 0u, 0u, 0u);
       if (r < nrows && c * 8 < a.D) {
         const int tok = div_group(a, r0 + r), g = (r0 + r) - tok * a.G;
@@ -196,7 +210,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
       if constexpr (PAGE16) {
         if (j >= ntile) return;
         const uint32_t dst = s_ring + (used % S) * G::stage;
-        const uint32_t bar = smem_u32(&full[warp][used % S]);
+        const uint32_t bar = smem_u32(&full[bwarp][used % S]);
         const uint32_t bytes = (uint32_t)box * 128u * (2 * NH);
         const uint32_t all = __popc(__ballot_sync(0xFFFFFFFFu, at.page >= 0)) * bytes;
         if (lane == 0) mbar_arrive_expect_tx(bar, all);
@@ -237,11 +251,11 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     Spot ahead = spot[S - 1];           // the next step's, looked up a step early
 #pragma unroll
     for (int i = 0; i < QP; ++i) {
-      const int at = i * kRowsThreads + tid, r = at / NC, c = at - r * NC;
-      *reinterpret_cast<uint4*>(smem + (G::smem - G::q_bytes) + tile_at<TM>(r, c)) = qp.v[i];
+      const int at = i * NT + tid, r = at / NC, c = at - r * NC;
+      *reinterpret_cast<uint4*>(q_mem + tile_at<TM>(r, c)) = qp.v[i];
     }
     // the next unit, found by a thread whose warp's first copies are on their way
-    if (tid == kRowsThreads - 32) {
+    if (tid == NT - 32) {
       un[cur ^ 1] = wk;
       unit_next<TM, TN>(a, un[cur ^ 1]);
     }
@@ -267,7 +281,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
       mx[mb][0] = mx[mb][1] = neg_inf();
       sum[mb][0] = sum[mb][1] = 0.f;
     }
-    __syncthreads();         // the queries are in shared memory
+    group_sync();         // the queries are in shared memory
 
     uint32_t qf[MB == 1 ? DP / 16 : 1][4];
     if constexpr (MB == 1) {
@@ -284,7 +298,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
       const uint32_t sv = sk + KC * G::row_bytes;
       const int k0 = first_key(j);
       if constexpr (PAGE16) {
-        const bool ok = mbar_wait_bounded(smem_u32(&full[warp][done % S]), (done / S) & 1, &s_abort,
+        const bool ok = mbar_wait_bounded(smem_u32(&full[bwarp][done % S]), (done / S) & 1, &s_abort,
                                           a.status);
         __syncwarp();
         if (!__all_sync(0xFFFFFFFFu, ok)) break;      // given up: reported, results void
@@ -442,14 +456,14 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     if constexpr (PAGE16) {
       // after giving up: copies in flight land before the ring is used again
       for (; done < used; ++done)
-        mbar_wait_bounded(smem_u32(&full[warp][done % S]), (done / S) & 1, &never, a.status);
+        mbar_wait_bounded(smem_u32(&full[bwarp][done % S]), (done / S) & 1, &never, a.status);
       __syncwarp();
     } else {
       cp_async_wait<0>();
     }
 
     // ---- join the warps ----------------------------------------------------
-    __syncthreads();          // every warp is done with the ring, the next unit is known
+    group_sync();          // every warp is done with the ring, the next unit is known
     cur ^= 1;
     if (un[cur].more) unit_loads(un[cur]);
 #pragma unroll
@@ -463,24 +477,24 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
         if (lc == 0) s_ml[warp][r] = make_float2(mx[mb][e], t);
 #pragma unroll
         for (int n = 0; n < ND; ++n)
-          *reinterpret_cast<float2*>(merge + (warp * TM + r) * DP + n * 8 + lc * 2) =
+          *reinterpret_cast<float2*>(merge + warp * kPartFloats + r * DP + n * 8 + lc * 2) =
               make_float2(o[mb][n][2 * e], o[mb][n][2 * e + 1]);
       }
-    __syncthreads();
+    group_sync();
     const bool whole = wk.whole();
-    const int64_t pslot = (int64_t)blockIdx.x * 2 + wk.slot();
-    for (int i = tid; i < nrows * (DP / 4); i += kRowsThreads) {
+    const int64_t pslot = ((int64_t)blockIdx.x * G::groups + group) * 2 + wk.slot();
+    for (int i = tid; i < nrows * (DP / 4); i += NT) {
       const int r = i / (DP / 4), c4 = i - r * (DP / 4);
       float m = neg_inf();
 #pragma unroll
-      for (int w = 0; w < kRowsWarps; ++w) m = fmaxf(m, s_ml[w][r].x);
+      for (int w = 0; w < W; ++w) m = fmaxf(m, s_ml[w][r].x);
       const float ref = m == neg_inf() ? 0.f : m;
       float l = 0.f;
       float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kRowsWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float f = ex2(s_ml[w][r].x - ref);
-        const float4 v = *reinterpret_cast<const float4*>(merge + (w * TM + r) * DP + c4 * 4);
+        const float4 v = *reinterpret_cast<const float4*>(merge + w * kPartFloats + r * DP + c4 * 4);
         l += f * s_ml[w][r].y;
         t.x += f * v.x; t.y += f * v.y; t.z += f * v.z; t.w += f * v.w;
       }
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
       }
     }
     if constexpr (PAGE16) fence_async_smem();
-    __syncthreads();          // the merge buffer is the ring again
+    group_sync();          // the merge buffer is the ring again
   }
 }
 
@@ -511,18 +525,21 @@ constexpr int kFewRows = 32;
 // Units of at most so many keys are not cut: the second launch costs more than
 // an even load is worth.
 constexpr int kWholeKeys = 1024;
+// Units of at most so many keys are a warp's, not a block's: there is nothing to
+// join and no one to wait for.
+constexpr int kWarpKeys = 256;
 
-template <int DP, int MB>
+template <int DP, int MB, int W>
 static int rows_ctas() {
   // CTAs an SM holds by shared memory (227 KiB, 1 KiB reserved a CTA)
-  constexpr int per = (227 * 1024) / (RowsGeo<DP, MB>::smem + 2048);
+  constexpr int per = (227 * 1024) / (RowsGeo<DP, MB, W>::smem + 2048);
   return num_sms() * (per < 4 ? per : 4);
 }
 
-template <int DP, int MB, bool PAGE16>
+template <int DP, int MB, int W, bool PAGE16>
 static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cudaStream_t s) {
-  using G = RowsGeo<DP, MB>;
-  auto kern = attn_rows_kernel<DP, MB, PAGE16>;
+  using G = RowsGeo<DP, MB, W>;
+  auto kern = attn_rows_kernel<DP, MB, W, PAGE16>;
   static SmemOnce once;
   cudaError_t e = once.set((const void*)kern, G::smem);
   if (e != cudaSuccess) return e;
@@ -530,7 +547,7 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cuda
   const int box = c.page_size % G::chunk == 0 ? G::chunk : 16;
   if (PAGE16 && (!map_kv(&mk, c.k, c, box) || !map_kv(&mv, c.v, c, box)))
     return cudaErrorInvalidValue;
-  const int n = rows_ctas<DP, MB>();
+  const int n = rows_ctas<DP, MB, W>();
   if (!a.whole) a.cuts = static_cast<Cut*>(ws);
   a.part_ml = reinterpret_cast<float2*>(static_cast<Cut*>(ws) + n);
   a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * G::TM);
@@ -546,18 +563,23 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cuda
   return e;
 }
 
-template <int DP>
-static cudaError_t launch_rows(const AttnArgs& a, const moe_kv_cache& c, int64_t rows,
-                               bool page16, void* ws, cudaStream_t s) {
-  if (rows <= 16)
-    return page16 ? launch_rows<DP, 1, true>(a, c, ws, s) : launch_rows<DP, 1, false>(a, c, ws, s);
-  return page16 ? launch_rows<DP, 2, true>(a, c, ws, s) : launch_rows<DP, 2, false>(a, c, ws, s);
+template <int DP, int MB>
+static cudaError_t launch_rows(const AttnArgs& a, const moe_kv_cache& c, int64_t keys, void* ws,
+                               cudaStream_t s) {
+  // uncut units of few keys, and enough of them to keep every SM busy: a warp each
+  if constexpr (MB == 1) {
+    if (a.whole && keys <= kWarpKeys && c.page_size % 16 == 0 &&
+        (int64_t)a.bt.B * a.Hkv >= 4 * num_sms())
+      return launch_rows<DP, MB, 1, true>(a, c, ws, s);
+  }
+  return c.page_size % 16 == 0 ? launch_rows<DP, MB, 4, true>(a, c, ws, s)
+                               : launch_rows<DP, MB, 4, false>(a, c, ws, s);
 }
 
 template <int DP, int MB>
 static size_t rows_ws() {
-  return (size_t)rows_ctas<DP, MB>() *
-         (sizeof(Cut) + 2 * RowsGeo<DP, MB>::TM * (DP + 2) * sizeof(float));
+  return (size_t)rows_ctas<DP, MB, 4>() *
+         (sizeof(Cut) + 2 * RowsGeo<DP, MB, 4>::TM * (DP + 2) * sizeof(float));
 }
 
 size_t attn_ws_bytes(int D) {
@@ -587,7 +609,6 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   a.status = status;
   a.rows_over = 0;
   a.rows_upto = 1 << 30;
-  const bool page16 = c.page_size % 16 == 0;
   const int64_t rows = (int64_t)b.max_q * a.G;
   const bool chunks = rows > kFewRows && attn_chunk_takes(c.page_size);
   // Both kernels where sequences may be of both kinds: not when all have max_q
@@ -601,9 +622,11 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
     const int64_t keys = a.window && seen < cap ? seen : cap;
     r.whole = keys <= kWholeKeys ? 1 : 0;
     r.least = r.whole ? 1 : kUnitCost + 2;
-    const int64_t most = both ? kFewRows : rows;
-    e = c.D <= 64 ? launch_rows<64>(r, c, most, page16, ws, s)
-                  : launch_rows<128>(r, c, most, page16, ws, s);
+    const bool one = rows <= 16;          // a tile of 16 rows, else of 32
+    if (c.D <= 64)
+      e = one ? launch_rows<64, 1>(r, c, keys, ws, s) : launch_rows<64, 2>(r, c, keys, ws, s);
+    else
+      e = one ? launch_rows<128, 1>(r, c, keys, ws, s) : launch_rows<128, 2>(r, c, keys, ws, s);
   }
   if (e == cudaSuccess && chunks) {
     if (both) a.rows_over = kFewRows;
