@@ -90,16 +90,6 @@ __device__ __noinline__ bool chunk_finite(uint32_t sv) {
   return !__any_sync(0xFFFFFFFFu, bad);
 }
 
-// The page and slot of key `key` of the sequence whose table row begins at
-// `table_at`; -1 for a page outside the cache.
-__device__ __forceinline__ int slot_of(const AttnArgs& a, int64_t table_at, int key, int& slot) {
-  const int pg = page_of(a.bt, key);
-  const int page = a.bt.table[table_at + pg];
-  slot = key - pg * a.bt.page_size;
-  if (page >= 0 && page < a.bt.n_pages) return page;
-  raise_status(a.status, MOE_ERR_DEVICE_INDEX);
-  return -1;
-}
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
@@ -152,17 +142,28 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
   volatile int never = 0;
   int used = 0, done = 0;      // ring slots filled and worked on by this warp so far
   // Where a step's keys are: lane g, its box of keys (PAGE16), or lane r, its
-  // key: page and slot; page -1: nothing to load.
+  // key: page and slot; slot -1: nothing to load. The page is what the table
+  // says, looked at only when it is used: a lookup waits for nothing.
   struct Spot {
     int page, slot;
   };
   auto lookup = [&](const Unit& w, int j) {
-    Spot p{-1, 0};
+    Spot p{0, -1};
     const int span = PAGE16 ? box : 1;
     const int key = (w.t0 + j) * TN + warp * KC + lane * span;
-    if (j < w.nt && lane * span < KC && key + span > w.lo && key < w.hi)
-      p.page = slot_of(a, (int64_t)w.b * a.bt.table_stride, key, p.slot);
+    if (j < w.nt && lane * span < KC && key + span > w.lo && key < w.hi) {
+      const int pg = page_of(a.bt, key);
+      p.page = a.bt.table[(int64_t)w.b * a.bt.table_stride + pg];
+      p.slot = key - pg * a.bt.page_size;
+    }
     return p;
+  };
+  // false: nothing to load, or a page outside the cache
+  auto usable = [&](const Spot& p) {
+    if (p.slot < 0) return false;
+    if (p.page >= 0 && p.page < a.bt.n_pages) return true;
+    raise_status(a.status, MOE_ERR_DEVICE_INDEX);
+    return false;
   };
   // a thread's pieces of a unit's queries (rows past the unit: zeros)
   constexpr int QP = TM * NC / NT > 0 ? TM * NC / NT : 1;
@@ -212,10 +213,11 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
         const uint32_t dst = s_ring + (used % S) * G::stage;
         const uint32_t bar = smem_u32(&full[bwarp][used % S]);
         const uint32_t bytes = (uint32_t)box * 128u * (2 * NH);
-        const uint32_t all = __popc(__ballot_sync(0xFFFFFFFFu, at.page >= 0)) * bytes;
+        const bool some = usable(at);
+        const uint32_t all = __popc(__ballot_sync(0xFFFFFFFFu, some)) * bytes;
         if (lane == 0) mbar_arrive_expect_tx(bar, all);
         __syncwarp();
-        if (at.page >= 0) {
+        if (some) {
 #pragma unroll
           for (int c = 0; c < NH; ++c) {
             const uint32_t d = dst + c * (KC * 128) + lane * box * 128;
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
           const int pc = lane % NC, pr = lane / NC;
           const int64_t mine = (int64_t)at.page * a.bt.page_stride +
                                (int64_t)at.slot * a.bt.token_stride;
-          const int64_t off = at.page >= 0 ? mine : -1;
+          const int64_t off = usable(at) ? mine : -1;
 #pragma unroll
           for (int i = 0; i < KC / kRowsPer; ++i) {
             const int r = i * kRowsPer + pr;
