@@ -5,14 +5,15 @@
 // of a sequence are n_q * G rows over the same keys: row r is token r / G,
 // head h * G + r % G. A unit is (sequence b, head h, row tile m of TM rows);
 // its keys are one range (the union of its rows' masks), cut into tiles of TN.
-// Units in the order (b, h, m) laid end to end, one step a tile and kUnitCost
-// steps more a unit (beginning and ending one takes about that long), make a
-// line; each of n CTAs takes an n-th of it. Every CTA so has the same work
+// Units in the order (b, h, m) laid end to end, one step a tile and `cost` steps
+// more a unit (beginning and ending one takes about that long), make a line;
+// each of n CTAs takes an n-th of it. Every CTA so has the same work
 // whatever the lengths, and writes at most two partial results: the unit it
 // enters in the middle (slot 0) and the unit it begins and does not end (slot
-// 1). A boundary within kUnitCost of a unit's beginning or end moves there. A
-// second launch joins the parts of each cut unit in order, so results do not
-// depend on timing.
+// 1). A boundary in a unit's first `cost` or last `snap` steps moves to its
+// beginning or end: `cost` in long stretches, where it saves a part, one step
+// in short ones, where evenness is worth more (kLongStretch). A second launch
+// joins the parts of each cut unit in order, so results do not depend on timing.
 #pragma once
 
 #include <atomic>
@@ -23,7 +24,7 @@ namespace moe {
 
 constexpr int kAttnMaxD = 128;
 constexpr int kAttnMaxKeys = 1 << 30;
-constexpr int kUnitCost = 2;
+constexpr int kLongStretch = 32;
 
 struct AttnBatch {
   const int32_t* cu_q;
@@ -70,6 +71,7 @@ struct AttnArgs {
   int causal, window;    // window 0: none
   int rows_over, rows_upto;   // sequences with rows in (rows_over, rows_upto] take part
   int whole;             // units are not cut: a CTA takes those that begin in its stretch
+  int cost;              // steps a unit takes beside its tiles
   int least;             // a stretch has at least so many steps
   struct Cut* cuts;      // [CTAs] the cut in front of each
   float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
@@ -154,7 +156,7 @@ struct Tiling {
     return p;
   }
   static __device__ __forceinline__ int weight(const AttnArgs& a, const Seq& s, int m) {
-    return span(a, s, m).nt + kUnitCost;
+    return span(a, s, m).nt + a.cost;
   }
 };
 
@@ -201,6 +203,7 @@ struct Unit {
   long long to_end;    // steps from the unit's first to the end of the stretch
   Seq s;
   int more;            // 0: the stretch has no further unit
+  int snap;
   int b, h, m, nm;
   int w, off, stop;    // the unit's steps; this CTA has [off, stop) of them
   int lo, hi;          // the keys of its rows
@@ -242,15 +245,15 @@ __device__ __forceinline__ long long head_weight(const AttnArgs& a, const Seq& s
 template <int TM, int TN>
 __device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
   const typename Tiling<TM, TN>::Span sp = Tiling<TM, TN>::span(a, u.s, u.m);
-  u.w = sp.nt + kUnitCost;
+  u.w = sp.nt + a.cost;
   u.stop = u.w;
   if (!a.whole && u.to_end < u.w) {
     const int e = (int)u.to_end;
-    if (e <= kUnitCost) {
+    if (e <= a.cost) {
       u.more = 0;
       return;
     }
-    if (u.w - e > kUnitCost) u.stop = e;
+    if (u.w - e > u.snap) u.stop = e;
   }
   u.more = 1;
   u.lo = sp.lo;
@@ -258,9 +261,9 @@ __device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
   const int rows = u.s.nq * a.G;
   u.all_lo = key_lo(a, u.s, div_group(a, min(u.m * TM + TM, rows) - 1));
   u.all_hi = key_hi(a, u.s, div_group(a, u.m * TM));
-  const int begin = max(u.off - kUnitCost, 0);
+  const int begin = max(u.off - a.cost, 0);
   u.t0 = sp.t0 + begin;
-  u.nt = max(u.stop - kUnitCost, 0) - begin;
+  u.nt = max(u.stop - a.cost, 0) - begin;
 }
 template <int TM, int TN>
 __device__ __forceinline__ void unit_next(const AttnArgs& a, Unit& u) {
@@ -296,8 +299,8 @@ __device__ __noinline__ void unit_first(const AttnArgs& a, const Place& place, i
   const long long unit0 = pl.x0 - off;
   u.to_end = pl.x1 - unit0;
   u.w = u.stop = Tiling<TM, TN>::weight(a, u.s, u.m);
-  const bool at_begin = a.whole ? off == 0 : off <= kUnitCost;
-  const bool at_end = a.whole || u.w - off <= kUnitCost;
+  const bool at_begin = a.whole ? off == 0 : off <= a.cost;
+  const bool at_end = a.whole || u.w - off <= u.snap;
   if (at_begin) {
     u.off = 0;
     unit_set<TM, TN>(a, u);
@@ -305,10 +308,10 @@ __device__ __noinline__ void unit_first(const AttnArgs& a, const Place& place, i
     unit_next<TM, TN>(a, u);
   } else {
     u.off = off;
-    if (pl.prev - unit0 <= kUnitCost) {
+    if (pl.prev - unit0 <= a.cost) {
       // the first cut of its unit; the last part is that of the CTA that has the
       // step the end's boundary is measured from
-      const long long y = unit0 + u.w - kUnitCost - 1, big = (long long)pl.rem * (pl.per + 1);
+      const long long y = unit0 + u.w - u.snap - 1, big = (long long)pl.rem * (pl.per + 1);
       c.first = cta - 1;
       c.last = 1 + (int)(y < big ? divide(y, pl.per + 1) : pl.rem + divide(y - big, pl.per));
       c.q0 = u.s.q0;
@@ -397,6 +400,7 @@ __device__ __noinline__ void locate(const AttnArgs& a, int cta, int n, Place& pl
         at.rem = ln.rem;
         at.tall = 0;
         us[tid * pitch].more = 0;
+        us[tid * pitch].snap = ln.per >= kLongStretch ? a.cost : 1;
         // a start at the line's end: no steps
         if (at.x0 >= total && a.cuts) a.cuts[c] = Cut{0, 0, 0, 0, -1, 0, {0, 0}};
       }

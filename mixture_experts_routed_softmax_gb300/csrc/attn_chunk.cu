@@ -47,6 +47,7 @@ constexpr int kChunkTN = 128;
 constexpr int kChunkThreads = 384;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kHelpWarp = 2, kScoreWarp = 3;
 constexpr float kRescaleAt = 16.f;
+constexpr int kChunkLeast = 6;
 
 template <int DP>
 struct ChunkGeo {
@@ -132,12 +133,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -166,15 +161,10 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr) : "memory");
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+               : "=r"(r)
+               : "r"(taddr)
+               : "memory");
 }
 // (x, y) * (a, a) + (b, b)
 __device__ __forceinline__ float2 fma2(float2 x, float a, float b) {
@@ -357,6 +347,8 @@ struct ChunkShared {
   uint32_t tmem;
   int abort;
   int issued;           // tiles whose loads have been issued
+  int q_had[2];         // of a half's queries: 0 none loaded, else 2 + the last load's parity
+  int never;            // 0
   int bad[8];           // per slot: an infinity or NaN among them
 };
 
@@ -367,7 +359,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                       const __grid_constant__ CUtensorMap mapK,
                       const __grid_constant__ CUtensorMap mapV, int box, int q_by_tma) {
   using G = ChunkGeo<DP>;
-  using TL = Tiling<kChunkTM, kChunkTN>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ ChunkShared sh;
   pdl_enter();
@@ -403,6 +394,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     sh.abort = 0;
     sh.issued = 0;
+    sh.never = 0;
+    sh.q_had[0] = sh.q_had[1] = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -415,8 +408,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uint32_t tmem = sh.tmem;
   // The warp's next unit is there (false: the end, or given up); it has read it.
   auto take_unit = [&](auto call, int u, bool& ok) {
-    ok = ok && wait_warp<decltype(call)::value>(smem_u32(&sh.unit_full[u & 3]), (u >> 2) & 1, abort,
-                                                a.status);
+    ok = ok && wait_warp<decltype(call)::value>(smem_u32(&sh.unit_full[u & 3]), (u >> 2) & 1,
+                                                abort, a.status);
     return ok && sh.unit[u & 3].more != 0;
   };
   auto give_unit = [&](int u) {
@@ -438,7 +431,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int u = 0;; ++u) {
         // the next unit (or that there is none) for every role
         Unit& un = sh.unit[u & 3];
-        ok = wait_warp<true>(smem_u32(&sh.unit_empty[u & 3]), ((u >> 2) & 1) ^ 1, abort, a.status);
+        ok = wait_warp<true>(smem_u32(&sh.unit_empty[u & 3]), ((u >> 2) & 1) ^ 1, abort,
+                             a.status);
         if (!ok) break;
         if (lane == 0) {
           if (u > 0) {
@@ -479,8 +473,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               const uint32_t dst = s_kv + slot * G::tile + lane * box_bytes;
 #pragma unroll
               for (int c = 0; c < G::halves; ++c)
-                tma_load_4d(dst + c * (kChunkTN * 128), kv ? (const void*)&mapV : (const void*)&mapK,
-                            bar, c * 64, pslot, wk.h, page);
+                tma_load_4d(dst + c * (kChunkTN * 128),
+                            kv ? (const void*)&mapV : (const void*)&mapK, bar, c * 64, pslot, wk.h,
+                            page);
             }
             ++fills;
             if (kv == 1 && lane == 0) *(volatile int*)&sh.issued = fills >> 1;
@@ -694,6 +689,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             ok = ok && mbar_doze_bounded(smem_u32(&sh.q_free[half]), had & 1, 200, abort, a.status);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
+          if (lane == 0) sh.q_had[half] = had == 2 ? 3 : 2;
           units = (units & ~(3u << (2 * half))) | ((had == 2 ? 3u : 2u) << (2 * half));
           const uint32_t bar = smem_u32(&sh.q_ready[half]);
           const uint32_t dst = s_q + half * G::q_half;
@@ -822,8 +818,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const uint32_t n = first_item + j * nh;
           const int buf = n % G::bufs;
           const uint32_t t_s = t_lane + buf * 128;
-          ok = ok && wait_warp<false>(smem_u32(&sh.s_full[half][mine % G::bufs]), (mine / G::bufs) & 1,
-                               abort, a.status);
+          ok = ok && wait_warp<false>(smem_u32(&sh.s_full[half][mine % G::bufs]),
+                                      (mine / G::bufs) & 1, abort, a.status);
           if (!ok) break;
           tc_fence_after();
           // the half's product before this one has ended, for who is to change O
@@ -882,12 +878,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // product: a tile that some row sees in part and that holds one is not
             // multiplied; its P V is added here, key by key over the rows that see it.
             const int t = first_tile + j, vslot = (2 * t + 1) % G::slots;
-            ok = ok && wait_warp<false>(smem_u32(&sh.v_seen[vslot]), seen >> vslot & 1, abort, a.status);
+            ok = ok && wait_warp<false>(smem_u32(&sh.v_seen[vslot]), seen >> vslot & 1, abort,
+                                        a.status);
             seen ^= 1u << vslot;
             const bool by_hand = ok && sh.bad[vslot] != 0;
             if (__any_sync(0xFFFFFFFFu, by_hand)) {
-              ok = ok && wait_warp<false>(smem_u32(&sh.kv_full[vslot]), ((2 * t + 1) / G::slots) & 1,
-                                   abort, a.status);
+              ok = ok && wait_warp<false>(smem_u32(&sh.kv_full[vslot]),
+                                          ((2 * t + 1) / G::slots) & 1, abort, a.status);
               if (j > 0) o_is_done();
               __syncwarp();
               add_by_hand<DP>(t_s, t_o, kv_mem + vslot * G::tile, k0, lo, hi, j > 0);
@@ -949,6 +946,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // after giving up: queries already asked for land before the CTA's shared memory
+  // goes away (waited for in the helper's own branch: 689 instead of 644 us a
+  // 4 x 4096-token prefill, by where the code then lies)
+  if (*abort && q_by_tma && tid < 2 && sh.q_had[tid])
+    wait_slowly(smem_u32(&sh.q_ready[tid]), sh.q_had[tid] & 1, &sh.never, a.status);
+  __syncwarp();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
@@ -982,6 +985,7 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
   cudaError_t e = once.set((const void*)kern, G::smem);
   if (e != cudaSuccess) return e;
   const int n = num_sms();
+  a.least = kChunkLeast;
   a.cuts = static_cast<Cut*>(ws);
   a.part_ml = reinterpret_cast<float2*>(a.cuts + n);
   a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * kChunkTM);

@@ -90,11 +90,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(
   pdl_enter();
   const Cut c = a.cuts[blockIdx.x + 1];
   if (c.first < 0) return;
-  // LN lanes an item (four columns of a row), each every LN-th part: one for a
-  // few parts, eight where a long unit has been cut many times and reading its
-  // parts in turn would be a chain of memory latencies.
-  const int parts = c.last - c.first;
-  if (parts <= 4) join_rows<TM, DP, 1>(a, c);
+  // LN lanes an item (four columns of a row), each every LN-th part, by which is
+  // fewer rounds of loads, four parts a round: eight for few rows cut many times.
+  const int parts = c.last - c.first, items = c.nrows * (DP / 4);
+  const int threads = kJoinThreads * gridDim.y;
+  const int one = ((items - 1) / threads + 1) * ((parts + 3) / 4);
+  const int eight = ((items * 8 - 1) / threads + 1) * ((parts + 31) / 32);
+  if (one < eight) join_rows<TM, DP, 1>(a, c);
   else join_rows<TM, DP, 8>(a, c);
 }
 

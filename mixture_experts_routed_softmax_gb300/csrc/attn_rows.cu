@@ -524,11 +524,8 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 // Up to so many rows (tokens x query heads of a key head) a sequence is worked on
 // by the kernel above; more go to the chunk kernel where its pages allow.
 constexpr int kFewRows = 32;
-// Units of at most so many keys are not cut: the second launch costs more than
-// an even load is worth.
-constexpr int kWholeKeys = 1024;
-// Units of at most so many keys are a warp's, not a block's: there is nothing to
-// join and no one to wait for.
+constexpr int kRowsCost = 2, kRowsLeast = 4;
+constexpr int kWholeTiles = 8;
 constexpr int kWarpKeys = 256;
 
 template <int DP, int MB, int W>
@@ -566,10 +563,11 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cuda
 }
 
 template <int DP, int MB>
-static cudaError_t launch_rows(const AttnArgs& a, const moe_kv_cache& c, int64_t keys, void* ws,
+static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, int64_t keys, void* ws,
                                cudaStream_t s) {
-  // uncut units of few keys, and enough of them to keep every SM busy: a warp each
-  if constexpr (MB == 1) {
+  a.whole = keys <= kWholeTiles * RowsGeo<DP, MB, 4>::TN ? 1 : 0;
+  a.least = a.whole ? 1 : kRowsLeast;
+  if constexpr (DP == 64 && MB == 1) {
     if (a.whole && keys <= kWarpKeys && c.page_size % 16 == 0 &&
         (int64_t)a.bt.B * a.Hkv >= 4 * num_sms())
       return launch_rows<DP, MB, 1, true>(a, c, ws, s);
@@ -622,8 +620,7 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
     if (both) r.rows_upto = kFewRows;
     const int64_t seen = (int64_t)a.window + b.max_q;
     const int64_t keys = a.window && seen < cap ? seen : cap;
-    r.whole = keys <= kWholeKeys ? 1 : 0;
-    r.least = r.whole ? 1 : kUnitCost + 2;
+    r.cost = kRowsCost;
     const bool one = rows <= 16;          // a tile of 16 rows, else of 32
     if (c.D <= 64)
       e = one ? launch_rows<64, 1>(r, c, keys, ws, s) : launch_rows<64, 2>(r, c, keys, ws, s);
@@ -632,7 +629,7 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   }
   if (e == cudaSuccess && chunks) {
     if (both) a.rows_over = kFewRows;
-    a.least = kUnitCost + 4;
+    a.cost = rows <= 128 ? 1 : 4;
     e = launch_attn_chunk(a, c, ws, s);
   }
   return e;

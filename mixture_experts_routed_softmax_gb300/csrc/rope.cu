@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
         const int end = a.bt.cu_q[b + 1], n = a.bt.kv_len[b];
         bool ok = n >= 0 && n <= a.bt.max_pages * a.bt.page_size && end <= a.bt.T;
         if (ok) c = n - end + (int)t;      // kv_len - n_q + (t - cu_q[b])
-        ok = ok && c >= 0 && c < n;
+        ok = ok && c >= 0 && c < n && a.bt.cu_q[b] <= t;
         if (ok) {
           const int pg = c / a.bt.page_size;
           const int page = a.bt.table[(int64_t)b * a.bt.table_stride + pg];
