@@ -308,19 +308,16 @@ __device__ __forceinline__ void scale_weights(uint32_t t_p, int n, float f) {
   }
 }
 // 64 scores to weights exp2(s * scale - ref), as bf16 pairs; their sum
-// (unrounded) is added to acc; the largest score.
-__device__ __forceinline__ float group_weights(const float* x, float scale, float ref,
-                                               uint32_t* pk, float2* acc) {
-  float mx[2] = {neg_inf(), neg_inf()};
+// (unrounded) is added to acc.
+__device__ __forceinline__ void group_weights(const float* x, float scale, float ref,
+                                              uint32_t* pk, float2& acc) {
 #pragma unroll
   for (int c = 0; c < 64; c += 2) {
     float2 t = fma2(make_float2(x[c], x[c + 1]), scale, -ref);
-    mx[(c >> 1) & 1] = max3(mx[(c >> 1) & 1], x[c], x[c + 1]);
     t = make_float2(ex2(t.x), ex2(t.y));
-    acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], t);
+    acc = add2(acc, t);
     pk[c / 2] = pack_bf16(t.x, t.y);
   }
-  return fmaxf(mx[0], mx[1]);
 }
 
 // Tiles [0, e0) and [e1, nt) of a unit are edge tiles: some row sees them in part.
@@ -830,30 +827,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tc_fence_after();
           };
           // In groups of 64 keys; a group's weights take the place of scores already
-          // read. The loop is kept rolled for the instruction cache (all 128 keys in
-          // line: 640 instead of 634 us a 2048-token chunk at D = 128, 790 instead
-          // of 675 us a 4 x 4096-token prefill at D = 64; groups of 32 with the next
-          // one loaded ahead: 716 and 700).
-          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // read. The loop is kept rolled, and the group's code there once, for the
+          // instruction cache (4 x 4096-token prefill at D = 64, 628 us; 2048 tokens
+          // over 31k keys at D = 128, 634 us): all 128 keys in line 894 and 661 us,
+          // groups of 32 700 and 730, the weights' code a second time after a moved
+          // reference 644 and 632.
+          float2 acc = make_float2(0.f, 0.f);
           auto group = [&](const float* x, int g) {
             uint32_t pk[32];
-            const float2 was[2] = {acc[0], acc[1]};
-            float top = group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk, acc);
+            float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+              mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], x[c], x[c + 1]);
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
             const bool grew = real && top * a.scale_log2 > m_ref + kRescaleAt;
             if (__builtin_expect(__any_sync(0xFFFFFFFFu, grew), 0)) {
               const float nm = grew ? top * a.scale_log2 : m_ref;
               const float f = nm == neg_inf() ? 1.f : ex2(m_ref - nm);
               m_ref = nm;
               l *= f;
-              acc[0] = make_float2(was[0].x * f, was[0].y * f);
-              acc[1] = make_float2(was[1].x * f, was[1].y * f);
+              acc = make_float2(acc.x * f, acc.y * f);
               scale_weights(t_s, g * 16, f);
               if (j > 0) {
                 o_is_done();
                 scale_rows<DP>(t_o, f);
               }
-              group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk, acc);
             }
+            group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk, acc);
             tmem_st32(t_s + g * 16, pk);
           };
           const bool masked = k0 + kChunkTN > warp_hi || k0 < warp_lo;
@@ -870,8 +870,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             group(x, g);
           }
-          acc[0] = add2(acc[0], acc[1]);
-          l += acc[0].x + acc[0].y;
+          l += acc.x + acc.y;
           tmem_st_wait();
           if (__builtin_expect(j < e0 || j >= e1, 0)) {
             // A zero weight does not keep an infinite or NaN value out of the
