@@ -120,3 +120,25 @@ def test_turns_are_exact_fractions():
             diff = (got - p * exact) % 1
             diff = min(diff, 1 - diff)
             assert diff <= abs(p) * Fraction(1, 1 << 65) + Fraction(1, 10 ** 30)
+
+
+def test_the_python_layer_refuses_what_does_not_fit(lib):
+    """Raised before any call: nothing here touches a device."""
+    import torch
+    from mixture_experts_routed_softmax_gb300 import attention as A
+    i32 = dict(dtype=torch.int32)
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        A.PagedAttention(kc, kc, 8)
+    with pytest.raises(ValueError, match="cu_q"):
+        A.KVBatch(torch.zeros(3, **i32), torch.zeros(2, **i32), torch.zeros(2, 4, **i32), 2)
+    with pytest.raises(ValueError, match="pair"):
+        A.Rope([], device="cpu")
+    for axis, n in (([0, 1], 1), ([0], 2), ([-1, 0], 1)):
+        with pytest.raises(ValueError, match="axis"):
+            A.Rope([1.0, 0.5], axis=axis, n_axes=n, device="cpu")
+    rope = A.Rope([1.0, 0.5], n_axes=2, device="cpu")
+    assert rope.rd == 4 and rope.args.n_axes == 2
+    q = torch.zeros(3, 2, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="pos"):
+        rope.apply(q, torch.zeros(2, 3, **i32), q)

@@ -483,3 +483,153 @@ def test_forward_is_append_then_attend():
     assert layer.status() == 0
     out, tol, _, _ = R.attention(b.q, c.kn, c.vn, c.cu, c.kv, c.table, layer.scale)
     _same(b.out, out, tol, "out")
+
+
+# ------------------------------------------------- schedules, references, joins --
+@pytest.mark.parametrize("D,ps,ql,kv", [(64, 16, [1, 3], [700, 400]), (128, 16, [1, 2], [500, 90]),
+                                        (80, 13, [1, 9], [300, 250]), (64, 64, [300], [700]),
+                                        (128, 24, [200, 40], [900, 300]), (40, 16, [90], [2000])])
+def test_references_move_on_the_way(D, ps, ql, kv):
+    """Scores that keep growing by far more than 2^16 in weight: sums, accumulators
+    and weights already rounded are rescaled between and inside tiles. A weight so
+    is rounded up to twice: twice the bound."""
+    c = Case(8, 2, D, ps, ql, kv, seed=30)
+    for b, n in enumerate(kv):
+        for j in range(n):
+            grow = 1.0 + 40.0 * j / n if j % 97 else 1.0 + 60.0 * j / n
+            c.kn[c.table[b][j // ps], :, j % ps] *= grow
+    sinks = torch.linspace(-5, 60, 8, device="cuda")
+    for s in (None, sinks):
+        layer, b = c.attend(sinks=s)
+        out, tol, lse, ltol = R.attention(c.q, c.kn, c.vn, c.cu, c.kv, c.table, layer.scale,
+                                          sinks=s)
+        _same(b.out, out, 2 * tol, "out")
+        _same(b.lse, lse, ltol, "lse")
+
+
+@pytest.mark.parametrize("D,ps,nq", [(64, 16, 1), (128, 64, 1), (128, 13, 3), (128, 8, 9),
+                                     (64, 24, 11), (128, 64, 7)])
+def test_one_long_sequence_in_many_parts(D, ps, nq):
+    c = Case(8, 2, D, ps, [nq], [30011], seed=31)
+    c.check()
+    c.check(sinks=torch.linspace(-3, 9, 8, device="cuda"), causal=False)
+
+
+@pytest.mark.parametrize("D,G,nq,window", [(64, 2, 1, 0), (64, 8, 2, 100), (40, 2, 3, 17),
+                                           (64, 1, 16, 90), (128, 2, 1, 100)])
+def test_many_short_units(D, G, nq, window):
+    """More uncut units than warps that work on them, empty ones in between."""
+    B = 90
+    kv = [(i * 53) % 240 for i in range(B)] if not window else [(i * 997) % 3000 for i in range(B)]
+    ql = [min(nq, n) if i % 7 else 0 for i, n in enumerate(kv)]
+    c = Case(8 * G, 8, D, 16, ql, kv, seed=32)
+    c.check(window=window, sinks=torch.linspace(-4, 4, 8 * G, device="cuda"))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_stretches(D):
+    """Enough units that cuts near a unit's end move there."""
+    c = Case(64, 16, D, 64, [1024, 700, 901, 1100], [1024, 1500, 901, 1111], seed=33)
+    c.check()
+    c = Case(16, 8, D, 16, [1] * 130, [(i * 211) % 3000 + 1 for i in range(130)], seed=34)
+    c.check()
+
+
+def test_a_captured_chunk_follows_its_lengths():
+    c = Case(16, 2, 64, 16, [100, 1, 60], [200, 80, 300], seed=35)
+    layer, b = c.attend()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.attend(c.q, c.batch, b)
+    c.kv = [150, 77, 60]
+    c.batch.kv_len.copy_(_i32(c.kv))
+    c.cu = [0, 90, 120, 161]
+    c.batch.cu_q.copy_(_i32(c.cu))
+    g.replay()
+    torch.cuda.synchronize()
+    out, tol, lse, ltol = R.attention(c.q, c.kn, c.vn, c.cu, c.kv, c.table, layer.scale)
+    _same(b.out, out, tol, "out")
+    _same(b.lse, lse, ltol, "lse")
+
+
+def test_tokens_in_front_of_the_first_sequence_are_refused():
+    A = _mod()
+    from mixture_experts_routed_softmax_gb300 import _lib
+    c = Case(4, 2, 64, 16, [3, 2], [40, 20], seed=36)
+    layer = A.PagedAttention(c.k_cache, c.v_cache, 4)
+    c.batch.cu_q[0] = 2                    # rows 0 and 1 are no sequence's
+    k = torch.randn(c.T, 2, 64, device="cuda").to(BF16)
+    before = c.kn.clone()
+    layer.append(k, k, c.batch)
+    assert layer.status() == _lib.MOE_ERR_DEVICE_INDEX
+    for j in (37, 38):
+        assert torch.equal(c.kn[c.table[0][j // 16], :, j % 16],
+                           before[c.table[0][j // 16], :, j % 16])
+    assert torch.equal(c.kn[c.table[0][2], :, 39 % 16], k[2])
+
+
+def test_shapes_that_do_not_fit_are_refused():
+    A = _mod()
+    c = Case(8, 2, 64, 16, [1, 1], [40, 20], seed=37)
+    layer = A.PagedAttention(c.k_cache, c.v_cache, 8)
+    b = layer.buffers(2, lse=True)
+    for q in (c.q[:1], c.q[:, :4], c.q.float(), c.q.transpose(1, 2).contiguous().transpose(1, 2)):
+        with pytest.raises(ValueError):
+            layer.attend(q, c.batch, b)
+    with pytest.raises(ValueError):
+        layer.attend(c.q, c.batch, layer.buffers(3, lse=True))
+    with pytest.raises(ValueError):
+        layer.append(c.q, c.q, c.batch)
+    with pytest.raises(ValueError):
+        layer.append(c.q[:, :2], c.q[:, :2], c.batch, q=c.q)
+    with pytest.raises(ValueError):
+        layer.append(c.q[:, :2], c.q[:, :2], c.batch, pos=_i32([0, 0]))
+    with pytest.raises(ValueError):
+        A.PagedAttention(c.k_cache, c.v_cache, 7)
+    with pytest.raises(ValueError):
+        A.KVBatch(c.batch.cu_q[:2], c.batch.kv_len, c.batch.page_table, 2)
+    rope = A.Rope.from_base(64, 10000.0)
+    with pytest.raises(ValueError):
+        rope.apply(c.q, _i32([0, 1, 2]), torch.empty_like(c.q))
+
+
+def test_a_block_of_attention_and_experts():
+    """examples/serve_block.py on a small shape: prompts in one ragged step, then
+    captured single-token steps; each step's attention against the 64-bit form
+    over the cache it left, the block against its parts."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "serve_block.py")
+    spec = importlib.util.spec_from_file_location("serve_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    _mod()
+    ql = [70, 3, 200]
+    blk = m.Block(d=256, Hq=8, Hkv=2, D=64, f=136, E=8, k=2, page_size=16, max_pages=20, B=3,
+                  window=90, seed=1)
+    x = torch.randn(sum(ql), 256, generator=torch.Generator(device="cuda").manual_seed(2),
+                    device="cuda").to(BF16)
+    last = blk.prefill(x, ql)
+    assert last.shape == (3, 256) and bool(last.isfinite().all())
+    dec = m.Decoder(blk, last)
+    assert torch.equal(dec.x, last) and blk.kv_len.tolist() == ql
+    lens = list(ql)
+    for _ in range(4):
+        before = dec.x.clone()
+        row = dec.step()
+        torch.cuda.synchronize()
+        lens = [n + 1 for n in lens]
+        assert blk.kv_len.tolist() == lens
+        # the same step without the graph, part by part: its append writes the
+        # same keys and values to the same slots
+        batch = blk.batch([1] * 3)
+        ab, mb = blk.buffers(3)
+        y = blk.step(before, batch, (ab, mb))
+        assert torch.equal(row, y)
+        a = blk.attn
+        out, tol, _, _ = R.attention(ab.q, a.k_cache, a.v_cache, [0, 1, 2, 3], lens,
+                                     blk.table.tolist(), a.scale, window=90, sinks=a.sinks)
+        _same(ab.out, out, tol, "out")
+    assert blk.attn.status() == 0
