@@ -389,9 +389,9 @@ size_t moe_decode_workspace_size(int64_t T, int d, int f, int E, int k);
  * of (page, head, slot) is the D elements at k + page * page_stride +
  * head * head_stride + slot * token_stride, values alike (elements, multiples
  * of 8; 64-bit offsets). [pages, heads, slots, D] keeps a head's page in one
- * piece; [pages, slots, heads, D] works as well. page_size: any >= 1 (the
- * chunk kernel on the tensor cores' own path takes multiples of 8, others run
- * the general kernel). */
+ * piece; [pages, slots, heads, D] works as well. page_size: any >= 1 (many
+ * tokens a sequence are fast with multiples of 8, best of 16 or more; single
+ * tokens with multiples of 16). */
 typedef struct {
   moe_bf16* k;
   moe_bf16* v;
@@ -458,7 +458,8 @@ int moe_rope(const moe_rotary* rot, const int32_t* pos, int64_t T, int D, int tr
  *  rot NULL: keys and queries are copied;  pos [n_axes, T] int32, or NULL: a
  *  token's cache position on every axis (0 for a row of no sequence)
  * A token whose cache position or page (not in [0, n_pages)) is outside the
- * cache raises MOE_ERR_DEVICE_INDEX and is not written. Pages that several
+ * cache, or that lies in front of cu_q[0], raises MOE_ERR_DEVICE_INDEX and is
+ * not written. Pages that several
  * sequences share must not be written by more than one of them. In place for
  * q as in moe_rope.
  * ------------------------------------------------------------------------ */
@@ -476,9 +477,10 @@ int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const mo
  *   lse[t, h] = log of that denominator.
  * A row that sees no key gives out = 0 (lse = sinks[h], or -inf). What lies in
  * the cache outside a row's keys does not reach it, be it infinite or NaN.
- * Scores, maxima and sums are fp32; the weights exp(s_j - max) are rounded to
- * bf16 for the product with V (the sum takes them unrounded); out is rounded
- * once. Results of two calls are bitwise equal on one GPU model.
+ * Scores and sums are fp32; the weights exp(s_j - r), r a score of the row that
+ * moves up when they exceed 2^16, are rounded to bf16 for the product with V
+ * (once more where r moves on the way; the sum takes them unrounded); out is
+ * rounded once. Results of two calls are bitwise equal on one GPU model.
  *  q, out [T, Hq, D] (out may not overlap q);  sinks [Hq] fp32 or NULL;
  *  lse [T, Hq] fp32 packed, or NULL;  scale finite and > 0
  *  ws: moe_attn_paged_workspace_size(Hq, Hkv, D) bytes, 256-byte aligned (its size

@@ -24,6 +24,10 @@ namespace moe {
 
 constexpr int kAttnMaxD = 128;
 constexpr int kAttnMaxKeys = 1 << 30;
+// Stretches of so many steps are long. Moving ends by `cost` steps everywhere: 777
+// tokens over 2500 keys (8 steps a CTA) 54 us; by one step everywhere: 4 x 2000
+// tokens with a window of 512 (66 steps) 159 us; by this rule 50 and 151 us (64
+// for the limit: 158 us; 16: 150 us).
 constexpr int kLongStretch = 32;
 
 struct AttnBatch {

@@ -7,15 +7,24 @@
 //   P = exp2(S * scale - max), rounded to bf16 over S's own columns
 //   O += P V       tcgen05.mma with P read from tensor memory
 // One pass with a running reference for the exponent: a row's is the maximum of
-// its first 64 keys, and is only moved (O, the sum and the tile's stored weights
-// rescaled) when a score exceeds it by more than 16 in powers of two. Weights of
-// up to 2^16 cost no precision, in bf16 or in the fp32 sums, and the accumulator
-// is next to never touched between products.
+// the first 64 keys it sees, and is only moved (O, the sum and the tile's stored
+// weights rescaled) when the weights of 64 keys sum to more than 2^16: nothing
+// looks for a maximum in the usual step. Weights of up to 2^16 cost no precision,
+// in bf16 or in the fp32 sums, and the accumulator is next to never touched
+// between products.
 //
 // The tensor cores and the exponentials are the two resources of like cost
 // (for D = 128 four 128x128x128 products and 32 Ki exponentials a tile), so
 // the halves alternate: while one half's scores are exponentiated, the other
-// half's products run.
+// half's products run. Measured, L2 flushed before each run:
+//   (a) 2048 tokens over 31k keys, 32 heads to 4, D = 128: 611 us, 1646 TFLOP/s,
+//       85% of what a large plain product reaches; the tensor pipe is the bound;
+//   (b) 4 x 4096 tokens from scratch, 64 heads to 8, D = 64: 618 us, 890 TFLOP/s,
+//       46%: as many exponentials as (a) for half the products. The softmax
+//       warps are the bound (some five instructions a score, every second issue
+//       slot taken, the exponential unit busy 37% of the time).
+// Choices below name their times for (a) and (b). A maximum of every score and
+// the reference moved by that: 634 and 627.
 //   warp 0           issues the products; owns tensor memory
 //   warp 1           loads K and V tiles by TMA through a ring, one box per
 //                    stretch of keys that neither a page nor a tile cuts; walks
@@ -30,8 +39,8 @@
 //   warps 4-7, 8-11  softmax of half 0 and 1: one row per thread (the row's
 //                    maximum and sum need no shuffles), the accumulator's
 //                    rescale, the epilogue. (Two threads a row, 64 keys each, and
-//                    so four softmax warps a scheduler: 692 and 881 us for the
-//                    two shapes below.)
+//                    so four softmax warps a scheduler: 692 and 881 when
+//                    one thread a row took 634 and 675.)
 #include "attn.cuh"
 #include "attn_join.cuh"
 #include "common.cuh"
@@ -46,7 +55,9 @@ constexpr int kChunkTM = 256;
 constexpr int kChunkTN = 128;
 constexpr int kChunkThreads = 384;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kHelpWarp = 2, kScoreWarp = 3;
-constexpr float kRescaleAt = 16.f;
+constexpr float kMoveAt = 65536.f;
+// The least steps of a stretch: a cut costs a part's round trip. 128 tokens over
+// 2500 keys, D = 128: 5 or 6 steps 42 us, 8 46 us, 12 50 us.
 constexpr int kChunkLeast = 6;
 
 template <int DP>
@@ -307,17 +318,19 @@ __device__ __forceinline__ void scale_weights(uint32_t t_p, int n, float f) {
     tmem_st16(t_p + c, w);
   }
 }
-// 64 scores to weights exp2(s * scale - ref), as bf16 pairs; their sum
-// (unrounded) is added to acc.
-__device__ __forceinline__ void group_weights(const float* x, float scale, float ref,
-                                              uint32_t* pk, float2& acc) {
+// 64 scores to weights exp2(s * scale - ref), as bf16 pairs; their unrounded sum.
+__device__ __forceinline__ float group_weights(const float* x, float scale, float ref,
+                                               uint32_t* pk) {
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
   for (int c = 0; c < 64; c += 2) {
     float2 t = fma2(make_float2(x[c], x[c + 1]), scale, -ref);
     t = make_float2(ex2(t.x), ex2(t.y));
-    acc = add2(acc, t);
+    acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], t);
     pk[c / 2] = pack_bf16(t.x, t.y);
   }
+  const float2 s = add2(acc[0], acc[1]);
+  return s.x + s.y;
 }
 
 // Tiles [0, e0) and [e1, nt) of a unit are edge tiles: some row sees them in part.
@@ -828,38 +841,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           };
           // In groups of 64 keys; a group's weights take the place of scores already
           // read. The loop is kept rolled, and the group's code there once, for the
-          // instruction cache (4 x 4096-token prefill at D = 64, 628 us; 2048 tokens
-          // over 31k keys at D = 128, 634 us): all 128 keys in line 894 and 661 us,
-          // groups of 32 700 and 730, the weights' code a second time after a moved
-          // reference 644 and 632.
-          float2 acc = make_float2(0.f, 0.f);
-          auto group = [&](const float* x, int g) {
-            uint32_t pk[32];
-            float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-            for (int c = 0; c < 64; c += 2)
-              mx[(c >> 1) & 3] = max3(mx[(c >> 1) & 3], x[c], x[c + 1]);
-            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-            const bool grew = real && top * a.scale_log2 > m_ref + kRescaleAt;
-            if (__builtin_expect(__any_sync(0xFFFFFFFFu, grew), 0)) {
-              const float nm = grew ? top * a.scale_log2 : m_ref;
-              const float f = nm == neg_inf() ? 1.f : ex2(m_ref - nm);
-              m_ref = nm;
-              l *= f;
-              acc = make_float2(acc.x * f, acc.y * f);
-              scale_weights(t_s, g * 16, f);
-              if (j > 0) {
-                o_is_done();
-                scale_rows<DP>(t_o, f);
-              }
-            }
-            group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk, acc);
-            tmem_st32(t_s + g * 16, pk);
-          };
+          // instruction cache ((a) and (b) before sums replaced the maxima: this form
+          // 634 and 628, all 128 keys in line 661 and 894, groups of 32 730 and 700, a
+          // second copy of the weights' code 632 and 644).
           const bool masked = k0 + kChunkTN > warp_hi || k0 < warp_lo;
           const RowMask mask{lo - k0, hi - k0};
 #pragma unroll 1
-          for (int g = 0; g < 4; g += 2) {       // g: in 32 keys
+          for (int g = 0; g < 4;) {             // g: in 32 keys
             float x[64];
             tmem_ld32f(t_s + g * 32, x);
             tmem_ld32f(t_s + g * 32 + 32, x + 32);
@@ -868,9 +856,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
               for (int c = 0; c < 64; ++c) x[c] = mask(x[c], g * 32 + c);
             }
-            group(x, g);
+            uint32_t pk[32];
+            const float sum =
+                group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk);
+            // NaN and infinities come here too: the reference is their row's maximum
+            // at most once, then they are stored
+            const bool check = real && (m_ref == neg_inf() || !(sum <= kMoveAt));
+            if (__builtin_expect(__any_sync(0xFFFFFFFFu, check), 0)) {
+              float top = x[0];
+#pragma unroll
+              for (int c = 1; c < 63; c += 2) top = max3(top, x[c], x[c + 1]);
+              top = fmaxf(top, x[63]) * a.scale_log2;
+              const bool grew = check && top > m_ref;
+              if (__any_sync(0xFFFFFFFFu, grew)) {
+                const float nm = grew ? top : m_ref;
+                const float f = nm == neg_inf() ? 1.f : ex2(m_ref - nm);
+                m_ref = nm;
+                l *= f;
+                scale_weights(t_s, g * 16, f);
+                if (j > 0) {
+                  o_is_done();
+                  scale_rows<DP>(t_o, f);
+                }
+                continue;        // once more: no score of the group is above now
+              }
+            }
+            l += sum;
+            tmem_st32(t_s + g * 16, pk);
+            g += 2;
           }
-          l += acc.x + acc.y;
           tmem_st_wait();
           if (__builtin_expect(j < e0 || j >= e1, 0)) {
             // A zero weight does not keep an infinite or NaN value out of the

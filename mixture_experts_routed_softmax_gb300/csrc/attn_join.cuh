@@ -65,7 +65,8 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const Cut& c) {
     }
 #pragma unroll
     for (int o = kItems; o < 32; o <<= 1) {
-      const float m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o), l = __shfl_xor_sync(0xFFFFFFFFu, t.l, o);
+      const float m = __shfl_xor_sync(0xFFFFFFFFu, t.m, o);
+      const float l = __shfl_xor_sync(0xFFFFFFFFu, t.l, o);
       const float4 v = make_float4(__shfl_xor_sync(0xFFFFFFFFu, t.o.x, o),
                                    __shfl_xor_sync(0xFFFFFFFFu, t.o.y, o),
                                    __shfl_xor_sync(0xFFFFFFFFu, t.o.z, o),
@@ -92,6 +93,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(
   if (c.first < 0) return;
   // LN lanes an item (four columns of a row), each every LN-th part, by which is
   // fewer rounds of loads, four parts a round: eight for few rows cut many times.
+  // Bound: the latency of a round. One lane always: 8 tokens over 400 to 9000 keys
+  // 44 instead of 32 us in all, 5 tokens over 100k keys 62 instead of 48; eight
+  // always: 128 tokens over 2500 keys 67 instead of 42.
   const int parts = c.last - c.first, items = c.nrows * (DP / 4);
   const int threads = kJoinThreads * gridDim.y;
   const int one = ((items - 1) / threads + 1) * ((parts + 3) / 4);

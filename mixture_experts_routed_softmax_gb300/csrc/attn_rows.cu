@@ -6,11 +6,11 @@
 // keys with a running reference and sum. With R rows over the keys the work is
 // 4 R D operations for 4 D bytes of a key and value, so up to a few dozen rows
 // the bound is reading the cache once. Hence: warps that never wait for each
-// other, each with its own keys (a quarter of a tile), its own ring of 16-byte
-// asynchronous copies, its own references, sums and accumulator, joined through
-// shared memory once per unit. The products run on mma.sync (m16n8k16): its
-// rate is far above what the copies feed, and it takes 16 rows where tcgen05
-// takes 128.
+// other, each with its own keys (a quarter of a tile), its own ring of
+// asynchronous copies (24 KiB in flight a warp, two CTAs of four an SM), its own
+// references, sums and accumulator, joined through shared memory once per unit.
+// The products run on mma.sync (m16n8k16): its rate is far above what the copies
+// feed, and it takes 16 rows where tcgen05 takes 128.
 //
 // A warp's step is 8 KiB of keys and values; what it costs beside the copies is
 // instructions, so a row's reference is held (the maximum of its first step)
@@ -18,6 +18,14 @@
 // rescaling in the usual step; and pages of a multiple of 16 keys come by TMA, a
 // box of keys an instruction of one lane, others by 16-byte copies with an
 // address a key (444 instead of some 230 instructions a step).
+//
+// Measured with the join, L2 flushed before each run: four sequences of 65k to
+// 131k keys, 32 heads to 4, D = 128, 169 us = 4.9 TB/s (145 us, 5.7 TB/s, back to
+// back; a plain copy runs at 6.8); 64 sequences of 17 to 16k keys, 64 heads to 8,
+// D = 64, 83 us = 3.9 TB/s (68 back to back). The steady state reads at 90 to 95%
+// of the copy's rate; the rest is some 15 us of beginning and end: two launches,
+// the schedule (3 us), the first keys (until 5 to 8 us), the parts' join. Loading
+// the next unit's first keys while a unit's parts are joined changed nothing.
 #include "attn.cuh"
 #include "attn_join.cuh"
 #include "common.cuh"
@@ -95,7 +103,8 @@ __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
 }
 
 // PAGE16: pages of a multiple of 16 keys; a step's keys come in boxes of `box`
-// (16, or the whole step), each in one page.
+// (16, or the whole step), each in one page. Three stages a warp: with four one
+// CTA an SM is left, and the sequences above take 175 and 89 us.
 template <int DP, int MB, int W, bool PAGE16>
 __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mapK,
@@ -300,8 +309,8 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
       const uint32_t sv = sk + KC * G::row_bytes;
       const int k0 = first_key(j);
       if constexpr (PAGE16) {
-        const bool ok = mbar_wait_bounded(smem_u32(&full[bwarp][done % S]), (done / S) & 1, &s_abort,
-                                          a.status);
+        const bool ok = mbar_wait_bounded(smem_u32(&full[bwarp][done % S]), (done / S) & 1,
+                                          &s_abort, a.status);
         __syncwarp();
         if (!__all_sync(0xFFFFFFFFu, ok)) break;      // given up: reported, results void
         // values of keys out of range are what the cache or an older step left:
@@ -420,7 +429,8 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
             for (int k = 0; k < 16; ++k) {
               // the weight of (row, key) is with lane lc = key % 8 / 2 of the row
               const int src = lr * 4 + ((k & 7) >> 1);
-              const uint32_t w4[2][2] = {{pf[mb][g][0], pf[mb][g][1]}, {pf[mb][g][2], pf[mb][g][3]}};
+              const uint32_t w4[2][2] = {{pf[mb][g][0], pf[mb][g][1]},
+                                         {pf[mb][g][2], pf[mb][g][3]}};
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const uint32_t w2 = __shfl_sync(0xFFFFFFFFu, k < 8 ? w4[0][e] : w4[1][e], src);
@@ -496,7 +506,8 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const float f = ex2(s_ml[w][r].x - ref);
-        const float4 v = *reinterpret_cast<const float4*>(merge + w * kPartFloats + r * DP + c4 * 4);
+        const float4 v =
+            *reinterpret_cast<const float4*>(merge + w * kPartFloats + r * DP + c4 * 4);
         l += f * s_ml[w][r].y;
         t.x += f * v.x; t.y += f * v.y; t.z += f * v.z; t.w += f * v.w;
       }
@@ -522,10 +533,25 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 
 // ------------------------------------------------------------------ host --
 // Up to so many rows (tokens x query heads of a key head) a sequence is worked on
-// by the kernel above; more go to the chunk kernel where its pages allow.
+// by the kernel above, in one row tile of 16 or 32; more go to the chunk kernel
+// where its pages allow. 64 sequences of 1000 to 3000 keys, 8 heads to a key head,
+// D = 64 and 128, the kernel above and the chunk kernel: 16 rows 42 / 48 and 67 /
+// 77 us, 32 rows 46 / 50 and 72 / 77 us, 40 rows 75 / 50 and 110 / 77 us.
 constexpr int kFewRows = 32;
+// Steps a unit costs beside its tiles (1 makes the 64 sequences above 89 instead
+// of 83 us, 4 changes nothing there and makes 31 tokens of D = 80 32 instead of
+// 30 us), and the least steps of a stretch (between 3 and 8 no difference).
 constexpr int kRowsCost = 2, kRowsLeast = 4;
+// Units of at most so many tiles (512 keys at D = 128, 1024 at D = 64) are not
+// cut: the second launch costs more than an even load is worth. One token over 4
+// key heads, D = 128, uncut / cut: 512 keys 18 / 20 us, 1024 keys 26 / 20 us; 16
+// sequences of 512 keys 20 / 22, of 1024 28 / 26; 128 of 1024 69 / 71.
 constexpr int kWholeTiles = 8;
+// Uncut units of at most so many keys are a warp's, not a block's, where there are
+// enough to keep every warp busy: nothing to join and no one to wait for. At D =
+// 64, 8 key heads, a warp's / a block's: 320 sequences of 128 keys 38 / 44 us, 256
+// keys 50 / 54, 512 keys 73 / 71; 64 sequences of 128 keys 20 / 18. At D = 128,
+// with 16 keys a step, a block's is never slower (320 x 256 keys 82 / 75 us).
 constexpr int kWarpKeys = 256;
 
 template <int DP, int MB, int W>
@@ -629,6 +655,11 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   }
   if (e == cudaSuccess && chunks) {
     if (both) a.rows_over = kFewRows;
+    // Steps a unit costs beside its tiles. Up to 128 rows tiles take as long as
+    // reading them does, beyond a unit's beginning and end are four tiles' work:
+    // drafts of 40 rows over 24-key pages 75 us at a cost of 1, 79 at 2, 89 at 4;
+    // 4 x 4096 tokens at D = 64 654 at 4, 686 at 2; 16 prompts of 100 to 3000
+    // tokens at D = 128 255 at 4, 278 at 2, 325 at 1.
     a.cost = rows <= 128 ? 1 : 4;
     e = launch_attn_chunk(a, c, ws, s);
   }
