@@ -390,8 +390,8 @@ size_t moe_decode_workspace_size(int64_t T, int d, int f, int E, int k);
  * head * head_stride + slot * token_stride, values alike (elements, multiples
  * of 8; 64-bit offsets). [pages, heads, slots, D] keeps a head's page in one
  * piece; [pages, slots, heads, D] works as well. page_size: any >= 1 (many
- * tokens a sequence are fast with multiples of 8, best of 16 or more; single
- * tokens with multiples of 16). */
+ * tokens a sequence are fastest with multiples of 16, then of 8; single tokens
+ * with multiples of 16). */
 typedef struct {
   moe_bf16* k;
   moe_bf16* v;

@@ -514,7 +514,7 @@ __device__ __forceinline__ RowEnd row_end(float m, float l, const float* sinks, 
 }
 
 // attn_chunk.cu
-bool attn_chunk_takes(int page_size);
+bool attn_chunk_boxes(int page_size);      // keys by TMA; else by 16-byte copies
 size_t attn_chunk_ws_bytes(int D);
 cudaError_t launch_attn_chunk(const AttnArgs& a, const moe_kv_cache& c, void* ws, cudaStream_t s);
 

@@ -27,8 +27,11 @@
 // the reference moved by that: 634 and 627.
 //   warp 0           issues the products; owns tensor memory
 //   warp 1           loads K and V tiles by TMA through a ring, one box per
-//                    stretch of keys that neither a page nor a tile cuts; walks
-//                    the CTA's units and hands them on to the others
+//                    stretch of keys that neither a page nor a tile cuts, or by
+//                    16-byte copies where that is fewer than 8 keys (then the
+//                    bound: 268 instead of 108 us for 2048 tokens over 4096 keys
+//                    in pages of 13, D = 128; boxes of 8 keys, pages of 24: 160,
+//                    by copies 267); walks the CTA's units and hands them on
 //   warp 2           the queries of a half, as soon as the unit before has had
 //                    its last scores; the values of tiles that some row sees in
 //                    part: out-of-range rows become zeros, and infinities and
@@ -282,6 +285,27 @@ __device__ __forceinline__ bool mbar_doze_bounded(uint32_t bar, uint32_t parity,
   return true;
 }
 
+// A K or V tile by 16-byte copies, for pages whose keys no box can take: lane i
+// has the element offsets of keys i, i + 32, .. (-1: zeros). By a whole warp.
+template <int DP>
+__device__ __noinline__ void gather_tile(const moe_bf16* base, uint32_t dst, int D, int64_t at0,
+                                         int64_t at1, int64_t at2, int64_t at3) {
+  constexpr int NC = DP / 8, kRows = 32 / NC;      // pieces of a row, rows of a copy
+  const int lane = threadIdx.x & 31, pc = lane % NC, pr = lane / NC;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int64_t at = i == 0 ? at0 : i == 1 ? at1 : i == 2 ? at2 : at3;
+#pragma unroll 4
+    for (int k = 0; k < 32; k += kRows) {
+      const int r = i * 32 + k + pr;
+      const int64_t o = __shfl_sync(0xFFFFFFFFu, at, k + pr);
+      const bool in = o >= 0 && pc * 8 < D;
+      cp_async16(dst + (pc >> 3) * (128 * 128) + r * 128 + (((pc ^ r) & 7) << 4),
+                 base + (in ? o + pc * 8 : 0), in);
+    }
+  }
+}
+
 // One tile's row of scores as a thread sees it: keys k0 .. k0 + 127, of which
 // the row sees [lo, hi). Masked by selection: a masked score's value, NaN or
 // not, is dropped.
@@ -362,7 +386,9 @@ struct ChunkShared {
   int bad[8];           // per slot: an infinity or NaN among them
 };
 
-template <int DP>
+// GATHER: pages whose keys no box can take (a kernel of its own: the other's loops
+// lose 4% to where this code would put them).
+template <int DP, bool GATHER>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     attn_chunk_kernel(const __grid_constant__ AttnArgs a,
                       const __grid_constant__ CUtensorMap mapQ,
@@ -438,9 +464,42 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       uint32_t phase = 0;
       int fills = 0;
       bool ok = true;
+      // With copies a tile is handed on when it has landed: after the next one's
+      // have been issued, or before a wait.
+      int landing = -1;           // the slot not handed on yet
+      auto hand_on = [&]() {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.kv_full[landing]));
+        landing = -1;
+      };
+      auto land = [&]() {
+        if (landing < 0) return;
+        cp_async_wait<0>();
+        hand_on();
+      };
+      struct Keys {
+        int page[4], slot[4];     // of keys lane + 32 i; slot -1: none
+      };
+      auto find_keys = [&](const Unit& w, int j) {
+        Keys p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = (w.t0 + j) * kChunkTN + lane + 32 * i;
+          p.page[i] = 0;
+          p.slot[i] = -1;
+          if (j < w.nt && key >= w.lo && key < w.hi) {
+            const int pg = page_of(a.bt, key);
+            p.page[i] = a.bt.table[(int64_t)w.b * a.bt.table_stride + pg];
+            p.slot[i] = key - pg * a.bt.page_size;
+          }
+        }
+        return p;
+      };
       for (int u = 0;; ++u) {
         // the next unit (or that there is none) for every role
         Unit& un = sh.unit[u & 3];
+        if constexpr (GATHER) land();
         ok = wait_warp<true>(smem_u32(&sh.unit_empty[u & 3]), ((u >> 2) & 1) ^ 1, abort,
                              a.status);
         if (!ok) break;
@@ -455,44 +514,84 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const Unit wk = un;
         if (!wk.more) break;
         const int nt = wk.nt;
+        Keys keys;
+        if constexpr (GATHER) keys = find_keys(wk, 0);
         for (int j = 0; j < nt && ok; ++j) {
-          const int key = (wk.t0 + j) * kChunkTN + lane * box;
-          const bool mine = lane < nbox && key < wk.hi && key + box > wk.lo;
-          int page = 0, pslot = 0;
-          if (mine) {
-            const int pg = page_of(a.bt, key);
-            page = a.bt.table[(int64_t)wk.b * a.bt.table_stride + pg];
-            pslot = key - pg * a.bt.page_size;
-            if (page < 0 || page >= a.bt.n_pages) {
-              raise_status(a.status, MOE_ERR_DEVICE_INDEX);
-              page = 0;
-            }
-          }
-          const uint32_t bytes =
-              __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes * (uint32_t)G::halves;
+          if constexpr (GATHER) {
+            int64_t at[4];
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = ok && mbar_doze_bounded(smem_u32(&sh.kv_empty[slot]), phase ^ 1u, 100, abort,
-                                         a.status);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            const uint32_t bar = smem_u32(&sh.kv_full[slot]);
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-            __syncwarp();
+            for (int i = 0; i < 4; ++i) {
+              at[i] = -1;
+              if (keys.slot[i] >= 0) {
+                if (keys.page[i] >= 0 && keys.page[i] < a.bt.n_pages)
+                  at[i] = (int64_t)keys.page[i] * a.bt.page_stride +
+                          (int64_t)keys.slot[i] * a.bt.token_stride + wk.h * a.head_stride;
+                else
+                  raise_status(a.status, MOE_ERR_DEVICE_INDEX);
+              }
+            }
+            keys = find_keys(wk, j + 1);
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+              const uint32_t empty = smem_u32(&sh.kv_empty[slot]);
+              if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(empty, phase ^ 1u))) {
+                land();
+                ok = mbar_doze_bounded(empty, phase ^ 1u, 100, abort, a.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+              }
+              gather_tile<DP>(kv ? a.v : a.k, s_kv + slot * G::tile, a.D, at[0], at[1], at[2],
+                              at[3]);
+              cp_async_commit();
+              if (landing >= 0) {
+                cp_async_wait<1>();
+                hand_on();
+              }
+              landing = slot;
+              ++fills;
+              if (kv == 1 && lane == 0) *(volatile int*)&sh.issued = fills >> 1;
+              if (++slot == G::slots) { slot = 0; phase ^= 1u; }
+            }
+          } else {
+            const int key = (wk.t0 + j) * kChunkTN + lane * box;
+            const bool mine = lane < nbox && key < wk.hi && key + box > wk.lo;
+            int page = 0, pslot = 0;
             if (mine) {
-              const uint32_t dst = s_kv + slot * G::tile + lane * box_bytes;
-#pragma unroll
-              for (int c = 0; c < G::halves; ++c)
-                tma_load_4d(dst + c * (kChunkTN * 128),
-                            kv ? (const void*)&mapV : (const void*)&mapK, bar, c * 64, pslot, wk.h,
-                            page);
+              const int pg = page_of(a.bt, key);
+              page = a.bt.table[(int64_t)wk.b * a.bt.table_stride + pg];
+              pslot = key - pg * a.bt.page_size;
+              if (page < 0 || page >= a.bt.n_pages) {
+                raise_status(a.status, MOE_ERR_DEVICE_INDEX);
+                page = 0;
+              }
             }
-            ++fills;
-            if (kv == 1 && lane == 0) *(volatile int*)&sh.issued = fills >> 1;
-            if (++slot == G::slots) { slot = 0; phase ^= 1u; }
+            const uint32_t bytes =
+                __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes * (uint32_t)G::halves;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              ok = ok && mbar_doze_bounded(smem_u32(&sh.kv_empty[slot]), phase ^ 1u, 100, abort,
+                                           a.status);
+              ok = __all_sync(0xFFFFFFFFu, ok);
+              if (!ok) break;
+              const uint32_t bar = smem_u32(&sh.kv_full[slot]);
+              if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+              __syncwarp();
+              if (mine) {
+                const uint32_t dst = s_kv + slot * G::tile + lane * box_bytes;
+#pragma unroll
+                for (int c = 0; c < G::halves; ++c)
+                  tma_load_4d(dst + c * (kChunkTN * 128),
+                              kv ? (const void*)&mapV : (const void*)&mapK, bar, c * 64, pslot,
+                              wk.h, page);
+              }
+              ++fills;
+              if (kv == 1 && lane == 0) *(volatile int*)&sh.issued = fills >> 1;
+              if (++slot == G::slots) { slot = 0; phase ^= 1u; }
+            }
           }
         }
       }
+      if constexpr (GATHER) land();
       if (*abort) {
         // copies already issued land before the CTA's shared memory goes away
         const int out = fills < G::slots ? fills : G::slots;
@@ -975,25 +1074,26 @@ static int kv_box(int page_size) {      // keys that neither a page nor a tile c
   return b;
 }
 
-bool attn_chunk_takes(int page_size) { return page_size % 8 == 0; }
+bool attn_chunk_boxes(int page_size) { return page_size % 8 == 0; }
 
 size_t attn_chunk_ws_bytes(int D) {
   const int DP = D <= 64 ? 64 : 128;
   return (size_t)num_sms() * (sizeof(Cut) + 2 * kChunkTM * (DP + 2) * sizeof(float));
 }
 
-template <int DP>
+template <int DP, bool GATHER>
 static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cudaStream_t s) {
   using G = ChunkGeo<DP>;
-  CUtensorMap mk, mv;
-  const int box = kv_box(c.page_size);
-  if (!map_kv(&mk, c.k, c, box) || !map_kv(&mv, c.v, c, box)) return cudaErrorInvalidValue;
+  CUtensorMap mk = {}, mv = {};
+  const int box = GATHER ? kChunkTN : kv_box(c.page_size);
+  if (!GATHER && (!map_kv(&mk, c.k, c, box) || !map_kv(&mv, c.v, c, box)))
+    return cudaErrorInvalidValue;
   // a half's 128 rows are whole tokens when G divides 128
   const int by_tma = 128 % a.G == 0 ? 1 : 0;
   CUtensorMap mq = mk;
   if (by_tma && !map_heads(&mq, a.q, a.D, a.Hq, a.bt.T, a.q_stride, a.G, 128 / a.G))
     return cudaErrorInvalidValue;
-  auto kern = attn_chunk_kernel<DP>;
+  auto kern = attn_chunk_kernel<DP, GATHER>;
   static SmemOnce once;
   cudaError_t e = once.set((const void*)kern, G::smem);
   if (e != cudaSuccess) return e;
@@ -1017,7 +1117,9 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
 
 cudaError_t launch_attn_chunk(const AttnArgs& a, const moe_kv_cache& c, void* ws,
                               cudaStream_t s) {
-  return c.D <= 64 ? launch_chunk<64>(a, c, ws, s) : launch_chunk<128>(a, c, ws, s);
+  if (!attn_chunk_boxes(c.page_size))
+    return c.D <= 64 ? launch_chunk<64, true>(a, c, ws, s) : launch_chunk<128, true>(a, c, ws, s);
+  return c.D <= 64 ? launch_chunk<64, false>(a, c, ws, s) : launch_chunk<128, false>(a, c, ws, s);
 }
 
 }  // namespace moe

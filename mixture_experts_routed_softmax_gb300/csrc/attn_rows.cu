@@ -1,6 +1,5 @@
 // attn_rows.cu — attention over the paged cache for few rows per key/value
-// head (decode, draft verification), and for page sizes the chunk kernel does
-// not take; the choice between the two.
+// head (decode, draft verification), and the choice between the two kernels.
 //
 // out = sum_j p_j v_j / sum_j p_j with p_j = exp(s_j - ref): one pass over the
 // keys with a running reference and sum. With R rows over the keys the work is
@@ -538,6 +537,13 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 // D = 64 and 128, the kernel above and the chunk kernel: 16 rows 42 / 48 and 67 /
 // 77 us, 32 rows 46 / 50 and 72 / 77 us, 40 rows 75 / 50 and 110 / 77 us.
 constexpr int kFewRows = 32;
+// Pages whose keys TMA cannot take (no multiple of 8) make the chunk kernel's loads
+// its bound: it is for as much work as this, in rows x keys of the page table.
+// Pages of 13, 32 heads to 4, D = 64 and 128, the kernel above and the chunk
+// kernel: 100 tokens over 2500 keys 30 / 46 and 44 / 62 us, 200 tokens 40 / 46 and
+// 60 / 63, 400 tokens 60 / 52 and 95 / 73, 8 x 200 over 2000 155 / 111 and 263 / 165,
+// 2048 over 4096 272 / 177 and 484 / 268.
+constexpr int64_t kGatherWork = (int64_t)1 << 24;
 // Steps a unit costs beside its tiles (1 makes the 64 sequences above 89 instead
 // of 83 us, 4 changes nothing there and makes 31 tokens of D = 80 32 instead of
 // 30 us), and the least steps of a stretch (between 3 and 8 no difference).
@@ -636,7 +642,8 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   a.rows_over = 0;
   a.rows_upto = 1 << 30;
   const int64_t rows = (int64_t)b.max_q * a.G;
-  const bool chunks = rows > kFewRows && attn_chunk_takes(c.page_size);
+  const bool chunks = rows > kFewRows && (attn_chunk_boxes(c.page_size) ||
+                                          (int64_t)b.T * Hq * cap >= kGatherWork);
   // Both kernels where sequences may be of both kinds: not when all have max_q
   // tokens, nor when one is all there is.
   const bool both = chunks && b.B > 1 && b.T != (int64_t)b.B * b.max_q;

@@ -633,3 +633,30 @@ def test_a_block_of_attention_and_experts():
                                      blk.table.tolist(), a.scale, window=90, sinks=a.sinks)
         _same(ab.out, out, tol, "out")
     assert blk.attn.status() == 0
+
+
+@pytest.mark.parametrize("D,ps,ql,kv,window", [
+    (64, 13, [700, 1, 300], [2000, 90, 310], 0), (128, 5, [900], [3000], 0),
+    (80, 1, [400, 50], [4000, 50], 77), (40, 100, [5, 1500], [700, 1500], 0),
+    (128, 13, [60] * 12, [900 + 31 * i for i in range(12)], 0)])
+def test_chunks_over_odd_pages(D, ps, ql, kv, window):
+    """Enough rows and keys for the chunk kernel to read pages no box fits."""
+    c = Case(16, 2, D, ps, ql, kv, seed=38)
+    c.check(window=window)
+    c.check(window=window, causal=False, sinks=torch.linspace(-4, 9, 16, device="cuda"))
+
+
+def test_odd_pages_that_do_not_exist_are_reported():
+    A = _mod()
+    from mixture_experts_routed_softmax_gb300 import _lib
+    c = Case(16, 2, 64, 13, [600, 500], [2000, 1900], seed=39)
+    layer = A.PagedAttention(c.k_cache, c.v_cache, 16)
+    b = layer.buffers(c.T)
+    layer.attend(c.q, c.batch, b)
+    assert layer.status() == 0
+    good = b.out.clone()
+    c.batch.page_table[0, 7] = c.k_cache.shape[0]
+    c.batch.page_table[0, 9] = -1
+    layer.attend(c.q, c.batch, b)
+    assert layer.status() == _lib.MOE_ERR_DEVICE_INDEX
+    assert torch.equal(b.out[600:], good[600:])
