@@ -958,8 +958,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             uint32_t pk[32];
             const float sum =
                 group_weights(x, a.scale_log2, m_ref == neg_inf() ? 0.f : m_ref, pk);
-            // NaN and infinities come here too: the reference is their row's maximum
-            // at most once, then they are stored
+            // Infinite and NaN sums come here as well; a reference that is the group's
+            // maximum does not move again, so they are stored the second time.
             const bool check = real && (m_ref == neg_inf() || !(sum <= kMoveAt));
             if (__builtin_expect(__any_sync(0xFFFFFFFFu, check), 0)) {
               float top = x[0];
