@@ -537,13 +537,19 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 // D = 64 and 128, the kernel above and the chunk kernel: 16 rows 42 / 48 and 67 /
 // 77 us, 32 rows 46 / 50 and 72 / 77 us, 40 rows 75 / 50 and 110 / 77 us.
 constexpr int kFewRows = 32;
-// Pages whose keys TMA cannot take (no multiple of 8) make the chunk kernel's loads
-// its bound: it is for as much work as this, in rows x keys of the page table.
-// Pages of 13, 32 heads to 4, D = 64 and 128, the kernel above and the chunk
-// kernel: 100 tokens over 2500 keys 30 / 46 and 44 / 62 us, 200 tokens 40 / 46 and
-// 60 / 63, 400 tokens 60 / 52 and 95 / 73, 8 x 200 over 2000 155 / 111 and 263 / 165,
-// 2048 over 4096 272 / 177 and 484 / 268.
-constexpr int64_t kGatherWork = (int64_t)1 << 24;
+// The chunk kernel is for as much work as this, in rows x keys (what the page table
+// or the window allows) x 64 or 128: below, its beginning and its join cost more
+// than the rows kernel takes, whose units are then few and short. Pages of 16, the
+// kernel above and the chunk kernel, D = 64 and 128: 200 tokens over 200 keys, 8
+// heads to a key head, 18 / 30 and 22 / 34 us; 300 over 900, 4 heads, 24 / 33 and
+// 34 / 40; 8 x 9 over 1000 27 / 28 and 32 / 32; 16 x 9 over 1000 30 / 30 and 44 /
+// 32; 200 over 2500 40 / 33 and 56 / 40.
+constexpr int64_t kChunkWork = (int64_t)1 << 28;
+// And for pages that TMA cannot take (no multiple of 8), where the loads are its
+// bound. Pages of 13, likewise: 100 tokens over 2500 keys 30 / 46 and 44 / 62 us,
+// 200 tokens 40 / 46 and 60 / 63, 400 tokens 60 / 52 and 95 / 73, 8 x 200 over 2000
+// 155 / 111 and 263 / 165, 2048 over 4096 272 / 177 and 484 / 268.
+constexpr int64_t kGatherWork = (int64_t)1 << 30;
 // Steps a unit costs beside its tiles (1 makes the 64 sequences above 89 instead
 // of 83 us, 4 changes nothing there and makes 31 tokens of D = 80 32 instead of
 // 30 us), and the least steps of a stretch (between 3 and 8 no difference).
@@ -642,8 +648,11 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   a.rows_over = 0;
   a.rows_upto = 1 << 30;
   const int64_t rows = (int64_t)b.max_q * a.G;
-  const bool chunks = rows > kFewRows && (attn_chunk_boxes(c.page_size) ||
-                                          (int64_t)b.T * Hq * cap >= kGatherWork);
+  const int64_t seen = (int64_t)a.window + b.max_q;
+  const int64_t keys = a.window && seen < cap ? seen : cap;      // of a sequence's tokens
+  const int64_t least_work = attn_chunk_boxes(c.page_size) ? kChunkWork : kGatherWork;
+  const bool chunks =
+      rows > kFewRows && (int64_t)b.T * Hq * keys >= least_work / (c.D <= 64 ? 64 : 128);
   // Both kernels where sequences may be of both kinds: not when all have max_q
   // tokens, nor when one is all there is.
   const bool both = chunks && b.B > 1 && b.T != (int64_t)b.B * b.max_q;
@@ -655,8 +664,6 @@ cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_
   if (!chunks || both) {
     AttnArgs r = a;
     if (both) r.rows_upto = few;
-    const int64_t seen = (int64_t)a.window + b.max_q;
-    const int64_t keys = a.window && seen < cap ? seen : cap;
     r.cost = kRowsCost;
     const bool one = (both ? few : rows) <= 16;          // a tile of 16 rows, else of 32
     if (c.D <= 64)

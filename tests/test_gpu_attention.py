@@ -660,3 +660,50 @@ def test_odd_pages_that_do_not_exist_are_reported():
     layer.attend(c.q, c.batch, b)
     assert layer.status() == _lib.MOE_ERR_DEVICE_INDEX
     assert torch.equal(b.out[600:], good[600:])
+
+
+# ------------------------------------------- small shapes on the chunk kernel --
+class WideCase(Case):
+    """A page table far wider than the sequences need and a large hint: what a
+    call of much work looks like to the choice of a kernel."""
+
+    def __init__(self, *args, **kw):
+        super().__init__(*args, **kw)
+        A = _mod()
+        width = (1 << 27) // (max(self.T, 1) * self.Hq * self.ps) + 2
+        t = torch.full((len(self.kv), max(width, len(self.table[0]) if self.table else 1)), -7,
+                       dtype=torch.int32)
+        for b, row in enumerate(self.table):
+            t[b, :len(row)] = torch.tensor(row, dtype=torch.int32)
+        self.batch = A.KVBatch(_i32(self.cu), _i32(self.kv), t.cuda(), self.T, 1 << 28)
+
+
+SMALL = ([(test_ragged_chunks, a) for a in LAYOUTS] +
+         [(test_windows, (w, ps)) for w in (1, 2, 16, 63, 64, 65, 130, 5000) for ps in (16, 13)] +
+         [(test_without_the_causal_mask, a) for a in ((64, 16), (128, 24), (80, 7))] +
+         [(test_sinks, ([4, 40, 1, 200, 9],)), (test_rows_without_keys, (False,)),
+          (test_rows_without_keys, (True,)), (test_rows_of_no_sequence_stay, ())] +
+         [(test_cache_layouts, (h, p, [140, 20], [300, 20])) for h in (True, False)
+          for p in (0, 8)] +
+         [(test_values_in_masked_places, (bad, D, ps, ql, kv))
+          for bad in (NAN, math.inf, -math.inf, -3.3895313892515355e38)
+          for D, ps, ql, kv in ((64, 16, [40], [90]), (128, 32, [200], [333]),
+                                (80, 13, [50], [50]))] +
+         [(test_values_behind_the_window, a) for a in ((64, 16, 64, 300, 40),
+                                                       (128, 13, 150, 400, 90))] +
+         [(test_pages_before_the_window_are_not_touched, ()),
+          (test_large_scores_and_lowest_values, ()), (test_offsets_past_32_bits, ()),
+          (test_twice_the_same_bits_and_another_stream, ()),
+          (test_a_captured_chunk_follows_its_lengths, ())] +
+         [(test_references_move_on_the_way, a)
+          for a in ((64, 64, [300], [700]), (128, 24, [200, 40], [900, 300]),
+                    (40, 16, [90], [2000]), (80, 13, [60], [250]))] +
+         [(test_bad_device_data_is_reported, (w,)) for w in ("page", "negative length", "rows")])
+
+
+@pytest.mark.parametrize("i", range(len(SMALL)),
+                         ids=[f"{t.__name__[5:]}-{i}" for i, (t, _) in enumerate(SMALL)])
+def test_small_shapes_on_the_chunk_kernel(i, monkeypatch):
+    test, args = SMALL[i]
+    monkeypatch.setitem(globals(), "Case", WideCase)
+    test(*args)
