@@ -592,14 +592,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
       }
       if constexpr (GATHER) land();
-      if (*abort) {
-        // copies already issued land before the CTA's shared memory goes away
-        const int out = fills < G::slots ? fills : G::slots;
-        volatile int never = 0;
-        for (int i = 0; i < out; ++i) {
-          if (--slot < 0) { slot = G::slots - 1; phase ^= 1u; }
-          mbar_wait_bounded(smem_u32(&sh.kv_full[slot]), phase, &never, a.status);
-        }
+      // Copies already issued land before the CTA's shared memory goes away,
+      // whether or not someone gives up: another role may do so after this warp
+      // has issued its last.
+      const int out = fills < G::slots ? fills : G::slots;
+      volatile int never = 0;
+      for (int i = 0; i < out; ++i) {
+        if (--slot < 0) { slot = G::slots - 1; phase ^= 1u; }
+        mbar_wait_bounded(smem_u32(&sh.kv_full[slot]), phase, &never, a.status);
       }
     } else if (warp == kMmaWarp || (G::split && warp == kScoreWarp)) {
       // ----------------------------------------------------------- products --
