@@ -247,41 +247,59 @@ __device__ __noinline__ void add_by_hand(uint32_t t_p, uint32_t t_o, const uint8
   }
 }
 
-// Waits until a count in shared memory has reached `need`; gives up like
-// mbar_wait_bounded.
-__device__ __forceinline__ bool count_wait_bounded(const int* count, int need,
-                                                   volatile int* abort_flag, int* status) {
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 1; *(const volatile int*)count < need; ++i) {
-    __nanosleep(200);
-    if ((i & 15u) == 0) {
-      if (*abort_flag) return false;
-      if (global_ns() - t0 > (uint64_t)kWaitLimitNs) {
-        *abort_flag = 1;
-        raise_status(status, MOE_ERR_DEVICE_TIMEOUT);
-        return false;
-      }
+// The limit of waits that may last a whole unit, which is as long as the cache:
+// it counts from the last tile whose loads were issued (`issued`, of the CTA), so
+// it ends a wait after kWaitLimitNs in which nothing moved, not one that is long.
+struct UnitLimit {
+  const volatile int* issued;
+  uint64_t t0;
+  int at;
+  __device__ __forceinline__ explicit UnitLimit(const int* issued_)
+      : issued(issued_), t0(global_ns()), at(*issued) {}
+  // to be asked now and then: true to give up
+  __device__ __forceinline__ bool over(volatile int* abort_flag, int* status) {
+    if (*abort_flag) return true;
+    const int now = *issued;
+    if (now != at) {
+      at = now;
+      t0 = global_ns();
+      return false;
     }
+    if (global_ns() - t0 <= (uint64_t)kWaitLimitNs) return false;
+    *abort_flag = 1;
+    raise_status(status, MOE_ERR_DEVICE_TIMEOUT);
+    return true;
+  }
+};
+// Waits until `need` tiles' loads have been issued.
+__device__ __forceinline__ bool issued_wait_bounded(const int* issued, int need,
+                                                    volatile int* abort_flag, int* status) {
+  UnitLimit limit(issued);
+  for (uint32_t i = 1; *limit.issued < need; ++i) {
+    __nanosleep(200);
+    if ((i & 15u) == 0 && limit.over(abort_flag, status)) return false;
   }
   return true;
 }
-
-// mbar_wait_bounded for a warp that has time: it sleeps between its looks, so
-// that it takes no issue slots from the warps it shares a scheduler with.
+// For a warp that has time: it sleeps between its looks, so that it takes no
+// issue slots from the warps it shares a scheduler with.
 __device__ __forceinline__ bool mbar_doze_bounded(uint32_t bar, uint32_t parity, uint32_t ns,
-                                                  volatile int* abort_flag, int* status) {
-  const uint64_t t0 = global_ns();
+                                                  const int* issued, volatile int* abort_flag,
+                                                  int* status) {
+  UnitLimit limit(issued);
   for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
     __nanosleep(ns);
-    if ((i & 15u) == 0) {
-      if (*abort_flag) return false;
-      if (global_ns() - t0 > (uint64_t)kWaitLimitNs) {
-        *abort_flag = 1;
-        raise_status(status, MOE_ERR_DEVICE_TIMEOUT);
-        return false;
-      }
-    }
+    if ((i & 15u) == 0 && limit.over(abort_flag, status)) return false;
   }
+  return true;
+}
+// For a unit to be handed on: the half without rows waits for the next one while
+// the other half works on its own.
+__device__ __noinline__ bool unit_wait_slowly(uint32_t bar, uint32_t parity, const int* issued,
+                                              volatile int* abort_flag, int* status) {
+  UnitLimit limit(issued);
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    if ((i & 63u) == 0 && limit.over(abort_flag, status)) return false;
   return true;
 }
 
@@ -443,17 +461,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   // The warp's next unit is there (false: the end, or given up); it has read it.
-  auto take_unit = [&](auto call, int u, bool& ok) {
-    ok = ok && wait_warp<decltype(call)::value>(smem_u32(&sh.unit_full[u & 3]), (u >> 2) & 1,
-                                                abort, a.status);
+  auto take_unit = [&](int u, bool& ok) {
+    if (!ok) return false;
+    const uint32_t bar = smem_u32(&sh.unit_full[u & 3]), parity = (u >> 2) & 1;
+    if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)))
+      ok = __all_sync(0xFFFFFFFFu,
+                      unit_wait_slowly(bar, parity, &sh.issued, abort, a.status));
     return ok && sh.unit[u & 3].more != 0;
   };
   auto give_unit = [&](int u) {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.unit_empty[u & 3]));
   };
-  using Call = std::true_type;
-  using Inline = std::false_type;
   if (warp < 4) {
     if (warp == kLoadWarp) {
       // -------------------------------------------------------------- loads --
@@ -536,7 +555,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               const uint32_t empty = smem_u32(&sh.kv_empty[slot]);
               if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(empty, phase ^ 1u))) {
                 land();
-                ok = mbar_doze_bounded(empty, phase ^ 1u, 100, abort, a.status);
+                ok = mbar_doze_bounded(empty, phase ^ 1u, 100, &sh.issued, abort, a.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
               }
@@ -569,8 +588,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 __popc(__ballot_sync(0xFFFFFFFFu, mine)) * box_bytes * (uint32_t)G::halves;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
-              ok = ok && mbar_doze_bounded(smem_u32(&sh.kv_empty[slot]), phase ^ 1u, 100, abort,
-                                           a.status);
+              ok = ok && mbar_doze_bounded(smem_u32(&sh.kv_empty[slot]), phase ^ 1u, 100,
+                                           &sh.issued, abort, a.status);
               ok = __all_sync(0xFFFFFFFFu, ok);
               if (!ok) break;
               const uint32_t bar = smem_u32(&sh.kv_full[slot]);
@@ -708,7 +727,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       using H0 = std::integral_constant<int, 0>;
       using H1 = std::integral_constant<int, 1>;
 
-      for (int u = 0; uniform(take_unit(Call{}, u, ok) ? 1u : 0u); ++u) {
+      for (int u = 0; uniform(take_unit(u, ok) ? 1u : 0u); ++u) {
         const Unit wk = sh.unit[u & 3];
         give_unit(u);
         const int nt = (int)uniform(wk.nt);
@@ -780,7 +799,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       int vslot = 1, gone = 0;              // gone: tiles gone by
       uint32_t vphase = 0, units = 0;     // units: two bits a half
       bool ok = true;
-      for (int u = 0; take_unit(Call{}, u, ok); ++u) {
+      for (int u = 0; take_unit(u, ok); ++u) {
         const Unit wk = sh.unit[u & 3];
         give_unit(u);
         const int nt = wk.nt;
@@ -795,7 +814,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           // 0: no unit of the half so far; else 2 + the parity of the last one's end
           const uint32_t had = units >> (2 * half) & 3;
           if (had)
-            ok = ok && mbar_doze_bounded(smem_u32(&sh.q_free[half]), had & 1, 200, abort, a.status);
+            ok = ok && mbar_doze_bounded(smem_u32(&sh.q_free[half]), had & 1, 200, &sh.issued,
+                                         abort, a.status);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           if (lane == 0) sh.q_had[half] = had == 2 ? 3 : 2;
@@ -840,7 +860,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // the tiles between are not waited for, so first the loads must have
             // come to this one: a barrier's parity tells one round of the ring
             // from the next, not from the one after
-            ok = count_wait_bounded(&sh.issued, gone + 1, abort, a.status) &&
+            ok = issued_wait_bounded(&sh.issued, gone + 1, abort, a.status) &&
                  mbar_wait_bounded(smem_u32(&sh.kv_full[vslot]), vphase, abort, a.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             const int k0 = (wk.t0 + j) * kChunkTN;
@@ -889,7 +909,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint32_t mine = 0;                // this half's items so far
     uint32_t seen = 0;
     bool ok = true;
-    for (int u = 0; take_unit(Inline{}, u, ok); ++u) {
+    for (int u = 0; take_unit(u, ok); ++u) {
       const Unit wk = sh.unit[u & 3];
       give_unit(u);
       const Seq s = wk.s;
