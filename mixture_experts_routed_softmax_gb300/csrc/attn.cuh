@@ -77,6 +77,7 @@ struct AttnArgs {
   int whole;             // units are not cut: a CTA takes those that begin in its stretch
   int cost;              // steps a unit takes beside its tiles
   int least;             // a stretch has at least so many steps
+  int piece;             // tiles whose sums one accumulator takes (unit_next)
   struct Cut* cuts;      // [CTAs] the cut in front of each
   float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
   float2* part_ml;       // [2 * CTAs][TM] their (max, sum)
@@ -212,7 +213,8 @@ struct Unit {
   int w, off, stop;    // the unit's steps; this CTA has [off, stop) of them
   int lo, hi;          // the keys of its rows
   int all_lo, all_hi;  // those every row sees
-  int t0, nt;          // tiles: the first, and this CTA's number of them
+  int t0, nt;          // tiles: the first, and this CTA's number of them (of the piece)
+  int begun, rest;     // pieces of the CTA's part: whether one came before, tiles that follow
 
   __device__ __forceinline__ bool whole() const { return off == 0 && stop == w; }
   __device__ __forceinline__ int slot() const { return off > 0 ? 0 : 1; }
@@ -265,12 +267,27 @@ __device__ __forceinline__ void unit_set(const AttnArgs& a, Unit& u) {
   const int rows = u.s.nq * a.G;
   u.all_lo = key_lo(a, u.s, div_group(a, min(u.m * TM + TM, rows) - 1));
   u.all_hi = key_hi(a, u.s, div_group(a, u.m * TM));
-  const int begin = max(u.off - a.cost, 0);
+  const int begin = max(u.off - a.cost, 0), nt = max(u.stop - a.cost, 0) - begin;
   u.t0 = sp.t0 + begin;
-  u.nt = max(u.stop - a.cost, 0) - begin;
+  u.nt = min(nt, a.piece);
+  u.rest = nt - u.nt;
+  u.begun = 0;
 }
+// The next unit, or the next piece of a long one. The matrix units cut what they add
+// to an accumulator at its last place, by up to 2^-23 of the sum each time, and this
+// adds up: a mean of values of one sign came out 0.5% low after 2^16 steps of 16
+// keys in one accumulator, 2.6% after 2^18. So a unit is worked on in pieces of
+// `piece` tiles; a piece's sums go where the CTA's part of the unit would, and the
+// next one's join them in fp32.
 template <int TM, int TN>
 __device__ __forceinline__ void unit_next(const AttnArgs& a, Unit& u) {
+  if (u.rest > 0) {
+    u.t0 += u.nt;
+    u.nt = min(u.rest, a.piece);
+    u.rest -= u.nt;
+    u.begun = 1;
+    return;
+  }
   u.to_end -= u.w;
   u.more = 0;
   if (u.stop < u.w || u.to_end <= 0) return;
@@ -302,6 +319,7 @@ __device__ __noinline__ void unit_first(const AttnArgs& a, const Place& place, i
   Cut c{0, 0, 0, 0, -1, 0, {0, 0}};
   const long long unit0 = pl.x0 - off;
   u.to_end = pl.x1 - unit0;
+  u.rest = 0;
   u.w = u.stop = Tiling<TM, TN>::weight(a, u.s, u.m);
   const bool at_begin = a.whole ? off == 0 : off <= a.cost;
   const bool at_end = a.whole || u.w - off <= u.snap;

@@ -59,6 +59,9 @@ constexpr int kChunkTN = 128;
 constexpr int kChunkThreads = 384;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kHelpWarp = 2, kScoreWarp = 3;
 constexpr float kMoveAt = 65536.f;
+// Tiles whose sums one accumulator takes (unit_next): 65536 keys. Another piece
+// costs what a unit's end and beginning do, some four tiles' work.
+constexpr int kChunkPiece = 512;
 // The least steps of a stretch: a cut costs a part's round trip. 128 tokens over
 // 2500 keys, D = 128: 5 or 6 steps 42 us, 8 46 us, 12 50 us.
 constexpr int kChunkLeast = 6;
@@ -359,6 +362,34 @@ __device__ __forceinline__ void scale_weights(uint32_t t_p, int n, float f) {
     for (int i = 0; i < 16; ++i) w[i] = pack_bf16(bf16_lo(w[i]) * f, bf16_hi(w[i]) * f);
     tmem_st16(t_p + c, w);
   }
+}
+// The sums of a row's pieces before join the row's: O, in tensor memory, and the
+// (reference, sum), which are returned.
+template <int DP>
+__device__ __noinline__ float2 join_before(const AttnArgs& a, uint32_t t_o, int slot, int row,
+                                           float m_ref, float l) {
+  const int64_t pslot = (int64_t)blockIdx.x * 2 + slot;
+  const float2 before = a.part_ml[pslot * kChunkTM + row];
+  const float m = fmaxf(before.x, m_ref), ref = m == neg_inf() ? 0.f : m;
+  const float f = ex2(m_ref - ref), g = ex2(before.x - ref);
+#pragma unroll 1
+  for (int c = 0; c < DP; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(t_o + c, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(
+          a.part_o + part_at<kChunkTM, DP>(pslot, row, (c + i) / 4));
+      o[i] = __float_as_uint(__uint_as_float(o[i]) * f + b.x * g);
+      o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) * f + b.y * g);
+      o[i + 2] = __float_as_uint(__uint_as_float(o[i + 2]) * f + b.z * g);
+      o[i + 3] = __float_as_uint(__uint_as_float(o[i + 3]) * f + b.w * g);
+    }
+    tmem_st16(t_o + c, o);
+  }
+  tmem_st_wait();
+  return make_float2(m, l * f + before.y * g);
 }
 // 64 scores to weights exp2(s * scale - ref), as bf16 pairs; their unrounded sum.
 __device__ __forceinline__ float group_weights(const float* x, float scale, float ref,
@@ -1034,9 +1065,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           ok = wait_warp<false>(smem_u32(&sh.o_done[half][i & 1]), (i >> 1) & 1, abort, a.status);
         if (!ok) break;
         tc_fence_after();
+        if (__builtin_expect(wk.begun, 0)) {
+          const float2 ml = join_before<DP>(a, t_o, wk.slot(), half * 128 + row, m_ref, l);
+          m_ref = ml.x;
+          l = ml.y;
+        }
       }
-      // ---- the unit's rows: final, or this CTA's part ------------------------
-      const bool whole = wk.whole();
+      // ---- the unit's rows: final, or this CTA's part (so far) ---------------
+      const bool whole = wk.whole() && wk.rest == 0;
       RowEnd e{1.f, 0.f};
       if (whole) e = row_end(m_ref, l, a.sinks, head);
       const int64_t pslot = (int64_t)blockIdx.x * 2 + wk.slot();
@@ -1119,6 +1155,7 @@ static cudaError_t launch_chunk(AttnArgs a, const moe_kv_cache& c, void* ws, cud
   if (e != cudaSuccess) return e;
   const int n = num_sms();
   a.least = kChunkLeast;
+  a.piece = kChunkPiece;
   a.cuts = static_cast<Cut*>(ws);
   a.part_ml = reinterpret_cast<float2*>(a.cuts + n);
   a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * kChunkTM);

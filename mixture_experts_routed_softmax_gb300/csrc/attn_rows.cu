@@ -605,6 +605,7 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, int64_t keys, 
                                cudaStream_t s) {
   a.whole = keys <= kWholeTiles * RowsGeo<DP, MB, 4>::TN ? 1 : 0;
   a.least = a.whole ? 1 : kRowsLeast;
+  a.piece = kAttnMaxKeys;
   if constexpr (DP == 64 && MB == 1) {
     if (a.whole && keys <= kWarpKeys && c.page_size % 16 == 0 &&
         (int64_t)a.bt.B * a.Hkv >= 4 * num_sms())

@@ -48,3 +48,67 @@ def test_units_that_take_seconds():
     layer, b = _repeated(H, H, D, ps, pages, [40], n, k, v)
     assert layer.status() == 0
     assert float((b.lse.double() - math.log(n)).abs().max()) <= 2.0 ** -17
+
+
+def _one_page(q, k, v, scale):
+    """Attention of q [nq, G, D] over the one page in 64 bits: out, sum of weights
+    times |values|, log-sum-exp, the largest sum of |terms| of a score."""
+    x, K, V = q.double().flatten(0, 1), k[0, 0].double(), v[0, 0].double()
+    s = x @ K.T * scale
+    lse = torch.logsumexp(s, 1, keepdim=True)
+    p = torch.exp(s - lse)
+    mag = (x.abs() @ K.abs().T * scale).amax(1, keepdim=True)
+    return [t.view(*q.shape[:2], -1) for t in (p @ V, p @ V.abs(), lse, mag)]
+
+
+# (new tokens, heads of the one key head): rows a unit. Enough sequences that units
+# are not cut into many parts.
+CHUNK = [(16, 16), (8, 16), (45, 5)]
+LONG = [(nq, G, 304, D, ps, 1 << 22) for nq, G in CHUNK for D in (64, 128)
+        for ps in (65536,)] + [(16, 16, 152, D, 65535, 1 << 21) for D in (40, 128)]
+
+
+@pytest.mark.parametrize("grow", [0.0, 30.0])
+@pytest.mark.parametrize("nq,G,B,D,ps,n", LONG)
+def test_long_sums(nq, G, B, D, ps, n, grow):
+    """Values of one sign, and weights that are all alike or grow along the page by
+    e^30, so that references move between and inside its 512 tiles.
+
+    The matrix unit cuts the 16 products it adds, and the sum they join, at the
+    sum's last place: 17 times 2^-23 of it in each 16-key step at most. An
+    accumulator takes 65536 keys, 4096 steps, and over these is half of its end in
+    the mean: 17 2^-23 2^11. Sums in fp32 (up to 1024 groups of 32 terms, joined up
+    to 64 times), half an ulp each: below 2^-13. Weights are rounded to bf16 up to
+    twice, and a score is off by e at most (tests/attention_ref.py)."""
+    u = torch.finfo(BF16).eps / 2
+    g = torch.Generator(device="cuda").manual_seed(nq * G + D)
+    k = torch.zeros(1, 1, ps, D, dtype=BF16, device="cuda")
+    v = (1.0 + torch.rand(1, 1, ps, D, generator=g, device="cuda")).to(BF16)
+    q = torch.randn(nq, G, D, generator=g, device="cuda").to(BF16)
+    scale = D ** -0.5
+    if grow:
+        q[..., 0] = 2.0
+        k[0, 0] = (0.3 * torch.randn(ps, D, generator=g, device="cuda")).to(BF16)
+        k[0, 0, :, 0] = torch.linspace(-grow / 2 / scale, 0.0, ps, device="cuda").to(BF16)
+    pages = n // ps
+    A = _mod()
+    layer = A.PagedAttention(k, v, G, causal=False)
+    T = B * nq
+    batch = A.KVBatch((torch.arange(B + 1, device="cuda") * nq).int(),
+                      torch.full((B,), pages * ps, dtype=torch.int32, device="cuda"),
+                      torch.zeros(B, pages, dtype=torch.int32, device="cuda"), T, nq)
+    b = layer.buffers(T, lse=True)
+    layer.attend(q.repeat(B, 1, 1), batch, b)
+    assert layer.status() == 0
+    out, a, lse, mag = _one_page(q, k, v, scale)
+    e = (D + 16) * 2.0 ** -23 * mag + 2.0 ** -20
+    sums = 2.0 ** -13
+    tol = u * out.abs() + (2 * u + 2 * e + 17 * 2.0 ** -12 + sums) * (1 + u) * a
+    if not grow:                     # weights of one: nothing is rounded
+        tol = u * out.abs() + (17 * 2.0 ** -12 + sums) * (1 + u) * a
+    err = (b.out.view(B, nq, G, D).double() - out).abs()
+    assert float((err / tol).max()) <= 1.0, float((err / out).max())
+    lse = lse[..., 0] + math.log(pages)
+    err = (b.lse.view(B, nq, G).double() - lse).abs()
+    ltol = e[..., 0] + sums + 2.0 ** -20 * (1 + lse.abs())
+    assert float((err / ltol).max()) <= 1.0, float(err.max())
