@@ -31,9 +31,14 @@
 #include "internal.h"
 #include "tmap.h"
 
+#include <algorithm>
+
 namespace moe {
 
 constexpr float kRowsRescaleAt = 16.f;
+// Keys whose sums a warp's accumulator takes (unit_next): four times as many of a
+// unit's where four warps share it.
+constexpr int kRowsPiece = 65536;
 
 constexpr int kRowsThreads = 128;
 
@@ -119,6 +124,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
   __shared__ Place pl;
   __shared__ Unit units[G::groups][2];
   __shared__ float2 s_mls[4][TM];
+  __shared__ float2 s_before[G::groups][2][TM];    // of the pieces before, by turns
   __shared__ uint64_t full[4][S];
   __shared__ int s_abort;
   const int lane = threadIdx.x & 31, bwarp = threadIdx.x >> 5;
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
     for (int j = 0; j < S; ++j) spot[j] = lookup(w, j);
     qp = load_q(w);
   };
-  int cur = 0;
+  int cur = 0, turn = 0;
   if (un[0].more) unit_loads(un[0]);
   while (un[cur].more) {
     const Unit wk = un[cur];
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
               make_float2(o[mb][n][2 * e], o[mb][n][2 * e + 1]);
       }
     group_sync();
-    const bool whole = wk.whole();
+    const bool whole = wk.whole() && wk.rest == 0;
     const int64_t pslot = ((int64_t)blockIdx.x * G::groups + group) * 2 + wk.slot();
     for (int i = tid; i < nrows * (DP / 4); i += NT) {
       const int r = i / (DP / 4), c4 = i - r * (DP / 4);
@@ -510,6 +516,15 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
         l += f * s_ml[w][r].y;
         t.x += f * v.x; t.y += f * v.y; t.z += f * v.z; t.w += f * v.w;
       }
+      float4* const part = reinterpret_cast<float4*>(a.part_o + part_at<TM, DP>(pslot, r, c4));
+      if (__builtin_expect(wk.begun, 0)) {
+        Part p{m, l, t};
+        const float2 before = s_before[group][turn ^ 1][r];
+        join_part(p, before.x, before.y, *part);
+        m = p.m;
+        l = p.l;
+        t = p.o;
+      }
       if (whole) {
         const int tok = div_group(a, r0 + r), head = h * a.G + (r0 + r) - tok * a.G;
         const RowEnd e = row_end(m, l, a.sinks, head);
@@ -521,10 +536,12 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
         }
         if (a.lse && c4 == 0) a.lse[(int64_t)(s.q0 + tok) * a.Hq + head] = e.lse;
       } else {
-        *reinterpret_cast<float4*>(a.part_o + part_at<TM, DP>(pslot, r, c4)) = t;
-        if (c4 == 0) a.part_ml[pslot * TM + r] = make_float2(m, l);
+        *part = t;
+        if (c4 == 0)
+          (wk.rest > 0 ? s_before[group][turn][r] : a.part_ml[pslot * TM + r]) = make_float2(m, l);
       }
     }
+    turn ^= 1;
     if constexpr (PAGE16) fence_async_smem();
     group_sync();          // the merge buffer is the ring again
   }
@@ -587,7 +604,8 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, void* ws, cuda
   const int n = rows_ctas<DP, MB, W>();
   if (!a.whole) a.cuts = static_cast<Cut*>(ws);
   a.part_ml = reinterpret_cast<float2*>(static_cast<Cut*>(ws) + n);
-  a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * G::TM);
+  a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)2 * n * G::groups * G::TM);
+  a.piece = kRowsPiece / G::chunk;
   timer_before(MOE_KERNEL_ATTN, s);
   e = launch_pdl(true, kern, dim3(n), dim3(kRowsThreads), G::smem, s, a, mk, mv, box);
   timer_after(MOE_KERNEL_ATTN, s);
@@ -605,7 +623,6 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, int64_t keys, 
                                cudaStream_t s) {
   a.whole = keys <= kWholeTiles * RowsGeo<DP, MB, 4>::TN ? 1 : 0;
   a.least = a.whole ? 1 : kRowsLeast;
-  a.piece = kAttnMaxKeys;
   if constexpr (DP == 64 && MB == 1) {
     if (a.whole && keys <= kWarpKeys && c.page_size % 16 == 0 &&
         (int64_t)a.bt.B * a.Hkv >= 4 * num_sms())
@@ -615,18 +632,17 @@ static cudaError_t launch_rows(AttnArgs a, const moe_kv_cache& c, int64_t keys, 
                                : launch_rows<DP, MB, 4, false>(a, c, ws, s);
 }
 
-template <int DP, int MB>
+template <int DP, int MB, int W>
 static size_t rows_ws() {
-  return (size_t)rows_ctas<DP, MB, 4>() *
-         (sizeof(Cut) + 2 * RowsGeo<DP, MB, 4>::TM * (DP + 2) * sizeof(float));
+  using G = RowsGeo<DP, MB, W>;
+  return (size_t)rows_ctas<DP, MB, W>() *
+         (sizeof(Cut) + 2 * G::groups * G::TM * (DP + 2) * sizeof(float));
 }
 
 size_t attn_ws_bytes(int D) {
-  const size_t a = D <= 64 ? rows_ws<64, 1>() : rows_ws<128, 1>();
-  const size_t b = D <= 64 ? rows_ws<64, 2>() : rows_ws<128, 2>();
   const size_t t = attn_chunk_ws_bytes(D);
-  const size_t ab = a > b ? a : b;
-  return t > ab ? t : ab;
+  if (D > 64) return std::max({rows_ws<128, 1, 4>(), rows_ws<128, 2, 4>(), t});
+  return std::max({rows_ws<64, 1, 4>(), rows_ws<64, 2, 4>(), rows_ws<64, 1, 1>(), t});
 }
 
 cudaError_t launch_attn(const moe_kv_cache& c, const moe_kv_batch& b, const moe_bf16* q,
