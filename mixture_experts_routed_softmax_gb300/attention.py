@@ -238,8 +238,11 @@ class PagedAttention:
         out = b.out if out is None else out
         T, Hq, D = batch.T, self.Hq, self.D
         lse, ws = b.lse, b.ws
-        if lse is not None and (lse.shape != (T, Hq) or not lse.is_contiguous()):
-            raise ValueError(f"lse: shape {tuple(lse.shape)}, expected {(T, Hq)}")
+        if lse is not None and (lse.dtype is not torch.float32 or not lse.is_cuda
+                                or lse.shape != (T, Hq) or not lse.is_contiguous()):
+            raise ValueError(f"lse: a packed fp32 CUDA tensor of shape {(T, Hq)} is needed")
+        if ws.dtype is not torch.uint8 or not ws.is_cuda or not ws.is_contiguous():
+            raise ValueError("ws: a packed uint8 CUDA tensor is needed (buffers() makes one)")
         _check("moe_attn_paged", self._call_attend(
             self._ref, batch._ref, q.data_ptr(), _view("q", q, T, Hq, D), Hq, self.scale,
             self.causal, self.window, self._sinks, out.data_ptr(), _view("out", out, T, Hq, D),

@@ -1,0 +1,113 @@
+"""What the Python layer of the attention operators refuses before any call, with
+stand-ins for CUDA tensors and for the library: nothing here touches a device."""
+import types
+
+import pytest
+import torch
+
+from mixture_experts_routed_softmax_gb300 import attention as A
+
+BF16 = torch.bfloat16
+
+
+class Tensor:
+    """A CUDA tensor as far as the checks look at one."""
+
+    def __init__(self, shape, dtype=BF16, strides=None, index=0):
+        self.shape, self.dtype = torch.Size(shape), dtype
+        self.is_cuda = index >= 0
+        self.device = torch.device("cuda", index) if self.is_cuda else torch.device("cpu")
+        if strides is None:
+            strides, n = [], 1
+            for d in reversed(shape):
+                strides.insert(0, n)
+                n *= d
+        self.strides = tuple(strides)
+
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return self.strides if i is None else self.strides[i]
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return self.strides == Tensor(self.shape).strides
+
+    def contiguous(self):
+        return self
+
+    def data_ptr(self):
+        return 0x1000
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The calls that reached the library."""
+    seen = []
+
+    def entry(name, result=0):
+        return lambda *a: seen.append((name, a)) or result
+
+    lib = types.SimpleNamespace(
+        moe_rope=entry("rope"), moe_kv_append=entry("append"), moe_attn_paged=entry("attend"),
+        moe_attn_paged_workspace_size=lambda *a: 512, moe_status=entry("status"))
+    monkeypatch.setattr(A._lib, "load", lambda: lib)
+    monkeypatch.setattr(A, "_current_stream", lambda index: 0)
+    return seen
+
+
+I32 = torch.int32
+
+
+def _layer(index=0, **kw):
+    c = Tensor((9, 2, 16, 64), index=index)
+    return A.PagedAttention(c, Tensor((9, 2, 16, 64), index=index), 8, **kw)
+
+
+def _batch(T=3, B=2, index=0):
+    return A.KVBatch(Tensor((B + 1,), I32, index=index), Tensor((B,), I32, index=index),
+                     Tensor((B, 4), I32, index=index), T)
+
+
+def _buffers(T=3, index=0, **kw):
+    b = dict(T=T, q=Tensor((T, 8, 64), index=index), out=Tensor((T, 8, 64), index=index),
+             lse=Tensor((T, 8), torch.float32, index=index),
+             ws=Tensor((512,), torch.uint8, index=index))
+    b.update(kw)
+    return A.AttnBuffers(**b)
+
+
+def test_the_stand_ins_pass(calls):
+    layer, q, k = _layer(), Tensor((3, 8, 64)), Tensor((3, 2, 64))
+    layer.append(k, k, _batch(), q=q, q_out=q)
+    layer.attend(q, _batch(), _buffers())
+    layer.attend(q, _batch(), _buffers(lse=None))
+    assert [c[0] for c in calls] == ["append", "attend", "attend"]
+    assert calls[1][1][13] == 512
+
+
+@pytest.mark.parametrize("lse", [
+    Tensor((3, 8), BF16), Tensor((3, 8), torch.float64), Tensor((3, 8), torch.float32, index=-1),
+    Tensor((3, 8), torch.float32, (16, 1)), Tensor((2, 8), torch.float32)],
+    ids=["bf16", "fp64", "cpu", "strided", "short"])
+def test_log_sum_exps_of_another_type_are_refused(calls, lse):
+    """The kernel writes four bytes an element, packed."""
+    with pytest.raises(ValueError, match="lse"):
+        _layer().attend(Tensor((3, 8, 64)), _batch(), _buffers(lse=lse))
+    assert not calls
+
+
+@pytest.mark.parametrize("ws", [
+    Tensor((512,), torch.float32), Tensor((512,), torch.uint8, index=-1),
+    Tensor((512,), torch.uint8, (2,))], ids=["fp32", "cpu", "strided"])
+def test_workspaces_of_another_type_are_refused(calls, ws):
+    """Its size in bytes is taken from its elements."""
+    with pytest.raises(ValueError, match="ws"):
+        _layer().attend(Tensor((3, 8, 64)), _batch(), _buffers(ws=ws))
+    assert not calls
