@@ -377,6 +377,8 @@ size_t moe_decode_workspace_size(int64_t T, int d, int f, int E, int k);
  * Conventions of these four calls, beside those at the top:
  *   - The structs are passed as HOST pointers; the arrays inside are device
  *     arrays. Nothing of a struct is kept after the call returns.
+ *   - Everything runs on the current device: the arrays, `stream` and the
+ *     workspace are its.
  *   - q, k, v, out are [T, H, D] views: heads packed (D elements apart), tokens
  *     a stride of their own apart (in elements, a multiple of 8, >= H*D), so
  *     slices of one projection's output need no copy.

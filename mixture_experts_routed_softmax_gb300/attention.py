@@ -3,7 +3,7 @@ positions (moe_rope), the append of new keys and values to a paged cache
 (moe_kv_append) and the attention of new tokens over it (moe_attn_paged).
 
 PyTorch supplies device memory and the stream; every step runs in the
-library's kernels. A serving step is ``PagedAttention.forward`` (append, then
+library's kernels, on the current device, which has to be the tensors'. A serving step is ``PagedAttention.forward`` (append, then
 attend); ``Rope.apply`` rotates without a cache, and with ``transpose=True``
 takes gradients back through the rotation in training.
 """
@@ -21,18 +21,32 @@ from . import _lib
 BF16 = torch.bfloat16
 _ref = _lib.ctypes.addressof
 _current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _view(name: str, t: torch.Tensor, T: int, H: int, D: int) -> int:
-    """Check a [T, H, D] bf16 view with packed heads; its token stride. (These
-    checks are a good part of a one-token call's host time: the usual case,
-    tokens of packed heads, is looked at first.)"""
-    if t.dtype is not BF16 or not t.is_cuda:
-        raise ValueError(f"{name}: a bf16 CUDA tensor is needed")
+def _stream(dev: int, stream) -> int:
+    """The raw stream of a call on tensors of device ``dev``. The library launches
+    on the current device, so that has to be theirs."""
+    if _current_device() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is "
+                         f"cuda:{_current_device()}")
+    if stream is None:
+        return _current_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream: one of cuda:{dev} is needed, not {stream.device}")
+    return stream.cuda_stream
+
+
+def _view(name: str, t: torch.Tensor, T: int, H: int, D: int, dev: int) -> int:
+    """Check a [T, H, D] bf16 view with packed heads on device ``dev``; its token
+    stride. (These checks are a good part of a one-token call's host time: the
+    usual case, tokens of packed heads, is looked at first.)"""
+    if t.dtype is not BF16 or t.get_device() != dev:
+        raise ValueError(f"{name}: a bf16 tensor on cuda:{dev} is needed")
     if t.shape != (T, H, D):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, H, D)}")
     st, sh, sd = t.stride()
@@ -101,8 +115,10 @@ class Rope:
     def _pos(self, pos: torch.Tensor, T: int) -> torch.Tensor:
         if pos.dim() == 1:
             pos = pos[None]
-        if pos.dtype is not torch.int32 or not pos.is_cuda or pos.shape != (self.n_axes, T):
-            raise ValueError(f"pos: an int32 CUDA tensor of shape {(self.n_axes, T)} is needed")
+        if (pos.dtype is not torch.int32 or pos.get_device() != self._dev
+                or pos.shape != (self.n_axes, T)):
+            raise ValueError(f"pos: an int32 tensor of shape {(self.n_axes, T)} on "
+                             f"cuda:{self._dev} is needed")
         if not pos.is_contiguous():
             raise ValueError("pos: its rows must be packed")
         return pos
@@ -111,20 +127,19 @@ class Rope:
         """q_out = R q (and k_out = R k), [T, H, D] views; pos [n_axes, T] (or [T])
         int32. transpose: R^T, the gradient's way back. In place is fine."""
         T, H, D = q.shape
-        pos = self._pos(pos, T)
+        pos, dev = self._pos(pos, T), self._dev
         Hk = 0 if k is None else int(k.shape[1])
         if (k is None) != (k_out is None):
             raise ValueError("k and k_out go together")
         ks = kos = 0
         kp = kop = None
         if k is not None:
-            ks, kos = _view("k", k, T, Hk, D), _view("k_out", k_out, T, Hk, D)
+            ks, kos = _view("k", k, T, Hk, D, dev), _view("k_out", k_out, T, Hk, D, dev)
             kp, kop = k.data_ptr(), k_out.data_ptr()
         _check("moe_rope", self._call(
             self._ref, pos.data_ptr(), T, D, int(transpose), q.data_ptr(),
-            _view("q", q, T, H, D), H, q_out.data_ptr(), _view("q_out", q_out, T, H, D),
-            kp, ks, Hk, kop, kos,
-            _current_stream(self._dev) if stream is None else stream.cuda_stream))
+            _view("q", q, T, H, D, dev), H, q_out.data_ptr(),
+            _view("q_out", q_out, T, H, D, dev), kp, ks, Hk, kop, kos, _stream(dev, stream)))
         return q_out
 
 
@@ -138,6 +153,9 @@ class KVBatch:
         self.cu_q = _int32("cu_q", cu_q, (B + 1,))
         self.kv_len = _int32("kv_len", kv_len, (B,))
         self.page_table = _int32("page_table", page_table, (B, page_table.shape[1]))
+        self._dev = cu_q.get_device()
+        if kv_len.get_device() != self._dev or page_table.get_device() != self._dev:
+            raise ValueError("cu_q, kv_len and page_table are on different devices")
         self.T, self.B = int(T), B
         pages = int(self.page_table.shape[1])
         stride = self.page_table.stride(0) if B > 1 else pages
@@ -176,6 +194,10 @@ class PagedAttention:
                 raise ValueError(f"{name}: a bf16 CUDA tensor of 4 axes with D packed is needed")
         if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
             raise ValueError("k_cache and v_cache differ in shape or strides")
+        for name, t in (("v_cache", v_cache), ("sinks", sinks),
+                        ("rope", None if rope is None else rope.turns)):
+            if t is not None and t.device != k_cache.device:
+                raise ValueError(f"{name} is on {t.device}, k_cache on {k_cache.device}")
         self.k_cache, self.v_cache = k_cache, v_cache
         ha, sa = (1, 2) if heads_first else (2, 1)
         self.n_pages, self.Hkv = int(k_cache.shape[0]), int(k_cache.shape[ha])
@@ -200,6 +222,7 @@ class PagedAttention:
         self._dev = self.device.index
 
     def buffers(self, T: int, lse: bool = False) -> AttnBuffers:
+        _stream(self._dev, None)       # the workspace's size is the current device's
         kw = dict(device=self.device)
         ws = int(self.lib.moe_attn_paged_workspace_size(self.Hq, self.Hkv, self.D))
         return AttnBuffers(
@@ -212,7 +235,9 @@ class PagedAttention:
         """The new tokens' keys (rotated) and values into the cache; q rotated
         into q_out when given. pos [n_axes, T] int32, or None: each token's
         position in its sequence."""
-        T, Hkv, Hq, D = batch.T, self.Hkv, self.Hq, self.D
+        T, Hkv, Hq, D, dev = batch.T, self.Hkv, self.Hq, self.D, self._dev
+        if batch._dev != dev:
+            raise ValueError(f"the batch is on cuda:{batch._dev}, the cache on cuda:{dev}")
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out go together")
         if pos is not None:
@@ -222,32 +247,36 @@ class PagedAttention:
         qs = qos = 0
         qp = qop = pp = None
         if q is not None:
-            qs, qos = _view("q", q, T, Hq, D), _view("q_out", q_out, T, Hq, D)
+            qs, qos = _view("q", q, T, Hq, D, dev), _view("q_out", q_out, T, Hq, D, dev)
             qp, qop = q.data_ptr(), q_out.data_ptr()
         if pos is not None:
             pp = pos.data_ptr()
         _check("moe_kv_append", self._call_append(
-            self._ref, batch._ref, self._rope, pp, k.data_ptr(), _view("k", k, T, Hkv, D),
-            v.data_ptr(), _view("v", v, T, Hkv, D), qp, qs, Hq, qop, qos,
-            _current_stream(self._dev) if stream is None else stream.cuda_stream))
+            self._ref, batch._ref, self._rope, pp, k.data_ptr(), _view("k", k, T, Hkv, D, dev),
+            v.data_ptr(), _view("v", v, T, Hkv, D, dev), qp, qs, Hq, qop, qos,
+            _stream(dev, stream)))
         return q_out
 
     def attend(self, q, batch: KVBatch, b: AttnBuffers, out=None, stream=None):
         """Attention of q [T, Hq, D] over the cache into ``out`` (default b.out);
         b.lse, when there, takes the log-sum-exp of every row."""
         out = b.out if out is None else out
-        T, Hq, D = batch.T, self.Hq, self.D
+        T, Hq, D, dev = batch.T, self.Hq, self.D, self._dev
+        if batch._dev != dev:
+            raise ValueError(f"the batch is on cuda:{batch._dev}, the cache on cuda:{dev}")
         lse, ws = b.lse, b.ws
-        if lse is not None and (lse.dtype is not torch.float32 or not lse.is_cuda
+        if lse is not None and (lse.dtype is not torch.float32 or lse.get_device() != dev
                                 or lse.shape != (T, Hq) or not lse.is_contiguous()):
-            raise ValueError(f"lse: a packed fp32 CUDA tensor of shape {(T, Hq)} is needed")
-        if ws.dtype is not torch.uint8 or not ws.is_cuda or not ws.is_contiguous():
-            raise ValueError("ws: a packed uint8 CUDA tensor is needed (buffers() makes one)")
+            raise ValueError(f"lse: a packed fp32 tensor of shape {(T, Hq)} on cuda:{dev} is "
+                             "needed")
+        if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: a packed uint8 tensor on cuda:{dev} is needed (buffers() "
+                             "makes one)")
         _check("moe_attn_paged", self._call_attend(
-            self._ref, batch._ref, q.data_ptr(), _view("q", q, T, Hq, D), Hq, self.scale,
-            self.causal, self.window, self._sinks, out.data_ptr(), _view("out", out, T, Hq, D),
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-            _current_stream(self._dev) if stream is None else stream.cuda_stream))
+            self._ref, batch._ref, q.data_ptr(), _view("q", q, T, Hq, D, dev), Hq, self.scale,
+            self.causal, self.window, self._sinks, out.data_ptr(),
+            _view("out", out, T, Hq, D, dev), None if lse is None else lse.data_ptr(),
+            ws.data_ptr(), ws.numel(), _stream(dev, stream)))
         return out
 
     def forward(self, q, k, v, batch: KVBatch, b: AttnBuffers, pos=None, stream=None):
@@ -257,5 +286,4 @@ class PagedAttention:
 
     def status(self, stream=None) -> int:
         """Synchronise and read (and clear) the device status word."""
-        return int(self.lib.moe_status(
-            _current_stream(self._dev) if stream is None else stream.cuda_stream))
+        return int(self.lib.moe_status(_stream(self._dev, stream)))

@@ -59,6 +59,7 @@ def calls(monkeypatch):
         moe_attn_paged_workspace_size=lambda *a: 512, moe_status=entry("status"))
     monkeypatch.setattr(A._lib, "load", lambda: lib)
     monkeypatch.setattr(A, "_current_stream", lambda index: 0)
+    monkeypatch.setattr(A, "_current_device", lambda: 0)
     return seen
 
 
@@ -111,3 +112,78 @@ def test_workspaces_of_another_type_are_refused(calls, ws):
     with pytest.raises(ValueError, match="ws"):
         _layer().attend(Tensor((3, 8, 64)), _batch(), _buffers(ws=ws))
     assert not calls
+
+
+def test_another_current_device_is_refused(calls, monkeypatch):
+    """The library launches on the current device."""
+    layer, batch, q, k = _layer(), _batch(), Tensor((3, 8, 64)), Tensor((3, 2, 64))
+    rope = _rope()
+    monkeypatch.setattr(A, "_current_device", lambda: 1)
+    for call in (lambda: layer.attend(q, batch, _buffers()),
+                 lambda: layer.append(k, k, batch), lambda: layer.buffers(3),
+                 lambda: layer.status(), lambda: rope.apply(q, Tensor((1, 3), I32), q)):
+        with pytest.raises(ValueError, match="current device is cuda:1"):
+            call()
+    assert not calls
+
+
+def _rope(index=0):
+    rope = A.Rope([1.0, 0.5], device="cpu")
+    rope.turns, rope._dev = Tensor((2,), torch.int64, index=index), index
+    return rope
+
+
+@pytest.mark.parametrize("what", ["q", "out", "lse", "ws", "batch", "stream"])
+def test_attention_over_two_devices_is_refused(calls, what):
+    q, b = Tensor((3, 8, 64), index=int(what == "q")), _buffers()
+    if what in ("out", "lse", "ws"):
+        t = getattr(b, what)
+        setattr(b, what, Tensor(t.shape, t.dtype, index=1))
+    stream = None
+    if what == "stream":
+        stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=64)
+    with pytest.raises(ValueError, match=what):
+        _layer().attend(q, _batch(index=int(what == "batch")), b, stream=stream)
+    assert not calls
+
+
+@pytest.mark.parametrize("what", ["k", "v", "q", "q_out", "pos", "batch"])
+def test_an_append_over_two_devices_is_refused(calls, what):
+    t = {n: Tensor(s, index=int(what == n)) for n, s in
+         (("k", (3, 2, 64)), ("v", (3, 2, 64)), ("q", (3, 8, 64)), ("q_out", (3, 8, 64)))}
+    pos = Tensor((1, 3), I32, index=int(what == "pos"))
+    with pytest.raises(ValueError, match=what):
+        _layer(rope=_rope()).append(t["k"], t["v"], _batch(index=int(what == "batch")), q=t["q"],
+                                    q_out=t["q_out"], pos=pos)
+    assert not calls
+
+
+@pytest.mark.parametrize("what", ["q", "q_out", "k", "k_out", "pos"])
+def test_a_rotation_over_two_devices_is_refused(calls, what):
+    t = {n: Tensor((3, 2, 64), index=int(what == n)) for n in ("q", "q_out", "k", "k_out")}
+    with pytest.raises(ValueError, match=what):
+        _rope().apply(t["q"], Tensor((1, 3), I32, index=int(what == "pos")), t["q_out"], k=t["k"],
+                      k_out=t["k_out"])
+    assert not calls
+
+
+def test_layers_and_batches_over_two_devices_are_refused(calls):
+    c, far = Tensor((9, 2, 16, 64)), Tensor((9, 2, 16, 64), index=1)
+    for args, kw in (((c, far, 8), {}), ((c, c, 8), {"rope": _rope(1)}),
+                     ((c, c, 8), {"sinks": Tensor((8,), torch.float32, index=1)})):
+        with pytest.raises(ValueError, match="cuda:1"):
+            A.PagedAttention(*args, **kw)
+    for i in range(3):
+        at = [int(i == j) for j in range(3)]
+        with pytest.raises(ValueError, match="different devices"):
+            A.KVBatch(Tensor((3,), I32, index=at[0]), Tensor((2,), I32, index=at[1]),
+                      Tensor((2, 4), I32, index=at[2]), 3)
+
+
+def test_another_device_works_where_it_is_the_current_one(calls, monkeypatch):
+    monkeypatch.setattr(A, "_current_device", lambda: 1)
+    layer, batch = _layer(1, rope=_rope(1)), _batch(index=1)
+    q, k = Tensor((3, 8, 64), index=1), Tensor((3, 2, 64), index=1)
+    layer.append(k, k, batch, q=q, q_out=q, pos=Tensor((1, 3), I32, index=1))
+    layer.attend(q, batch, _buffers(index=1))
+    assert [c[0] for c in calls] == ["append", "attend"]
