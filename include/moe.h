@@ -408,10 +408,11 @@ typedef struct {
  * cu_q[b] .. cu_q[b+1] - 1 of the [T, ...] arrays and the last ones of its
  * kv_len[b] tokens in the cache (so its token i sits at cache position
  * kv_len[b] - n_q + i); position c lies in page page_table[b * table_stride +
- * c / page_size], slot c % page_size. Sequences may be empty; rows at or past
- * cu_q[B] belong to none. Table entries past a sequence's last page are not
- * read. max_q: the largest number of new tokens of a sequence, a hint the
- * kernel is chosen by; a wrong one costs time only. */
+ * c / page_size], slot c % page_size. Sequences may be empty, and there may be
+ * none (B = 0; the arrays may be NULL); rows at or past cu_q[B] belong to
+ * none. Table entries past a sequence's last page are not read. max_q: the
+ * largest number of new tokens of a sequence, a hint the kernel is chosen by; a
+ * wrong one costs time only. */
 typedef struct {
   const int32_t* cu_q;        /* [B + 1], ascending, cu_q[0] = 0 */
   const int32_t* kv_len;      /* [B], new tokens included */

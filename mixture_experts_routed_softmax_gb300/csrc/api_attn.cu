@@ -87,7 +87,6 @@ int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const mo
   if (!rc) rc = check_tokens(batch->T, (int64_t)cache->Hkv + (q ? Hq : 0));
   if (rc) return rc;
   if (batch->T == 0) return MOE_OK;
-  if (batch->B == 0) return MOE_ERR_ARG;
   rc = check_view(k, k_stride, cache->Hkv, cache->D);
   if (!rc) rc = check_view(v, v_stride, cache->Hkv, cache->D);
   if (!rc && q) rc = check_view(q, q_stride, Hq, cache->D);
