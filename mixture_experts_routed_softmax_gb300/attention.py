@@ -28,6 +28,14 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _c_int(name: str, v) -> int:
+    """A size that means the same from 2^31 - 1 on, for a C int (ctypes would take
+    its low 32 bits)."""
+    if int(v) < 0:
+        raise ValueError(f"{name}: {v} is negative")
+    return min(int(v), 2 ** 31 - 1)
+
+
 def _stream(dev: int, stream) -> int:
     """The raw stream of a call on tensors of device ``dev``. The library launches
     on the current device, so that has to be theirs."""
@@ -160,7 +168,8 @@ class KVBatch:
         pages = int(self.page_table.shape[1])
         stride = self.page_table.stride(0) if B > 1 else pages
         self.args = _lib.KVBatchArgs(_p(self.cu_q), _p(self.kv_len), _p(self.page_table), stride,
-                                     self.T, B, pages, self.T if max_q is None else int(max_q))
+                                     self.T, B, pages,
+                                     _c_int("max_q", self.T if max_q is None else max_q))
         self._ref = _ref(self.args)
 
 
@@ -209,7 +218,7 @@ class PagedAttention:
                                   or sinks.device.type != "cuda"):
             raise ValueError(f"sinks: fp32 [{self.Hq}] on the device is needed")
         self.sinks = None if sinks is None else sinks.contiguous()
-        self.rope, self.causal, self.window = rope, bool(causal), int(window)
+        self.rope, self.causal, self.window = rope, bool(causal), _c_int("window", window)
         self.scale = 1.0 / math.sqrt(self.D) if scale is None else float(scale)
         self.device = k_cache.device
         st = k_cache.stride()

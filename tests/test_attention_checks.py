@@ -187,3 +187,20 @@ def test_another_device_works_where_it_is_the_current_one(calls, monkeypatch):
     layer.append(k, k, batch, q=q, q_out=q, pos=Tensor((1, 3), I32, index=1))
     layer.attend(q, batch, _buffers(index=1))
     assert [c[0] for c in calls] == ["append", "attend"]
+
+
+@pytest.mark.parametrize("v", [2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1])
+def test_windows_and_hints_past_a_c_int(calls, v):
+    """Not their low 32 bits: a window of 2^32 + 5 keys is not one of 5."""
+    _layer(window=v).attend(Tensor((3, 8, 64)), _batch(), _buffers())
+    name, args = calls.pop()
+    assert name == "attend" and args[7] == 2 ** 31 - 1
+    batch = A.KVBatch(Tensor((3,), I32), Tensor((2,), I32), Tensor((2, 4), I32), 3, max_q=v)
+    assert batch.args.max_q == 2 ** 31 - 1
+
+
+def test_negative_windows_and_hints_are_refused(calls):
+    with pytest.raises(ValueError, match="window"):
+        _layer(window=-1)
+    with pytest.raises(ValueError, match="max_q"):
+        A.KVBatch(Tensor((3,), I32), Tensor((2,), I32), Tensor((2, 4), I32), 3, max_q=-1)
