@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import attention_ref as R
-from test_gpu_attention import _i32, _mod, _rot, _same
+from test_gpu_attention import Case, _i32, _mod, _rot, _same
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -33,3 +33,21 @@ def test_rows_of_a_batch_without_sequences(positions):
     _same(b.q, ref, tol, "q")
     assert torch.equal(cache, before)
     assert bool((b.out == 7).all()) and bool((b.lse == 7).all())
+
+
+@pytest.mark.parametrize("window", [0, 800])
+@pytest.mark.parametrize("ps", [16, 13])
+@pytest.mark.parametrize("alone", [True, False])
+def test_chunks_among_more_sequences_than_threads(alone, ps, window):
+    """600 sequences, most of them empty or single tokens, chunks of several row tiles
+    in front of and behind the 384th (a block looks at so many at a time). `alone`: the
+    hint makes one kernel take all of them, else each takes its own."""
+    B, Hq, Hkv = 600, 8, 1
+    ql = [1 if i % 6 == 5 else 0 for i in range(B)]
+    for i, n in {3: 650, 200: 431, 383: 380, 384: 333, 385: 64, 520: 512, 598: 389}.items():
+        ql[i] = n
+    ql[100] += 5 * B - sum(ql)             # on average five: 40 rows of a key head
+    assert 0 < ql[100] < 200
+    kv = [max(n, 1) + (i * 37) % 90 if n < 9 else n + (i * 53) % 400 for i, n in enumerate(ql)]
+    c = Case(Hq, Hkv, 64, ps, ql, kv, seed=40)
+    c.check(max_q=5 if alone else 700, window=window)
