@@ -576,12 +576,13 @@ constexpr int kRowsCost = 2, kRowsLeast = 4;
 // key heads, D = 128, uncut / cut: 512 keys 18 / 20 us, 1024 keys 26 / 20 us; 16
 // sequences of 512 keys 20 / 22, of 1024 28 / 26; 128 of 1024 69 / 71.
 constexpr int kWholeTiles = 8;
-// Uncut units of at most so many keys are a warp's, not a block's, where there are
-// enough to keep every warp busy: nothing to join and no one to wait for. At D =
-// 64, 8 key heads, a warp's / a block's: 320 sequences of 128 keys 38 / 44 us, 256
-// keys 50 / 54, 512 keys 73 / 71; 64 sequences of 128 keys 20 / 18. At D = 128,
-// with 16 keys a step, a block's is never slower (320 x 256 keys 82 / 75 us).
-constexpr int kWarpKeys = 256;
+// Uncut units of at most so many keys are a warp's, not a block's, from four units
+// an SM on (an SM holds eight warps): nothing to join and no one to wait for. At D =
+// 64, 8 key heads, a warp's / a block's: 80 sequences of 144 keys 22 / 24 us, 128 26 /
+// 28, 176 34 / 34, 320 47 / 52; of 176 keys 23 / 24, 27 / 29, 38 / 35 and 52 / 53; of
+// 240 keys 24 / 25, 30 / 31, 43 / 38 and 61 / 55; 64 sequences of 112 keys 20 / 18. At
+// D = 128, with 16 keys a step, a block's is never slower (320 x 256 keys 82 / 75 us).
+constexpr int kWarpKeys = 192;
 
 template <int DP, int MB, int W>
 static int rows_ctas() {

@@ -51,3 +51,13 @@ def test_chunks_among_more_sequences_than_threads(alone, ps, window):
     kv = [max(n, 1) + (i * 37) % 90 if n < 9 else n + (i * 53) % 400 for i, n in enumerate(ql)]
     c = Case(Hq, Hkv, 64, ps, ql, kv, seed=40)
     c.check(max_q=5 if alone else 700, window=window)
+
+
+@pytest.mark.parametrize("G,nq,window", [(2, 1, 0), (8, 2, 0), (4, 3, 20)])
+def test_many_units_of_a_few_keys(G, nq, window):
+    """Enough of them for a warp each, empty ones in between."""
+    kv = [(i * 53) % 176 for i in range(90)]
+    ql = [min(nq, n) if i % 7 else 0 for i, n in enumerate(kv)]
+    c = Case(8 * G, 8, 64, 16, ql, kv, seed=41)
+    assert len(c.table[0]) * 16 <= 192
+    c.check(window=window, sinks=torch.linspace(-4, 4, 8 * G, device="cuda"))
