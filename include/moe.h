@@ -410,9 +410,12 @@ typedef struct {
  * kv_len[b] - n_q + i); position c lies in page page_table[b * table_stride +
  * c / page_size], slot c % page_size. Sequences may be empty, and there may be
  * none (B = 0; the arrays may be NULL); rows at or past cu_q[B] belong to
- * none. Table entries past a sequence's last page are not read. max_q: the
- * largest number of new tokens of a sequence, a hint the kernel is chosen by; a
- * wrong one costs time only. */
+ * none. Table entries past a sequence's last page are not read. The kernel is
+ * chosen by max_q, the largest number of new tokens of a sequence (a hint: a
+ * wrong one costs time only), and by the keys that the table's max_pages or the
+ * window allow a sequence: a table far wider than the sequences need costs time
+ * where they are short (200 tokens over 200 keys, 64 heads to 8, D = 64: 30
+ * instead of 24 us; 320 single tokens over 128 keys 47 instead of 44). */
 typedef struct {
   const int32_t* cu_q;        /* [B + 1], ascending, cu_q[0] = 0 */
   const int32_t* kv_len;      /* [B], new tokens included */
@@ -483,7 +486,9 @@ int moe_kv_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const mo
  * Scores and sums are fp32; the weights exp(s_j - r), r a score of the row that
  * moves up when they exceed 2^16, are rounded to bf16 for the product with V
  * (once more where r moves on the way; the sum takes them unrounded); out is
- * rounded once. Results of two calls are bitwise equal on one GPU model.
+ * rounded once. An accumulator takes up to 65536 keys of a row, and those of a
+ * longer one are joined in fp32, so that long sums lose no more than short ones.
+ * Results of two calls are bitwise equal on one GPU model.
  *  q, out [T, Hq, D] (out may not overlap q);  sinks [Hq] fp32 or NULL;
  *  lse [T, Hq] fp32 packed, or NULL;  scale finite and > 0
  *  ws: moe_attn_paged_workspace_size(Hq, Hkv, D) bytes, 256-byte aligned (its size

@@ -3,9 +3,10 @@ positions (moe_rope), the append of new keys and values to a paged cache
 (moe_kv_append) and the attention of new tokens over it (moe_attn_paged).
 
 PyTorch supplies device memory and the stream; every step runs in the
-library's kernels, on the current device, which has to be the tensors'. A serving step is ``PagedAttention.forward`` (append, then
-attend); ``Rope.apply`` rotates without a cache, and with ``transpose=True``
-takes gradients back through the rotation in training.
+library's kernels, on the current device, which has to be the tensors'. A
+serving step is ``PagedAttention.forward`` (append, then attend); ``Rope.apply``
+rotates without a cache, and with ``transpose=True`` takes gradients back
+through the rotation in training.
 """
 from __future__ import annotations
 
@@ -154,7 +155,9 @@ class Rope:
 class KVBatch:
     """A ragged batch: cu_q [B+1], kv_len [B] (new tokens included), page_table
     [B, max_pages], all int32 on the device; T rows; max_q: the largest number
-    of new tokens of one sequence (a hint: T always works)."""
+    of new tokens of one sequence (a hint: T always works). The kernel is chosen
+    by max_q and by the keys that the table's width allows a sequence, so a narrow
+    table serves short sequences faster (include/moe.h, moe_kv_batch)."""
 
     def __init__(self, cu_q, kv_len, page_table, T: int, max_q: Optional[int] = None):
         B = int(kv_len.shape[0])

@@ -79,8 +79,8 @@ struct AttnArgs {
   int least;             // a stretch has at least so many steps
   int piece;             // tiles whose sums one accumulator takes (unit_next)
   struct Cut* cuts;      // [CTAs] the cut in front of each
-  float* part_o;         // [2 * CTAs][TM][DP] unnormalised partial outputs
-  float2* part_ml;       // [2 * CTAs][TM] their (max, sum)
+  float* part_o;         // [2 * CTAs (or groups)][TM][DP] unnormalised partial outputs
+  float2* part_ml;       // [2 * CTAs (or groups)][TM] their (max, sum)
   int* status;
 };
 

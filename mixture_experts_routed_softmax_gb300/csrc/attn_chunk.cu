@@ -4,7 +4,8 @@
 // A unit is 256 rows (two halves of 128) of one sequence and key/value head
 // against its key range, in tiles of 128 keys. Per tile and half:
 //   S = Q K^T      tcgen05.mma, both operands in shared memory, S in tensor memory
-//   P = exp2(S * scale - max), rounded to bf16 over S's own columns
+//   P = exp2(S * scale - max), rounded to bf16 over S's own columns (the product
+//                  takes both operands in one type, V's)
 //   O += P V       tcgen05.mma with P read from tensor memory
 // One pass with a running reference for the exponent: a row's is the maximum of
 // the first 64 keys it sees, and is only moved (O, the sum and the tile's stored
@@ -19,10 +20,11 @@
 // half's products run. Measured, L2 flushed before each run:
 //   (a) 2048 tokens over 31k keys, 32 heads to 4, D = 128: 611 us, 1646 TFLOP/s,
 //       85% of what a large plain product reaches; the tensor pipe is the bound;
-//   (b) 4 x 4096 tokens from scratch, 64 heads to 8, D = 64: 618 us, 890 TFLOP/s,
+//   (b) 4 x 4096 tokens from scratch, 64 heads to 8, D = 64: 620 us, 890 TFLOP/s,
 //       46%: as many exponentials as (a) for half the products. The softmax
 //       warps are the bound (some five instructions a score, every second issue
-//       slot taken, the exponential unit busy 37% of the time).
+//       slot taken, the exponential unit busy 39% and the tensor pipe 37% of the
+//       time).
 // Choices below name their times for (a) and (b). A maximum of every score and
 // the reference moved by that: 634 and 627.
 //   warp 0           issues the products; owns tensor memory
@@ -38,7 +40,8 @@
 //                    NaN are looked for
 //   warp 3           D <= 64: issues S = Q K^T, warp 0 only O += P V. There an
 //                    item's products take 512 cycles, less than one warp takes
-//                    to issue both beside busy softmax warps on its scheduler
+//                    to issue both beside busy softmax warps on its scheduler.
+//                    D > 64: nothing
 //   warps 4-7, 8-11  softmax of half 0 and 1: one row per thread (the row's
 //                    maximum and sum need no shuffles), the accumulator's
 //                    rescale, the epilogue. (Two threads a row, 64 keys each, and

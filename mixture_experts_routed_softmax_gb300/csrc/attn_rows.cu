@@ -19,9 +19,9 @@
 // address a key (444 instead of some 230 instructions a step).
 //
 // Measured with the join, L2 flushed before each run: four sequences of 65k to
-// 131k keys, 32 heads to 4, D = 128, 169 us = 4.9 TB/s (145 us, 5.7 TB/s, back to
-// back; a plain copy runs at 6.8); 64 sequences of 17 to 16k keys, 64 heads to 8,
-// D = 64, 83 us = 3.9 TB/s (68 back to back). The steady state reads at 90 to 95%
+// 131k keys, 32 heads to 4, D = 128, 168 us = 5.0 TB/s (145 us, 5.7 TB/s, a graph
+// replayed back to back; a plain copy runs at 6.8); 64 sequences of 17 to 16k keys,
+// 64 heads to 8, D = 64, 85 us = 3.8 TB/s (69 likewise). The steady state reads at 90 to 95%
 // of the copy's rate; the rest is some 15 us of beginning and end: two launches,
 // the schedule (3 us), the first keys (until 5 to 8 us), the parts' join. Loading
 // the next unit's first keys while a unit's parts are joined changed nothing.
@@ -559,8 +559,9 @@ __global__ void __launch_bounds__(kRowsThreads) attn_rows_kernel(
 // 77 us, 32 rows 46 / 50 and 72 / 77 us, 40 rows 75 / 50 and 110 / 77 us.
 constexpr int kFewRows = 32;
 // The chunk kernel is for as much work as this, in rows x keys (what the page table
-// or the window allows) x 64 or 128: below, its beginning and its join cost more
-// than the rows kernel takes, whose units are then few and short. Pages of 16, the
+// or the window allows; where a table is far wider than the sequences need, so are
+// short chunks the other kernel's) x 64 or 128: below, its beginning and its join cost
+// more than the rows kernel takes, whose units are then few and short. Pages of 16, the
 // kernel above and the chunk kernel, D = 64 and 128: 200 tokens over 200 keys, 8
 // heads to a key head, 18 / 30 and 22 / 34 us; 300 over 900, 4 heads, 24 / 33 and
 // 34 / 40; 8 x 9 over 1000 27 / 28 and 32 / 32; 16 x 9 over 1000 30 / 30 and 44 /
