@@ -507,6 +507,89 @@ int moe_attn_paged(const moe_kv_cache* cache, const moe_kv_batch* batch, const m
 size_t moe_attn_paged_workspace_size(int Hq, int Hkv, int D);
 
 /* ------------------------------------------------------------------------
+ * The scored router: the choice of experts by softmax or sigmoid scores, with a
+ * bias that balances the load, groups of experts, and weights that are
+ * renormalised or not; its gradient.
+ * (No counterpart on the source pages: the formulas below are the definition.)
+ *   s = softmax(l) over the E experts, or sigmoid(l);    c = s + balance
+ *   groups: the E experts in n_groups equal runs of neighbours; a group ranks by
+ *     the sum of its group_rank largest c (masked experts left out); the
+ *     topk_groups first ones stay, ties to the lower group
+ *   S = the k largest c of the groups that stay, in descending order, ties to the
+ *     lower index
+ *   w_j = scale * s_j / sum_S s (renormalise), or scale * s_j
+ * The choice is that of scores in 64 bits: where fp32 scores lie too near to one
+ * another to tell, the token is decided again from doubles. Without a balance, and
+ * with one group or group_rank 1, it goes by the logits themselves.
+ * Masked experts: a logit of -inf or NaN has score 0 and is chosen, in index
+ * order and with weight 0, only where fewer than k others remain; so is one whose
+ * choice value is NaN, with the weight of its score. A token whose chosen scores are all 0
+ * gets weights 0 and no gradient. A logit of +inf takes the whole softmax
+ * (shared with others of its kind).
+ * The struct is passed as a HOST pointer; balance is a device array.
+ * ------------------------------------------------------------------------ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+typedef struct {
+  const float* balance;   /* [E] fp32, or NULL: added for the choice alone, without gradient */
+  int32_t E;              /* <= 1024 */
+  int32_t k;              /* <= 32, <= topk_groups * (E / n_groups) */
+  int32_t score;          /* MOE_SCORE_* */
+  int32_t n_groups;       /* >= 1, divides E */
+  int32_t topk_groups;    /* 1 .. n_groups */
+  int32_t group_rank;     /* 1: a group's largest value; 2: the sum of its two largest */
+  int32_t renormalise;
+  float scale;            /* finite */
+} moe_router;
+
+/* moe_select — the choice and its weights from given logits.
+ *  logits [T, E] fp32;  forced_idx [T, k] int32 or NULL: the caller's choice, whose
+ *  weights are computed (an id outside [0, E) raises MOE_ERR_DEVICE_INDEX, weight 0);
+ *  topk_idx [T, k] int32 out;  topk_w [T, k] fp32 out */
+int moe_select(const moe_router* router, const float* logits, const int32_t* forced_idx, int64_t T,
+               int32_t* topk_idx, float* topk_w, moe_stream_t stream);
+
+/* moe_select_bwd — the logits' gradient from that of the weights (the choice is
+ * piecewise constant):
+ *   renormalise: q = w / scale, h_j = w_j (g_j - sum_i q_i g_i);
+ *     softmax dl_j = h_j, sigmoid dl_j = h_j (1 - s_j), 0 elsewhere
+ *   otherwise: sigmoid dl_j = scale g_j s_j (1 - s_j), 0 elsewhere;
+ *     softmax dl_e = scale p_e ([e in S] g_e - sum_j p_j g_j) for every expert
+ *  d_topk_w [T, k] fp32;  logits, topk_idx as of moe_select;  d_logits [T, E] fp32 out,
+ *  written whole, or added to (accumulate != 0: the gradient of a loss on the
+ *  logits themselves may lie there). An expert named by several slots takes the
+ *  sum of their terms; an id outside [0, E) raises MOE_ERR_DEVICE_INDEX and has none. */
+int moe_select_bwd(const moe_router* router, const float* d_topk_w, const float* logits,
+                   const int32_t* topk_idx, int64_t T, int accumulate, float* d_logits,
+                   moe_stream_t stream);
+
+/* moe_route_scored — moe_route with a scored router: the logits x . W_r (+ bias), as
+ * there, and moe_select on them. bias moves scores and choice; ws as moe_route's
+ * (MOE_WS_ROUTE, for E and k of the router). */
+int moe_route_scored(const moe_router* router, const moe_bf16* x, const float* w_router,
+                     const float* bias, const int32_t* forced_idx, int64_t T, int d,
+                     float* logits, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
+                     moe_stream_t stream);
+
+/* moe_logits_bwd — from d_logits [T, E] fp32 to the router's weight and bias and the
+ * layer's input:
+ *   dW_r = x^T . d_logits,  dbias = its column sums,
+ *   dx[t] += d_logits[t] . W_r^T            (dxp == NULL: read-modify-write), or
+ *   dx[t]  = sum_p dxp[dst_row[p]] + d_logits[t] . W_r^T   (as moe_route_bwd)
+ * in fp32, sums in a fixed order, dx rounded once.
+ *  dense: 0 where rows have few non-zero entries (any number is right), else the
+ *  product for dx runs on the tensor cores, from the first 16 significant bits of
+ *  d_logits. k, S: slots of dst_row [T*(k+S)] (used with dxp).
+ *  dx_inout [T, d] bf16;  dw_router [d, E] fp32 out;  dbias [E] fp32 out or NULL
+ *  ws: moe_logits_bwd_workspace_size(T, d, E, dense) bytes, 256-byte aligned. */
+int moe_logits_bwd(const float* d_logits, const float* w_router, const moe_bf16* x, int64_t T,
+                   int d, int E, int dense, int k, int S, moe_bf16* dx_inout, const float* dxp,
+                   const int32_t* dst_row, float* dw_router, float* dbias, void* ws,
+                   size_t ws_bytes, moe_stream_t stream);
+/* 0 for arguments the call rejects. */
+size_t moe_logits_bwd_workspace_size(int64_t T, int d, int E, int dense);
+
+/* ------------------------------------------------------------------------
  * Workspace sizes (bytes) for the calls that take `ws`. Any 256-byte-aligned
  * device buffer of at least this size works; its contents need no
  * initialisation and are scratch after the call.
@@ -552,6 +635,10 @@ const char* moe_status_str(int code);
 #define MOE_KERNEL_ROPE          15
 #define MOE_KERNEL_ATTN          16
 #define MOE_KERNEL_ATTN_COMBINE  17
+#define MOE_KERNEL_SELECT        18
+#define MOE_KERNEL_SELECT_BWD    19
+#define MOE_KERNEL_LOGITS_BWD    20
+#define MOE_KERNEL_LAST          20
 int moe_timer_start(int kernel, int max_launches);
 int moe_timer_read(float* total_ms, int* launches);
 

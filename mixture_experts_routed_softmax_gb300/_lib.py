@@ -40,6 +40,12 @@ SIGNATURES = {
     "moe_kv_append": (_I, [_P, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I, _P, _I64, _P]),
     "moe_attn_paged": (_I, [_P, _P, _P, _I64, _I, _F, _I, _I, _P, _P, _I64, _P, _P, _SZ, _P]),
     "moe_attn_paged_workspace_size": (_SZ, [_I, _I, _I]),
+    "moe_select": (_I, [_P, _P, _P, _I64, _P, _P, _P]),
+    "moe_select_bwd": (_I, [_P, _P, _P, _P, _I64, _I, _P, _P]),
+    "moe_route_scored": (_I, [_P, _P, _P, _P, _P, _I64, _I, _P, _P, _P, _P, _SZ, _P]),
+    "moe_logits_bwd": (_I, [_P, _P, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ,
+                            _P]),
+    "moe_logits_bwd_workspace_size": (_SZ, [_I64, _I, _I, _I]),
     "moe_workspace_size": (_SZ, [_I, _I64, _I, _I, _I, _I]),
     "moe_row_capacity": (_I64, [_I64, _I, _I, _I]),
     "moe_status": (_I, [_P]),
@@ -84,6 +90,17 @@ class Rotary(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class RouterArgs(ctypes.Structure):
+    """moe_router: scores, balance, groups and weights of a choice of experts."""
+    _fields_ = [("balance", _P), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_rank", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+
 MOE_WS_PERMUTE = 1
 MOE_WS_ROUTE_BWD = 2
 MOE_WS_ROUTE = 3
@@ -93,6 +110,7 @@ KERNELS = {
     "combine": 6, "combine_bwd": 7, "down_dgrad": 8, "gateup_dgrad": 9,
     "wgrad_down": 10, "wgrad_gateup": 11, "route_bwd": 12,
     "decode": 13, "fused_fwd": 14, "rope": 15, "attn": 16, "attn_combine": 17,
+    "select": 18, "select_bwd": 19, "logits_bwd": 20,
 }
 
 _lib = None

@@ -136,7 +136,7 @@ int moe_status(moe_stream_t stream) {
 }
 
 int moe_timer_start(int kernel, int max_launches) {
-  if (kernel < MOE_KERNEL_ROUTER_LOGITS || kernel > MOE_KERNEL_ATTN_COMBINE || max_launches <= 0)
+  if (kernel < MOE_KERNEL_ROUTER_LOGITS || kernel > MOE_KERNEL_LAST || max_launches <= 0)
     return MOE_ERR_ARG;
   std::lock_guard<std::mutex> lock(g_timer.mu);
   if (g_timer.kernel != 0) return MOE_ERR_ARG;

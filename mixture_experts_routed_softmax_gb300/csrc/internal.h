@@ -27,6 +27,8 @@ cudaError_t launch_route_small(const moe_bf16* x, const float* w_router, const f
                                const int32_t* forced, int64_t T, int d, int E, int k,
                                float* logits, int32_t* topk_idx, float* topk_w, void* ws,
                                int* status, cudaStream_t s);
+cudaError_t launch_router_small_partial(const moe_bf16* x, const float* w_router, int64_t T, int d,
+                                        int E, void* ws, int* slices, cudaStream_t s);
 cudaError_t launch_router_logits(const moe_bf16* x, const float* w_router, const float* bias,
                                  int64_t T, int d, int E, float* logits, void* ws, int* status,
                                  cudaStream_t s);
@@ -39,6 +41,24 @@ cudaError_t launch_route_bwd(const float* d_topk_w, const float* topk_w, const i
                              int k, int S, int align, moe_bf16* dx_inout, const float* dxp,
                              const int32_t* dst_row, float* dw_router, float* dbias, void* ws,
                              int* status, cudaStream_t s);
+
+// select.cu
+cudaError_t launch_select(const moe_router& r, const float* logits, const int32_t* forced,
+                          int64_t T, int32_t* topk_idx, float* topk_w, int* status,
+                          cudaStream_t s);
+cudaError_t launch_select_small(const moe_router& r, const float* part, int ns, int64_t T,
+                                const float* bias, const int32_t* forced, float* logits,
+                                int32_t* topk_idx, float* topk_w, int* status, cudaStream_t s);
+cudaError_t launch_select_bwd(const moe_router& r, const float* d_topk_w, const float* logits,
+                              const int32_t* topk_idx, int64_t T, int accumulate, float* d_logits,
+                              int* status, cudaStream_t s);
+
+// logits_bwd.cu
+size_t logits_bwd_ws_bytes(int64_t T, int d, int E, int dense);
+cudaError_t launch_logits_bwd(const float* d_logits, const float* w_router, const moe_bf16* x,
+                              int64_t T, int d, int E, int dense, int k, int S, moe_bf16* dx,
+                              const float* dxp, const int32_t* dst_row, float* dw_router,
+                              float* dbias, void* ws, int* status, cudaStream_t s);
 
 // permute.cu
 size_t permute_ws_bytes(int64_t T, int k, int E);

@@ -166,16 +166,7 @@ __global__ void __launch_bounds__(256) router_small_topk_kernel(
   __shared__ float lrow[kMaxExperts];
   const int64_t t = blockIdx.x;
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    float sum = 0.f;
-    for (int s0 = 0; s0 < ns; s0 += 8) {
-      float v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        v[u] = s0 + u < ns ? __ldg(part + ((int64_t)(s0 + u) * T + t) * E + e) : 0.f;
-#pragma unroll
-      for (int u = 0; u < 8; ++u) sum += v[u];
-    }
-    sum += bias ? bias[e] : 0.f;
+    const float sum = router_small_sum(part, ns, T, t, E, e) + (bias ? bias[e] : 0.f);
     lrow[e] = sum;
     logits[t * E + e] = sum;
   }
@@ -193,22 +184,31 @@ static void launch_small_topk(const float* part, int ns, int64_t T, int E, int k
              part, ns, T, E, k, bias, forced, logits, topk_idx, topk_w, status);
 }
 
+// The first launch of a few tokens' routing: the row slices' partial logits into ws.
+// *slices: how many there are.
+cudaError_t launch_router_small_partial(const moe_bf16* x, const float* w_router, int64_t T, int d,
+                                        int E, void* ws, int* slices, cudaStream_t s) {
+  const int rs = small_slice_rows(d), ns = (d + rs - 1) / rs;
+  *slices = ns;
+  const dim3 grid((unsigned)((E + kSmallCols - 1) / kSmallCols), (unsigned)ns,
+                  (unsigned)((T + kSmallTok - 1) / kSmallTok));
+  timer_before(MOE_KERNEL_ROUTER_LOGITS, s);
+  launch_pdl(pdl_for_tokens(T), router_small_partial_kernel, dim3(grid), dim3(kSmallWarps * 32), 0,
+             s, x, w_router, T, d, E, rs, static_cast<float*>(ws));
+  note_launches(1);
+  timer_after(MOE_KERNEL_ROUTER_LOGITS, s);
+  return cudaGetLastError();
+}
+
 // The whole routing of a few tokens: two launches (partials; logits + top-k).
 cudaError_t launch_route_small(const moe_bf16* x, const float* w_router, const float* bias,
                                const int32_t* forced, int64_t T, int d, int E, int k,
                                float* logits, int32_t* topk_idx, float* topk_w, void* ws,
                                int* status, cudaStream_t s) {
-  const int rs = small_slice_rows(d), ns = (d + rs - 1) / rs;
-  float* part = static_cast<float*>(ws);
-  const dim3 grid((unsigned)((E + kSmallCols - 1) / kSmallCols), (unsigned)ns,
-                  (unsigned)((T + kSmallTok - 1) / kSmallTok));
-  timer_before(MOE_KERNEL_ROUTER_LOGITS, s);
-  launch_pdl(pdl_for_tokens(T), router_small_partial_kernel, dim3(grid), dim3(kSmallWarps * 32), 0,
-             s, x, w_router, T, d, E, rs, part);
-  note_launches(1);
-  timer_after(MOE_KERNEL_ROUTER_LOGITS, s);
-  cudaError_t e = cudaGetLastError();
+  int ns = 0;
+  const cudaError_t e = launch_router_small_partial(x, w_router, T, d, E, ws, &ns, s);
   if (e != cudaSuccess) return e;
+  const float* part = static_cast<const float*>(ws);
   timer_before(MOE_KERNEL_TOPK, s);
   const int nv = (E + 31) / 32;
   if (nv <= 1) launch_small_topk<1>(part, ns, T, E, k, bias, forced, logits, topk_idx, topk_w, status, s);

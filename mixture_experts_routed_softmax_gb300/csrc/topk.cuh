@@ -15,6 +15,22 @@ __device__ __forceinline__ bool ranks_above(float va, int ia, float vb, int ib) 
   return va > vb || (va == vb && ia < ib);
 }
 
+// the sum of the router's row-slice partials [ns, T, E] (route.cu) of token t and
+// expert e in slice order, eight loads in flight
+__device__ __forceinline__ float router_small_sum(const float* __restrict__ part, int ns,
+                                                  int64_t T, int64_t t, int E, int e) {
+  float sum = 0.f;
+  for (int s0 = 0; s0 < ns; s0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      v[u] = s0 + u < ns ? __ldg(part + ((int64_t)(s0 + u) * T + t) * E + e) : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) sum += v[u];
+  }
+  return sum;
+}
+
 // lrow: the token's E logits; forced: its k caller-chosen experts or NULL;
 // writes idx_out[0..k) and w_out[0..k)
 template <int NV>   // logits per lane: 32 * NV >= E

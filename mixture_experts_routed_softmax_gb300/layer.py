@@ -65,6 +65,9 @@ class Buffers:
     ws_fused: Optional[torch.Tensor] = None
     ws_route_bwd: Optional[torch.Tensor] = None
     ws_expert_bwd: Optional[torch.Tensor] = None
+    # a scored router's gradient of the logits and its workspace
+    d_logits: Optional[torch.Tensor] = None
+    ws_logits_bwd: Optional[torch.Tensor] = None
     # the input of the last forward (the router backward reads it)
     x: Optional[torch.Tensor] = None
 
@@ -76,11 +79,13 @@ class MoELayer:
     bf16, w_down [E+S, f, d] bf16 (the E routed experts, then the S shared
     experts every token goes through with weight 1); top-k routing; ``align``
     pads each expert's rows; ``act`` = (limit, alpha, up_offset) of the
-    clamped SwiGLU, or None for the plain SwiGLU.
+    clamped SwiGLU, or None for the plain SwiGLU. ``router``: a
+    ``router.Router`` of the same E and k that chooses and weights the experts
+    instead of the renormalised softmax.
     """
 
     def __init__(self, w_router, bias, w_gate, w_up, w_down, k: int, align: int = 128,
-                 act=None):
+                 act=None, router=None):
         self.lib = _lib.load()
         self.w_router = w_router.contiguous()
         self.bias = None if bias is None else bias.contiguous()
@@ -99,12 +104,21 @@ class MoELayer:
         if dev.type != "cuda":
             raise RuntimeError("MoELayer runs on a CUDA device only")
         self.device = dev
+        if router is not None and (router.E, router.k) != (self.E, k):
+            raise ValueError(f"the router chooses {router.k} of {router.E} experts, the layer "
+                             f"{k} of {self.E}")
+        if router is not None and router.balance is not None and router.balance.device != dev:
+            raise ValueError(f"the router's balance is on {router.balance.device}, the layer on "
+                             f"{dev}")
+        self.router = router
 
     @classmethod
-    def from_inputs(cls, inp: dict, k: int, align: int = 128, device="cuda", act=None):
+    def from_inputs(cls, inp: dict, k: int, align: int = 128, device="cuda", act=None,
+                    router=None):
         mv = lambda t: None if t is None else t.to(device)  # noqa: E731
         return cls(mv(inp["w_router"]), mv(inp.get("bias")), mv(inp["w_gate"]),
-                   mv(inp["w_up"]), mv(inp["w_down"]), k, align, act)
+                   mv(inp["w_up"]), mv(inp["w_down"]), k, align, act,
+                   router)
 
     def _act(self):
         return None if self.act is None else _lib.ctypes.addressof(self.act)
@@ -112,7 +126,10 @@ class MoELayer:
     def row_capacity(self, T: int) -> int:
         return int(self.lib.moe_row_capacity(T, self.k + self.S, self.E + self.S, self.align))
 
-    def buffers(self, T: int, backward: bool = True) -> Buffers:
+    def buffers(self, T: int, backward: bool = True, logits_loss: bool = False) -> Buffers:
+        """Buffers of T tokens. logits_loss: the backward of a layer with a scored
+        router will also take the gradient of a loss on the logits (route_bwd's
+        accumulate), which needs a larger workspace."""
         E, d, f, k, S = self.E, self.d, self.f, self.k, self.S
         R = self.row_capacity(T)
         kw = dict(device=self.device)
@@ -151,13 +168,24 @@ class MoELayer:
             b.dw_down = torch.empty(E + S, f, d, dtype=BF16, **kw)
             b.dw_router = torch.empty(d, E, dtype=torch.float32, **kw)
             b.dbias = torch.empty(E, dtype=torch.float32, **kw)
-            b.ws_route_bwd = torch.empty(max(ws_r, 256), dtype=torch.uint8, **kw)
+            if self.router is None:
+                b.ws_route_bwd = torch.empty(max(ws_r, 256), dtype=torch.uint8, **kw)
+            else:
+                ws_l = int(self.lib.moe_logits_bwd_workspace_size(
+                    T, d, E, self.router.dense or logits_loss))
+                b.d_logits = torch.empty(T, E, dtype=torch.float32, **kw)
+                b.ws_logits_bwd = torch.empty(max(ws_l, 256), dtype=torch.uint8, **kw)
             ws_e = int(self.lib.moe_expert_bwd_workspace_size(R, f))
             b.ws_expert_bwd = torch.empty(max(ws_e, 256), dtype=torch.uint8, **kw)
         return b
 
     # ------------------------------------------------------------- calls --
     def route(self, x, b: Buffers, forced_idx=None, stream=None):
+        if self.router is not None:
+            _lib.call("moe_route_scored", self.router._ref, _p(x), _p(self.w_router),
+                      _p(self.bias), _p(forced_idx), b.T, self.d, _p(b.logits), _p(b.topk_idx),
+                      _p(b.topk_w), _p(b.ws_route), b.ws_route.numel(), _stream(stream))
+            return
         _lib.call("moe_route", _p(x), _p(self.w_router), _p(self.bias), _p(forced_idx),
                   b.T, self.d, self.E, self.k, _p(b.logits), _p(b.topk_idx), _p(b.topk_w),
                   _p(b.ws_route), b.ws_route.numel(), _stream(stream))
@@ -186,11 +214,27 @@ class MoELayer:
                   _p(b.dw_gate), _p(b.dw_up), _p(b.dw_down), _p(b.ws_expert_bwd),
                   b.ws_expert_bwd.numel(), _stream(stream))
 
-    def route_bwd(self, b: Buffers, fused=True, stream=None, x=None):
+    def route_bwd(self, b: Buffers, fused=True, stream=None, x=None, accumulate=False):
         """Router backward. fused: dx = permute transpose of dXp + the router's
         term in one pass; else dx (already holding the permute transpose) += it.
-        x: the layer input (default: the one the last forward recorded in b)."""
+        x: the layer input (default: the one the last forward recorded in b).
+        accumulate (with a scored router): the choice's gradient is added to what
+        b.d_logits holds, the gradient of a loss on the logits themselves; that
+        may reach every expert, so dx then takes the product for dense rows
+        (buffers made with logits_loss=True)."""
         x = b.x if x is None else x
+        if self.router is not None:
+            dense = self.router.dense or accumulate
+            ws = b.ws_logits_bwd
+            _lib.call("moe_select_bwd", self.router._ref, _p(b.d_topk_w), _p(b.logits),
+                      _p(b.topk_idx), b.T, int(accumulate), _p(b.d_logits), _stream(stream))
+            _lib.call("moe_logits_bwd", _p(b.d_logits), _p(self.w_router), _p(x), b.T, self.d,
+                      self.E, int(dense), self.k, self.S, _p(b.dx), _p(b.dxp) if fused else None,
+                      _p(b.dst_row) if fused else None, _p(b.dw_router), _p(b.dbias), _p(ws),
+                      ws.numel(), _stream(stream))
+            return
+        if accumulate:
+            raise ValueError("accumulate: a layer with a scored router is needed")
         _lib.call("moe_route_bwd", _p(b.d_topk_w), _p(b.topk_w), _p(b.topk_idx),
                   _p(self.w_router), _p(b.offsets), _p(b.src_pair), _p(x), b.T, self.d,
                   self.E, self.k, self.S, self.align, _p(b.dx), _p(b.dxp) if fused else None,
@@ -284,9 +328,9 @@ class MoELayer:
         """The whole forward of T <= 8 tokens in one launch (moe_decode_fwd);
         b from decode_buffers(T). Fills b.logits, b.topk_idx, b.topk_w, b.y.
         Routed experts with the plain SwiGLU only."""
-        if self.S or self.act is not None:
+        if self.S or self.act is not None or self.router is not None:
             raise ValueError("the one-launch decode forward takes routed experts with the plain "
-                             "SwiGLU only")
+                             "SwiGLU and softmax routing only")
         b.x = x
         _lib.call("moe_decode_fwd", _p(x), _p(self.w_router), _p(self.bias), _p(forced_idx),
                   b.T, self.d, self.f, self.E, self.k, _p(self.w_gate), _p(self.w_up),
