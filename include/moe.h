@@ -590,6 +590,77 @@ int moe_logits_bwd(const float* d_logits, const float* w_router, const moe_bf16*
 size_t moe_logits_bwd_workspace_size(int64_t T, int d, int E, int dense);
 
 /* ------------------------------------------------------------------------
+ * Weights in 4 bits with group scales, for inference: their making, the product
+ * of a few (or many) rows with them, and the experts' forward with them.
+ * (No counterpart on the source pages, which bind small-M experts to the bandwidth of
+ * their weights; the formulas below are the definition.)
+ *   W[e, k, n] = value(code[e, k, n]) * scale[e, k / group, n]
+ * Kinds of code: MOE_W4_INT4, two's complement -8 .. 7; MOE_W4_FP4, a sign, two bits of
+ * exponent and one of mantissa: +-{0, 1/2, 1, 3/2, 2, 3, 4, 6}.
+ * Scales are bf16, one for `group` neighbouring rows k (32, 64 or 128; the last
+ * group may be short) of a column.
+ * `codes` and `scales` are the library's own layout (moe_w4_codes_bytes,
+ * moe_w4_scales_bytes), written by moe_w4_quantise or moe_w4_pack and read by the
+ * others; both 16-byte aligned. The struct is passed as a HOST pointer.
+ * Limits: K, N multiples of 8, at most 65536; E <= 1024.
+ * ------------------------------------------------------------------------ */
+#define MOE_W4_INT4 0
+#define MOE_W4_FP4  1
+typedef struct {
+  uint8_t* codes;
+  moe_bf16* scales;
+  int32_t E, K, N;
+  int32_t group;
+  int32_t kind;
+} moe_w4;
+/* Bytes of the arrays (0 for sizes the calls reject). */
+size_t moe_w4_codes_bytes(int E, int K, int N);
+size_t moe_w4_scales_bytes(int E, int K, int N, int group);
+
+/* moe_w4_quantise — src [E, K, N] bf16 into w. With a the largest magnitude of a group:
+ *   int4: scale = a / 7 with its significand rounded up to five bits, codes the nearest
+ *         of -7 .. 7;  fp4: scale = the least power of two with a <= 6 scale, codes the
+ *         nearest; halves to the even code, a step less where bf16 does not hold the value.
+ * code * scale is then exactly a bf16 value. A group with a < 2^-120 becomes zeros; one
+ * that holds an infinity or NaN gets scale NaN, which its products show. */
+int moe_w4_quantise(const moe_w4* w, const moe_bf16* src, moe_stream_t stream);
+/* moe_w4_pack — given codes [E, K, N] (a byte each, the low four bits) and scales
+ * [E, ceil(K / group), N] bf16 into w: any scales, of any quantiser. Arrays 8-byte aligned. */
+int moe_w4_pack(const moe_w4* w, const uint8_t* codes, const moe_bf16* scales,
+                moe_stream_t stream);
+/* moe_w4_dequantise — dst [E, K, N] bf16 = code * scale, rounded (exact after
+ * moe_w4_quantise). */
+int moe_w4_dequantise(const moe_w4* w, moe_bf16* dst, moe_stream_t stream);
+
+/* moe_w4_linear — y = x W for one matrix (w->E = 1), fp32 sums, rounded once.
+ *  x [T, K] bf16, rows x_stride elements apart (a multiple of 8, >= K); y [T, N] bf16, or
+ *  fp32 (y_fp32 != 0), rows y_stride elements apart (>= N). y may not overlap x.
+ *  ws: moe_w4_linear_workspace_size(w, T) bytes, 256-byte aligned, one call at a time per
+ *  buffer (may be NULL where that is 0). */
+int moe_w4_linear(const moe_w4* w, const moe_bf16* x, int64_t x_stride, int64_t T, void* y,
+                  int64_t y_stride, int y_fp32, void* ws, size_t ws_bytes, moe_stream_t stream);
+size_t moe_w4_linear_workspace_size(const moe_w4* w, int64_t T);
+
+/* moe_expert_fwd_w4 — the whole expert part of the forward (moe_permute, moe_expert_fwd,
+ * moe_combine) with 4-bit weights:
+ *   A = act(x W_gate[e], x W_up[e]) rounded to bf16,
+ *   y[t] = sum_j w[t, j] A W_down[e_j]  + the S shared experts' outputs (weight 1)
+ * in fp32 sums in slot order, y rounded once. Weights are exact in the products
+ * of few rows; with many rows (the tensor-memory kernel) code * scale is rounded to
+ * bf16 first, which is exact after moe_w4_quantise.
+ *  gate, up [E+S, d, f] of one kind and group;  down [E+S, f, d] of any;  act: as in
+ *  moe_expert_fwd;  x [T, d] bf16;  topk_idx [T, k] int32, topk_w [T, k] fp32 (an id outside
+ *  [0, E) raises MOE_ERR_DEVICE_INDEX and its pair is left out);  y [T, d] bf16 out
+ *  ws: moe_expert_fwd_w4_workspace_size bytes, 256-byte aligned, one call at a time per
+ *  buffer. Two calls on one GPU model give bitwise equal results.
+ * Limits: k + S <= 32, E + S <= 1024. */
+int moe_expert_fwd_w4(const moe_w4* gate, const moe_w4* up, const moe_w4* down,
+                      const moe_swiglu* act, const moe_bf16* x, const int32_t* topk_idx,
+                      const float* topk_w, int64_t T, int k, int E, int S, moe_bf16* y, void* ws,
+                      size_t ws_bytes, moe_stream_t stream);
+size_t moe_expert_fwd_w4_workspace_size(int64_t T, int k, int E, int S, int d, int f);
+
+/* ------------------------------------------------------------------------
  * Workspace sizes (bytes) for the calls that take `ws`. Any 256-byte-aligned
  * device buffer of at least this size works; its contents need no
  * initialisation and are scratch after the call.
@@ -638,7 +709,9 @@ const char* moe_status_str(int code);
 #define MOE_KERNEL_SELECT        18
 #define MOE_KERNEL_SELECT_BWD    19
 #define MOE_KERNEL_LOGITS_BWD    20
-#define MOE_KERNEL_LAST          20
+#define MOE_KERNEL_W4_PACK       21
+#define MOE_KERNEL_W4_ROWS       22
+#define MOE_KERNEL_LAST          22
 int moe_timer_start(int kernel, int max_launches);
 int moe_timer_read(float* total_ms, int* launches);
 

@@ -46,6 +46,15 @@ SIGNATURES = {
     "moe_logits_bwd": (_I, [_P, _P, _P, _I64, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ,
                             _P]),
     "moe_logits_bwd_workspace_size": (_SZ, [_I64, _I, _I, _I]),
+    "moe_w4_codes_bytes": (_SZ, [_I, _I, _I]),
+    "moe_w4_scales_bytes": (_SZ, [_I, _I, _I, _I]),
+    "moe_w4_quantise": (_I, [_P, _P, _P]),
+    "moe_w4_pack": (_I, [_P, _P, _P, _P]),
+    "moe_w4_dequantise": (_I, [_P, _P, _P]),
+    "moe_w4_linear": (_I, [_P, _P, _I64, _I64, _P, _I64, _I, _P, _SZ, _P]),
+    "moe_w4_linear_workspace_size": (_SZ, [_P, _I64]),
+    "moe_expert_fwd_w4": (_I, [_P, _P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_expert_fwd_w4_workspace_size": (_SZ, [_I64, _I, _I, _I, _I, _I]),
     "moe_workspace_size": (_SZ, [_I, _I64, _I, _I, _I, _I]),
     "moe_row_capacity": (_I64, [_I64, _I, _I, _I]),
     "moe_status": (_I, [_P]),
@@ -98,6 +107,14 @@ class RouterArgs(ctypes.Structure):
                 ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class W4(ctypes.Structure):
+    """moe_w4: matrices in 4-bit codes with group scales."""
+    _fields_ = [("codes", _P), ("scales", _P), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("group", ctypes.c_int32), ("kind", ctypes.c_int32)]
+
+
+MOE_W4_INT4 = 0
+MOE_W4_FP4 = 1
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 
@@ -110,7 +127,7 @@ KERNELS = {
     "combine": 6, "combine_bwd": 7, "down_dgrad": 8, "gateup_dgrad": 9,
     "wgrad_down": 10, "wgrad_gateup": 11, "route_bwd": 12,
     "decode": 13, "fused_fwd": 14, "rope": 15, "attn": 16, "attn_combine": 17,
-    "select": 18, "select_bwd": 19, "logits_bwd": 20,
+    "select": 18, "select_bwd": 19, "logits_bwd": 20, "w4_pack": 21, "w4_rows": 22,
 }
 
 _lib = None

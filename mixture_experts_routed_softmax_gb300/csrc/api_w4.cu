@@ -1,0 +1,156 @@
+// api_w4.cu — the C ABI of the 4-bit weights (include/moe.h): argument checks,
+// then the launches.
+#include "internal.h"
+#include "w4.cuh"
+
+using namespace moe;
+
+static bool on(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+static int cuda_code(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+static size_t al256w(size_t b) { return (b + 255) & ~(size_t)255; }
+
+static int check_dims(int E, int K, int N) {
+  if (E <= 0 || K <= 0 || N <= 0) return MOE_ERR_ARG;
+  if (E > kMaxExperts || K % 8 != 0 || N % 8 != 0 || K > 65536 || N > 65536)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+static bool group_ok(int g) { return g == 32 || g == 64 || g == 128; }
+static int check_w4(const moe_w4* w) {
+  if (!w || !w->codes || !w->scales || !on(w->codes, 16) || !on(w->scales, 16)) return MOE_ERR_ARG;
+  if (w->kind != MOE_W4_INT4 && w->kind != MOE_W4_FP4) return MOE_ERR_ARG;
+  if (!group_ok(w->group)) return MOE_ERR_ARG;
+  return check_dims(w->E, w->K, w->N);
+}
+static int check_T(int64_t T) {
+  return T < 0 ? MOE_ERR_ARG : T >= ((int64_t)1 << 26) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// Tokens of one launch over the experts: as many as its look through the choices holds.
+static int64_t rows_tokens(int64_t T, int k) {
+  const int64_t n = kRowsMaxPairs / k;
+  return T < n ? T : n;
+}
+
+extern "C" {
+
+size_t moe_w4_codes_bytes(int E, int K, int N) {
+  return check_dims(E, K, N) ? 0 : (size_t)E * w4_codes_per_expert(K, N);
+}
+size_t moe_w4_scales_bytes(int E, int K, int N, int group) {
+  return check_dims(E, K, N) || !group_ok(group)
+             ? 0
+             : (size_t)E * w4_scales_per_expert(K, N, group) * sizeof(moe_bf16);
+}
+
+int moe_w4_quantise(const moe_w4* w, const moe_bf16* src, moe_stream_t stream) {
+  const int rc = check_w4(w);
+  if (rc) return rc;
+  if (!src || !on(src, 16)) return MOE_ERR_ARG;
+  return cuda_code(launch_w4_pack(*w, src, nullptr, nullptr,
+                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_w4_pack(const moe_w4* w, const uint8_t* codes, const moe_bf16* scales,
+                moe_stream_t stream) {
+  const int rc = check_w4(w);
+  if (rc) return rc;
+  if (!codes || !scales || !on(codes, 8) || !on(scales, 2)) return MOE_ERR_ARG;
+  return cuda_code(launch_w4_pack(*w, nullptr, codes, scales,
+                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_w4_dequantise(const moe_w4* w, moe_bf16* dst, moe_stream_t stream) {
+  const int rc = check_w4(w);
+  if (rc) return rc;
+  if (!dst || !on(dst, 16)) return MOE_ERR_ARG;
+  return cuda_code(launch_w4_unpack(*w, dst, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_w4_linear_workspace_size(const moe_w4* w, int64_t T) {
+  (void)w;
+  (void)T;
+  return 0;
+}
+
+int moe_w4_linear(const moe_w4* w, const moe_bf16* x, int64_t x_stride, int64_t T, void* y,
+                  int64_t y_stride, int y_fp32, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_w4(w);
+  if (!rc) rc = check_T(T);
+  if (rc) return rc;
+  if (w->E != 1) return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !y || !on(x, 16) || !on(y, y_fp32 ? 4 : 2)) return MOE_ERR_ARG;
+  if (x_stride < w->K || x_stride % 8 != 0 || y_stride < w->N) return MOE_ERR_ARG;
+  const size_t need = moe_w4_linear_workspace_size(w, T);
+  if (need && (!ws || ws_bytes < need || !on(ws, 256))) return MOE_ERR_ARG;
+  int* st = device_status_ptr();
+  if (!st) return MOE_ERR_CUDA;
+  return cuda_code(launch_w4_linear_rows(*w, x, x_stride, T, y, y_stride, y_fp32, st,
+                                         reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_expert_fwd_w4_workspace_size(int64_t T, int k, int E, int S, int d, int f) {
+  if (check_T(T) || T == 0 || k <= 0 || k > E || S < 0 || k + S > kMaxTopK ||
+      check_dims(E + S, d, f))
+    return 0;
+  const int64_t rows = rows_tokens(T, k) * (k + S);
+  return al256w((size_t)rows * f * 2) + al256w((size_t)rows * d * 4);
+}
+
+int moe_expert_fwd_w4(const moe_w4* gate, const moe_w4* up, const moe_w4* down,
+                      const moe_swiglu* act, const moe_bf16* x, const int32_t* topk_idx,
+                      const float* topk_w, int64_t T, int k, int E, int S, moe_bf16* y, void* ws,
+                      size_t ws_bytes, moe_stream_t stream) {
+  int rc = check_w4(gate);
+  if (!rc) rc = check_w4(up);
+  if (!rc) rc = check_w4(down);
+  if (!rc) rc = check_T(T);
+  if (rc) return rc;
+  if (k <= 0 || E <= 0 || k > E || S < 0) return MOE_ERR_ARG;
+  if (k + S > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+  const int d = gate->K, f = gate->N;
+  if (gate->E != E + S || up->E != E + S || down->E != E + S || up->K != d || up->N != f ||
+      down->K != f || down->N != d)
+    return MOE_ERR_ARG;
+  if (up->kind != gate->kind || up->group != gate->group) return MOE_ERR_ARG;
+  W4Experts q{};
+  if (!act) {
+    q.act = ActParams{INFINITY, 1.0f, 0.0f};
+  } else {
+    if (!(act->limit > 0.0f) || act->alpha != act->alpha || act->up_offset != act->up_offset)
+      return MOE_ERR_ARG;
+    q.act = ActParams{act->limit, act->alpha, act->up_offset};
+  }
+  if (T == 0) return MOE_OK;
+  if (!x || !topk_idx || !topk_w || !y || !on(x, 16) || !on(y, 16)) return MOE_ERR_ARG;
+  if (!ws || !on(ws, 256) || ws_bytes < moe_expert_fwd_w4_workspace_size(T, k, E, S, d, f))
+    return MOE_ERR_ARG;
+  int* st = device_status_ptr();
+  if (!st) return MOE_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  q.gate = gate;
+  q.up = up;
+  q.down = down;
+  q.k = k;
+  q.E = E;
+  q.S = S;
+  q.d = d;
+  q.f = f;
+  const int64_t most = rows_tokens(T, k);
+  moe_bf16* A = static_cast<moe_bf16*>(ws);
+  float* yp = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                       al256w((size_t)most * (k + S) * f * 2));
+  cudaError_t e = cudaSuccess;
+  for (int64_t t0 = 0; t0 < T && e == cudaSuccess; t0 += most) {
+    q.T = T - t0 < most ? T - t0 : most;
+    q.x = x + t0 * d;
+    q.topk_idx = topk_idx + t0 * k;
+    q.topk_w = topk_w + t0 * k;
+    e = launch_w4_experts_rows(q, A, yp, st, s);
+    if (e == cudaSuccess) e = launch_w4_combine(q, yp, y + t0 * d, s);
+  }
+  return cuda_code(e);
+}
+
+}  // extern "C"

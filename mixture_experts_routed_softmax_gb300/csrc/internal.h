@@ -137,6 +137,28 @@ cudaError_t launch_wgrad_gateup(const GroupedDims& g, const moe_bf16* xp, const 
                                 const moe_bf16* dU, moe_bf16* dw_gate, moe_bf16* dw_up,
                                 int* status, cudaStream_t s);
 
+// 4-bit weights: w4_pack.cu (src: weights to quantise, or NULL: codes and scales to lay out)
+cudaError_t launch_w4_pack(const moe_w4& w, const moe_bf16* src, const uint8_t* codes,
+                           const moe_bf16* scales, cudaStream_t s);
+cudaError_t launch_w4_unpack(const moe_w4& w, moe_bf16* dst, cudaStream_t s);
+// w4_rows.cu
+constexpr int kRowsMaxPairs = 2048;   // token-expert pairs of one launch
+struct W4Experts {
+  const moe_w4 *gate, *up, *down;
+  ActParams act;
+  const moe_bf16* x;
+  const int32_t* topk_idx;
+  const float* topk_w;
+  int64_t T;
+  int k, E, S, d, f;
+};
+cudaError_t launch_w4_linear_rows(const moe_w4& w, const moe_bf16* x, int64_t x_stride, int64_t T,
+                                  void* y, int64_t y_stride, int y_fp32, int* status,
+                                  cudaStream_t s);
+// A [T*(k+S), f] and yp [T*(k+S), d], rows by pair (T*k <= kRowsMaxPairs)
+cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, int* status,
+                                   cudaStream_t s);
+cudaError_t launch_w4_combine(const W4Experts& q, const float* yp, moe_bf16* y, cudaStream_t s);
 
 // rope.cu
 cudaError_t launch_rope(const moe_rotary* rot, const int32_t* pos, int64_t T, int D,

@@ -1,0 +1,133 @@
+// w4.cuh — weights in 4 bits with group scales: how they lie in memory and how a
+// thread turns its codes into bf16 values.
+//
+// A matrix [K, N] stands as W[k, n] = value(code[k, n]) * scale[k / group, n].
+// Kinds: int4, -8 .. 7; fp4, +-{0, 1/2, 1, 3/2, 2, 3, 4, 6} (a sign, two bits of
+// exponent, one of mantissa). Scales are bf16.
+//
+// Codes lie in tiles of 16 columns n by 64 rows k, 512 bytes each, the tiles of a
+// column block one after the other: a block's weights are one contiguous stream.
+// In a tile lane (g, t) = (lane / 4, lane % 4) owns 16 bytes, columns g and g + 8 at
+// the rows 8t .. 8t + 7 of either half of 32. So the 16 bytes are
+//   - the A operand of four m16n8k16 products whose B operand is 8 neighbouring
+//     elements of a row of x (the order of k inside a product is free as long
+//     as both sides agree): word j is product j, pair i of it register i; and
+//   - four runs of eight neighbouring k, 16 bytes of bf16 each, the unit in which
+//     a K-major operand in shared memory is swizzled.
+// Register i of product j takes, low and high half: i & 1 = 0: column g, 1: column
+// g + 8; rows 32 (j / 2) + 8t + 4 (j % 2) + 2 (i / 2) + {0, 1}.
+// Where a pair's bits lie in the low 16 bits of its word (the high 16 bits hold
+// the odd row alike):
+//   int4: bits 4i .. 4i + 3, the code plus 8
+//   fp4:  sign and three magnitude bits where a shift leaves them in a bf16's
+//         place: i = 0: 15, 8..6; 1: 12, 5..3; 2: 9, 2..0; 3: 14, 11..10 and 13
+//
+// Scales lie by steps of 128 rows: [block of 16 columns][step][g][groups of the
+// step][columns g, g + 8].
+#pragma once
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+constexpr int kW4Tile = 512;                       // bytes of a tile of codes
+__host__ __device__ constexpr int w4_kblocks(int K) { return (K + 63) / 64; }
+__host__ __device__ constexpr int w4_nblocks(int N) { return (N + 15) / 16; }
+__host__ __device__ constexpr int w4_steps(int K) { return (K + 127) / 128; }
+// groups of a step of 128 rows
+__host__ __device__ constexpr int w4_gps(int group) { return 128 / group; }
+__host__ __device__ constexpr int64_t w4_codes_per_expert(int K, int N) {
+  return (int64_t)w4_nblocks(N) * w4_kblocks(K) * kW4Tile;
+}
+// elements
+__host__ __device__ constexpr int64_t w4_scales_per_expert(int K, int N, int group) {
+  return (int64_t)w4_nblocks(N) * w4_steps(K) * 16 * w4_gps(group);
+}
+
+// the bit of a pair's low half that holds bit b (0: lowest) of the fp4 code
+__host__ __device__ constexpr int fp4_bit(int i, int b) {
+  return i == 0   ? (b == 3 ? 15 : 6 + b)
+         : i == 1 ? (b == 3 ? 12 : 3 + b)
+         : i == 2 ? (b == 3 ? 9 : b)
+                  : (b == 3 ? 14 : b == 0 ? 13 : 9 + b);
+}
+
+// a code (two's complement, or sign and magnitude) at its place in a word
+__device__ __forceinline__ uint32_t w4_place(uint32_t code, int i, int odd, bool fp4) {
+  uint32_t v;
+  if (fp4) {
+    v = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) v |= ((code >> b) & 1u) << fp4_bit(i, b);
+  } else {
+    v = (code ^ 8u) << (4 * i);
+  }
+  return v << (16 * odd);
+}
+__device__ __forceinline__ uint32_t w4_code_at(uint32_t word, int i, int odd, bool fp4) {
+  const uint32_t v = word >> (16 * odd);
+  if (!fp4) return ((v >> (4 * i)) & 15u) ^ 8u;
+  uint32_t c = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) c |= ((v >> fp4_bit(i, b)) & 1u) << b;
+  return c;
+}
+__device__ __forceinline__ float w4_value(uint32_t code, bool fp4) {
+  if (!fp4) return (float)((int)(code ^ 8u) - 8);
+  const uint32_t e = (code >> 1) & 3u, m = code & 1u;
+  const float a = e ? (float)((2 + m) << (e - 1)) * 0.5f : 0.5f * (float)m;
+  return code & 8u ? -a : a;
+}
+
+// The experts' gated activation (moe_swiglu); NaN stays NaN.
+__device__ __forceinline__ float gated(float g, float u, const ActParams& a) {
+  const float gc = g > a.limit ? a.limit : g;
+  const float uc = u > a.limit ? a.limit : u < -a.limit ? -a.limit : u;
+  return __fdividef(gc, 1.0f + __expf(-a.alpha * gc)) * (uc + a.c);
+}
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// A word's four pairs as bf16 with an offset or factor of the kind:
+//   int4: 128 + 8 + value (0x4300 holds 128 with steps of 1)
+//   fp4:  2^-126 value: the code's exponent and mantissa as the low end of bf16's,
+//         which has subnormals where fp4 has them
+template <bool FP4>
+__device__ __forceinline__ void w4_raw(uint32_t w, uint32_t* r) {
+  if (FP4) {
+    r[0] = w & 0x81C081C0u;
+    r[1] = (w << 3) & 0x81C081C0u;
+    r[2] = (w << 6) & 0x81C081C0u;
+    r[3] = ((w << 1) & 0x80008000u) | ((w >> 3) & 0x01800180u) | ((w >> 7) & 0x00400040u);
+  } else {
+    r[0] = (w & 0x000F000Fu) | 0x43004300u;
+    r[1] = ((w >> 4) & 0x000F000Fu) | 0x43004300u;
+    r[2] = ((w >> 8) & 0x000F000Fu) | 0x43004300u;
+    r[3] = ((w >> 12) & 0x000F000Fu) | 0x43004300u;
+  }
+}
+// the values themselves (exact)
+template <bool FP4>
+__device__ __forceinline__ void w4_decode(uint32_t w, uint32_t* r) {
+  w4_raw<FP4>(w, r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = FP4 ? mul_bf16x2(r[i], 0x7E807E80u)           // 2^126
+               : sub_bf16x2(r[i], 0x43084308u);          // 136
+}
+
+}  // namespace moe

@@ -338,6 +338,17 @@ class MoELayer:
                   _p(b.ws_decode), b.ws_decode.numel(), _stream(stream))
         return b.y
 
+    # ----------------------------------------------------- 4-bit weights --
+    def quantised(self, kind: str = "int4", group: int = 32, stream=None):
+        """The layer for inference with its experts in 4 bits (w4.MoELayer4): the
+        router's weight, bias and scoring by reference, the experts' quantised."""
+        from . import w4
+        q = [w4.Weights4.quantise(w, kind, group, stream)
+             for w in (self.w_gate, self.w_up, self.w_down)]
+        act = None if self.act is None else (self.act.limit, self.act.alpha, self.act.up_offset)
+        return w4.MoELayer4(self.w_router, self.bias,
+                            w4.Experts4(*q, k=self.k, E=self.E, act=act), self.router)
+
     def status(self, stream=None) -> int:
         """Synchronise and read (and clear) the device status word."""
         return int(self.lib.moe_status(_stream(stream)))
