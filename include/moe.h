@@ -711,7 +711,8 @@ const char* moe_status_str(int code);
 #define MOE_KERNEL_LOGITS_BWD    20
 #define MOE_KERNEL_W4_PACK       21
 #define MOE_KERNEL_W4_ROWS       22
-#define MOE_KERNEL_LAST          22
+#define MOE_KERNEL_W4_TILES      23
+#define MOE_KERNEL_LAST          23
 int moe_timer_start(int kernel, int max_launches);
 int moe_timer_read(float* total_ms, int* launches);
 

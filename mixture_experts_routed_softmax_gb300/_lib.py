@@ -127,7 +127,7 @@ KERNELS = {
     "combine": 6, "combine_bwd": 7, "down_dgrad": 8, "gateup_dgrad": 9,
     "wgrad_down": 10, "wgrad_gateup": 11, "route_bwd": 12,
     "decode": 13, "fused_fwd": 14, "rope": 15, "attn": 16, "attn_combine": 17,
-    "select": 18, "select_bwd": 19, "logits_bwd": 20, "w4_pack": 21, "w4_rows": 22,
+    "select": 18, "select_bwd": 19, "logits_bwd": 20, "w4_pack": 21, "w4_rows": 22, "w4_tiles": 23,
 }
 
 _lib = None

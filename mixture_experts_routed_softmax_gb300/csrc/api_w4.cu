@@ -26,10 +26,41 @@ static int check_T(int64_t T) {
   return T < 0 ? MOE_ERR_ARG : T >= ((int64_t)1 << 26) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-// Tokens of one launch over the experts: as many as its look through the choices holds.
-static int64_t rows_tokens(int64_t T, int k) {
-  const int64_t n = kRowsMaxPairs / k;
-  return T < n ? T : n;
+// Few rows go through the rows kernel (w4_rows.cu), many through tensor memory
+// (w4_tiles.cu).
+static bool linear_by_tiles(int64_t T) { return T > 32; }
+static bool experts_by_tiles(int64_t T, int k, int E) {
+  return T * k > kRowsMaxPairs || T * k > (int64_t)16 * E;
+}
+
+// The workspace of the experts' forward.
+struct ExpertWs {
+  size_t A, yp, xp, counts, offsets, dst_row, src_pair, permute, total;
+  int64_t R_cap;
+};
+constexpr int kTileAlign = 16;
+static ExpertWs expert_ws(int64_t T, int k, int E, int S, int d, int f) {
+  ExpertWs w{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t was = at;
+    at += al256w(bytes);
+    return was;
+  };
+  const bool tiles = experts_by_tiles(T, k, E);
+  w.R_cap = T * (k + S) + (tiles ? (int64_t)(E + S) * (kTileAlign - 1) : 0);
+  w.A = take((size_t)w.R_cap * f * 2);
+  w.yp = take((size_t)w.R_cap * d * 4);
+  if (tiles) {
+    w.xp = take((size_t)w.R_cap * d * 2);
+    w.counts = take((size_t)(E + S) * 4);
+    w.offsets = take((size_t)(E + S + 1) * 8);
+    w.dst_row = take((size_t)T * (k + S) * 4);
+    w.src_pair = take((size_t)w.R_cap * 4);
+    w.permute = take(permute_ws_bytes(T, k, E));
+  }
+  w.total = at;
+  return w;
 }
 
 extern "C" {
@@ -86,16 +117,17 @@ int moe_w4_linear(const moe_w4* w, const moe_bf16* x, int64_t x_stride, int64_t 
   if (need && (!ws || ws_bytes < need || !on(ws, 256))) return MOE_ERR_ARG;
   int* st = device_status_ptr();
   if (!st) return MOE_ERR_CUDA;
-  return cuda_code(launch_w4_linear_rows(*w, x, x_stride, T, y, y_stride, y_fp32, st,
-                                         reinterpret_cast<cudaStream_t>(stream)));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_code(linear_by_tiles(T)
+                       ? launch_w4_linear_tiles(*w, x, x_stride, T, y, y_stride, y_fp32, st, s)
+                       : launch_w4_linear_rows(*w, x, x_stride, T, y, y_stride, y_fp32, st, s));
 }
 
 size_t moe_expert_fwd_w4_workspace_size(int64_t T, int k, int E, int S, int d, int f) {
   if (check_T(T) || T == 0 || k <= 0 || k > E || S < 0 || k + S > kMaxTopK ||
       check_dims(E + S, d, f))
     return 0;
-  const int64_t rows = rows_tokens(T, k) * (k + S);
-  return al256w((size_t)rows * f * 2) + al256w((size_t)rows * d * 4);
+  return expert_ws(T, k, E, S, d, f).total;
 }
 
 int moe_expert_fwd_w4(const moe_w4* gate, const moe_w4* up, const moe_w4* down,
@@ -137,19 +169,29 @@ int moe_expert_fwd_w4(const moe_w4* gate, const moe_w4* up, const moe_w4* down,
   q.S = S;
   q.d = d;
   q.f = f;
-  const int64_t most = rows_tokens(T, k);
-  moe_bf16* A = static_cast<moe_bf16*>(ws);
-  float* yp = reinterpret_cast<float*>(static_cast<char*>(ws) +
-                                       al256w((size_t)most * (k + S) * f * 2));
-  cudaError_t e = cudaSuccess;
-  for (int64_t t0 = 0; t0 < T && e == cudaSuccess; t0 += most) {
-    q.T = T - t0 < most ? T - t0 : most;
-    q.x = x + t0 * d;
-    q.topk_idx = topk_idx + t0 * k;
-    q.topk_w = topk_w + t0 * k;
-    e = launch_w4_experts_rows(q, A, yp, st, s);
-    if (e == cudaSuccess) e = launch_w4_combine(q, yp, y + t0 * d, s);
+  q.T = T;
+  q.x = x;
+  q.topk_idx = topk_idx;
+  q.topk_w = topk_w;
+  const ExpertWs w = expert_ws(T, k, E, S, d, f);
+  if (w.R_cap >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  char* p = static_cast<char*>(ws);
+  moe_bf16* A = reinterpret_cast<moe_bf16*>(p + w.A);
+  float* yp = reinterpret_cast<float*>(p + w.yp);
+  if (!experts_by_tiles(T, k, E)) {
+    cudaError_t e = launch_w4_experts_rows(q, A, yp, st, s);
+    if (e == cudaSuccess) e = launch_w4_combine(q, yp, y, s);
+    return cuda_code(e);
   }
+  moe_bf16* xp = reinterpret_cast<moe_bf16*>(p + w.xp);
+  int64_t* offsets = reinterpret_cast<int64_t*>(p + w.offsets);
+  int32_t* dst_row = reinterpret_cast<int32_t*>(p + w.dst_row);
+  cudaError_t e = launch_permute(topk_idx, T, k, E, S, kTileAlign, x, d, w.R_cap,
+                                 reinterpret_cast<int32_t*>(p + w.counts), offsets, dst_row,
+                                 reinterpret_cast<int32_t*>(p + w.src_pair), xp, p + w.permute, st,
+                                 s);
+  if (e == cudaSuccess) e = launch_w4_experts_tiles(q, xp, offsets, w.R_cap, A, yp, st, s);
+  if (e == cudaSuccess) e = launch_combine(yp, dst_row, topk_w, T, k, S, d, y, s);
   return cuda_code(e);
 }
 

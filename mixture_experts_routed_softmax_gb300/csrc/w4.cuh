@@ -7,15 +7,15 @@
 //
 // Codes lie in tiles of 16 columns n by 64 rows k, 512 bytes each, the tiles of a
 // column block one after the other: a block's weights are one contiguous stream.
-// In a tile lane (g, t) = (lane / 4, lane % 4) owns 16 bytes, columns g and g + 8 at
-// the rows 8t .. 8t + 7 of either half of 32. So the 16 bytes are
-//   - the A operand of four m16n8k16 products whose B operand is 8 neighbouring
-//     elements of a row of x (the order of k inside a product is free as long
-//     as both sides agree): word j is product j, pair i of it register i; and
-//   - four runs of eight neighbouring k, 16 bytes of bf16 each, the unit in which
-//     a K-major operand in shared memory is swizzled.
-// Register i of product j takes, low and high half: i & 1 = 0: column g, 1: column
-// g + 8; rows 32 (j / 2) + 8t + 4 (j % 2) + 2 (i / 2) + {0, 1}.
+// In a tile lane (g, t) = (lane / 4, lane % 4) owns 16 bytes, columns g and g + 8 at the
+// rows 16j + 4t .. + 3, word j = 0 .. 3. So word j is
+//   - the A operand of an m16n8k16 product whose B operand is four neighbouring
+//     elements of a row of x (the order of k inside a product is free as long as
+//     both sides agree): pair i of the word is register i; and
+//   - a lane's part of 16 rows by 16 k of a tensor-memory operand (the 16x256b
+//     shape), columns of 32 bits in the natural order of k.
+// Register i of word j takes, low and high half: i & 1 = 0: column g, 1: column g + 8;
+// rows 16j + 4t + 2 (i / 2) + {0, 1}.
 // Where a pair's bits lie in the low 16 bits of its word (the high 16 bits hold
 // the odd row alike):
 //   int4: bits 4i .. 4i + 3, the code plus 8

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {
           const int n = c0 + g + 8 * (i & 1);
-          const int r = 64 * (kb & 1) + 32 * (j >> 1) + 8 * t + 4 * (j & 1) + 2 * (i >> 1) + odd;
+          const int r = 64 * (kb & 1) + 16 * j + 4 * t + 2 * (i >> 1) + odd;
           const float v = tile[r][n];
           // a group is 32, 64 or 128 rows: r / group without a division
           const uint32_t code =
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kPackThreads) w4_unpack_kernel(W4View w,
       const uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r0 = 64 * (kb & 1) + 32 * (j >> 1) + 8 * t + 4 * (j & 1);
+        const int r0 = 64 * (kb & 1) + 16 * j + 4 * t;
         const int gr = (r0 * gps) >> 7;
         uint32_t p[4];
         w4_decode<FP4>(word[j], p);

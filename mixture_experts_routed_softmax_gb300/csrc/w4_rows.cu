@@ -183,14 +183,14 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(RowsArgs a) {
           }
         }
       }
-      uint4 xv[NT][4];
+      uint2 xv[NT][8];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int k = 128 * step + 32 * h + 8 * t;
-          xv[nt][h] = make_uint4(0u, 0u, 0u, 0u);
-          if (xr[nt] && k < a.K) xv[nt][h] = *reinterpret_cast<const uint4*>(xr[nt] + k);
+        for (int h = 0; h < 8; ++h) {
+          const int k = 128 * step + 16 * h + 4 * t;
+          xv[nt][h] = make_uint2(0u, 0u);
+          if (xr[nt] && k < a.K) xv[nt][h] = *reinterpret_cast<const uint2*>(xr[nt] + k);
         }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -206,10 +206,11 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(RowsArgs a) {
           uint32_t av[4];
           w4_decode<FP4>((h & 1) ? c.z : c.x, av);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(part[nt], av, xv[nt][h].x, xv[nt][h].y);
+          for (int nt = 0; nt < NT; ++nt) mma16816(part[nt], av, xv[nt][2 * h].x, xv[nt][2 * h].y);
           w4_decode<FP4>((h & 1) ? c.w : c.y, av);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(part[nt], av, xv[nt][h].z, xv[nt][h].w);
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(part[nt], av, xv[nt][2 * h + 1].x, xv[nt][2 * h + 1].y);
           if (h % (4 / GPS) == 4 / GPS - 1) {
             const uint32_t s = sw[r][h / (4 / GPS)];
             const float lo = bf16_lo(s), hi = bf16_hi(s);

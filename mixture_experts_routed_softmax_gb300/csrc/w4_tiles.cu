@@ -1,0 +1,480 @@
+// w4_tiles.cu — products of many rows with 4-bit weights (layout: w4.cuh) on the
+// 5th-generation tensor cores: a linear layer, and the experts' gate/up and down
+// products over the padded expert-grouped layout (permute.cu).
+//
+//   D[n, r] += W^T[n, k] x^T[k, r]
+// The weights are the A operand, 128 columns n of two matrices (gate and up) or of two
+// neighbouring runs of one, 64 k a step; up to 128 rows of x are the B operand, N = their
+// number rounded up to 16. A lives in tensor memory: sixteen warps take a 512-byte
+// tile of codes each a step, turn it into bf16 code * scale in registers (w4_decode, one
+// more product), and store it as the 16x256b shape, whose lanes hold just what a lane's
+// codes are. So the bf16 weights never pass through shared memory, whose bandwidth the
+// products' B operand and the codes share, and each code is read from L2 once for 128 rows.
+// code * scale is rounded to bf16 there; scales of few bits (moe_w4_quantise's) make it exact.
+//
+// Roles (28 warps): 0 loads rows of x by TMA, a step a stage; 3 streams the codes
+// and scales, contiguous runs of four steps a tile, by bulk copies; 4-19 the sixteen above;
+// 1 issues the products; 20-27 take the finished tile from tensor memory (a thread a
+// column n, so a warp stores 32 neighbouring columns of a row). Tensor memory: 2 x 128
+// columns of accumulators, four stages of 64 columns of A. Every wait is bounded.
+//
+// An expert's rows are cut into equal chunks of at most 128; tiles of one run of columns
+// follow one another, so that its codes are in L2 for the second chunk.
+#include "tmap.h"
+#include "w4.cuh"
+
+namespace moe {
+
+enum class TileMode { Linear, GateUp, Down };
+
+constexpr int kTileRows = 128;              // rows of x a tile, at most
+constexpr int kXStages = 4;                 // of x and of A, in step
+constexpr int kXBytes = kTileRows * 128;    // 64 k of 128 rows
+constexpr int kCStages = 3;                 // of codes: four steps each
+constexpr int kCSteps = 4;
+constexpr int kCBytes = 16 * kCSteps * kW4Tile;
+constexpr int kDecWarp0 = 4, kDecWarps = 16, kOutWarp0 = 20, kOutWarps = 8;
+constexpr int kTileThreads = 32 * (kOutWarp0 + kOutWarps);
+constexpr int kAccCols = 256;               // two accumulators of 128 columns
+constexpr int kTileSmem =
+    1024 + kXStages * kXBytes + kCStages * (kCBytes + 4096) + 4 * (kMaxExperts + 1) + 256;
+
+struct TileArgs {
+  const uint8_t* codes[2];
+  const moe_bf16* scales[2];
+  int K, N, E;
+  const int64_t* offsets;      // NULL: one matrix, T rows
+  int64_t T;
+  ActParams act;
+  void* out;
+  int64_t out_stride;
+  int out_fp32;
+  int* status;
+};
+
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// untiled copy: 16-byte aligned addresses, size a multiple of 16
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// For a whole warp: true in all lanes, or (given up) false in all.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                         int* status) {
+  if (__builtin_expect(__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)), 1)) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status));
+}
+
+struct Tile {
+  int e, n0, rows;
+  int64_t m0;
+};
+
+template <TileMode M, bool FP4, int GPS>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    w4_tiles_kernel(const __grid_constant__ CUtensorMap mapX, const TileArgs a) {
+  pdl_enter();
+  constexpr int kSBytes = 64 * GPS;                    // scales of a tile's two steps of 128
+  constexpr int kWide = M == TileMode::GateUp ? 128 : 256;   // columns n a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~(uintptr_t)1023);
+  uint8_t* s_codes = smem + kXStages * kXBytes;
+  uint8_t* s_scales = s_codes + kCStages * kCBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_scales + kCStages * 4096);
+  int* tstart = reinterpret_cast<int*>(bars + 32);
+  const uint32_t bar0 = smem_u32(bars);
+  auto x_full = [&](int s) { return bar0 + 8u * s; };
+  auto a_full = [&](int s) { return bar0 + 8u * (kXStages + s); };
+  auto empty = [&](int s) { return bar0 + 8u * (2 * kXStages + s); };      // x and A of a stage
+  auto c_full = [&](int s) { return bar0 + 8u * (3 * kXStages + s); };
+  auto c_empty = [&](int s) { return bar0 + 8u * (3 * kXStages + kCStages + s); };
+  const uint32_t acc_full = bar0 + 8u * (3 * kXStages + 2 * kCStages);
+  const uint32_t acc_empty = acc_full + 8, drain = acc_full + 16;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 28);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  static_assert(3 * kXStages + 2 * kCStages + 3 <= 28, "barriers");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kXStages; ++s) {
+      mbar_init(x_full(s), 1);
+      mbar_init(a_full(s), kDecWarps);
+      mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < kCStages; ++s) {
+      mbar_init(c_full(s), 1);
+      mbar_init(c_empty(s), kDecWarps);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, kOutWarps);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mapX);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(s_tmem), 512);
+    tmem_relinquish();
+  }
+  const int nN = (a.N + kWide - 1) / kWide;
+  // tstart[e]: tiles before expert e
+  auto rows_of = [&](int e) {
+    return a.offsets ? (int)(a.offsets[e + 1] - a.offsets[e]) : (int)a.T;
+  };
+  for (int e = threadIdx.x; e < a.E; e += kTileThreads)
+    tstart[e + 1] = (rows_of(e) + kTileRows - 1) / kTileRows * nN;
+  __syncthreads();
+  if (warp == 3) {
+    int run = 0;
+    for (int b = 0; b < a.E; b += 32) {
+      const int e = b + lane;
+      int v = e < a.E ? tstart[e + 1] : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, off);
+        if (lane >= off) v += o;
+      }
+      if (e < a.E) tstart[e + 1] = run + v;
+      run += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (lane == 0) tstart[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int total = tstart[a.E];
+  const int kbs = w4_kblocks(a.K), steps = w4_steps(a.K), nbs = w4_nblocks(a.N);
+
+  auto tile_at = [&](int i) {
+    int lo = 0, hi = a.E;                   // the last expert with tstart[lo] <= i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tstart[mid] <= i) lo = mid; else hi = mid;
+    }
+    Tile t;
+    t.e = lo;
+    const int L = rows_of(lo), chunks = (L + kTileRows - 1) / kTileRows;
+    const int size = ((L + 15) / 16 + chunks - 1) / chunks * 16;
+    const int at = i - tstart[lo], c = at % chunks;
+    t.n0 = at / chunks * kWide;
+    t.rows = min(size, L - c * size);       // (chunks of up to eight sixteens: none is empty)
+    t.m0 = (a.offsets ? a.offsets[lo] : 0) + (int64_t)c * size;
+    return t;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- rows of x --
+    int s = 0, fills = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    if (lane == 0) {
+      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+        const Tile t = tile_at(i);
+        const int boxes = (t.rows + 31) / 32;
+        for (int ks = 0; ks < kbs; ++ks) {
+          if (!mbar_wait_bounded(empty(s), ph ^ 1u, s_abort, a.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(x_full(s), boxes * 4096);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_3d(smem_u32(smem) + s * kXBytes + b * 4096, &mapX, x_full(s), ks * 64, 0,
+                        (int)t.m0 + 32 * b);
+          ++fills;
+          if (++s == kXStages) { s = 0; ph ^= 1u; }
+        }
+      }
+      // copies already issued land before the block's shared memory goes away
+      volatile int never = 0;
+      for (int n = fills < kXStages ? fills : kXStages; n > 0; --n) {
+        if (--s < 0) { s = kXStages - 1; ph ^= 1u; }
+        mbar_wait_bounded(x_full(s), ph, &never, a.status);
+      }
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------ codes and scales --
+    // lanes 0-15 copy a tile's codes each, 16-31 its scales
+    int s = 0, fills = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const int j = lane & 15, mat = j >> 3, nbl = j & 7;
+    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      const Tile t = tile_at(i);
+      const int nb = t.n0 / 16 + (M == TileMode::GateUp ? nbl : 8 * mat + nbl);
+      const int m = M == TileMode::GateUp ? mat : 0;
+      const int present = __popc(__ballot_sync(0xFFFFFFFFu, lane < 16 && nb < nbs));
+      const uint8_t* src =
+          lane < 16 ? a.codes[m] + t.e * w4_codes_per_expert(a.K, a.N) + (int64_t)nb * kbs * kW4Tile
+                    : reinterpret_cast<const uint8_t*>(a.scales[m] +
+                                                       t.e * w4_scales_per_expert(a.K, a.N, 128 / GPS) +
+                                                       (int64_t)nb * steps * 16 * GPS);
+      for (int ks = 0; ks < kbs; ks += kCSteps) {
+        if (!wait_all(c_empty(s), ph ^ 1u, s_abort, a.status)) {
+          ok = false;
+          break;
+        }
+        const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
+        const uint32_t cb = n * kW4Tile, sb = (n + 1) / 2 * 32 * GPS;
+        if (lane == 0) mbar_arrive_expect_tx(c_full(s), present * (cb + sb));
+        __syncwarp();
+        if (nb < nbs) {
+          if (lane < 16)
+            bulk_load(smem_u32(s_codes) + s * kCBytes + j * kCSteps * kW4Tile,
+                      src + (int64_t)ks * kW4Tile, cb, c_full(s));
+          else
+            bulk_load(smem_u32(s_scales) + s * 4096 + j * kSBytes,
+                      src + (int64_t)(ks / 2) * 32 * GPS, sb, c_full(s));
+        }
+        ++fills;
+        if (++s == kCStages) { s = 0; ph ^= 1u; }
+      }
+    }
+    volatile int never = 0;
+    for (int n = fills < kCStages ? fills : kCStages; n > 0; --n) {
+      if (--s < 0) { s = kCStages - 1; ph ^= 1u; }
+      mbar_wait_bounded(c_full(s), ph, &never, a.status);
+    }
+  } else if (warp >= kDecWarp0 && warp < kOutWarp0) {
+    // ------------------------------------------------------- codes into bf16 --
+    const int q = warp & 3, i4 = (warp - kDecWarp0) >> 2, mat = i4 >> 1, half = i4 & 1;
+    const int slot = 8 * mat + 2 * q + half, g = lane >> 2;
+    const uint32_t lane_at = (uint32_t)(32 * q + 16 * half) << 16;
+    int s = 0, cs = 0;
+    uint32_t ph = 0, cph = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      const Tile t = tile_at(i);
+      for (int ks = 0; ks < kbs; ++ks) {
+        const int sub = ks % kCSteps;
+        if (sub == 0 && !wait_all(c_full(cs), cph, s_abort, a.status)) {
+          ok = false;
+          break;
+        }
+        const uint4 c = *reinterpret_cast<const uint4*>(s_codes + cs * kCBytes +
+                                                        (slot * kCSteps + sub) * kW4Tile + 16 * lane);
+        const uint8_t* sp = s_scales + cs * 4096 + slot * kSBytes + (sub >> 1) * 32 * GPS + g * 4 * GPS;
+        uint32_t sw[2];
+        if (GPS == 4) {
+          const uint2 v = *reinterpret_cast<const uint2*>(sp + 8 * (sub & 1));
+          sw[0] = v.x;
+          sw[1] = v.y;
+        } else {
+          sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(sp + (GPS == 2 ? 4 * (sub & 1) : 0));
+        }
+        uint32_t r[16];
+        const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t p[4];
+          w4_decode<FP4>(word[j], p);
+          const uint32_t lo = __byte_perm(sw[j >> 1], 0, 0x1010), hi = __byte_perm(sw[j >> 1], 0, 0x3232);
+          r[4 * j + 0] = mul_bf16x2(p[0], lo);
+          r[4 * j + 1] = mul_bf16x2(p[2], lo);
+          r[4 * j + 2] = mul_bf16x2(p[1], hi);
+          r[4 * j + 3] = mul_bf16x2(p[3], hi);
+        }
+        if (sub == kCSteps - 1 || ks == kbs - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(c_empty(cs));
+          if (++cs == kCStages) { cs = 0; cph ^= 1u; }
+        }
+        if (!wait_all(empty(s), ph ^ 1u, s_abort, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st_16x256b_x4(tmem + lane_at + kAccCols + 64 * s + 32 * mat, r);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(a_full(s));
+        if (++s == kXStages) { s = 0; ph ^= 1u; }
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- products --
+    int s = 0;
+    uint32_t ph = 0, acc_ph = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      const Tile t = tile_at(i);
+      if (!wait_all(acc_empty, acc_ph ^ 1u, s_abort, a.status)) break;
+      const uint32_t idesc = idesc_bf16(128, (t.rows + 15) & ~15, 0, 0);
+      for (int ks = 0; ks < kbs; ++ks) {
+        if (!wait_all(x_full(s), ph, s_abort, a.status) ||
+            !wait_all(a_full(s), ph, s_abort, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t xa = smem_u32(smem) + s * kXBytes, at = tmem + kAccCols + 64 * s;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t bd = sdesc_sw128(xa + 32 * kk, 16, 1024);
+            umma_tmem_a(tmem, at + 8 * kk, bd, idesc, ks > 0 || kk > 0);
+            umma_tmem_a(tmem + 128, at + 32 + 8 * kk, bd, idesc, ks > 0 || kk > 0);
+          }
+          umma_commit(empty(s));
+        }
+        __syncwarp();
+        if (++s == kXStages) { s = 0; ph ^= 1u; }
+      }
+      if (!ok) break;
+      if (lane == 0) umma_commit(acc_full);
+      __syncwarp();
+      acc_ph ^= 1u;
+    }
+    // every product has ended before tensor memory is freed
+    if (lane == 0) {
+      umma_commit(drain);
+      volatile int never = 0;
+      mbar_wait_bounded(drain, 0, &never, a.status);
+    }
+  } else if (warp >= kOutWarp0) {
+    // --------------------------------------------------------------- results --
+    const int q = warp & 3, part = (warp - kOutWarp0) >> 2;
+    const uint32_t at = tmem + ((uint32_t)(32 * q) << 16);
+    uint32_t ph = 0;
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+      const Tile t = tile_at(i);
+      if (!wait_all(acc_full, ph, s_abort, a.status)) break;
+      ph ^= 1u;
+      tc_fence_after();
+      const int n = t.n0 + 32 * q + lane;
+      for (int c0 = 16 * part; c0 < t.rows; c0 += 32) {
+        uint32_t v[2][16];
+        tmem_ld16(at + c0, v[0]);
+        tmem_ld16(at + 128 + c0, v[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const int64_t row = t.m0 + c0 + c;
+          if (c0 + c >= t.rows) continue;
+          const float v0 = __uint_as_float(v[0][c]), v1 = __uint_as_float(v[1][c]);
+          if (M == TileMode::GateUp) {
+            if (n < a.N)
+              static_cast<moe_bf16*>(a.out)[row * a.out_stride + n] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(gated(v0, v1, a.act)));
+          } else if (M == TileMode::Down || a.out_fp32) {
+            float* o = static_cast<float*>(a.out) + row * a.out_stride + n;
+            if (n < a.N) o[0] = v0;
+            if (n + 128 < a.N) o[128] = v1;
+          } else {
+            moe_bf16* o = static_cast<moe_bf16*>(a.out) + row * a.out_stride + n;
+            if (n < a.N) o[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v0));
+            if (n + 128 < a.N) o[128] = __bfloat16_as_ushort(__float2bfloat16_rn(v1));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// -------------------------------------------------------------------- host --
+template <TileMode M, bool FP4, int GPS>
+static cudaError_t run_tiles(const CUtensorMap& x, const TileArgs& a, bool pdl, cudaStream_t s) {
+  const auto kernel = w4_tiles_kernel<M, FP4, GPS>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(pdl, kernel, dim3(num_sms()), dim3(kTileThreads), kTileSmem, s, x, a);
+}
+
+template <TileMode M>
+static cudaError_t tiles(const TileArgs& a, const moe_w4& w, const moe_bf16* x, int64_t rows,
+                         int64_t stride, bool pdl, cudaStream_t s) {
+  CUtensorMap map;
+  if (!map_heads(&map, x, a.K, 1, rows, stride, 1, 32)) return cudaErrorInvalidValue;
+  const int gps = w4_gps(w.group);
+  timer_before(MOE_KERNEL_W4_TILES, s);
+  cudaError_t e;
+  if (w.kind == MOE_W4_FP4)
+    e = gps == 4   ? run_tiles<M, true, 4>(map, a, pdl, s)
+        : gps == 2 ? run_tiles<M, true, 2>(map, a, pdl, s)
+                   : run_tiles<M, true, 1>(map, a, pdl, s);
+  else
+    e = gps == 4   ? run_tiles<M, false, 4>(map, a, pdl, s)
+        : gps == 2 ? run_tiles<M, false, 2>(map, a, pdl, s)
+                   : run_tiles<M, false, 1>(map, a, pdl, s);
+  note_launches(1);
+  timer_after(MOE_KERNEL_W4_TILES, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_w4_linear_tiles(const moe_w4& w, const moe_bf16* x, int64_t x_stride, int64_t T,
+                                   void* y, int64_t y_stride, int y_fp32, int* status,
+                                   cudaStream_t s) {
+  TileArgs a{};
+  a.codes[0] = w.codes;
+  a.scales[0] = w.scales;
+  a.K = w.K;
+  a.N = w.N;
+  a.E = 1;
+  a.T = T;
+  a.out = y;
+  a.out_stride = y_stride;
+  a.out_fp32 = y_fp32;
+  a.status = status;
+  return tiles<TileMode::Linear>(a, w, x, T, x_stride, pdl_for_tokens(T), s);
+}
+
+cudaError_t launch_w4_experts_tiles(const W4Experts& q, const moe_bf16* xp, const int64_t* offsets,
+                                    int64_t R_cap, moe_bf16* A, float* yp, int* status,
+                                    cudaStream_t s) {
+  const bool pdl = pdl_for_tokens(q.T);
+  TileArgs a{};
+  a.codes[0] = q.gate->codes;
+  a.codes[1] = q.up->codes;
+  a.scales[0] = q.gate->scales;
+  a.scales[1] = q.up->scales;
+  a.K = q.d;
+  a.N = q.f;
+  a.E = q.E + q.S;
+  a.offsets = offsets;
+  a.act = q.act;
+  a.out = A;
+  a.out_stride = q.f;
+  a.status = status;
+  cudaError_t e = tiles<TileMode::GateUp>(a, *q.gate, xp, R_cap, q.d, pdl, s);
+  a.codes[0] = q.down->codes;
+  a.scales[0] = q.down->scales;
+  a.K = q.f;
+  a.N = q.d;
+  a.out = yp;
+  a.out_stride = q.d;
+  if (e == cudaSuccess) e = tiles<TileMode::Down>(a, *q.down, A, R_cap, q.f, pdl, s);
+  return e;
+}
+
+}  // namespace moe
