@@ -264,7 +264,7 @@ __device__ const double kExp2_32[32] = {
 // times the Taylor series of the rest r, |r| <= log(2) / 64 (r^6 / 720 < 2^-48; k times the
 // rounding of log(2) / 32 < 2^-47). Terms below
 // 2^-60 of the largest are left out.
-__device__ __noinline__ double denominator_64(const float* lrow, int E, int lane, float m) {
+static __device__ __noinline__ double denominator_64(const float* lrow, int E, int lane, float m) {
   const double tab = kExp2_32[lane], md = (double)m;
   double z = 0.0;
 #pragma unroll 4
@@ -297,7 +297,7 @@ __device__ __forceinline__ Row64 row_64(const SelArgs& a, const float* lrow, int
   return Row64{lrow, m, a.sigmoid || masked(m) ? 1.0 : denominator_64(lrow, a.E, lane, m)};
 }
 // the sort key of expert e's choice value
-__device__ __noinline__ u64 key_64(const SelArgs& a, const Row64& r, int e) {
+static __device__ __noinline__ u64 key_64(const SelArgs& a, const Row64& r, int e) {
   const float l = r.lrow[e];
   const u64 none = sort_key(-(double)INFINITY);
   if (masked(l)) return none;
@@ -310,7 +310,7 @@ __device__ __noinline__ u64 key_64(const SelArgs& a, const Row64& r, int e) {
 // The groups' border: `rank` is this lane's group's rank in fp32 (lanes L * g hold group
 // g's, n_groups <= 32), sure and kept by the fp32 ranks or in question. Those in question are
 // ranked again. Returns whether this lane's group stays.
-__device__ __noinline__ bool settle_groups(const SelArgs& a, const Row64& r, int lane, int L,
+static __device__ __noinline__ bool settle_groups(const SelArgs& a, const Row64& r, int lane, int L,
                                            bool question, bool sure) {
   const int gs = a.E / a.n_groups;
   const u64 none = sort_key(-(double)INFINITY);
@@ -350,7 +350,7 @@ __device__ __noinline__ bool settle_groups(const SelArgs& a, const Row64& r, int
 // The whole choice in 64 bits, for what the above do not take: more than 32 values near
 // a border (equal logits), groups that are no whole lanes. In loops, for short code.
 // Returns slot `lane`'s expert (lanes < k). row: E keys and, with groups, E more.
-__device__ __noinline__ int choose_64(const SelArgs& a, const Row64& r, int lane, u64* row) {
+static __device__ __noinline__ int choose_64(const SelArgs& a, const Row64& r, int lane, u64* row) {
   const u64 none = sort_key(-(double)INFINITY);
   for (int e = lane; e < a.E; e += 32) row[e] = key_64(a, r, e);
   __syncwarp();

@@ -106,28 +106,47 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 //   int4: 128 + 8 + value (0x4300 holds 128 with steps of 1)
 //   fp4:  2^-126 value: the code's exponent and mantissa as the low end of bf16's,
 //         which has subnormals where fp4 has them
+// then the values themselves (exact). The constants are held in registers that the compiler
+// does not know the contents of: it would load them again for every pair.
 template <bool FP4>
-__device__ __forceinline__ void w4_raw(uint32_t w, uint32_t* r) {
-  if (FP4) {
-    r[0] = w & 0x81C081C0u;
-    r[1] = (w << 3) & 0x81C081C0u;
-    r[2] = (w << 6) & 0x81C081C0u;
-    r[3] = ((w << 1) & 0x80008000u) | ((w >> 3) & 0x01800180u) | ((w >> 7) & 0x00400040u);
-  } else {
-    r[0] = (w & 0x000F000Fu) | 0x43004300u;
-    r[1] = ((w >> 4) & 0x000F000Fu) | 0x43004300u;
-    r[2] = ((w >> 8) & 0x000F000Fu) | 0x43004300u;
-    r[3] = ((w >> 12) & 0x000F000Fu) | 0x43004300u;
+struct W4Decoder {
+  uint32_t mask, base, last, sign;
+  __device__ __forceinline__ W4Decoder() {
+    if (FP4) {
+      asm volatile("mov.u32 %0, 0x81C081C0;" : "=r"(mask));
+      asm volatile("mov.u32 %0, 0x01800180;" : "=r"(base));
+      asm volatile("mov.u32 %0, 0x00400040;" : "=r"(sign));
+      asm volatile("mov.u32 %0, 0x7E807E80;" : "=r"(last));       // 2^126
+    } else {
+      asm volatile("mov.u32 %0, 0x000F000F;" : "=r"(mask));
+      asm volatile("mov.u32 %0, 0x43004300;" : "=r"(base));
+      asm volatile("mov.u32 %0, 0x43084308;" : "=r"(last));       // 136
+      sign = 0;
+    }
   }
-}
-// the values themselves (exact)
-template <bool FP4>
-__device__ __forceinline__ void w4_decode(uint32_t w, uint32_t* r) {
-  w4_raw<FP4>(w, r);
+  static __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));   // (a & b) | c
+    return r;
+  }
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t* r) const {
+    if (FP4) {
+      r[0] = w & mask;
+      r[1] = (w << 3) & mask;
+      r[2] = (w << 6) & mask;
+      r[3] = and_or(w >> 3, base, (w << 1) & 0x80008000u);
+      r[3] = and_or(w >> 7, sign, r[3]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = FP4 ? mul_bf16x2(r[i], 0x7E807E80u)           // 2^126
-               : sub_bf16x2(r[i], 0x43084308u);          // 136
-}
+      for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], last);
+    } else {
+      r[0] = and_or(w, mask, base);
+      r[1] = and_or(w >> 4, mask, base);
+      r[2] = and_or(w >> 8, mask, base);
+      r[3] = and_or(w >> 12, mask, base);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = sub_bf16x2(r[i], last);
+    }
+  }
+};
 
 }  // namespace moe

@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kPackThreads) w4_unpack_kernel(W4View w,
   const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int nb = n0 / 16 + tid / 32, c0 = 16 * (tid / 32);
   const int gps = w4_gps(w.group), kbs = w4_kblocks(w.K);
+  const W4Decoder<FP4> decode;
   if (nb < w4_nblocks(w.N)) {
     const moe_bf16* sp = w.scales + (int64_t)e * w4_scales_per_expert(w.K, w.N, w.group) +
                          (((int64_t)nb * w4_steps(w.K) + step) * 8 + g) * 2 * gps;
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kPackThreads) w4_unpack_kernel(W4View w,
         const int r0 = 64 * (kb & 1) + 16 * j + 4 * t;
         const int gr = (r0 * gps) >> 7;
         uint32_t p[4];
-        w4_decode<FP4>(word[j], p);
+        decode(word[j], p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float s = __bfloat162float(__ushort_as_bfloat16(sp[2 * gr + (i & 1)]));

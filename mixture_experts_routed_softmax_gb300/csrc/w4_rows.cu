@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(RowsArgs a) {
       if (rows == 0 || (a.by_pair && list[0] != y)) return;
     }
   }
+  const W4Decoder<FP4> decode;
   const int kbs = w4_kblocks(a.K), steps = w4_steps(a.K);
   const int nb0 = blockIdx.x * RB, nbs = w4_nblocks(a.N);
   const uint8_t* codes[MATS];
@@ -204,10 +205,10 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(RowsArgs a) {
           }
           const uint4 c = cw[r][h >> 1];
           uint32_t av[4];
-          w4_decode<FP4>((h & 1) ? c.z : c.x, av);
+          decode((h & 1) ? c.z : c.x, av);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816(part[nt], av, xv[nt][2 * h].x, xv[nt][2 * h].y);
-          w4_decode<FP4>((h & 1) ? c.w : c.y, av);
+          decode((h & 1) ? c.w : c.y, av);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma16816(part[nt], av, xv[nt][2 * h + 1].x, xv[nt][2 * h + 1].y);

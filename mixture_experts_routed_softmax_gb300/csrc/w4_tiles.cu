@@ -6,7 +6,7 @@
 // The weights are the A operand, 128 columns n of two matrices (gate and up) or of two
 // neighbouring runs of one, 64 k a step; up to 128 rows of x are the B operand, N = their
 // number rounded up to 16. A lives in tensor memory: sixteen warps take a 512-byte
-// tile of codes each a step, turn it into bf16 code * scale in registers (w4_decode, one
+// tile of codes each a step, turn it into bf16 code * scale in registers (W4Decoder, one
 // more product), and store it as the 16x256b shape, whose lanes hold just what a lane's
 // codes are. So the bf16 weights never pass through shared memory, whose bandwidth the
 // products' B operand and the codes share, and each code is read from L2 once for 128 rows.
@@ -28,16 +28,17 @@ namespace moe {
 enum class TileMode { Linear, GateUp, Down };
 
 constexpr int kTileRows = 128;              // rows of x a tile, at most
-constexpr int kXStages = 4;                 // of x and of A, in step
+constexpr int kXStages = 8;                 // of x
+constexpr int kAStages = 4;                 // of A in tensor memory
 constexpr int kXBytes = kTileRows * 128;    // 64 k of 128 rows
-constexpr int kCStages = 3;                 // of codes: four steps each
+constexpr int kCStages = 2;                 // of codes: four steps each
 constexpr int kCSteps = 4;
 constexpr int kCBytes = 16 * kCSteps * kW4Tile;
 constexpr int kDecWarp0 = 4, kDecWarps = 16, kOutWarp0 = 20, kOutWarps = 8;
 constexpr int kTileThreads = 32 * (kOutWarp0 + kOutWarps);
 constexpr int kAccCols = 256;               // two accumulators of 128 columns
 constexpr int kTileSmem =
-    1024 + kXStages * kXBytes + kCStages * (kCBytes + 4096) + 4 * (kMaxExperts + 1) + 256;
+    1024 + kXStages * kXBytes + kCStages * (kCBytes + 4096) + 4 * (kMaxExperts + 1) + 512;
 
 struct TileArgs {
   const uint8_t* codes[2];
@@ -70,6 +71,16 @@ __device__ __forceinline__ void umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 // untiled copy: 16-byte aligned addresses, size a multiple of 16
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -79,11 +90,35 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-// For a whole warp: true in all lanes, or (given up) false in all.
+// A bounded wait of one lane that sleeps in the barrier (10 us at a time) instead of taking
+// issue slots from the warps that decode; false as mbar_wait_bounded.
+static __device__ __noinline__ bool wait_asleep(uint32_t bar, uint32_t parity,
+                                                volatile int* abort_flag, int* status) {
+  const uint64_t t0 = global_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(10000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > (uint64_t)kWaitLimitNs) {
+      *abort_flag = 1;
+      raise_status(status, MOE_ERR_DEVICE_TIMEOUT);
+      return false;
+    }
+  }
+}
+// For a whole warp: true in all lanes, or (given up) false in all. The loop is out of
+// line: the roles' steady state has to stay small enough to be fetched.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* status) {
   if (__builtin_expect(__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)), 1)) return true;
-  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status));
+  return __all_sync(0xFFFFFFFFu, wait_asleep(bar, parity, abort_flag, status));
 }
 
 struct Tile {
@@ -103,25 +138,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t* s_codes = smem + kXStages * kXBytes;
   uint8_t* s_scales = s_codes + kCStages * kCBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_scales + kCStages * 4096);
-  int* tstart = reinterpret_cast<int*>(bars + 32);
+  int* tstart = reinterpret_cast<int*>(bars + 40);
   const uint32_t bar0 = smem_u32(bars);
   auto x_full = [&](int s) { return bar0 + 8u * s; };
-  auto a_full = [&](int s) { return bar0 + 8u * (kXStages + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (2 * kXStages + s); };      // x and A of a stage
-  auto c_full = [&](int s) { return bar0 + 8u * (3 * kXStages + s); };
-  auto c_empty = [&](int s) { return bar0 + 8u * (3 * kXStages + kCStages + s); };
-  const uint32_t acc_full = bar0 + 8u * (3 * kXStages + 2 * kCStages);
+  auto x_empty = [&](int s) { return bar0 + 8u * (kXStages + s); };
+  auto a_full = [&](int s) { return bar0 + 8u * (2 * kXStages + s); };
+  auto a_empty = [&](int s) { return bar0 + 8u * (2 * kXStages + kAStages + s); };
+  auto c_full = [&](int s) { return bar0 + 8u * (2 * kXStages + 2 * kAStages + s); };
+  auto c_empty = [&](int s) { return bar0 + 8u * (2 * kXStages + 2 * kAStages + kCStages + s); };
+  const uint32_t acc_full = bar0 + 8u * (2 * kXStages + 2 * kAStages + 2 * kCStages);
   const uint32_t acc_empty = acc_full + 8, drain = acc_full + 16;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 28);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 36);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  static_assert(3 * kXStages + 2 * kCStages + 3 <= 28, "barriers");
+  static_assert(2 * kXStages + 2 * kAStages + 2 * kCStages + 3 <= 36, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXStages; ++s) {
       mbar_init(x_full(s), 1);
+      mbar_init(x_empty(s), 1);
+    }
+    for (int s = 0; s < kAStages; ++s) {
       mbar_init(a_full(s), kDecWarps);
-      mbar_init(empty(s), 1);
+      mbar_init(a_empty(s), 1);
     }
     for (int s = 0; s < kCStages; ++s) {
       mbar_init(c_full(s), 1);
@@ -195,7 +234,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const Tile t = tile_at(i);
         const int boxes = (t.rows + 31) / 32;
         for (int ks = 0; ks < kbs; ++ks) {
-          if (!mbar_wait_bounded(empty(s), ph ^ 1u, s_abort, a.status)) {
+          if (!wait_asleep(x_empty(s), ph ^ 1u, s_abort, a.status)) {
             ok = false;
             break;
           }
@@ -259,97 +298,121 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp >= kDecWarp0 && warp < kOutWarp0) {
     // ------------------------------------------------------- codes into bf16 --
+    // A step's stores to tensor memory are waited for when the next step's values are
+    // ready, so that their latency is not the warp's own.
     const int q = warp & 3, i4 = (warp - kDecWarp0) >> 2, mat = i4 >> 1, half = i4 & 1;
     const int slot = 8 * mat + 2 * q + half, g = lane >> 2;
-    const uint32_t lane_at = (uint32_t)(32 * q + 16 * half) << 16;
-    int s = 0, cs = 0;
+    const uint32_t dst0 = tmem + ((uint32_t)(32 * q + 16 * half) << 16) + kAccCols + 32 * mat;
+    const uint8_t* codes0 = s_codes + slot * kCSteps * kW4Tile + 16 * lane;
+    const uint8_t* scales0 = s_scales + slot * kSBytes + g * 4 * GPS;
+    const uint32_t full0 = a_full(0), empty0 = a_empty(0);
+    const W4Decoder<FP4> decode;
+    int s = 0, cs = 0, before = -1;          // before: the stage whose stores are under way
     uint32_t ph = 0, cph = 0;
     bool ok = true;
+    auto stored = [&]() {
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full0 + 8u * before);
+    };
     for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
-      const Tile t = tile_at(i);
-      for (int ks = 0; ks < kbs; ++ks) {
-        const int sub = ks % kCSteps;
-        if (sub == 0 && !wait_all(c_full(cs), cph, s_abort, a.status)) {
+      for (int ks = 0; ks < kbs && ok; ks += kCSteps) {
+        if (!wait_all(c_full(cs), cph, s_abort, a.status)) {
           ok = false;
           break;
         }
-        const uint4 c = *reinterpret_cast<const uint4*>(s_codes + cs * kCBytes +
-                                                        (slot * kCSteps + sub) * kW4Tile + 16 * lane);
-        const uint8_t* sp = s_scales + cs * 4096 + slot * kSBytes + (sub >> 1) * 32 * GPS + g * 4 * GPS;
-        uint32_t sw[2];
-        if (GPS == 4) {
-          const uint2 v = *reinterpret_cast<const uint2*>(sp + 8 * (sub & 1));
-          sw[0] = v.x;
-          sw[1] = v.y;
-        } else {
-          sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(sp + (GPS == 2 ? 4 * (sub & 1) : 0));
-        }
-        uint32_t r[16];
-        const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+        const uint8_t* cp = codes0 + cs * kCBytes;
+        const uint8_t* sp = scales0 + cs * 4096;
+        const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
+#pragma unroll 1
+        for (int sub = 0; sub < n; ++sub) {
+          const uint4 c = *reinterpret_cast<const uint4*>(cp);
+          uint32_t sw[2];
+          if (GPS == 4) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sp);
+            sw[0] = v.x;
+            sw[1] = v.y;
+          } else {
+            sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(sp);
+          }
+          cp += kW4Tile;
+          // the next step: the other half of these 128 rows, or the next 128
+          sp += (sub & 1) ? 32 * GPS - (GPS == 4 ? 8 : GPS == 2 ? 4 : 0)
+                          : (GPS == 4 ? 8 : GPS == 2 ? 4 : 0);
+          uint32_t r[16];
+          const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t p[4];
-          w4_decode<FP4>(word[j], p);
-          const uint32_t lo = __byte_perm(sw[j >> 1], 0, 0x1010), hi = __byte_perm(sw[j >> 1], 0, 0x3232);
-          r[4 * j + 0] = mul_bf16x2(p[0], lo);
-          r[4 * j + 1] = mul_bf16x2(p[2], lo);
-          r[4 * j + 2] = mul_bf16x2(p[1], hi);
-          r[4 * j + 3] = mul_bf16x2(p[3], hi);
+          for (int j = 0; j < 4; ++j) {
+            uint32_t p[4];
+            decode(word[j], p);
+            const uint32_t lo = __byte_perm(sw[j >> 1], 0, 0x1010);
+            const uint32_t hi = __byte_perm(sw[j >> 1], 0, 0x3232);
+            r[4 * j + 0] = mul_bf16x2(p[0], lo);
+            r[4 * j + 1] = mul_bf16x2(p[2], lo);
+            r[4 * j + 2] = mul_bf16x2(p[1], hi);
+            r[4 * j + 3] = mul_bf16x2(p[3], hi);
+          }
+          if (before >= 0) stored();
+          if (!wait_all(empty0 + 8u * s, ph ^ 1u, s_abort, a.status)) {
+            ok = false;
+            before = -1;
+            break;
+          }
+          tc_fence_after();
+          tmem_st_16x256b_x4(dst0 + 64 * s, r);
+          before = s;
+          if (++s == kAStages) { s = 0; ph ^= 1u; }
         }
-        if (sub == kCSteps - 1 || ks == kbs - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(c_empty(cs));
-          if (++cs == kCStages) { cs = 0; cph ^= 1u; }
-        }
-        if (!wait_all(empty(s), ph ^ 1u, s_abort, a.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        tmem_st_16x256b_x4(tmem + lane_at + kAccCols + 64 * s + 32 * mat, r);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
+        if (lane == 0) mbar_arrive(c_empty(cs));
         __syncwarp();
-        if (lane == 0) mbar_arrive(a_full(s));
-        if (++s == kXStages) { s = 0; ph ^= 1u; }
+        if (++cs == kCStages) { cs = 0; cph ^= 1u; }
       }
     }
+    if (before >= 0) stored();
   } else if (warp == 1) {
     // -------------------------------------------------------------- products --
-    int s = 0;
-    uint32_t ph = 0, acc_ph = 0;
+    // Addresses and descriptors go through a shuffle once, so that they stay in uniform
+    // registers: issued by a lane of a divergent branch, a step's eight products took
+    // that lane 840 cycles, longer than the decoding.
+    const bool leader = elect_one();
+    const uint32_t td = uniform(tmem), bars_u = uniform(bar0);
+    const uint64_t bd0 = sdesc_sw128(smem_u32(smem), 16, 1024);
+    const uint32_t b_lo = uniform((uint32_t)bd0), b_hi = uniform((uint32_t)(bd0 >> 32));
+    int s = 0, xs = 0;
+    uint32_t ph = 0, xph = 0, acc_ph = 0;
     bool ok = true;
     for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
       const Tile t = tile_at(i);
       if (!wait_all(acc_empty, acc_ph ^ 1u, s_abort, a.status)) break;
-      const uint32_t idesc = idesc_bf16(128, (t.rows + 15) & ~15, 0, 0);
+      const uint32_t idesc = uniform(idesc_bf16(128, (t.rows + 15) & ~15, 0, 0));
       for (int ks = 0; ks < kbs; ++ks) {
-        if (!wait_all(x_full(s), ph, s_abort, a.status) ||
+        if (!wait_all(x_full(xs), xph, s_abort, a.status) ||
             !wait_all(a_full(s), ph, s_abort, a.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t xa = smem_u32(smem) + s * kXBytes, at = tmem + kAccCols + 64 * s;
+        const uint32_t at = td + kAccCols + 64 * s, b = b_lo + xs * (kXBytes >> 4);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t bd = sdesc_sw128(xa + 32 * kk, 16, 1024);
-            umma_tmem_a(tmem, at + 8 * kk, bd, idesc, ks > 0 || kk > 0);
-            umma_tmem_a(tmem + 128, at + 32 + 8 * kk, bd, idesc, ks > 0 || kk > 0);
+            const uint64_t bd = ((uint64_t)b_hi << 32) | (b + kk * (32 >> 4));
+            umma_tmem_a(td, at + 8 * kk, bd, idesc, ks > 0 || kk > 0);
+            umma_tmem_a(td + 128, at + 32 + 8 * kk, bd, idesc, ks > 0 || kk > 0);
           }
-          umma_commit(empty(s));
+          umma_commit(bars_u + 8u * (2 * kXStages + kAStages + s));     // a_empty
+          umma_commit(bars_u + 8u * (kXStages + xs));                   // x_empty
         }
-        __syncwarp();
-        if (++s == kXStages) { s = 0; ph ^= 1u; }
+        if (++s == kAStages) { s = 0; ph ^= 1u; }
+        if (++xs == kXStages) { xs = 0; xph ^= 1u; }
       }
       if (!ok) break;
-      if (lane == 0) umma_commit(acc_full);
-      __syncwarp();
+      if (leader) umma_commit(acc_full);
       acc_ph ^= 1u;
     }
     // every product has ended before tensor memory is freed
-    if (lane == 0) {
+    if (leader) {
       umma_commit(drain);
       volatile int never = 0;
       mbar_wait_bounded(drain, 0, &never, a.status);
@@ -366,27 +429,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc_fence_after();
       const int n = t.n0 + 32 * q + lane;
       for (int c0 = 16 * part; c0 < t.rows; c0 += 32) {
-        uint32_t v[2][16];
-        tmem_ld16(at + c0, v[0]);
-        tmem_ld16(at + 128 + c0, v[1]);
+        uint32_t v0[16], v1[16];
+        tmem_ld16(at + c0, v0);
+        tmem_ld16(at + 128 + c0, v1);
         tmem_ld_wait();
+        const int64_t first = (t.m0 + c0) * a.out_stride + n;
+        const int here = t.rows - c0;       // rows of these sixteen
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const int64_t row = t.m0 + c0 + c;
-          if (c0 + c >= t.rows) continue;
-          const float v0 = __uint_as_float(v[0][c]), v1 = __uint_as_float(v[1][c]);
+          const float f0 = __uint_as_float(v0[c]), f1 = __uint_as_float(v1[c]);
+          const bool in0 = c < here && n < a.N, in1 = c < here && n + 128 < a.N;
+          const int64_t o = first + c * a.out_stride;
           if (M == TileMode::GateUp) {
-            if (n < a.N)
-              static_cast<moe_bf16*>(a.out)[row * a.out_stride + n] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(gated(v0, v1, a.act)));
+            const float y = gated(f0, f1, a.act);
+            if (in0)
+              static_cast<moe_bf16*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
           } else if (M == TileMode::Down || a.out_fp32) {
-            float* o = static_cast<float*>(a.out) + row * a.out_stride + n;
-            if (n < a.N) o[0] = v0;
-            if (n + 128 < a.N) o[128] = v1;
+            if (in0) static_cast<float*>(a.out)[o] = f0;
+            if (in1) static_cast<float*>(a.out)[o + 128] = f1;
           } else {
-            moe_bf16* o = static_cast<moe_bf16*>(a.out) + row * a.out_stride + n;
-            if (n < a.N) o[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v0));
-            if (n + 128 < a.N) o[128] = __bfloat16_as_ushort(__float2bfloat16_rn(v1));
+            if (in0)
+              static_cast<moe_bf16*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(f0));
+            if (in1)
+              static_cast<moe_bf16*>(a.out)[o + 128] = __bfloat16_as_ushort(__float2bfloat16_rn(f1));
           }
         }
       }
