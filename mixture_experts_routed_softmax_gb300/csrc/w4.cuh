@@ -5,8 +5,10 @@
 // Kinds: int4, -8 .. 7; fp4, +-{0, 1/2, 1, 3/2, 2, 3, 4, 6} (a sign, two bits of
 // exponent, one of mantissa). Scales are bf16.
 //
-// Codes lie in tiles of 16 columns n by 64 rows k, 512 bytes each, the tiles of a
-// column block one after the other: a block's weights are one contiguous stream.
+// Codes lie in tiles of 16 columns n by 64 rows k, 512 bytes each. 8 x 4 of them, 128
+// columns by 256 rows, are one contiguous piece (16 KB, one copy into shared memory), column
+// block after column block and in one row after row; then come the next 256 rows of the
+// same columns (w4_tile_at). At the right and lower edge pieces are as small as what there is.
 // In a tile lane (g, t) = (lane / 4, lane % 4) owns 16 bytes, columns g and g + 8 at the
 // rows 16j + 4t .. + 3, word j = 0 .. 3. So word j is
 //   - the A operand of an m16n8k16 product whose B operand is four neighbouring
@@ -22,8 +24,8 @@
 //   fp4:  sign and three magnitude bits where a shift leaves them in a bf16's
 //         place: i = 0: 15, 8..6; 1: 12, 5..3; 2: 9, 2..0; 3: 14, 11..10 and 13
 //
-// Scales lie by steps of 128 rows: [block of 16 columns][step][g][groups of the
-// step][columns g, g + 8].
+// Scales lie in the same pieces, by steps of 128 rows: a step of 16 columns holds
+// [g][groups of the step][columns g, g + 8] (w4_scales_at).
 #pragma once
 #include "common.cuh"
 #include "internal.h"
@@ -42,6 +44,20 @@ __host__ __device__ constexpr int64_t w4_codes_per_expert(int K, int N) {
 // elements
 __host__ __device__ constexpr int64_t w4_scales_per_expert(int K, int N, int group) {
   return (int64_t)w4_nblocks(N) * w4_steps(K) * 16 * w4_gps(group);
+}
+
+// bytes in front of the tile of column block nb and row block kb, in an expert
+__host__ __device__ __forceinline__ int64_t w4_tile_at(int nb, int kb, int nbs, int kbs) {
+  const int b = nb & ~7, cb = nbs - b < 8 ? nbs - b : 8;
+  const int c = kb & ~3, m = kbs - c < 4 ? kbs - c : 4;
+  return ((int64_t)b * kbs + (int64_t)c * cb + (nb - b) * m + (kb - c)) * kW4Tile;
+}
+// elements in front of the scales of column block nb and step `st`
+__host__ __device__ __forceinline__ int64_t w4_scales_at(int nb, int st, int nbs, int steps,
+                                                         int gps) {
+  const int b = nb & ~7, cb = nbs - b < 8 ? nbs - b : 8;
+  const int c = st & ~1, m = steps - c < 2 ? 1 : 2;
+  return ((int64_t)b * steps + (int64_t)c * cb + (nb - b) * m + (st - c)) * 16 * gps;
 }
 
 // the bit of a pair's low half that holds bit b (0: lowest) of the fp4 code

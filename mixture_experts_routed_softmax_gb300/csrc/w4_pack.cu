@@ -145,11 +145,11 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
         }
     uint4* dst = reinterpret_cast<uint4*>(w.codes +
                                           (int64_t)e * w4_codes_per_expert(w.K, w.N) +
-                                          ((int64_t)nb * kbs + kb) * kW4Tile);
+                                          w4_tile_at(nb, kb, w4_nblocks(w.N), kbs));
     dst[lane] = make_uint4(word[0], word[1], word[2], word[3]);
   }
   moe_bf16* out = w.scales + (int64_t)e * w4_scales_per_expert(w.K, w.N, w.group) +
-                  ((int64_t)nb * w4_steps(w.K) + step) * 16 * gps;
+                  w4_scales_at(nb, step, w4_nblocks(w.N), w4_steps(w.K), gps);
   for (int i = lane; i < 16 * gps; i += 32) {
     const int gg = i / (2 * gps), gr = (i / 2) % gps, hi = i & 1;
     out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(sc[gr][c0 + gg + 8 * hi]));
@@ -170,11 +170,12 @@ __global__ void __launch_bounds__(kPackThreads) w4_unpack_kernel(W4View w,
   const W4Decoder<FP4> decode;
   if (nb < w4_nblocks(w.N)) {
     const moe_bf16* sp = w.scales + (int64_t)e * w4_scales_per_expert(w.K, w.N, w.group) +
-                         (((int64_t)nb * w4_steps(w.K) + step) * 8 + g) * 2 * gps;
+                         w4_scales_at(nb, step, w4_nblocks(w.N), w4_steps(w.K), gps) +
+                         2 * gps * g;
     for (int kb = 2 * step; kb < 2 * step + 2 && kb < kbs; ++kb) {
       const uint4 v = *reinterpret_cast<const uint4*>(
           w.codes + (int64_t)e * w4_codes_per_expert(w.K, w.N) +
-          ((int64_t)nb * kbs + kb) * kW4Tile + 16 * lane);
+          w4_tile_at(nb, kb, w4_nblocks(w.N), kbs) + 16 * lane);
       const uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

@@ -168,11 +168,11 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(RowsArgs a) {
 #pragma unroll
         for (int q = 0; q < GPS; ++q) sw[r][q] = 0u;
         if (nb < nbs) {
-          const uint8_t* src = codes[m] + ((int64_t)nb * kbs + 2 * step) * kW4Tile;
+          const uint8_t* src = codes[m] + w4_tile_at(nb, 2 * step, nbs, kbs);
           cw[r][0] = ldg_stream(src);
           if (second) cw[r][1] = ldg_stream(src + kW4Tile);
           const uint32_t* sp = reinterpret_cast<const uint32_t*>(
-              scales[m] + ((int64_t)nb * steps + step) * 16 * GPS);
+              scales[m] + w4_scales_at(nb, step, nbs, steps, GPS));
           if (GPS == 4) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(sp));
             sw[r][0] = v.x; sw[r][1 % GPS] = v.y; sw[r][2 % GPS] = v.z; sw[r][3 % GPS] = v.w;

@@ -13,7 +13,7 @@
 // code * scale is rounded to bf16 there; scales of few bits (moe_w4_quantise's) make it exact.
 //
 // Roles (28 warps): 0 loads rows of x by TMA, a step a stage; 3 streams the codes
-// and scales, contiguous runs of four steps a tile, by bulk copies; 4-19 the sixteen above;
+// and scales, a contiguous piece of four steps a matrix, by bulk copies; 4-19 the sixteen above;
 // 1 issues the products; 20-27 take the finished tile from tensor memory (a thread a
 // column n, so a warp stores 32 neighbouring columns of a row). Tensor memory: 2 x 128
 // columns of accumulators, four stages of 64 columns of A. Every wait is bounded.
@@ -130,7 +130,6 @@ template <TileMode M, bool FP4, int GPS>
 __global__ void __launch_bounds__(kTileThreads, 1)
     w4_tiles_kernel(const __grid_constant__ CUtensorMap mapX, const TileArgs a) {
   pdl_enter();
-  constexpr int kSBytes = 64 * GPS;                    // scales of a tile's two steps of 128
   constexpr int kWide = M == TileMode::GateUp ? 128 : 256;   // columns n a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -226,66 +225,81 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------- rows of x --
+    const bool leader = elect_one();
+    const uint32_t x0 = uniform(smem_u32(smem)), full0 = uniform(bar0);
     int s = 0, fills = 0;
     uint32_t ph = 0;
     bool ok = true;
-    if (lane == 0) {
-      for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
-        const Tile t = tile_at(i);
-        const int boxes = (t.rows + 31) / 32;
-        for (int ks = 0; ks < kbs; ++ks) {
-          if (!wait_asleep(x_empty(s), ph ^ 1u, s_abort, a.status)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(x_full(s), boxes * 4096);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_3d(smem_u32(smem) + s * kXBytes + b * 4096, &mapX, x_full(s), ks * 64, 0,
-                        (int)t.m0 + 32 * b);
-          ++fills;
-          if (++s == kXStages) { s = 0; ph ^= 1u; }
+    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      const Tile t = tile_at(i);
+      const int boxes = uniform((t.rows + 31) / 32), m0 = uniform((int)t.m0);
+      for (int ks = 0; ks < kbs; ++ks) {
+        if (!wait_all(x_empty(s), ph ^ 1u, s_abort, a.status)) {
+          ok = false;
+          break;
         }
+        const uint32_t full = full0 + 8u * s, dst = x0 + s * kXBytes;
+        if (leader) {
+          mbar_arrive_expect_tx(full, boxes * 4096);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (b < boxes) tma_load_3d(dst + b * 4096, &mapX, full, ks * 64, 0, m0 + 32 * b);
+        }
+        ++fills;
+        if (++s == kXStages) { s = 0; ph ^= 1u; }
       }
-      // copies already issued land before the block's shared memory goes away
-      volatile int never = 0;
-      for (int n = fills < kXStages ? fills : kXStages; n > 0; --n) {
-        if (--s < 0) { s = kXStages - 1; ph ^= 1u; }
-        mbar_wait_bounded(x_full(s), ph, &never, a.status);
-      }
+    }
+    // copies already issued land before the block's shared memory goes away
+    volatile int never = 0;
+    for (int n = fills < kXStages ? fills : kXStages; n > 0; --n) {
+      if (--s < 0) { s = kXStages - 1; ph ^= 1u; }
+      mbar_wait_bounded(x_full(s), ph, &never, a.status);
     }
   } else if (warp == 3) {
     // ------------------------------------------------------ codes and scales --
-    // lanes 0-15 copy a tile's codes each, 16-31 its scales
+    // a piece of each matrix a stage: 128 columns by 256 rows of codes, their scales
+    const bool leader = elect_one();
+    const uint32_t codes_s = uniform(smem_u32(s_codes)), scales_s = uniform(smem_u32(s_scales));
+    const uint32_t full0 = uniform(c_full(0));
     int s = 0, fills = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const int j = lane & 15, mat = j >> 3, nbl = j & 7;
     for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
       const Tile t = tile_at(i);
-      const int nb = t.n0 / 16 + (M == TileMode::GateUp ? nbl : 8 * mat + nbl);
-      const int m = M == TileMode::GateUp ? mat : 0;
-      const int present = __popc(__ballot_sync(0xFFFFFFFFu, lane < 16 && nb < nbs));
-      const uint8_t* src =
-          lane < 16 ? a.codes[m] + t.e * w4_codes_per_expert(a.K, a.N) + (int64_t)nb * kbs * kW4Tile
-                    : reinterpret_cast<const uint8_t*>(a.scales[m] +
-                                                       t.e * w4_scales_per_expert(a.K, a.N, 128 / GPS) +
-                                                       (int64_t)nb * steps * 16 * GPS);
+      const int64_t ec = t.e * w4_codes_per_expert(a.K, a.N);
+      const int64_t es = t.e * w4_scales_per_expert(a.K, a.N, 128 / GPS);
+      int cb[2];
+      const uint8_t* csrc[2];
+      const moe_bf16* ssrc[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int nb = t.n0 / 16 + (M == TileMode::GateUp ? 0 : 8 * m);
+        const int mat = M == TileMode::GateUp ? m : 0;
+        cb[m] = uniform(max(0, min(8, nbs - nb)));
+        csrc[m] = a.codes[mat] + ec + (int64_t)nb * kbs * kW4Tile;
+        ssrc[m] = a.scales[mat] + es + (int64_t)nb * steps * 16 * GPS;
+      }
       for (int ks = 0; ks < kbs; ks += kCSteps) {
         if (!wait_all(c_empty(s), ph ^ 1u, s_abort, a.status)) {
           ok = false;
           break;
         }
         const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
-        const uint32_t cb = n * kW4Tile, sb = (n + 1) / 2 * 32 * GPS;
-        if (lane == 0) mbar_arrive_expect_tx(c_full(s), present * (cb + sb));
-        __syncwarp();
-        if (nb < nbs) {
-          if (lane < 16)
-            bulk_load(smem_u32(s_codes) + s * kCBytes + j * kCSteps * kW4Tile,
-                      src + (int64_t)ks * kW4Tile, cb, c_full(s));
-          else
-            bulk_load(smem_u32(s_scales) + s * 4096 + j * kSBytes,
-                      src + (int64_t)(ks / 2) * 32 * GPS, sb, c_full(s));
+        const uint32_t cbytes = n * kW4Tile, sbytes = (n + 1) / 2 * 32 * GPS;
+        const uint32_t full = full0 + 8u * s;
+        if (leader) {
+          mbar_arrive_expect_tx(full, (cb[0] + cb[1]) * (cbytes + sbytes));
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            if (cb[m]) {
+              bulk_load(codes_s + s * kCBytes + m * (kCBytes / 2), csrc[m], cb[m] * cbytes, full);
+              bulk_load(scales_s + s * 4096 + m * 2048, ssrc[m], cb[m] * sbytes, full);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          csrc[m] += cb[m] * cbytes;
+          ssrc[m] += cb[m] * sbytes / 2;
         }
         ++fills;
         if (++s == kCStages) { s = 0; ph ^= 1u; }
@@ -301,10 +315,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // A step's stores to tensor memory are waited for when the next step's values are
     // ready, so that their latency is not the warp's own.
     const int q = warp & 3, i4 = (warp - kDecWarp0) >> 2, mat = i4 >> 1, half = i4 & 1;
-    const int slot = 8 * mat + 2 * q + half, g = lane >> 2;
+    const int slot = 2 * q + half, g = lane >> 2;
     const uint32_t dst0 = tmem + ((uint32_t)(32 * q + 16 * half) << 16) + kAccCols + 32 * mat;
-    const uint8_t* codes0 = s_codes + slot * kCSteps * kW4Tile + 16 * lane;
-    const uint8_t* scales0 = s_scales + slot * kSBytes + g * 4 * GPS;
+    const uint8_t* codes0 = s_codes + mat * (kCBytes / 2) + 16 * lane;
+    const uint8_t* scales0 = s_scales + mat * 2048 + g * 4 * GPS;
     const uint32_t full0 = a_full(0), empty0 = a_empty(0);
     const W4Decoder<FP4> decode;
     int s = 0, cs = 0, before = -1;          // before: the stage whose stores are under way
@@ -322,47 +336,52 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = false;
           break;
         }
-        const uint8_t* cp = codes0 + cs * kCBytes;
-        const uint8_t* sp = scales0 + cs * 4096;
         const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
+        const uint8_t* cp = codes0 + cs * kCBytes + slot * n * kW4Tile;
+        const uint8_t* sp = scales0 + cs * 4096 + slot * ((n + 1) / 2) * 32 * GPS;
 #pragma unroll 1
-        for (int sub = 0; sub < n; ++sub) {
-          const uint4 c = *reinterpret_cast<const uint4*>(cp);
-          uint32_t sw[2];
+        for (int sub = 0; sub < n && ok; sub += 2) {
+          uint32_t sw[4];                  // of the step's runs of 32 rows
           if (GPS == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(sp);
+            sw[0] = v.x; sw[1] = v.y; sw[2] = v.z; sw[3] = v.w;
+          } else if (GPS == 2) {
             const uint2 v = *reinterpret_cast<const uint2*>(sp);
-            sw[0] = v.x;
-            sw[1] = v.y;
+            sw[0] = sw[1] = v.x;
+            sw[2] = sw[3] = v.y;
           } else {
-            sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(sp);
+            sw[0] = sw[1] = sw[2] = sw[3] = *reinterpret_cast<const uint32_t*>(sp);
           }
-          cp += kW4Tile;
-          // the next step: the other half of these 128 rows, or the next 128
-          sp += (sub & 1) ? 32 * GPS - (GPS == 4 ? 8 : GPS == 2 ? 4 : 0)
-                          : (GPS == 4 ? 8 : GPS == 2 ? 4 : 0);
-          uint32_t r[16];
-          const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+          sp += 32 * GPS;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t p[4];
-            decode(word[j], p);
-            const uint32_t lo = __byte_perm(sw[j >> 1], 0, 0x1010);
-            const uint32_t hi = __byte_perm(sw[j >> 1], 0, 0x3232);
-            r[4 * j + 0] = mul_bf16x2(p[0], lo);
-            r[4 * j + 1] = mul_bf16x2(p[2], lo);
-            r[4 * j + 2] = mul_bf16x2(p[1], hi);
-            r[4 * j + 3] = mul_bf16x2(p[3], hi);
+          for (int h = 0; h < 2; ++h) {
+            if (sub + h >= n) break;
+            const uint4 c = *reinterpret_cast<const uint4*>(cp + h * kW4Tile);
+            uint32_t r[16];
+            const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t p[4];
+              decode(word[j], p);
+              const uint32_t w = sw[2 * h + (j >> 1)];
+              const uint32_t lo = __byte_perm(w, 0, 0x1010), hi = __byte_perm(w, 0, 0x3232);
+              r[4 * j + 0] = mul_bf16x2(p[0], lo);
+              r[4 * j + 1] = mul_bf16x2(p[2], lo);
+              r[4 * j + 2] = mul_bf16x2(p[1], hi);
+              r[4 * j + 3] = mul_bf16x2(p[3], hi);
+            }
+            if (before >= 0) stored();
+            if (!wait_all(empty0 + 8u * s, ph ^ 1u, s_abort, a.status)) {
+              ok = false;
+              before = -1;
+              break;
+            }
+            tc_fence_after();
+            tmem_st_16x256b_x4(dst0 + 64 * s, r);
+            before = s;
+            if (++s == kAStages) { s = 0; ph ^= 1u; }
           }
-          if (before >= 0) stored();
-          if (!wait_all(empty0 + 8u * s, ph ^ 1u, s_abort, a.status)) {
-            ok = false;
-            before = -1;
-            break;
-          }
-          tc_fence_after();
-          tmem_st_16x256b_x4(dst0 + 64 * s, r);
-          before = s;
-          if (++s == kAStages) { s = 0; ph ^= 1u; }
+          cp += 2 * kW4Tile;
         }
         if (lane == 0) mbar_arrive(c_empty(cs));
         __syncwarp();
