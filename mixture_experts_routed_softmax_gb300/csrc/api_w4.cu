@@ -71,7 +71,7 @@ size_t moe_w4_codes_bytes(int E, int K, int N) {
 size_t moe_w4_scales_bytes(int E, int K, int N, int group) {
   return check_dims(E, K, N) || !group_ok(group)
              ? 0
-             : (size_t)E * w4_scales_per_expert(K, N, group) * sizeof(moe_bf16);
+             : w4_flags_at(E, K, N, group) * sizeof(moe_bf16) + ((size_t)E * 4 + 15) / 16 * 16;
 }
 
 int moe_w4_quantise(const moe_w4* w, const moe_bf16* src, moe_stream_t stream) {

@@ -118,26 +118,31 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return r;
 }
 
-// A word's four pairs as bf16 with an offset or factor of the kind:
+// A word's four pairs as bf16 values (exact), from an offset or factor of the kind:
 //   int4: 128 + 8 + value (0x4300 holds 128 with steps of 1)
 //   fp4:  2^-126 value: the code's exponent and mantissa as the low end of bf16's,
 //         which has subnormals where fp4 has them
-// then the values themselves (exact). The constants are held in registers that the compiler
-// does not know the contents of: it would load them again for every pair.
+// scaled: value * scale, rounded to bf16 once. `plain` scales (plain_scale) take one
+// operation a pair instead of two:
+//   int4: 160 + 4 value in place of 136 + value, fma(that, scale / 4, -40 scale): with five
+//         significant bits in a scale 40 scale has eight, so the sum rounds as the product does
+//   fp4:  scale * 2^126 in one factor
+// The constants are held in registers that the compiler does not know the contents of: it
+// would load them again for every pair.
 template <bool FP4>
 struct W4Decoder {
-  uint32_t mask, base, last, sign;
+  uint32_t mask, base, last, mask2;
   __device__ __forceinline__ W4Decoder() {
     if (FP4) {
       asm volatile("mov.u32 %0, 0x81C081C0;" : "=r"(mask));
       asm volatile("mov.u32 %0, 0x01800180;" : "=r"(base));
-      asm volatile("mov.u32 %0, 0x00400040;" : "=r"(sign));
+      asm volatile("mov.u32 %0, 0x00400040;" : "=r"(mask2));
       asm volatile("mov.u32 %0, 0x7E807E80;" : "=r"(last));       // 2^126
     } else {
       asm volatile("mov.u32 %0, 0x000F000F;" : "=r"(mask));
       asm volatile("mov.u32 %0, 0x43004300;" : "=r"(base));
       asm volatile("mov.u32 %0, 0x43084308;" : "=r"(last));       // 136
-      sign = 0;
+      asm volatile("mov.u32 %0, 0x003C003C;" : "=r"(mask2));
     }
   }
   static __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
@@ -145,13 +150,16 @@ struct W4Decoder {
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));   // (a & b) | c
     return r;
   }
+  __device__ __forceinline__ void raw_fp4(uint32_t w, uint32_t* r) const {
+    r[0] = w & mask;
+    r[1] = (w << 3) & mask;
+    r[2] = (w << 6) & mask;
+    r[3] = and_or(w >> 3, base, (w << 1) & 0x80008000u);
+    r[3] = and_or(w >> 7, mask2, r[3]);
+  }
   __device__ __forceinline__ void operator()(uint32_t w, uint32_t* r) const {
     if (FP4) {
-      r[0] = w & mask;
-      r[1] = (w << 3) & mask;
-      r[2] = (w << 6) & mask;
-      r[3] = and_or(w >> 3, base, (w << 1) & 0x80008000u);
-      r[3] = and_or(w >> 7, sign, r[3]);
+      raw_fp4(w, r);
 #pragma unroll
       for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], last);
     } else {
@@ -163,6 +171,50 @@ struct W4Decoder {
       for (int i = 0; i < 4; ++i) r[i] = sub_bf16x2(r[i], last);
     }
   }
+  // factors of a scale pair (both halves the same) for `scaled`
+  struct Factor {
+    uint32_t f, c;
+  };
+  template <bool PLAIN>
+  __device__ __forceinline__ Factor factor(uint32_t s2) const {
+    if (!PLAIN) return Factor{s2, 0u};
+    if (FP4) return Factor{mul_bf16x2(s2, last), 0u};
+    return Factor{mul_bf16x2(s2, 0x3E803E80u), mul_bf16x2(s2, 0xC220C220u)};   // 1/4, -40
+  }
+  template <bool PLAIN>
+  __device__ __forceinline__ void scaled(uint32_t w, const Factor& lo, const Factor& hi,
+                                         uint32_t* r) const {
+    if (!PLAIN) {
+      (*this)(w, r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], (i & 1) ? hi.f : lo.f);
+    } else if (FP4) {
+      raw_fp4(w, r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], (i & 1) ? hi.f : lo.f);
+    } else {
+      r[0] = and_or(w << 2, mask2, base);
+      r[1] = and_or(w >> 2, mask2, base);
+      r[2] = and_or(w >> 6, mask2, base);
+      r[3] = and_or(w >> 10, mask2, base);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        r[i] = fma_bf16x2(r[i], (i & 1) ? hi.f : lo.f, (i & 1) ? hi.c : lo.c);
+    }
+  }
 };
+
+// Whether a scale (bf16 bits) takes the short form of `scaled`: int4, at most five
+// significant bits and far from either end of the range; fp4, below 2. NaN and 0 do.
+__device__ __forceinline__ bool plain_scale(uint32_t bits, bool fp4) {
+  const uint32_t a = bits & 0x7FFFu;
+  if (a == 0u || a > 0x7F80u) return true;
+  if (fp4) return a < 0x4000u;
+  return (a & 7u) == 0u && a >= 0x0800u && a < 0x7700u;
+}
+// The arrays of scales end with a word an expert: not 0 where some scale is not plain.
+__host__ __device__ __forceinline__ int64_t w4_flags_at(int64_t E, int K, int N, int group) {
+  return E * w4_scales_per_expert(K, N, group);          // elements; a multiple of 16
+}
 
 }  // namespace moe

@@ -150,10 +150,15 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
   }
   moe_bf16* out = w.scales + (int64_t)e * w4_scales_per_expert(w.K, w.N, w.group) +
                   w4_scales_at(nb, step, w4_nblocks(w.N), w4_steps(w.K), gps);
+  bool plain = true;
   for (int i = lane; i < 16 * gps; i += 32) {
     const int gg = i / (2 * gps), gr = (i / 2) % gps, hi = i & 1;
     out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(sc[gr][c0 + gg + 8 * hi]));
+    plain = plain && plain_scale(out[i], FP4);
   }
+  // (or-ed: the order does not matter)
+  if (!plain)
+    atomicOr(reinterpret_cast<uint32_t*>(w.scales + w4_flags_at(w.E, w.K, w.N, w.group)) + e, 1u);
 }
 
 // Back to bf16 [E, K, N]: code * scale, rounded (exact for the scales above).
@@ -214,8 +219,11 @@ cudaError_t launch_w4_pack(const moe_w4& w, const moe_bf16* src, const uint8_t* 
   const bool fp4 = w.kind == MOE_W4_FP4;
   const auto kernel = src ? (fp4 ? w4_pack_kernel<0, true> : w4_pack_kernel<0, false>)
                           : (fp4 ? w4_pack_kernel<1, true> : w4_pack_kernel<1, false>);
-  const cudaError_t e = launch_pdl(false, kernel, pack_grid(w), dim3(kPackThreads), 0, s,
-                                   w4_view(w), src, codes, scales);
+  cudaError_t e = cudaMemsetAsync(w.scales + w4_flags_at(w.E, w.K, w.N, w.group), 0,
+                                  (size_t)w.E * 4, s);
+  if (e == cudaSuccess)
+    e = launch_pdl(false, kernel, pack_grid(w), dim3(kPackThreads), 0, s, w4_view(w), src, codes,
+                   scales);
   note_launches(1);
   timer_after(MOE_KERNEL_W4_PACK, s);
   return e != cudaSuccess ? e : cudaGetLastError();

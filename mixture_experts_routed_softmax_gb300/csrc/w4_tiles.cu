@@ -3,23 +3,27 @@
 // products over the padded expert-grouped layout (permute.cu).
 //
 //   D[n, r] += W^T[n, k] x^T[k, r]
-// The weights are the A operand, 128 columns n of two matrices (gate and up) or of two
-// neighbouring runs of one, 64 k a step; up to 128 rows of x are the B operand, N = their
-// number rounded up to 16. A lives in tensor memory: sixteen warps take a 512-byte
-// tile of codes each a step, turn it into bf16 code * scale in registers (W4Decoder, one
-// more product), and store it as the 16x256b shape, whose lanes hold just what a lane's
-// codes are. So the bf16 weights never pass through shared memory, whose bandwidth the
-// products' B operand and the codes share, and each code is read from L2 once for 128 rows.
-// code * scale is rounded to bf16 there; scales of few bits (moe_w4_quantise's) make it exact.
+// The weights are the A operand, 128 columns n, 128 k a stage; up to 256 rows of x are the
+// B operand, N = their number rounded up to 16. A lives in tensor memory: sixteen warps take
+// a 512-byte tile of codes each a stage, turn it into bf16 code * scale in registers
+// (W4Decoder), and store it as the 16x256b shape, whose lanes hold just what a lane's codes are. So
+// the bf16 weights never pass through shared memory, whose bandwidth the products' B operand
+// needs, and the codes are decoded once for 256 rows: that takes 300 cycles of instruction issue
+// a 64 k, the products 2 N. code * scale is rounded to bf16 there; scales of few bits
+// (moe_w4_quantise's) make it exact.
 //
-// Roles (28 warps): 0 loads rows of x by TMA, a step a stage; 3 streams the codes
-// and scales, a contiguous piece of four steps a matrix, by bulk copies; 4-19 the sixteen above;
-// 1 issues the products; 20-27 take the finished tile from tensor memory (a thread a
-// column n, so a warp stores 32 neighbouring columns of a row). Tensor memory: 2 x 128
-// columns of accumulators, four stages of 64 columns of A. Every wait is bounded.
+// The 128 columns: two runs of 64, of gate and up or of one matrix. Sixteen columns of each
+// make up a warp's 32 lanes of tensor memory, so that gate and up of a column meet by a shuffle.
 //
-// An expert's rows are cut into equal chunks of at most 128; tiles of one run of columns
-// follow one another, so that its codes are in L2 for the second chunk.
+// Roles (28 warps): 0 loads rows of x by TMA, 64 k a stage; 3 streams the codes
+// and scales, contiguous pieces of 64 columns by 256 rows, by bulk copies; 4-19 the sixteen
+// above; 1 issues the products; 20-27 take the finished tile from tensor memory (a thread a
+// column). Tensor memory: 256 columns of accumulators (two tiles of up to 128 rows, so that one
+// is taken out while the next is summed, or one of more), four stages of 64 columns of A. Every wait is
+// bounded.
+//
+// An expert's rows are cut into equal chunks of at most 256; tiles of one run of columns
+// follow one another, so that its codes are in L2 for the next chunk.
 #include "tmap.h"
 #include "w4.cuh"
 
@@ -27,18 +31,19 @@ namespace moe {
 
 enum class TileMode { Linear, GateUp, Down };
 
-constexpr int kTileRows = 128;              // rows of x a tile, at most
-constexpr int kXStages = 8;                 // of x
-constexpr int kAStages = 4;                 // of A in tensor memory
-constexpr int kXBytes = kTileRows * 128;    // 64 k of 128 rows
-constexpr int kCStages = 2;                 // of codes: four steps each
-constexpr int kCSteps = 4;
-constexpr int kCBytes = 16 * kCSteps * kW4Tile;
+constexpr int kTileRows = 256;              // rows of x a tile, at most
+constexpr int kXStages = 5;                 // of x: 64 k of 256 rows
+constexpr int kXBytes = kTileRows * 128;
+constexpr int kAStages = 4;                 // of A in tensor memory: 128 k of 128 columns
+constexpr int kCStages = 3;                 // of codes: 256 k
+constexpr int kCSteps = 4;                  // (in 64 k)
+constexpr int kCBytes = 8 * kCSteps * kW4Tile;
+constexpr int kSBytes = 2048;               // and their scales, at most
 constexpr int kDecWarp0 = 4, kDecWarps = 16, kOutWarp0 = 20, kOutWarps = 8;
 constexpr int kTileThreads = 32 * (kOutWarp0 + kOutWarps);
-constexpr int kAccCols = 256;               // two accumulators of 128 columns
-constexpr int kTileSmem =
-    1024 + kXStages * kXBytes + kCStages * (kCBytes + 4096) + 4 * (kMaxExperts + 1) + 512;
+constexpr int kAccCols = 256;               // accumulators: two halves of 128 columns
+constexpr int kTileSmem = 1024 + kXStages * kXBytes + kCStages * (kCBytes + kSBytes) +
+                          4 * (kMaxExperts + 1) + 512;
 
 struct TileArgs {
   const uint8_t* codes[2];
@@ -121,6 +126,11 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
   return __all_sync(0xFFFFFFFFu, wait_asleep(bar, parity, abort_flag, status));
 }
 
+template <bool B>
+struct Bool {
+  static constexpr bool value = B;
+};
+
 struct Tile {
   int e, n0, rows;
   int64_t m0;
@@ -130,13 +140,13 @@ template <TileMode M, bool FP4, int GPS>
 __global__ void __launch_bounds__(kTileThreads, 1)
     w4_tiles_kernel(const __grid_constant__ CUtensorMap mapX, const TileArgs a) {
   pdl_enter();
-  constexpr int kWide = M == TileMode::GateUp ? 128 : 256;   // columns n a tile
+  constexpr int kWide = M == TileMode::GateUp ? 64 : 128;    // columns n a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~(uintptr_t)1023);
   uint8_t* s_codes = smem + kXStages * kXBytes;
   uint8_t* s_scales = s_codes + kCStages * kCBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_scales + kCStages * 4096);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_scales + kCStages * kSBytes);
   int* tstart = reinterpret_cast<int*>(bars + 40);
   const uint32_t bar0 = smem_u32(bars);
   auto x_full = [&](int s) { return bar0 + 8u * s; };
@@ -146,10 +156,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   auto c_full = [&](int s) { return bar0 + 8u * (2 * kXStages + 2 * kAStages + s); };
   auto c_empty = [&](int s) { return bar0 + 8u * (2 * kXStages + 2 * kAStages + kCStages + s); };
   const uint32_t acc_full = bar0 + 8u * (2 * kXStages + 2 * kAStages + 2 * kCStages);
-  const uint32_t acc_empty = acc_full + 8, drain = acc_full + 16;
+  const uint32_t acc_empty = acc_full + 16, drain = acc_full + 32;       // of either half
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 36);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  static_assert(2 * kXStages + 2 * kAStages + 2 * kCStages + 3 <= 36, "barriers");
+  static_assert(2 * kXStages + 2 * kAStages + 2 * kCStages + 5 <= 36, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -165,8 +175,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       mbar_init(c_full(s), 1);
       mbar_init(c_empty(s), kDecWarps);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, kOutWarps);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(acc_full + 8 * h, 1);
+      mbar_init(acc_empty + 8 * h, kOutWarps);
+    }
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbar_init();
@@ -218,7 +230,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int size = ((L + 15) / 16 + chunks - 1) / chunks * 16;
     const int at = i - tstart[lo], c = at % chunks;
     t.n0 = at / chunks * kWide;
-    t.rows = min(size, L - c * size);       // (chunks of up to eight sixteens: none is empty)
+    t.rows = min(size, L - c * size);       // (chunks of up to sixteen sixteens: none is empty)
     t.m0 = (a.offsets ? a.offsets[lo] : 0) + (int64_t)c * size;
     return t;
   };
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (leader) {
           mbar_arrive_expect_tx(full, boxes * 4096);
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
+          for (int b = 0; b < kTileRows / 32; ++b)
             if (b < boxes) tma_load_3d(dst + b * 4096, &mapX, full, ks * 64, 0, m0 + 32 * b);
         }
         ++fills;
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp == 3) {
     // ------------------------------------------------------ codes and scales --
-    // a piece of each matrix a stage: 128 columns by 256 rows of codes, their scales
+    // a piece of either run a stage: 64 columns by 256 rows of codes, their scales
     const bool leader = elect_one();
     const uint32_t codes_s = uniform(smem_u32(s_codes)), scales_s = uniform(smem_u32(s_scales));
     const uint32_t full0 = uniform(c_full(0));
@@ -268,16 +280,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const Tile t = tile_at(i);
       const int64_t ec = t.e * w4_codes_per_expert(a.K, a.N);
       const int64_t es = t.e * w4_scales_per_expert(a.K, a.N, 128 / GPS);
-      int cb[2];
+      // A run of 64 columns is the first or second half of a block of 128, whose tiles of
+      // 256 rows lie together: cb of its cw tiles, the first at tile c0 of them.
+      int cb[2], c0[2], cw[2];
       const uint8_t* csrc[2];
       const moe_bf16* ssrc[2];
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const int nb = t.n0 / 16 + (M == TileMode::GateUp ? 0 : 8 * m);
+        const int nb = t.n0 / 16 + (M == TileMode::GateUp ? 0 : 4 * m);
         const int mat = M == TileMode::GateUp ? m : 0;
-        cb[m] = uniform(max(0, min(8, nbs - nb)));
-        csrc[m] = a.codes[mat] + ec + (int64_t)nb * kbs * kW4Tile;
-        ssrc[m] = a.scales[mat] + es + (int64_t)nb * steps * 16 * GPS;
+        c0[m] = uniform(nb & 7);
+        cw[m] = uniform(min(8, nbs - (nb & ~7)));
+        cb[m] = uniform(max(0, min(4, nbs - nb)));
+        csrc[m] = a.codes[mat] + ec + (int64_t)(nb & ~7) * kbs * kW4Tile;
+        ssrc[m] = a.scales[mat] + es + (int64_t)(nb & ~7) * steps * 16 * GPS;
       }
       for (int ks = 0; ks < kbs; ks += kCSteps) {
         if (!wait_all(c_empty(s), ph ^ 1u, s_abort, a.status)) {
@@ -292,14 +308,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int m = 0; m < 2; ++m)
             if (cb[m]) {
-              bulk_load(codes_s + s * kCBytes + m * (kCBytes / 2), csrc[m], cb[m] * cbytes, full);
-              bulk_load(scales_s + s * 4096 + m * 2048, ssrc[m], cb[m] * sbytes, full);
+              bulk_load(codes_s + s * kCBytes + m * (kCBytes / 2), csrc[m] + c0[m] * cbytes,
+                        cb[m] * cbytes, full);
+              bulk_load(scales_s + s * kSBytes + m * (kSBytes / 2),
+                        ssrc[m] + c0[m] * sbytes / 2, cb[m] * sbytes, full);
             }
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          csrc[m] += cb[m] * cbytes;
-          ssrc[m] += cb[m] * sbytes / 2;
+          csrc[m] += cw[m] * cbytes;
+          ssrc[m] += cw[m] * sbytes / 2;
         }
         ++fills;
         if (++s == kCStages) { s = 0; ph ^= 1u; }
@@ -312,13 +330,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp >= kDecWarp0 && warp < kOutWarp0) {
     // ------------------------------------------------------- codes into bf16 --
-    // A step's stores to tensor memory are waited for when the next step's values are
+    // A stage's stores to tensor memory are waited for when the next stage's values are
     // ready, so that their latency is not the warp's own.
-    const int q = warp & 3, i4 = (warp - kDecWarp0) >> 2, mat = i4 >> 1, half = i4 & 1;
-    const int slot = 2 * q + half, g = lane >> 2;
-    const uint32_t dst0 = tmem + ((uint32_t)(32 * q + 16 * half) << 16) + kAccCols + 32 * mat;
-    const uint8_t* codes0 = s_codes + mat * (kCBytes / 2) + 16 * lane;
-    const uint8_t* scales0 = s_scales + mat * 2048 + g * 4 * GPS;
+    const int q = warp & 3, i4 = (warp - kDecWarp0) >> 2, half = i4 & 1, odd = i4 >> 1;
+    const int g = lane >> 2;
+    const uint32_t dst0 = tmem + ((uint32_t)(32 * q + 16 * half) << 16) + kAccCols + 32 * odd;
+    const uint8_t* codes0 = s_codes + half * (kCBytes / 2) + 16 * lane + odd * kW4Tile;
+    const uint8_t* scales0 =
+        s_scales + half * (kSBytes / 2) + g * 4 * GPS + odd * (GPS == 4 ? 8 : GPS == 2 ? 4 : 0);
     const uint32_t full0 = a_full(0), empty0 = a_empty(0);
     const W4Decoder<FP4> decode;
     int s = 0, cs = 0, before = -1;          // before: the stage whose stores are under way
@@ -331,57 +350,63 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) mbar_arrive(full0 + 8u * before);
     };
     for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+      const Tile t = tile_at(i);
+      const bool plain =
+          reinterpret_cast<const uint32_t*>(a.scales[M == TileMode::GateUp ? half : 0] +
+                                            w4_flags_at(a.E, a.K, a.N, 128 / GPS))[t.e] == 0u;
       for (int ks = 0; ks < kbs && ok; ks += kCSteps) {
         if (!wait_all(c_full(cs), cph, s_abort, a.status)) {
           ok = false;
           break;
         }
         const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
-        const uint8_t* cp = codes0 + cs * kCBytes + slot * n * kW4Tile;
-        const uint8_t* sp = scales0 + cs * 4096 + slot * ((n + 1) / 2) * 32 * GPS;
+        const uint8_t* cp = codes0 + cs * kCBytes + q * n * kW4Tile;
+        const uint8_t* sp = scales0 + cs * kSBytes + q * ((n + 1) / 2) * 32 * GPS;
 #pragma unroll 1
-        for (int sub = 0; sub < n && ok; sub += 2) {
-          uint32_t sw[4];                  // of the step's runs of 32 rows
-          if (GPS == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(sp);
-            sw[0] = v.x; sw[1] = v.y; sw[2] = v.z; sw[3] = v.w;
-          } else if (GPS == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(sp);
-            sw[0] = sw[1] = v.x;
-            sw[2] = sw[3] = v.y;
-          } else {
-            sw[0] = sw[1] = sw[2] = sw[3] = *reinterpret_cast<const uint32_t*>(sp);
-          }
-          sp += 32 * GPS;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (sub + h >= n) break;
-            const uint4 c = *reinterpret_cast<const uint4*>(cp + h * kW4Tile);
-            uint32_t r[16];
+        for (int sub = 0; sub < n; sub += 2, cp += 2 * kW4Tile, sp += 32 * GPS) {
+          uint32_t r[16];
+          const bool there = sub + odd < n;       // the last 64 rows may be the first half alone
+          if (there) {
+            const uint4 c = *reinterpret_cast<const uint4*>(cp);
+            uint32_t sw[2];                       // of the 64 rows' runs of 32
+            if (GPS == 4) {
+              const uint2 v = *reinterpret_cast<const uint2*>(sp);
+              sw[0] = v.x;
+              sw[1] = v.y;
+            } else {
+              sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(sp);
+            }
             const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+            auto values = [&](auto P) {
+              constexpr bool PLAIN = decltype(P)::value;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t p[4];
-              decode(word[j], p);
-              const uint32_t w = sw[2 * h + (j >> 1)];
-              const uint32_t lo = __byte_perm(w, 0, 0x1010), hi = __byte_perm(w, 0, 0x3232);
-              r[4 * j + 0] = mul_bf16x2(p[0], lo);
-              r[4 * j + 1] = mul_bf16x2(p[2], lo);
-              r[4 * j + 2] = mul_bf16x2(p[1], hi);
-              r[4 * j + 3] = mul_bf16x2(p[3], hi);
-            }
-            if (before >= 0) stored();
-            if (!wait_all(empty0 + 8u * s, ph ^ 1u, s_abort, a.status)) {
-              ok = false;
-              before = -1;
-              break;
-            }
-            tc_fence_after();
-            tmem_st_16x256b_x4(dst0 + 64 * s, r);
-            before = s;
-            if (++s == kAStages) { s = 0; ph ^= 1u; }
+              for (int j = 0; j < 4; ++j) {
+                uint32_t p[4];
+                const uint32_t w = sw[j >> 1];
+                decode.template scaled<PLAIN>(
+                    word[j], decode.template factor<PLAIN>(__byte_perm(w, 0, 0x1010)),
+                    decode.template factor<PLAIN>(__byte_perm(w, 0, 0x3232)), p);
+                r[4 * j + 0] = p[0];
+                r[4 * j + 1] = p[2];
+                r[4 * j + 2] = p[1];
+                r[4 * j + 3] = p[3];
+              }
+            };
+            if (plain)
+              values(Bool<true>());
+            else
+              values(Bool<false>());
           }
-          cp += 2 * kW4Tile;
+          if (before >= 0) stored();
+          if (!wait_all(empty0 + 8u * s, ph ^ 1u, s_abort, a.status)) {
+            ok = false;
+            before = -1;
+            break;
+          }
+          tc_fence_after();
+          if (there) tmem_st_16x256b_x4(dst0 + 64 * s, r);
+          before = s;
+          if (++s == kAStages) { s = 0; ph ^= 1u; }
         }
         if (lane == 0) mbar_arrive(c_empty(cs));
         __syncwarp();
@@ -398,37 +423,48 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t td = uniform(tmem), bars_u = uniform(bar0);
     const uint64_t bd0 = sdesc_sw128(smem_u32(smem), 16, 1024);
     const uint32_t b_lo = uniform((uint32_t)bd0), b_hi = uniform((uint32_t)(bd0 >> 32));
-    int s = 0, xs = 0;
-    uint32_t ph = 0, xph = 0, acc_ph = 0;
+    int s = 0, xs = 0, h = 0;
+    uint32_t ph = 0, xph = 0, used = 0;      // used: a bit a half of the accumulators, its phase
     bool ok = true;
     for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
       const Tile t = tile_at(i);
-      if (!wait_all(acc_empty, acc_ph ^ 1u, s_abort, a.status)) break;
-      const uint32_t idesc = uniform(idesc_bf16(128, (t.rows + 15) & ~15, 0, 0));
-      for (int ks = 0; ks < kbs; ++ks) {
-        if (!wait_all(x_full(xs), xph, s_abort, a.status) ||
-            !wait_all(a_full(s), ph, s_abort, a.status)) {
+      const int N = uniform((t.rows + 15) & ~15);
+      if (N > 128) {                         // both halves, from the first column on
+        h = 0;
+        if (!wait_all(acc_empty + 8, (used >> 1 & 1u) ^ 1u, s_abort, a.status)) break;
+        used ^= 2u;
+      }
+      if (!wait_all(acc_empty + 8 * h, (used >> h & 1u) ^ 1u, s_abort, a.status)) break;
+      used ^= 1u << h;
+      const uint32_t idesc = idesc_bf16(128, N, 0, 0), d = td + 128 * h;
+      for (int ks = 0; ks < kbs; ks += 2) {
+        if (!wait_all(a_full(s), ph, s_abort, a.status)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint32_t at = td + kAccCols + 64 * s, b = b_lo + xs * (kXBytes >> 4);
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t bd = ((uint64_t)b_hi << 32) | (b + kk * (32 >> 4));
-            umma_tmem_a(td, at + 8 * kk, bd, idesc, ks > 0 || kk > 0);
-            umma_tmem_a(td + 128, at + 32 + 8 * kk, bd, idesc, ks > 0 || kk > 0);
+        for (int k2 = 0; k2 < 2 && ks + k2 < kbs; ++k2) {
+          if (!wait_all(x_full(xs), xph, s_abort, a.status)) {
+            ok = false;
+            break;
           }
-          umma_commit(bars_u + 8u * (2 * kXStages + kAStages + s));     // a_empty
-          umma_commit(bars_u + 8u * (kXStages + xs));                   // x_empty
+          tc_fence_after();
+          const uint32_t at = td + kAccCols + 64 * s + 32 * k2, b = b_lo + xs * (kXBytes >> 4);
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_tmem_a(d, at + 8 * kk, ((uint64_t)b_hi << 32) | (b + kk * (32 >> 4)), idesc,
+                          ks + k2 > 0 || kk > 0);
+            umma_commit(bars_u + 8u * (kXStages + xs));                  // x_empty
+          }
+          if (++xs == kXStages) { xs = 0; xph ^= 1u; }
         }
+        if (!ok) break;
+        if (leader) umma_commit(bars_u + 8u * (2 * kXStages + kAStages + s));     // a_empty
         if (++s == kAStages) { s = 0; ph ^= 1u; }
-        if (++xs == kXStages) { xs = 0; xph ^= 1u; }
       }
       if (!ok) break;
-      if (leader) umma_commit(acc_full);
-      acc_ph ^= 1u;
+      if (leader) umma_commit(acc_full + 8 * h);
+      h = N > 128 ? 0 : h ^ 1;
     }
     // every product has ended before tensor memory is freed
     if (leader) {
@@ -440,43 +476,61 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // --------------------------------------------------------------- results --
     const int q = warp & 3, part = (warp - kOutWarp0) >> 2;
     const uint32_t at = tmem + ((uint32_t)(32 * q) << 16);
-    uint32_t ph = 0;
+    // this lane's column: of the first run (lanes 0-15) or the second
+    const bool second = lane >= 16;
+    const int col = 16 * q + (lane & 15) + (M != TileMode::GateUp && second ? 64 : 0);
+    uint32_t seen = 0;                       // a bit a half: its phase
+    int h = 0;
     for (int i = blockIdx.x; i < total; i += gridDim.x) {
       const Tile t = tile_at(i);
-      if (!wait_all(acc_full, ph, s_abort, a.status)) break;
-      ph ^= 1u;
+      const bool wide = t.rows > 128;
+      if (wide) h = 0;
+      if (!wait_all(acc_full + 8 * h, seen >> h & 1u, s_abort, a.status)) break;
+      seen ^= 1u << h;
       tc_fence_after();
-      const int n = t.n0 + 32 * q + lane;
+      const int n = t.n0 + col;
       for (int c0 = 16 * part; c0 < t.rows; c0 += 32) {
-        uint32_t v0[16], v1[16];
-        tmem_ld16(at + c0, v0);
-        tmem_ld16(at + 128 + c0, v1);
+        uint32_t v[16];
+        tmem_ld16(at + 128 * h + c0, v);
         tmem_ld_wait();
         const int64_t first = (t.m0 + c0) * a.out_stride + n;
-        const int here = t.rows - c0;       // rows of these sixteen
+        const int here = n < a.N ? t.rows - c0 : 0;          // rows of these sixteen
+        if (M == TileMode::GateUp) {
+          // of two rows the lower lanes, which hold gates, take the first, the upper ones,
+          // which hold the same columns' ups, the second
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float f0 = __uint_as_float(v0[c]), f1 = __uint_as_float(v1[c]);
-          const bool in0 = c < here && n < a.N, in1 = c < here && n + 128 < a.N;
-          const int64_t o = first + c * a.out_stride;
-          if (M == TileMode::GateUp) {
-            const float y = gated(f0, f1, a.act);
-            if (in0)
-              static_cast<moe_bf16*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-          } else if (M == TileMode::Down || a.out_fp32) {
-            if (in0) static_cast<float*>(a.out)[o] = f0;
-            if (in1) static_cast<float*>(a.out)[o + 128] = f1;
-          } else {
-            if (in0)
-              static_cast<moe_bf16*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(f0));
-            if (in1)
-              static_cast<moe_bf16*>(a.out)[o + 128] = __bfloat16_as_ushort(__float2bfloat16_rn(f1));
+          for (int c = 0; c < 16; c += 2) {
+            const float got = __uint_as_float(
+                __shfl_xor_sync(0xFFFFFFFFu, second ? v[c] : v[c + 1], 16));
+            const float gt = second ? got : __uint_as_float(v[c]);
+            const float up = second ? __uint_as_float(v[c + 1]) : got;
+            const int cc = c + second;
+            const float y = gated(gt, up, a.act);
+            if (cc < here)
+              static_cast<moe_bf16*>(a.out)[first + cc * a.out_stride] =
+                  __bfloat16_as_ushort(__float2bfloat16_rn(y));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float f = __uint_as_float(v[c]);
+            const int64_t o = first + c * a.out_stride;
+            if (c < here) {
+              if (M == TileMode::Down || a.out_fp32)
+                static_cast<float*>(a.out)[o] = f;
+              else
+                static_cast<moe_bf16*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(f));
+            }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
+      if (lane == 0) {
+        mbar_arrive(acc_empty + 8 * h);
+        if (wide) mbar_arrive(acc_empty + 8);
+      }
+      h = wide ? 0 : h ^ 1;
     }
   }
   tc_fence_before();

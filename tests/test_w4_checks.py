@@ -51,8 +51,8 @@ def test_sizes(L):
     lib = L.load()
     # 2880 rows: 45 blocks of 64; 640 columns: 40 blocks of 16; 23 steps of 128 rows
     assert lib.moe_w4_codes_bytes(3, 2880, 640) == 3 * 40 * 45 * 512
-    assert lib.moe_w4_scales_bytes(3, 2880, 640, 32) == 3 * 40 * 23 * 16 * 4 * 2
-    assert lib.moe_w4_scales_bytes(3, 2880, 640, 128) == 3 * 40 * 23 * 16 * 2
+    assert lib.moe_w4_scales_bytes(3, 2880, 640, 32) == 3 * 40 * 23 * 16 * 4 * 2 + 16
+    assert lib.moe_w4_scales_bytes(3, 2880, 640, 128) == 3 * 40 * 23 * 16 * 2 + 16
     assert lib.moe_w4_codes_bytes(1, 8, 8) == 512
     for bad in ((0, 64, 64), (1, 60, 64), (1, 64, 4), (1025, 64, 64), (1, 65544, 64)):
         assert lib.moe_w4_codes_bytes(*bad) == 0
