@@ -118,31 +118,37 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return r;
 }
 
-// A word's four pairs as bf16 values (exact), from an offset or factor of the kind:
-//   int4: 128 + 8 + value (0x4300 holds 128 with steps of 1)
-//   fp4:  2^-126 value: the code's exponent and mantissa as the low end of bf16's,
-//         which has subnormals where fp4 has them
-// scaled: value * scale, rounded to bf16 once. `plain` scales (plain_scale) take one
-// operation a pair instead of two:
-//   int4: 160 + 4 value in place of 136 + value, fma(that, scale / 4, -40 scale): with five
-//         significant bits in a scale 40 scale has eight, so the sum rounds as the product does
-//   fp4:  scale * 2^126 in one factor
+// A word's four pairs as bf16. In place, or moved by a shift for two or three of them, a
+// masked code is a bf16 already, a very small one:
+//   int4: bits 0-3 or 4-7 hold u = value + 8; bf16's first two binades are one even scale,
+//         so that is u 2^-133 or u 2^-129, and value * f = fma(that, f 2^133 or 2^129, -8 f)
+//   fp4:  the code's exponent and mantissa are the low end of bf16's, which has subnormals
+//         where fp4 has them: 2^-126 value
+// values: the code's value (fp4), or 2^-13 of it (int4: 2^133 is no bf16), exact; kUnit gives
+//   the factor back.
+// scaled: 2^-16 code * scale, rounded to bf16 once, one operation a pair; for scales in the
+//   wide range of plain_scale. general: code * scale for any other scale.
 // The constants are held in registers that the compiler does not know the contents of: it
 // would load them again for every pair.
 template <bool FP4>
 struct W4Decoder {
-  uint32_t mask, base, last, mask2;
+  static constexpr float kUnit = FP4 ? 1.f : 8192.f;        // of values
+  static constexpr float kScaled = 65536.f;                 // of scaled
+  uint32_t m0, m1, m2, f0, f1, c;
   __device__ __forceinline__ W4Decoder() {
     if (FP4) {
-      asm volatile("mov.u32 %0, 0x81C081C0;" : "=r"(mask));
-      asm volatile("mov.u32 %0, 0x01800180;" : "=r"(base));
-      asm volatile("mov.u32 %0, 0x00400040;" : "=r"(mask2));
-      asm volatile("mov.u32 %0, 0x7E807E80;" : "=r"(last));       // 2^126
+      asm volatile("mov.u32 %0, 0x81C081C0;" : "=r"(m0));
+      asm volatile("mov.u32 %0, 0x01800180;" : "=r"(m1));
+      asm volatile("mov.u32 %0, 0x00400040;" : "=r"(m2));
+      asm volatile("mov.u32 %0, 0x7E807E80;" : "=r"(f0));       // 2^126
+      f1 = c = 0;
     } else {
-      asm volatile("mov.u32 %0, 0x000F000F;" : "=r"(mask));
-      asm volatile("mov.u32 %0, 0x43004300;" : "=r"(base));
-      asm volatile("mov.u32 %0, 0x43084308;" : "=r"(last));       // 136
-      asm volatile("mov.u32 %0, 0x003C003C;" : "=r"(mask2));
+      asm volatile("mov.u32 %0, 0x000F000F;" : "=r"(m0));
+      asm volatile("mov.u32 %0, 0x00F000F0;" : "=r"(m1));
+      asm volatile("mov.u32 %0, 0x7B807B80;" : "=r"(f0));       // 2^120
+      asm volatile("mov.u32 %0, 0x79807980;" : "=r"(f1));       // 2^116
+      asm volatile("mov.u32 %0, 0xBA80BA80;" : "=r"(c));        // -2^-10
+      m2 = 0;
     }
   }
   static __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
@@ -150,67 +156,60 @@ struct W4Decoder {
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));   // (a & b) | c
     return r;
   }
-  __device__ __forceinline__ void raw_fp4(uint32_t w, uint32_t* r) const {
-    r[0] = w & mask;
-    r[1] = (w << 3) & mask;
-    r[2] = (w << 6) & mask;
-    r[3] = and_or(w >> 3, base, (w << 1) & 0x80008000u);
-    r[3] = and_or(w >> 7, mask2, r[3]);
-  }
-  __device__ __forceinline__ void operator()(uint32_t w, uint32_t* r) const {
+  __device__ __forceinline__ void raw(uint32_t w, uint32_t* r) const {
     if (FP4) {
-      raw_fp4(w, r);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], last);
+      r[0] = w & m0;
+      r[1] = (w << 3) & m0;
+      r[2] = (w << 6) & m0;
+      r[3] = and_or(w >> 3, m1, (w << 1) & 0x80008000u);
+      r[3] = and_or(w >> 7, m2, r[3]);
     } else {
-      r[0] = and_or(w, mask, base);
-      r[1] = and_or(w >> 4, mask, base);
-      r[2] = and_or(w >> 8, mask, base);
-      r[3] = and_or(w >> 12, mask, base);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = sub_bf16x2(r[i], last);
+      r[0] = w & m0;
+      r[1] = w & m1;
+      r[2] = (w >> 8) & m0;
+      r[3] = (w >> 8) & m1;
     }
   }
-  // factors of a scale pair (both halves the same) for `scaled`
+  __device__ __forceinline__ void values(uint32_t w, uint32_t* r) const {
+    raw(w, r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = FP4 ? mul_bf16x2(r[i], f0) : fma_bf16x2(r[i], (i & 1) ? f1 : f0, c);
+  }
+  // a column's scale (both halves the same) for `scaled`: of column g (HI = 0) or g + 8
   struct Factor {
     uint32_t f, c;
   };
-  template <bool PLAIN>
-  __device__ __forceinline__ Factor factor(uint32_t s2) const {
-    if (!PLAIN) return Factor{s2, 0u};
-    if (FP4) return Factor{mul_bf16x2(s2, last), 0u};
-    return Factor{mul_bf16x2(s2, 0x3E803E80u), mul_bf16x2(s2, 0xC220C220u)};   // 1/4, -40
+  template <int HI>
+  static __device__ __forceinline__ Factor factor(uint32_t s2) {
+    if (FP4) return Factor{mul_bf16x2(s2, 0x76807680u), 0u};                  // 2^110
+    return Factor{mul_bf16x2(s2, HI ? 0x78007800u : 0x7A007A00u),             // 2^113, 2^117
+                  mul_bf16x2(s2, 0xB900B900u)};                               // -2^-13
   }
-  template <bool PLAIN>
   __device__ __forceinline__ void scaled(uint32_t w, const Factor& lo, const Factor& hi,
                                          uint32_t* r) const {
-    if (!PLAIN) {
-      (*this)(w, r);
+    raw(w, r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], (i & 1) ? hi.f : lo.f);
-    } else if (FP4) {
-      raw_fp4(w, r);
+    for (int i = 0; i < 4; ++i) {
+      const Factor& k = (i & 1) ? hi : lo;
+      r[i] = FP4 ? mul_bf16x2(r[i], k.f) : fma_bf16x2(r[i], k.f, k.c);
+    }
+  }
+  __device__ __forceinline__ void general(uint32_t w, uint32_t lo2, uint32_t hi2,
+                                          uint32_t* r) const {
+    values(w, r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = mul_bf16x2(r[i], (i & 1) ? hi.f : lo.f);
-    } else {
-      r[0] = and_or(w << 2, mask2, base);
-      r[1] = and_or(w >> 2, mask2, base);
-      r[2] = and_or(w >> 6, mask2, base);
-      r[3] = and_or(w >> 10, mask2, base);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r[i] = fma_bf16x2(r[i], (i & 1) ? hi.f : lo.f, (i & 1) ? hi.c : lo.c);
+    for (int i = 0; i < 4; ++i) {
+      if (!FP4) r[i] = mul_bf16x2(r[i], 0x46004600u);                          // 2^13
+      r[i] = mul_bf16x2(r[i], (i & 1) ? hi2 : lo2);
     }
   }
 };
 
-// Whether a scale (bf16 bits) takes the short form of `scaled`: int4, at most five
-// significant bits and far from either end of the range; fp4, below 2. NaN and 0 do.
-__device__ __forceinline__ bool plain_scale(uint32_t bits, bool fp4) {
+// Whether `scaled` takes a scale (bf16 bits): 2^-100 <= |scale| < 2^9, 0 or NaN.
+__device__ __forceinline__ bool plain_scale(uint32_t bits) {
   const uint32_t a = bits & 0x7FFFu;
-  if (a == 0u || a > 0x7F80u) return true;
-  if (fp4) return a < 0x4000u;
-  return (a & 7u) == 0u && a >= 0x0800u && a < 0x7700u;
+  return a == 0u || a > 0x7F80u || (a >= 0x0D80u && a < 0x4400u);
 }
 // The arrays of scales end with a word an expert: not 0 where some scale is not plain.
 __host__ __device__ __forceinline__ int64_t w4_flags_at(int64_t E, int K, int N, int group) {

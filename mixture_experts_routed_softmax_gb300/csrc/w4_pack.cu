@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
   for (int i = lane; i < 16 * gps; i += 32) {
     const int gg = i / (2 * gps), gr = (i / 2) % gps, hi = i & 1;
     out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(sc[gr][c0 + gg + 8 * hi]));
-    plain = plain && plain_scale(out[i], FP4);
+    plain = plain && plain_scale(out[i]);
   }
   // (or-ed: the order does not matter)
   if (!plain)
@@ -187,12 +187,13 @@ __global__ void __launch_bounds__(kPackThreads) w4_unpack_kernel(W4View w,
         const int r0 = 64 * (kb & 1) + 16 * j + 4 * t;
         const int gr = (r0 * gps) >> 7;
         uint32_t p[4];
-        decode(word[j], p);
+        decode.values(word[j], p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float s = __bfloat162float(__ushort_as_bfloat16(sp[2 * gr + (i & 1)]));
           const int n = c0 + g + 8 * (i & 1), r = r0 + 2 * (i >> 1);
-          const uint32_t o = pack_bf16(bf16_lo(p[i]) * s, bf16_hi(p[i]) * s);
+          const uint32_t o =
+              pack_bf16(bf16_lo(p[i]) * decode.kUnit * s, bf16_hi(p[i]) * decode.kUnit * s);
           tile[r][n] = (moe_bf16)(o & 0xFFFFu);
           tile[r + 1][n] = (moe_bf16)(o >> 16);
         }

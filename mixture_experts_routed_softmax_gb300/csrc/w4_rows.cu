@@ -205,16 +205,16 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(RowsArgs a) {
           }
           const uint4 c = cw[r][h >> 1];
           uint32_t av[4];
-          decode((h & 1) ? c.z : c.x, av);
+          decode.values((h & 1) ? c.z : c.x, av);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816(part[nt], av, xv[nt][2 * h].x, xv[nt][2 * h].y);
-          decode((h & 1) ? c.w : c.y, av);
+          decode.values((h & 1) ? c.w : c.y, av);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma16816(part[nt], av, xv[nt][2 * h + 1].x, xv[nt][2 * h + 1].y);
           if (h % (4 / GPS) == 4 / GPS - 1) {
             const uint32_t s = sw[r][h / (4 / GPS)];
-            const float lo = bf16_lo(s), hi = bf16_hi(s);
+            const float lo = bf16_lo(s) * decode.kUnit, hi = bf16_hi(s) * decode.kUnit;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               acc[r][nt][0] = fmaf(lo, part[nt][0], acc[r][nt][0]);

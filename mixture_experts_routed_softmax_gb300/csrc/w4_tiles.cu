@@ -3,9 +3,9 @@
 // products over the padded expert-grouped layout (permute.cu).
 //
 //   D[n, r] += W^T[n, k] x^T[k, r]
-// The weights are the A operand, 128 columns n, 128 k a stage; up to 256 rows of x are the
+// The weights are the A operand, 128 columns n, 256 k a stage; up to 256 rows of x are the
 // B operand, N = their number rounded up to 16. A lives in tensor memory: sixteen warps take
-// a 512-byte tile of codes each a stage, turn it into bf16 code * scale in registers
+// two 512-byte tiles of codes each a stage, turn it into bf16 code * scale in registers
 // (W4Decoder), and store it as the 16x256b shape, whose lanes hold just what a lane's codes are. So
 // the bf16 weights never pass through shared memory, whose bandwidth the products' B operand
 // needs, and the codes are decoded once for 256 rows: that takes 300 cycles of instruction issue
@@ -19,7 +19,7 @@
 // and scales, contiguous pieces of 64 columns by 256 rows, by bulk copies; 4-19 the sixteen
 // above; 1 issues the products; 20-27 take the finished tile from tensor memory (a thread a
 // column). Tensor memory: 256 columns of accumulators (two tiles of up to 128 rows, so that one
-// is taken out while the next is summed, or one of more), four stages of 64 columns of A. Every wait is
+// is taken out while the next is summed, or one of more), two stages of 128 columns of A. Every wait is
 // bounded.
 //
 // An expert's rows are cut into equal chunks of at most 256; tiles of one run of columns
@@ -34,7 +34,7 @@ enum class TileMode { Linear, GateUp, Down };
 constexpr int kTileRows = 256;              // rows of x a tile, at most
 constexpr int kXStages = 5;                 // of x: 64 k of 256 rows
 constexpr int kXBytes = kTileRows * 128;
-constexpr int kAStages = 4;                 // of A in tensor memory: 128 k of 128 columns
+constexpr int kAStages = 2;                 // of A in tensor memory: 256 k of 128 columns
 constexpr int kCStages = 3;                 // of codes: 256 k
 constexpr int kCSteps = 4;                  // (in 64 k)
 constexpr int kCBytes = 8 * kCSteps * kW4Tile;
@@ -119,11 +119,26 @@ static __device__ __noinline__ bool wait_asleep(uint32_t bar, uint32_t parity,
   }
 }
 // For a whole warp: true in all lanes, or (given up) false in all. The loop is out of
-// line: the roles' steady state has to stay small enough to be fetched.
+// line: the roles' steady state has to stay small.
+static __device__ __noinline__ bool wait_slowly_w4(uint32_t bar, uint32_t parity,
+                                                   volatile int* abort_flag, int* status) {
+  __syncwarp();
+  return __all_sync(0xFFFFFFFFu, wait_asleep(bar, parity, abort_flag, status));
+}
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                          int* status) {
+  // (a phase once seen complete by one lane is complete for every lane that asks later)
   if (__builtin_expect(__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)), 1)) return true;
-  return __all_sync(0xFFFFFFFFu, wait_asleep(bar, parity, abort_flag, status));
+  return wait_slowly_w4(bar, parity, abort_flag, status);
+}
+// The same for the warps that wait a whole tile long: they look now and then.
+__device__ __forceinline__ bool wait_patiently(uint32_t bar, uint32_t parity,
+                                               volatile int* abort_flag, int* status) {
+  for (int i = 0; i < 100; ++i) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    __nanosleep(200);
+  }
+  return wait_slowly_w4(bar, parity, abort_flag, status);
 }
 
 template <bool B>
@@ -218,6 +233,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int total = tstart[a.E];
   const int kbs = w4_kblocks(a.K), steps = w4_steps(a.K), nbs = w4_nblocks(a.N);
 
+  // whether an expert's scales (of run `half`) take the short form
+  auto plain_of = [&](int e, int half) {
+    const moe_bf16* p = M == TileMode::GateUp && half ? a.scales[1] : a.scales[0];
+    return reinterpret_cast<const uint32_t*>(p + w4_flags_at(a.E, a.K, a.N, 128 / GPS))[e] == 0u;
+  };
   auto tile_at = [&](int i) {
     int lo = 0, hi = a.E;                   // the last expert with tstart[lo] <= i
     while (hi - lo > 1) {
@@ -330,8 +350,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp >= kDecWarp0 && warp < kOutWarp0) {
     // ------------------------------------------------------- codes into bf16 --
-    // A stage's stores to tensor memory are waited for when the next stage's values are
-    // ready, so that their latency is not the warp's own.
+    // A stage's stores to tensor memory are waited for when the first values of the next
+    // are ready, so that their latency is not the warp's own.
     const int q = warp & 3, i4 = (warp - kDecWarp0) >> 2, half = i4 & 1, odd = i4 >> 1;
     const int g = lane >> 2;
     const uint32_t dst0 = tmem + ((uint32_t)(32 * q + 16 * half) << 16) + kAccCols + 32 * odd;
@@ -340,80 +360,76 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         s_scales + half * (kSBytes / 2) + g * 4 * GPS + odd * (GPS == 4 ? 8 : GPS == 2 ? 4 : 0);
     const uint32_t full0 = a_full(0), empty0 = a_empty(0);
     const W4Decoder<FP4> decode;
-    int s = 0, cs = 0, before = -1;          // before: the stage whose stores are under way
+    int s = 0, cs = 0;
     uint32_t ph = 0, cph = 0;
-    bool ok = true;
+    bool ok = true, before = false;          // before: the other stage's stores are under way
     auto stored = [&]() {
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full0 + 8u * before);
+      if (lane == 0) mbar_arrive(full0 + 8u * (s ^ 1));
     };
+    static_assert(kAStages == 2, "the other stage");
     for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
       const Tile t = tile_at(i);
-      const bool plain =
-          reinterpret_cast<const uint32_t*>(a.scales[M == TileMode::GateUp ? half : 0] +
-                                            w4_flags_at(a.E, a.K, a.N, 128 / GPS))[t.e] == 0u;
-      for (int ks = 0; ks < kbs && ok; ks += kCSteps) {
-        if (!wait_all(c_full(cs), cph, s_abort, a.status)) {
-          ok = false;
-          break;
-        }
-        const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
-        const uint8_t* cp = codes0 + cs * kCBytes + q * n * kW4Tile;
-        const uint8_t* sp = scales0 + cs * kSBytes + q * ((n + 1) / 2) * 32 * GPS;
-#pragma unroll 1
-        for (int sub = 0; sub < n; sub += 2, cp += 2 * kW4Tile, sp += 32 * GPS) {
-          uint32_t r[16];
-          const bool there = sub + odd < n;       // the last 64 rows may be the first half alone
-          if (there) {
-            const uint4 c = *reinterpret_cast<const uint4*>(cp);
+      const bool plain = plain_of(t.e, half);
+      // All of the tile's stages of 256 rows, two tiles of codes a warp. (Where the last rows
+      // are fewer, some warps decode what lies there; no product reads it.)
+      auto stages = [&](auto P) {
+        constexpr bool PLAIN = decltype(P)::value;
+        for (int ks = 0; ks < kbs; ks += kCSteps) {
+          if (!wait_all(c_full(cs), cph, s_abort, a.status)) return false;
+          const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
+          const uint8_t* cp = codes0 + cs * kCBytes + q * n * kW4Tile;
+          const uint8_t* sp = scales0 + cs * kSBytes + q * ((n + 1) / 2) * 32 * GPS;
+#pragma unroll
+          for (int sub = 0; sub < 2; ++sub) {
+            const uint4 c = *reinterpret_cast<const uint4*>(cp + sub * 2 * kW4Tile);
             uint32_t sw[2];                       // of the 64 rows' runs of 32
             if (GPS == 4) {
-              const uint2 v = *reinterpret_cast<const uint2*>(sp);
+              const uint2 v = *reinterpret_cast<const uint2*>(sp + sub * 32 * GPS);
               sw[0] = v.x;
               sw[1] = v.y;
             } else {
-              sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(sp);
+              sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(sp + sub * 32 * GPS);
             }
+            uint32_t r[16];
             const uint32_t word[4] = {c.x, c.y, c.z, c.w};
-            auto values = [&](auto P) {
-              constexpr bool PLAIN = decltype(P)::value;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t p[4];
-                const uint32_t w = sw[j >> 1];
-                decode.template scaled<PLAIN>(
-                    word[j], decode.template factor<PLAIN>(__byte_perm(w, 0, 0x1010)),
-                    decode.template factor<PLAIN>(__byte_perm(w, 0, 0x3232)), p);
-                r[4 * j + 0] = p[0];
-                r[4 * j + 1] = p[2];
-                r[4 * j + 2] = p[1];
-                r[4 * j + 3] = p[3];
-              }
-            };
-            if (plain)
-              values(Bool<true>());
-            else
-              values(Bool<false>());
+            for (int j = 0; j < 4; ++j) {
+              uint32_t p[4];
+              const uint32_t lo = __byte_perm(sw[j >> 1], 0, 0x1010);
+              const uint32_t hi = __byte_perm(sw[j >> 1], 0, 0x3232);
+              if (PLAIN)
+                decode.scaled(word[j], decode.template factor<0>(lo), decode.template factor<1>(hi),
+                              p);
+              else
+                decode.general(word[j], lo, hi, p);
+              r[4 * j + 0] = p[0];
+              r[4 * j + 1] = p[2];
+              r[4 * j + 2] = p[1];
+              r[4 * j + 3] = p[3];
+            }
+            if (sub == 0) {
+              if (before) stored();
+              before = false;
+              if (!wait_all(empty0 + 8u * s, ph ^ 1u, s_abort, a.status)) return false;
+              tc_fence_after();
+            }
+            tmem_st_16x256b_x4(dst0 + 128 * s + 64 * sub, r);
           }
-          if (before >= 0) stored();
-          if (!wait_all(empty0 + 8u * s, ph ^ 1u, s_abort, a.status)) {
-            ok = false;
-            before = -1;
-            break;
-          }
-          tc_fence_after();
-          if (there) tmem_st_16x256b_x4(dst0 + 64 * s, r);
-          before = s;
-          if (++s == kAStages) { s = 0; ph ^= 1u; }
+          before = true;
+          s ^= 1;
+          if (s == 0) ph ^= 1u;
+          if (lane == 0) mbar_arrive(c_empty(cs));
+          __syncwarp();
+          if (++cs == kCStages) { cs = 0; cph ^= 1u; }
         }
-        if (lane == 0) mbar_arrive(c_empty(cs));
-        __syncwarp();
-        if (++cs == kCStages) { cs = 0; cph ^= 1u; }
-      }
+        return true;
+      };
+      ok = plain ? stages(Bool<true>()) : stages(Bool<false>());
     }
-    if (before >= 0) stored();
+    if (before) stored();
   } else if (warp == 1) {
     // -------------------------------------------------------------- products --
     // Addresses and descriptors go through a shuffle once, so that they stay in uniform
@@ -437,18 +453,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!wait_all(acc_empty + 8 * h, (used >> h & 1u) ^ 1u, s_abort, a.status)) break;
       used ^= 1u << h;
       const uint32_t idesc = idesc_bf16(128, N, 0, 0), d = td + 128 * h;
-      for (int ks = 0; ks < kbs; ks += 2) {
+      for (int ks = 0; ks < kbs; ks += kCSteps) {
         if (!wait_all(a_full(s), ph, s_abort, a.status)) {
           ok = false;
           break;
         }
-        for (int k2 = 0; k2 < 2 && ks + k2 < kbs; ++k2) {
+        const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
+        for (int k2 = 0; k2 < n; ++k2) {
           if (!wait_all(x_full(xs), xph, s_abort, a.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t at = td + kAccCols + 64 * s + 32 * k2, b = b_lo + xs * (kXBytes >> 4);
+          const uint32_t at = td + kAccCols + 128 * s + 32 * k2, b = b_lo + xs * (kXBytes >> 4);
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -485,14 +502,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const Tile t = tile_at(i);
       const bool wide = t.rows > 128;
       if (wide) h = 0;
-      if (!wait_all(acc_full + 8 * h, seen >> h & 1u, s_abort, a.status)) break;
+      if (!wait_patiently(acc_full + 8 * h, seen >> h & 1u, s_abort, a.status)) break;
       seen ^= 1u << h;
       tc_fence_after();
       const int n = t.n0 + col;
+      const float unit = plain_of(t.e, second) ? W4Decoder<FP4>::kScaled : 1.f;
       for (int c0 = 16 * part; c0 < t.rows; c0 += 32) {
         uint32_t v[16];
         tmem_ld16(at + 128 * h + c0, v);
         tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * unit);
         const int64_t first = (t.m0 + c0) * a.out_stride + n;
         const int here = n < a.N ? t.rows - c0 : 0;          // rows of these sixteen
         if (M == TileMode::GateUp) {
