@@ -15,15 +15,21 @@
 // The 128 columns: two runs of 64, of gate and up or of one matrix. Sixteen columns of each
 // make up a warp's 32 lanes of tensor memory, so that gate and up of a column meet by a shuffle.
 //
-// Roles (28 warps): 0 loads rows of x by TMA, 64 k a stage; 3 streams the codes
+// Roles (28 warps): 0 loads rows of x by TMA, 64 k a stage, 128 or 256 where rows are few; 3 streams the codes
 // and scales, contiguous pieces of 64 columns by 256 rows, by bulk copies; 4-19 the sixteen
 // above; 1 issues the products; 20-27 take the finished tile from tensor memory (a thread a
 // column). Tensor memory: 256 columns of accumulators (two tiles of up to 128 rows, so that one
 // is taken out while the next is summed, or one of more), two stages of 128 columns of A. Every wait is
 // bounded.
 //
+// Two blocks of a cluster work on neighbouring columns of the same rows: each loads half of
+// them and hands it to both (TMA multicast). At 144 rows a tile the rows of x came in at a rate that
+// L2 gave out no faster, 50 bytes a cycle and SM; a row loaded once for 256 columns needs half.
+//
 // An expert's rows are cut into equal chunks of at most 256; tiles of one run of columns
 // follow one another, so that its codes are in L2 for the next chunk.
+#include <mutex>
+
 #include "tmap.h"
 #include "w4.cuh"
 
@@ -32,7 +38,7 @@ namespace moe {
 enum class TileMode { Linear, GateUp, Down };
 
 constexpr int kTileRows = 256;              // rows of x a tile, at most
-constexpr int kXStages = 5;                 // of x: 64 k of 256 rows
+constexpr int kXStages = 5;                 // of x: 64 k of 256 rows, 128 of 128, 256 of 64
 constexpr int kXBytes = kTileRows * 128;
 constexpr int kAStages = 2;                 // of A in tensor memory: 256 k of 128 columns
 constexpr int kCStages = 3;                 // of codes: 256 k
@@ -74,6 +80,23 @@ __device__ __forceinline__ void umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, ui
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// one box into both blocks of the cluster, counted on the barrier at this offset in each
+__device__ __forceinline__ void tma_load_3d_both(uint32_t dst, const void* map, uint32_t bar,
+                                                 int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "h"((uint16_t)3)
+      : "memory");
+}
+// one arrival at the barrier at this offset in both, when the products so far are done
+__device__ __forceinline__ void umma_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
       : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
@@ -149,6 +172,9 @@ struct Bool {
 struct Tile {
   int e, n0, rows;
   int64_t m0;
+  // boxes of 32 rows, and steps of 64 k that fit a stage of x
+  __device__ __forceinline__ int boxes() const { return (rows + 31) / 32; }
+  __device__ __forceinline__ int per_stage() const { return rows <= 64 ? 4 : rows <= 128 ? 2 : 1; }
 };
 
 template <TileMode M, bool FP4, int GPS>
@@ -180,7 +206,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXStages; ++s) {
       mbar_init(x_full(s), 1);
-      mbar_init(x_empty(s), 1);
+      mbar_init(x_empty(s), 2);            // both blocks' products
     }
     for (int s = 0; s < kAStages; ++s) {
       mbar_init(a_full(s), kDecWarps);
@@ -203,7 +229,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tmem_alloc(smem_u32(s_tmem), 512);
     tmem_relinquish();
   }
-  const int nN = (a.N + kWide - 1) / kWide;
+  const int nN = (a.N + 2 * kWide - 1) / (2 * kWide);         // pairs of tiles
+  const int rank = (int)cluster_ctarank(), first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   // tstart[e]: tiles before expert e
   auto rows_of = [&](int e) {
     return a.offsets ? (int)(a.offsets[e + 1] - a.offsets[e]) : (int)a.T;
@@ -228,6 +255,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                            // the other block's barriers are there
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const int total = tstart[a.E];
@@ -249,7 +277,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int L = rows_of(lo), chunks = (L + kTileRows - 1) / kTileRows;
     const int size = ((L + 15) / 16 + chunks - 1) / chunks * 16;
     const int at = i - tstart[lo], c = at % chunks;
-    t.n0 = at / chunks * kWide;
+    t.n0 = (at / chunks * 2 + rank) * kWide;
     t.rows = min(size, L - c * size);       // (chunks of up to sixteen sixteens: none is empty)
     t.m0 = (a.offsets ? a.offsets[lo] : 0) + (int64_t)c * size;
     return t;
@@ -262,20 +290,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int s = 0, fills = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    for (int i = first; i < total && ok; i += stride) {
       const Tile t = tile_at(i);
-      const int boxes = uniform((t.rows + 31) / 32), m0 = uniform((int)t.m0);
-      for (int ks = 0; ks < kbs; ++ks) {
+      const int boxes = uniform(t.boxes()), per = uniform(t.per_stage());
+      const int m0 = uniform((int)t.m0);
+      for (int ks = 0; ks < kbs; ks += per) {
         if (!wait_all(x_empty(s), ph ^ 1u, s_abort, a.status)) {
           ok = false;
           break;
         }
         const uint32_t full = full0 + 8u * s, dst = x0 + s * kXBytes;
+        const int n = boxes * min(per, kbs - ks);
         if (leader) {
-          mbar_arrive_expect_tx(full, boxes * 4096);
-#pragma unroll
-          for (int b = 0; b < kTileRows / 32; ++b)
-            if (b < boxes) tma_load_3d(dst + b * 4096, &mapX, full, ks * 64, 0, m0 + 32 * b);
+          mbar_arrive_expect_tx(full, n * 4096);
+          // every other box is this block's to load
+          int b = rank, k = ks;
+          for (int u = rank; u < n; u += 2) {
+            while (b >= boxes) {
+              b -= boxes;
+              ++k;
+            }
+            tma_load_3d_both(dst + u * 4096, &mapX, full, k * 64, 0, m0 + 32 * b);
+            b += 2;
+          }
         }
         ++fills;
         if (++s == kXStages) { s = 0; ph ^= 1u; }
@@ -296,7 +333,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int s = 0, fills = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    for (int i = first; i < total && ok; i += stride) {
       const Tile t = tile_at(i);
       const int64_t ec = t.e * w4_codes_per_expert(a.K, a.N);
       const int64_t es = t.e * w4_scales_per_expert(a.K, a.N, 128 / GPS);
@@ -370,7 +407,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (lane == 0) mbar_arrive(full0 + 8u * (s ^ 1));
     };
     static_assert(kAStages == 2, "the other stage");
-    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    for (int i = first; i < total && ok; i += stride) {
       const Tile t = tile_at(i);
       const bool plain = plain_of(t.e, half);
       // All of the tile's stages of 256 rows, two tiles of codes a warp. (Where the last rows
@@ -442,9 +479,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int s = 0, xs = 0, h = 0;
     uint32_t ph = 0, xph = 0, used = 0;      // used: a bit a half of the accumulators, its phase
     bool ok = true;
-    for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+    for (int i = first; i < total && ok; i += stride) {
       const Tile t = tile_at(i);
-      const int N = uniform((t.rows + 15) & ~15);
+      const int N = uniform((t.rows + 15) & ~15), per = uniform(t.per_stage());
+      const uint32_t step_b = uniform(t.boxes() * (4096 >> 4));
       if (N > 128) {                         // both halves, from the first column on
         h = 0;
         if (!wait_all(acc_empty + 8, (used >> 1 & 1u) ^ 1u, s_abort, a.status)) break;
@@ -459,19 +497,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           break;
         }
         const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
-        for (int k2 = 0; k2 < n; ++k2) {
+        for (int k2 = 0; k2 < n; k2 += per) {
           if (!wait_all(x_full(xs), xph, s_abort, a.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t at = td + kAccCols + 128 * s + 32 * k2, b = b_lo + xs * (kXBytes >> 4);
+          const int m = min(per, n - k2);
+          uint32_t at = td + kAccCols + 128 * s + 32 * k2, b = b_lo + xs * (kXBytes >> 4);
           if (leader) {
+            for (int j = 0; j < m; ++j, at += 32, b += step_b) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_tmem_a(d, at + 8 * kk, ((uint64_t)b_hi << 32) | (b + kk * (32 >> 4)), idesc,
-                          ks + k2 > 0 || kk > 0);
-            umma_commit(bars_u + 8u * (kXStages + xs));                  // x_empty
+              for (int kk = 0; kk < 4; ++kk)
+                umma_tmem_a(d, at + 8 * kk, ((uint64_t)b_hi << 32) | (b + kk * (32 >> 4)), idesc,
+                            ks + k2 + j > 0 || kk > 0);
+            }
+            umma_commit_both(bars_u + 8u * (kXStages + xs));             // x_empty
           }
           if (++xs == kXStages) { xs = 0; xph ^= 1u; }
         }
@@ -498,7 +539,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int col = 16 * q + (lane & 15) + (M != TileMode::GateUp && second ? 64 : 0);
     uint32_t seen = 0;                       // a bit a half: its phase
     int h = 0;
-    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+    for (int i = first; i < total; i += stride) {
       const Tile t = tile_at(i);
       const bool wide = t.rows > 128;
       if (wide) h = 0;
@@ -555,6 +596,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                            // no copy or arrival for this block is still to come
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, 512);
 }
@@ -563,10 +605,42 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 template <TileMode M, bool FP4, int GPS>
 static cudaError_t run_tiles(const CUtensorMap& x, const TileArgs& a, bool pdl, cudaStream_t s) {
   const auto kernel = w4_tiles_kernel<M, FP4, GPS>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(pdl, kernel, dim3(num_sms()), dim3(kTileThreads), kTileSmem, s, x, a);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_pdl
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = kTileSmem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  // as many clusters as the device holds at a time (a device's blocks are asked for once)
+  static int clusters[64] = {};
+  static std::mutex mu;
+  int dev = 0, n = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!clusters[dev]) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+      if (e != cudaSuccess) return e;
+      cfg.gridDim = dim3((unsigned)(num_sms() & ~1));
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = num_sms() / 2;
+      }
+      clusters[dev] = n;
+    }
+    n = clusters[dev];
+  }
+  cfg.gridDim = dim3((unsigned)(2 * n));
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, x, a);
 }
 
 template <TileMode M>
