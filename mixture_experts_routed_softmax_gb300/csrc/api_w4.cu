@@ -27,10 +27,14 @@ static int check_T(int64_t T) {
 }
 
 // Few rows go through the rows kernel (w4_rows.cu), many through tensor memory
-// (w4_tiles.cu).
-static bool linear_by_tiles(int64_t T) { return T > 32; }
+// (w4_tiles.cu). Measured, rows against tiles: 4096 x 38912, 8 rows 22 against 28 us, 16 rows 38
+// against 28. Experts, int4 in groups of 32, by rows an expert on average: 2048 x 768, top-8 of
+// 128, 2 rows 90 against 110 us, 4 122 against 127, 8 231 against 139; 2880 x 2880, top-4 of 32, 4
+// rows 130 against 140 us, 8 217 against 157; 2560 x 640, top-10 of 512, 640 pairs 310 against 294,
+// 1280 pairs 439 against 377 (a block of the rows kernel looks through all of them).
+static bool linear_by_tiles(int64_t T) { return T > 8; }
 static bool experts_by_tiles(int64_t T, int k, int E) {
-  return T * k > kRowsMaxPairs || T * k > (int64_t)16 * E;
+  return T * k > kRowsMaxPairs || T * k > (int64_t)4 * E;
 }
 
 // The workspace of the experts' forward.

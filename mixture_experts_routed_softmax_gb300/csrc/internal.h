@@ -142,7 +142,7 @@ cudaError_t launch_w4_pack(const moe_w4& w, const moe_bf16* src, const uint8_t* 
                            const moe_bf16* scales, cudaStream_t s);
 cudaError_t launch_w4_unpack(const moe_w4& w, moe_bf16* dst, cudaStream_t s);
 // w4_rows.cu
-constexpr int kRowsMaxPairs = 2048;   // token-expert pairs of one launch
+constexpr int kRowsMaxPairs = 512;    // token-expert pairs of one launch
 struct W4Experts {
   const moe_w4 *gate, *up, *down;
   ActParams act;

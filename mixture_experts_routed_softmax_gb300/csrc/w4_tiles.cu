@@ -49,7 +49,7 @@ constexpr int kDecWarp0 = 4, kDecWarps = 16, kOutWarp0 = 20, kOutWarps = 8;
 constexpr int kTileThreads = 32 * (kOutWarp0 + kOutWarps);
 constexpr int kAccCols = 256;               // accumulators: two halves of 128 columns
 constexpr int kTileSmem = 1024 + kXStages * kXBytes + kCStages * (kCBytes + kSBytes) +
-                          4 * (kMaxExperts + 1) + 512;
+                          8 * (kMaxExperts + 2) + 512;
 
 struct TileArgs {
   const uint8_t* codes[2];
@@ -231,12 +231,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   }
   const int nN = (a.N + 2 * kWide - 1) / (2 * kWide);         // pairs of tiles
   const int rank = (int)cluster_ctarank(), first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-  // tstart[e]: tiles before expert e
-  auto rows_of = [&](int e) {
-    return a.offsets ? (int)(a.offsets[e + 1] - a.offsets[e]) : (int)a.T;
-  };
-  for (int e = threadIdx.x; e < a.E; e += kTileThreads)
-    tstart[e + 1] = (rows_of(e) + kTileRows - 1) / kTileRows * nN;
+  // tstart[e]: pairs of tiles before expert e; rstart[e]: rows
+  int* rstart = tstart + a.E + 1;
+  for (int e = threadIdx.x; e < a.E; e += kTileThreads) {
+    const int r0 = a.offsets ? (int)a.offsets[e] : 0;
+    const int r1 = a.offsets ? (int)a.offsets[e + 1] : (int)a.T;
+    rstart[e] = r0;
+    if (e == a.E - 1) rstart[a.E] = r1;
+    tstart[e + 1] = (r1 - r0 + kTileRows - 1) / kTileRows * nN;
+  }
   __syncthreads();
   if (warp == 3) {
     int run = 0;
@@ -274,12 +277,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     Tile t;
     t.e = lo;
-    const int L = rows_of(lo), chunks = (L + kTileRows - 1) / kTileRows;
+    const int L = rstart[lo + 1] - rstart[lo], chunks = (L + kTileRows - 1) / kTileRows;
     const int size = ((L + 15) / 16 + chunks - 1) / chunks * 16;
     const int at = i - tstart[lo], c = at % chunks;
     t.n0 = (at / chunks * 2 + rank) * kWide;
     t.rows = min(size, L - c * size);       // (chunks of up to sixteen sixteens: none is empty)
-    t.m0 = (a.offsets ? a.offsets[lo] : 0) + (int64_t)c * size;
+    t.m0 = rstart[lo] + (int64_t)c * size;
     return t;
   };
 
@@ -548,34 +551,30 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc_fence_after();
       const int n = t.n0 + col;
       const float unit = plain_of(t.e, second) ? W4Decoder<FP4>::kScaled : 1.f;
+      bool half0 = true;                     // the first 128 columns are still to be given back
       for (int c0 = 16 * part; c0 < t.rows; c0 += 32) {
         uint32_t v[16];
         tmem_ld16(at + 128 * h + c0, v);
         tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * unit);
-        const int64_t first = (t.m0 + c0) * a.out_stride + n;
+        const int64_t first_at = (t.m0 + c0) * a.out_stride + n;
         const int here = n < a.N ? t.rows - c0 : 0;          // rows of these sixteen
         if (M == TileMode::GateUp) {
           // of two rows the lower lanes, which hold gates, take the first, the upper ones,
           // which hold the same columns' ups, the second
+          moe_bf16* o = static_cast<moe_bf16*>(a.out) + first_at + second * a.out_stride;
 #pragma unroll
           for (int c = 0; c < 16; c += 2) {
-            const float got = __uint_as_float(
-                __shfl_xor_sync(0xFFFFFFFFu, second ? v[c] : v[c + 1], 16));
-            const float gt = second ? got : __uint_as_float(v[c]);
-            const float up = second ? __uint_as_float(v[c + 1]) : got;
-            const int cc = c + second;
-            const float y = gated(gt, up, a.act);
-            if (cc < here)
-              static_cast<moe_bf16*>(a.out)[first + cc * a.out_stride] =
-                  __bfloat16_as_ushort(__float2bfloat16_rn(y));
+            const float mine0 = __uint_as_float(v[c]) * unit, mine1 = __uint_as_float(v[c + 1]) * unit;
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, second ? mine0 : mine1, 16);
+            const float y = gated(second ? got : mine0, second ? mine1 : got, a.act);
+            if (c + second < here) *o = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+            o += 2 * a.out_stride;
           }
         } else {
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const float f = __uint_as_float(v[c]);
-            const int64_t o = first + c * a.out_stride;
+            const float f = __uint_as_float(v[c]) * unit;
+            const int64_t o = first_at + c * a.out_stride;
             if (c < here) {
               if (M == TileMode::Down || a.out_fp32)
                 static_cast<float*>(a.out)[o] = f;
@@ -584,11 +583,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
           }
         }
+        if (wide && c0 + 32 >= 128 && half0) {
+          half0 = false;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty);
+        }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(acc_empty + 8 * h);
+        if (half0) mbar_arrive(acc_empty + 8 * h);
         if (wide) mbar_arrive(acc_empty + 8);
       }
       h = wide ? 0 : h ^ 1;
