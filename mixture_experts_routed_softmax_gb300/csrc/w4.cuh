@@ -60,34 +60,7 @@ __host__ __device__ __forceinline__ int64_t w4_scales_at(int nb, int st, int nbs
   return ((int64_t)b * steps + (int64_t)c * cb + (nb - b) * m + (st - c)) * 16 * gps;
 }
 
-// the bit of a pair's low half that holds bit b (0: lowest) of the fp4 code
-__host__ __device__ constexpr int fp4_bit(int i, int b) {
-  return i == 0   ? (b == 3 ? 15 : 6 + b)
-         : i == 1 ? (b == 3 ? 12 : 3 + b)
-         : i == 2 ? (b == 3 ? 9 : b)
-                  : (b == 3 ? 14 : b == 0 ? 13 : 9 + b);
-}
-
-// a code (two's complement, or sign and magnitude) at its place in a word
-__device__ __forceinline__ uint32_t w4_place(uint32_t code, int i, int odd, bool fp4) {
-  uint32_t v;
-  if (fp4) {
-    v = 0;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) v |= ((code >> b) & 1u) << fp4_bit(i, b);
-  } else {
-    v = (code ^ 8u) << (4 * i);
-  }
-  return v << (16 * odd);
-}
-__device__ __forceinline__ uint32_t w4_code_at(uint32_t word, int i, int odd, bool fp4) {
-  const uint32_t v = word >> (16 * odd);
-  if (!fp4) return ((v >> (4 * i)) & 15u) ^ 8u;
-  uint32_t c = 0;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) c |= ((v >> fp4_bit(i, b)) & 1u) << b;
-  return c;
-}
+// what a code (two's complement, or sign and magnitude) stands for
 __device__ __forceinline__ float w4_value(uint32_t code, bool fp4) {
   if (!fp4) return (float)((int)(code ^ 8u) - 8);
   const uint32_t e = (code >> 1) & 3u, m = code & 1u;

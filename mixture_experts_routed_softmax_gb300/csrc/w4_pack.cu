@@ -11,15 +11,16 @@
 // A group whose a is below 2^-120 becomes zeros (scale 0); one with an infinity
 // or NaN gets scale NaN and stays visible as such.
 //
-// Memory-bound: 2 bytes read and 1/2 + 2/group written a weight. A block takes 64
-// columns by 128 rows through shared memory: rows of 128 bytes come in, whole
-// tiles of 512 bytes go out.
+// Bound by memory in floor (2 bytes read and 1/2 + 2/group written a weight), by some ten
+// instructions a weight in practice. A block takes 64 columns by 128 rows through shared
+// memory: rows of 128 bytes come in, whole tiles of 512 bytes go out.
 #include "w4.cuh"
 
 namespace moe {
 
 constexpr int kPackN = 64;            // columns of a block: four tiles
 constexpr int kPackThreads = 128;
+constexpr int kPackPitch = kPackN + 2;   // bf16 a row: 33 words, so that rows shift banks
 
 struct W4View {
   uint8_t* codes;
@@ -44,7 +45,9 @@ __device__ __forceinline__ float group_scale(float a, bool fp4) {
   return __uint_as_float(((b >> 23) - up) << 23);
 }
 
-__device__ __forceinline__ uint32_t nearest_code(float w, float s, bool fp4) {
+// The code of one weight in any case: at the top of the range the nearest value may be one that
+// bf16 does not hold.
+__device__ __noinline__ uint32_t nearest_code(float w, float s, bool fp4) {
   if (!(s > 0.f)) return 0u;
   const float q = __fdiv_rn(w, s);
   const float a = fabsf(q);
@@ -53,10 +56,37 @@ __device__ __forceinline__ uint32_t nearest_code(float w, float s, bool fp4) {
           : a < 2.f ? __float2int_rn(2.f * a)
           : a < 4.f ? __float2int_rn(a) + 2
                     : __float2int_rn(0.5f * a) + 4;
-  // at the top of the range the nearest value may be one that bf16 does not hold
   if (s > 1e37f && n > 0 && w4_value((uint32_t)n, fp4) * s > 3.3895314e38f) --n;
   if (!fp4) return (uint32_t)(q < 0.f ? -n : n) & 15u;
   return (uint32_t)n | (n && q < 0.f ? 8u : 0u);
+}
+
+// Two weights to int4 codes, by r = 1 / scale rounded. w / scale is half a step or at least
+// 2^-9 away from one (w has eight significant bits, scale five, the quotient is below
+// 7.5), w r is off by 2^-20: rounded to 2^-10 (the first two additions) it is on the right side, or
+// on the half itself, which the third rounds to the even code. The sum's last bits
+// are the code in two's complement.
+__device__ __forceinline__ uint32_t int4_code(float w, float r) {
+  const float q = __fadd_rn(__fadd_rn(__fmul_rn(w, r), 12288.0f), -12288.0f);
+  return __float_as_uint(__fadd_rn(q, 12582912.0f)) & 15u;
+}
+// Two weights (w r exact: r is a power of two) to fp4 codes, the first in the low four bits
+__device__ __forceinline__ uint32_t fp4_codes(float w0, float w1, float r0, float r1) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}\n"
+      : "=r"(d)
+      : "f"(w0 * r0), "f"(w1 * r1));
+  return d;
+}
+// A word of codes side by side (pair i in bits 4i of either half) to the kind's places
+template <bool FP4>
+__device__ __forceinline__ uint32_t w4_arrange(uint32_t x) {
+  if (!FP4) return x ^ 0x88888888u;
+  return ((x << 6) & 0x01C001C0u) | ((x << 12) & 0x80008000u) | ((x >> 1) & 0x40384038u) |
+         ((x << 5) & 0x10001000u) | ((x >> 8) & 0x00070007u) | ((x >> 2) & 0x02000200u) |
+         ((x << 1) & 0x20002000u) | ((x >> 3) & 0x0C000C00u);
 }
 
 // SRC 0: bf16 weights [E, K, N], quantised here; 1: codes [E, K, N] (a byte each) and
@@ -66,51 +96,54 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
     W4View w, const moe_bf16* __restrict__ src, const uint8_t* __restrict__ codes,
     const moe_bf16* __restrict__ scales) {
   pdl_enter();
-  __shared__ float tile[128][kPackN + 1];             // weights, then codes
-  __shared__ float amax[8][kPackN];                   // of 16 rows each
-  __shared__ float sc[4][kPackN];                     // the step's groups
+  __shared__ __align__(16) moe_bf16 tile[128 * kPackPitch];   // weights, or codes
+  __shared__ uint32_t amax[8][kPackN / 2];            // of 16 rows each, two columns a word
+  __shared__ float sc[4][kPackN], rs[4][kPackN];      // the step's groups: scale, its inverse
   const int e = blockIdx.z, step = blockIdx.y, n0 = blockIdx.x * kPackN;
   const int tid = threadIdx.x;
   const int gps = w4_gps(w.group), groups = (w.K + w.group - 1) / w.group;
-  // rows of 64 columns, 16 bytes (8 with one byte a code) a thread
+#pragma unroll 4
   for (int i = tid; i < 128 * (kPackN / 8); i += kPackThreads) {
     const int r = i / (kPackN / 8), c = (i % (kPackN / 8)) * 8;
     const int k = step * 128 + r;
-    float v[8] = {};
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (k < w.K && n0 + c < w.N) {
       const int64_t at = ((int64_t)e * w.K + k) * w.N + n0 + c;
       if (SRC == 0) {
-        unpack8(*reinterpret_cast<const uint4*>(src + at), v);
+        v = *reinterpret_cast<const uint4*>(src + at);
       } else {
-        const uint2 b = *reinterpret_cast<const uint2*>(codes + at);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[j] = __uint_as_float(((j < 4 ? b.x : b.y) >> (8 * (j & 3))) & 15u);
+        const uint2 b = *reinterpret_cast<const uint2*>(codes + at);     // a byte to 16 bits
+        v = make_uint4(__byte_perm(b.x, 0, 0x4140), __byte_perm(b.x, 0, 0x4342),
+                       __byte_perm(b.y, 0, 0x4140), __byte_perm(b.y, 0, 0x4342));
       }
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) tile[r][c + j] = v[j];
+    uint32_t* d = reinterpret_cast<uint32_t*>(tile + r * kPackPitch + c);
+    d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
   }
   __syncthreads();
+  bool odd = false;                    // a scale that the fast forms do not take
   if (SRC == 0) {
-    for (int i = tid; i < 8 * kPackN; i += kPackThreads) {
-      const int n = i % kPackN, part = i / kPackN;
-      float a = 0.f;
-      bool odd = false;                // an infinity or NaN
+    for (int i = tid; i < 8 * (kPackN / 2); i += kPackThreads) {
+      const int n2 = i % (kPackN / 2), part = i / (kPackN / 2);
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(tile + 16 * part * kPackPitch) + n2;
+      uint32_t a = 0;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float v = fabsf(tile[16 * part + r][n]);
-        odd |= !(v < INFINITY);
-        a = fmaxf(a, v);
+        // magnitudes (NaN stays NaN)
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(p[r * (kPackPitch / 2)] & 0x7FFF7FFFu));
       }
-      amax[part][n] = odd ? INFINITY : a;
+      amax[part][n2] = a;
     }
     __syncthreads();
     for (int i = tid; i < gps * kPackN; i += kPackThreads) {
       const int n = i % kPackN, gr = i / kPackN, parts = 8 / gps;
-      float a = 0.f;
-      for (int p = 0; p < parts; ++p) a = fmaxf(a, amax[gr * parts + p][n]);
-      sc[gr][n] = group_scale(a, FP4);
+      uint32_t a = 0;
+      for (int p = 0; p < parts; ++p)
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(amax[gr * parts + p][n / 2]));
+      const float s = group_scale((n & 1) ? bf16_hi(a) : bf16_lo(a), FP4);
+      sc[gr][n] = s;
+      rs[gr][n] = s > 0.f ? 1.0f / s : 0.f;           // (0 codes for scales 0 and NaN)
+      odd |= s > 1e37f;
     }
   } else {
     for (int i = tid; i < gps * kPackN; i += kPackThreads) {
@@ -121,35 +154,60 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
                       : 0.f;
     }
   }
-  __syncthreads();
+  const bool slow = __syncthreads_or(odd);
   // a warp a tile of 16 columns, its two tiles of 64 rows one after the other
   const int lane = tid & 31, nb = n0 / 16 + tid / 32, g = lane >> 2, t = lane & 3;
   if (nb >= w4_nblocks(w.N)) return;
   const int c0 = 16 * (tid / 32);
-  const int kbs = w4_kblocks(w.K);
+  const int kbs = w4_kblocks(w.K), nbs = w4_nblocks(w.N);
   for (int kb = 2 * step; kb < 2 * step + 2 && kb < kbs; ++kb) {
-    uint32_t word[4] = {};
+    uint32_t word[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j) {
+      const int r0 = 64 * (kb & 1) + 16 * j + 4 * t, gr = (r0 * gps) >> 7;
+      uint32_t x = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int hi = 0; hi < 2; ++hi) {                 // column g, column g + 8
+        const int n = c0 + g + 8 * hi;
+        const moe_bf16* p = tile + r0 * kPackPitch + n;
+        uint32_t v[4];
 #pragma unroll
-        for (int odd = 0; odd < 2; ++odd) {
-          const int n = c0 + g + 8 * (i & 1);
-          const int r = 64 * (kb & 1) + 16 * j + 4 * t + 2 * (i >> 1) + odd;
-          const float v = tile[r][n];
-          // a group is 32, 64 or 128 rows: r / group without a division
-          const uint32_t code =
-              SRC == 0 ? nearest_code(v, sc[(r * gps) >> 7][n], FP4) : __float_as_uint(v);
-          word[j] |= w4_place(code, i, odd, FP4);
+        for (int q = 0; q < 4; ++q) v[q] = p[q * kPackPitch];
+        // rows 0, 1 are pair hi, rows 2, 3 pair 2 + hi; odd rows in the high half
+        if (SRC == 1) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x |= (v[q] & 15u) << (4 * hi + 8 * (q >> 1) + 16 * (q & 1));
+        } else if (slow) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            x |= nearest_code(__uint_as_float(v[q] << 16), sc[gr][n], FP4)
+                 << (4 * hi + 8 * (q >> 1) + 16 * (q & 1));
+        } else {
+          const float r = rs[gr][n];
+          if (FP4) {
+            const uint32_t even = fp4_codes(__uint_as_float(v[0] << 16), __uint_as_float(v[2] << 16), r, r);
+            const uint32_t uneven = fp4_codes(__uint_as_float(v[1] << 16), __uint_as_float(v[3] << 16), r, r);
+            // four bits each of rows 0, 2 to bits 0 and 8 of the low half, of 1, 3 of the high
+            const uint32_t b = even | (uneven << 16);
+            x |= ((b & 0x000F000Fu) | ((b & 0x00F000F0u) << 4)) << (4 * hi);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              x |= int4_code(__uint_as_float(v[q] << 16), r)
+                   << (4 * hi + 8 * (q >> 1) + 16 * (q & 1));
+          }
         }
+      }
+      word[j] = w4_arrange<FP4>(x);
+    }
     uint4* dst = reinterpret_cast<uint4*>(w.codes +
                                           (int64_t)e * w4_codes_per_expert(w.K, w.N) +
-                                          w4_tile_at(nb, kb, w4_nblocks(w.N), kbs));
+                                          w4_tile_at(nb, kb, nbs, kbs));
     dst[lane] = make_uint4(word[0], word[1], word[2], word[3]);
   }
   moe_bf16* out = w.scales + (int64_t)e * w4_scales_per_expert(w.K, w.N, w.group) +
-                  w4_scales_at(nb, step, w4_nblocks(w.N), w4_steps(w.K), gps);
+                  w4_scales_at(nb, step, nbs, w4_steps(w.K), gps);
   bool plain = true;
   for (int i = lane; i < 16 * gps; i += 32) {
     const int gg = i / (2 * gps), gr = (i / 2) % gps, hi = i & 1;
