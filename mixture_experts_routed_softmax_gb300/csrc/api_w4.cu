@@ -27,12 +27,15 @@ static int check_T(int64_t T) {
 }
 
 // Few rows go through the rows kernel (w4_rows.cu), many through tensor memory
-// (w4_tiles.cu). Measured, rows against tiles: 4096 x 38912, 8 rows 22 against 28 us, 16 rows 38
-// against 28. Experts, int4 in groups of 32, by rows an expert on average: 2048 x 768, top-8 of
+// (w4_tiles.cu). Measured, rows against tiles: 8192 x 8192, 8 rows 14.5 against 23 us, 16 rows 26
+// against 23; 4096 x 2880, 16 rows 7.6 against 13.5, 32 rows 13.3 against 13.8; 2048 x 2048, 64
+// rows 9.7 against 10.0, 96 rows 13.9 against 11.3. Experts, int4 in groups of 32, by rows an expert on average: 2048 x 768, top-8 of
 // 128, 2 rows 90 against 110 us, 4 122 against 127, 8 231 against 139; 2880 x 2880, top-4 of 32, 4
 // rows 130 against 140 us, 8 217 against 157; 2560 x 640, top-10 of 512, 640 pairs 310 against 294,
 // 1280 pairs 439 against 377 (a block of the rows kernel looks through all of them).
-static bool linear_by_tiles(int64_t T) { return T > 8; }
+static bool linear_by_tiles(int64_t T, int K, int N) {
+  return T > 8 && (double)T * K * N > 3.4e8;
+}
 static bool experts_by_tiles(int64_t T, int k, int E) {
   return T * k > kRowsMaxPairs || T * k > (int64_t)4 * E;
 }
@@ -122,7 +125,7 @@ int moe_w4_linear(const moe_w4* w, const moe_bf16* x, int64_t x_stride, int64_t 
   int* st = device_status_ptr();
   if (!st) return MOE_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_code(linear_by_tiles(T)
+  return cuda_code(linear_by_tiles(T, w->K, w->N)
                        ? launch_w4_linear_tiles(*w, x, x_stride, T, y, y_stride, y_fp32, st, s)
                        : launch_w4_linear_rows(*w, x, x_stride, T, y, y_stride, y_fp32, st, s));
 }
@@ -183,9 +186,7 @@ int moe_expert_fwd_w4(const moe_w4* gate, const moe_w4* up, const moe_w4* down,
   moe_bf16* A = reinterpret_cast<moe_bf16*>(p + w.A);
   float* yp = reinterpret_cast<float*>(p + w.yp);
   if (!experts_by_tiles(T, k, E)) {
-    cudaError_t e = launch_w4_experts_rows(q, A, yp, st, s);
-    if (e == cudaSuccess) e = launch_w4_combine(q, yp, y, s);
-    return cuda_code(e);
+    return cuda_code(launch_w4_experts_rows(q, A, yp, y, st, s));
   }
   moe_bf16* xp = reinterpret_cast<moe_bf16*>(p + w.xp);
   int64_t* offsets = reinterpret_cast<int64_t*>(p + w.offsets);

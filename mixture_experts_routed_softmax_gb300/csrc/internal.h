@@ -155,9 +155,9 @@ struct W4Experts {
 cudaError_t launch_w4_linear_rows(const moe_w4& w, const moe_bf16* x, int64_t x_stride, int64_t T,
                                   void* y, int64_t y_stride, int y_fp32, int* status,
                                   cudaStream_t s);
-// A [T*(k+S), f] and yp [T*(k+S), d], rows by pair (T*k <= kRowsMaxPairs)
-cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, int* status,
-                                   cudaStream_t s);
+// A [T*(k+S), f] and yp [T*(k+S), d] scratch, rows by pair (T*k <= kRowsMaxPairs); y [T, d]
+cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, moe_bf16* y,
+                                   int* status, cudaStream_t s);
 // w4_tiles.cu: rows in the padded layout (offsets, xp of launch_permute)
 cudaError_t launch_w4_linear_tiles(const moe_w4& w, const moe_bf16* x, int64_t x_stride, int64_t T,
                                    void* y, int64_t y_stride, int y_fp32, int* status,
@@ -165,7 +165,6 @@ cudaError_t launch_w4_linear_tiles(const moe_w4& w, const moe_bf16* x, int64_t x
 cudaError_t launch_w4_experts_tiles(const W4Experts& q, const moe_bf16* xp, const int64_t* offsets,
                                     int64_t R_cap, moe_bf16* A, float* yp, int* status,
                                     cudaStream_t s);
-cudaError_t launch_w4_combine(const W4Experts& q, const float* yp, moe_bf16* y, cudaStream_t s);
 
 // rope.cu
 cudaError_t launch_rope(const moe_rotary* rot, const int32_t* pos, int64_t T, int D,

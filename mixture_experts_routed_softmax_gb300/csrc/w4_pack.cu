@@ -61,7 +61,7 @@ __device__ __noinline__ uint32_t nearest_code(float w, float s, bool fp4) {
   return (uint32_t)n | (n && q < 0.f ? 8u : 0u);
 }
 
-// Two weights to int4 codes, by r = 1 / scale rounded. w / scale is half a step or at least
+// A weight to an int4 code, by r = 1 / scale rounded. w / scale is half a step or at least
 // 2^-9 away from one (w has eight significant bits, scale five, the quotient is below
 // 7.5), w r is off by 2^-20: rounded to 2^-10 (the first two additions) it is on the right side, or
 // on the half itself, which the third rounds to the even code. The sum's last bits

@@ -269,6 +269,98 @@ __global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(RowsArgs a) {
   }
 }
 
+// One token's down products and their weighted sum over its experts in one go: a block takes
+// 16 columns of all of them, its warps the steps of 128 k of expert after expert, four
+// at a time so that 4 KB a warp are on their way. y [d], rows A by slot (k choices, S shared).
+template <bool FP4, int GPS>
+__global__ void __launch_bounds__(kRowThreads) w4_token_kernel(RowsArgs a,
+                                                               const float* __restrict__ w) {
+  constexpr int U = 4;
+  __shared__ float red[kRowWarps][16];
+  __shared__ int expert[32];
+  __shared__ float weight[32];
+  pdl_enter();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int slots = a.k + a.S;
+  if (threadIdx.x < slots) {
+    const int j = threadIdx.x;
+    const int id = j < a.k ? a.idx[j] : a.E + j - a.k;
+    // (an id out of range is reported by the gate/up products)
+    expert[j] = j < a.k && (id < 0 || id >= a.E) ? -1 : id;
+    weight[j] = j < a.k ? w[j] : 1.f;
+  }
+  __syncthreads();
+  const W4Decoder<FP4> decode;
+  const int kbs = w4_kblocks(a.K), steps = w4_steps(a.K), nbs = w4_nblocks(a.N), nb = blockIdx.x;
+  float acc[4] = {};
+  for (int u0 = warp * U; u0 < slots * steps; u0 += kRowWarps * U) {
+    uint4 cw[U][2];
+    uint32_t sw[U][GPS];
+    uint2 xv[U][8];
+    float f[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int slot = min((u0 + i) / steps, slots - 1), step = (u0 + i) - slot * steps;
+      const int id = step < steps ? expert[slot] : -1;
+      f[i] = decode.kUnit * weight[slot];
+      const uint32_t zero = FP4 ? 0u : 0x88888888u;
+      cw[i][0] = cw[i][1] = make_uint4(zero, zero, zero, zero);
+#pragma unroll
+      for (int q = 0; q < GPS; ++q) sw[i][q] = 0u;
+      if (id >= 0) {
+        const uint8_t* src = a.codes[0] + id * w4_codes_per_expert(a.K, a.N) +
+                             w4_tile_at(nb, 2 * step, nbs, kbs) + 16 * lane;
+        cw[i][0] = ldg_stream(src);
+        if (2 * step + 1 < kbs) cw[i][1] = ldg_stream(src + kW4Tile);
+        const uint32_t* sp = reinterpret_cast<const uint32_t*>(
+            a.scales[0] + id * w4_scales_per_expert(a.K, a.N, 128 / GPS) +
+            w4_scales_at(nb, step, nbs, steps, GPS) + 2 * GPS * g);
+#pragma unroll
+        for (int q = 0; q < GPS; ++q) sw[i][q] = __ldg(sp + q);
+      }
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        const int k = 128 * step + 16 * h + 4 * t;
+        xv[i][h] = make_uint2(0u, 0u);
+        // (the other columns of the product's B operand stay zeros)
+        if (id >= 0 && g == 0 && k < a.K)
+          xv[i][h] = *reinterpret_cast<const uint2*>(a.x + slot * a.x_stride + k);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float part[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if (h % (4 / GPS) == 0) part[0] = part[1] = part[2] = part[3] = 0.f;
+        const uint4 c = cw[i][h >> 1];
+        uint32_t av[4];
+        decode.values((h & 1) ? c.z : c.x, av);
+        mma16816(part, av, xv[i][2 * h].x, xv[i][2 * h].y);
+        decode.values((h & 1) ? c.w : c.y, av);
+        mma16816(part, av, xv[i][2 * h + 1].x, xv[i][2 * h + 1].y);
+        if (h % (4 / GPS) == 4 / GPS - 1) {
+          const uint32_t s = sw[i][h / (4 / GPS)];
+          acc[0] = fmaf(bf16_lo(s) * f[i], part[0], acc[0]);
+          acc[2] = fmaf(bf16_hi(s) * f[i], part[2], acc[2]);
+        }
+      }
+    }
+  }
+  if (t == 0) {                              // column 0: this token
+    red[warp][g] = acc[0];
+    red[warp][g + 8] = acc[2];
+  }
+  __syncthreads();
+  const int n = nb * 16 + (int)threadIdx.x;
+  if (threadIdx.x < 16 && n < a.N) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRowWarps; ++i) sum += red[i][threadIdx.x];
+    static_cast<moe_bf16*>(a.out)[n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+  }
+}
+
 // y[t] = sum_j w[t, j] Yp[t k + j] + the shared experts' rows, in slot order; a pair
 // whose expert is out of range is left out. A warp takes 256 columns of a token.
 __global__ void __launch_bounds__(256) w4_combine_kernel(
@@ -321,12 +413,24 @@ static cudaError_t run_rows(const RowsArgs& a, int units, cudaStream_t s) {
   return launch_pdl(true, kernel, dim3(gx, units), dim3(kRowThreads), smem, s, a);
 }
 
+// Blocks of 16 columns a block takes (RB): as many as leave two blocks an SM, since the rows of
+// x are loaded once for all of them; fewer for small matrices (2880 x 5120, one row: SAME us with
+// 4, 2, 1).
+template <RowsMode M, bool FP4, int GPS, int NT, int RB>
+static cudaError_t run_rows_rb(const RowsArgs& a, int units, cudaStream_t s) {
+  if constexpr (RB > 1) {
+    if ((int64_t)((w4_nblocks(a.N) + RB - 1) / RB) * units < 2 * num_sms())
+      return run_rows_rb<M, FP4, GPS, NT, RB / 2>(a, units, s);
+  }
+  return run_rows<M, FP4, GPS, NT, RB>(a, units, s);
+}
+
 template <RowsMode M, bool FP4, int GPS>
 static cudaError_t run_rows_nt(const RowsArgs& a, int units, int nt, cudaStream_t s) {
   constexpr int RB = M == RowsMode::GateUp ? 2 : 4;
-  return nt <= 1   ? run_rows<M, FP4, GPS, 1, RB>(a, units, s)
-         : nt <= 2 ? run_rows<M, FP4, GPS, 2, RB>(a, units, s)
-                   : run_rows<M, FP4, GPS, 4, RB / 2>(a, units, s);
+  return nt <= 1   ? run_rows_rb<M, FP4, GPS, 1, RB>(a, units, s)
+         : nt <= 2 ? run_rows_rb<M, FP4, GPS, 2, RB>(a, units, s)
+                   : run_rows_rb<M, FP4, GPS, 4, RB / 2>(a, units, s);
 }
 
 template <RowsMode M>
@@ -372,8 +476,19 @@ cudaError_t launch_w4_linear_rows(const moe_w4& w, const moe_bf16* x, int64_t x_
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, int* status,
-                                   cudaStream_t s) {
+static cudaError_t launch_w4_combine(const W4Experts& q, const float* yp, moe_bf16* y, cudaStream_t s) {
+  timer_before(MOE_KERNEL_COMBINE, s);
+  const int64_t warps = q.T * (((int64_t)q.d / 8 + 31) / 32);
+  const cudaError_t e =
+      launch_pdl(pdl_for_tokens(q.T), w4_combine_kernel, dim3((unsigned)((warps + 7) / 8)),
+                 dim3(256), 0, s, yp, q.topk_idx, q.topk_w, q.T, q.k, q.E, q.S, q.d, y);
+  note_launches(1);
+  timer_after(MOE_KERNEL_COMBINE, s);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, moe_bf16* y,
+                                   int* status, cudaStream_t s) {
   const int64_t P = q.T * q.k;
   RowsArgs a{};
   a.codes[0] = q.gate->codes;
@@ -404,20 +519,26 @@ cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, i
   a.x = A;
   a.x_stride = q.f;
   a.out = yp;
-  if (e == cudaSuccess) e = rows<RowsMode::Down>(a, *q.down, units, nt, s);
+  if (q.T == 1) {
+    // one token: no rows of single experts, no launch to add them up (one of 128 experts
+    // of 2048 x 768, top-8: SAME us)
+    a.out = y;
+    const int gps = w4_gps(q.down->group);
+    const auto kernel = q.down->kind == MOE_W4_FP4
+                            ? (gps == 4   ? w4_token_kernel<true, 4>
+                               : gps == 2 ? w4_token_kernel<true, 2>
+                                          : w4_token_kernel<true, 1>)
+                            : (gps == 4   ? w4_token_kernel<false, 4>
+                               : gps == 2 ? w4_token_kernel<false, 2>
+                                          : w4_token_kernel<false, 1>);
+    if (e == cudaSuccess)
+      e = launch_pdl(true, kernel, dim3(w4_nblocks(q.d)), dim3(kRowThreads), 0, s, a, q.topk_w);
+  } else if (e == cudaSuccess) {
+    e = rows<RowsMode::Down>(a, *q.down, units, nt, s);
+  }
   note_launches(2);
   timer_after(MOE_KERNEL_W4_ROWS, s);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-cudaError_t launch_w4_combine(const W4Experts& q, const float* yp, moe_bf16* y, cudaStream_t s) {
-  timer_before(MOE_KERNEL_COMBINE, s);
-  const int64_t warps = q.T * (((int64_t)q.d / 8 + 31) / 32);
-  const cudaError_t e =
-      launch_pdl(pdl_for_tokens(q.T), w4_combine_kernel, dim3((unsigned)((warps + 7) / 8)),
-                 dim3(256), 0, s, yp, q.topk_idx, q.topk_w, q.T, q.k, q.E, q.S, q.d, y);
-  note_launches(1);
-  timer_after(MOE_KERNEL_COMBINE, s);
+  if (e == cudaSuccess && q.T > 1) e = launch_w4_combine(q, yp, y, s);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
