@@ -632,7 +632,8 @@ int moe_w4_pack(const moe_w4* w, const uint8_t* codes, const moe_bf16* scales,
  * moe_w4_quantise). */
 int moe_w4_dequantise(const moe_w4* w, moe_bf16* dst, moe_stream_t stream);
 
-/* moe_w4_linear — y = x W for one matrix (w->E = 1), fp32 sums, rounded once.
+/* moe_w4_linear — y = x W for one matrix (w->E = 1), fp32 sums, rounded once; with many rows
+ * code * scale is rounded to bf16 first (as in moe_expert_fwd_w4).
  *  x [T, K] bf16, rows x_stride elements apart (a multiple of 8, >= K); y [T, N] bf16, or
  *  fp32 (y_fp32 != 0), rows y_stride elements apart (>= N). y may not overlap x.
  *  ws: moe_w4_linear_workspace_size(w, T) bytes, 256-byte aligned, one call at a time per

@@ -27,9 +27,9 @@ static int check_T(int64_t T) {
 }
 
 // Few rows go through the rows kernel (w4_rows.cu), many through tensor memory
-// (w4_tiles.cu). Measured, rows against tiles: 8192 x 8192, 8 rows 14.5 against 23 us, 16 rows 26
-// against 23; 4096 x 2880, 16 rows 7.6 against 13.5, 32 rows 13.3 against 13.8; 2048 x 2048, 64
-// rows 9.7 against 10.0, 96 rows 13.9 against 11.3. Experts, int4 in groups of 32, by rows an expert on average: 2048 x 768, top-8 of
+// (w4_tiles.cu). Measured, rows against tiles: 8192 x 8192, 8 rows 14.5 against 17 us, 16 rows 26
+// against 17; 4096 x 2880, 16 rows 7.6 against 10.5, 32 rows 13.3 against 10.7; 2048 x 2048, 64
+// rows 9.7 against 10.0, 96 rows 13.9 against 10.1. Experts, int4 in groups of 32, by rows an expert on average: 2048 x 768, top-8 of
 // 128, 2 rows 90 against 110 us, 4 122 against 127, 8 231 against 139; 2880 x 2880, top-4 of 32, 4
 // rows 130 against 140 us, 8 217 against 157; 2560 x 640, top-10 of 512, 640 pairs 310 against 294,
 // 1280 pairs 439 against 377 (a block of the rows kernel looks through all of them).
@@ -106,9 +106,9 @@ int moe_w4_dequantise(const moe_w4* w, moe_bf16* dst, moe_stream_t stream) {
 }
 
 size_t moe_w4_linear_workspace_size(const moe_w4* w, int64_t T) {
-  (void)w;
-  (void)T;
-  return 0;
+  if (!w || check_dims(w->E, w->K, w->N) || check_T(T) || !linear_by_tiles(T, w->K, w->N)) return 0;
+  const int n = w4_linear_splits(T, w->K, w->N);
+  return n > 1 ? (size_t)n * T * w->N * sizeof(float) : 0;
 }
 
 int moe_w4_linear(const moe_w4* w, const moe_bf16* x, int64_t x_stride, int64_t T, void* y,
@@ -126,7 +126,8 @@ int moe_w4_linear(const moe_w4* w, const moe_bf16* x, int64_t x_stride, int64_t 
   if (!st) return MOE_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return cuda_code(linear_by_tiles(T, w->K, w->N)
-                       ? launch_w4_linear_tiles(*w, x, x_stride, T, y, y_stride, y_fp32, st, s)
+                       ? launch_w4_linear_tiles(*w, x, x_stride, T, y, y_stride, y_fp32,
+                                                static_cast<float*>(ws), st, s)
                        : launch_w4_linear_rows(*w, x, x_stride, T, y, y_stride, y_fp32, st, s));
 }
 

@@ -159,8 +159,9 @@ cudaError_t launch_w4_linear_rows(const moe_w4& w, const moe_bf16* x, int64_t x_
 cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, moe_bf16* y,
                                    int* status, cudaStream_t s);
 // w4_tiles.cu: rows in the padded layout (offsets, xp of launch_permute)
+int w4_linear_splits(int64_t T, int K, int N);     // part: that many [T, N], where more than one
 cudaError_t launch_w4_linear_tiles(const moe_w4& w, const moe_bf16* x, int64_t x_stride, int64_t T,
-                                   void* y, int64_t y_stride, int y_fp32, int* status,
+                                   void* y, int64_t y_stride, int y_fp32, float* part, int* status,
                                    cudaStream_t s);
 cudaError_t launch_w4_experts_tiles(const W4Experts& q, const moe_bf16* xp, const int64_t* offsets,
                                     int64_t R_cap, moe_bf16* A, float* yp, int* status,

@@ -61,6 +61,8 @@ struct TileArgs {
   void* out;
   int64_t out_stride;
   int out_fp32;
+  int splits;                  // Linear: K in so many runs of stages, partial sums in fp32 to
+  float* part;                 // part [splits][T][N] where there are several
   int* status;
 };
 
@@ -171,6 +173,8 @@ struct Bool {
 
 struct Tile {
   int e, n0, rows;
+  int kb0, kb1;               // its steps of 64 k
+  int sp;
   int64_t m0;
   // boxes of 32 rows, and steps of 64 k that fit a stage of x
   __device__ __forceinline__ int boxes() const { return (rows + 31) / 32; }
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int r1 = a.offsets ? (int)a.offsets[e + 1] : (int)a.T;
     rstart[e] = r0;
     if (e == a.E - 1) rstart[a.E] = r1;
-    tstart[e + 1] = (r1 - r0 + kTileRows - 1) / kTileRows * nN;
+    tstart[e + 1] = (r1 - r0 + kTileRows - 1) / kTileRows * nN * a.splits;
   }
   __syncthreads();
   if (warp == 3) {
@@ -279,7 +283,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     t.e = lo;
     const int L = rstart[lo + 1] - rstart[lo], chunks = (L + kTileRows - 1) / kTileRows;
     const int size = ((L + 15) / 16 + chunks - 1) / chunks * 16;
-    const int at = i - tstart[lo], c = at % chunks;
+    int at = i - tstart[lo];
+    t.sp = 0;
+    t.kb0 = 0;
+    t.kb1 = kbs;
+    if (M == TileMode::Linear && a.splits > 1) {
+      // whole stages of kCSteps, as even as they go
+      const int all = (kbs + kCSteps - 1) / kCSteps;
+      t.sp = at % a.splits;
+      at /= a.splits;
+      t.kb0 = all * t.sp / a.splits * kCSteps;
+      t.kb1 = min(kbs, all * (t.sp + 1) / a.splits * kCSteps);
+    }
+    const int c = at % chunks;
     t.n0 = (at / chunks * 2 + rank) * kWide;
     t.rows = min(size, L - c * size);       // (chunks of up to sixteen sixteens: none is empty)
     t.m0 = rstart[lo] + (int64_t)c * size;
@@ -297,13 +313,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const Tile t = tile_at(i);
       const int boxes = uniform(t.boxes()), per = uniform(t.per_stage());
       const int m0 = uniform((int)t.m0);
-      for (int ks = 0; ks < kbs; ks += per) {
+      for (int ks = t.kb0; ks < t.kb1; ks += per) {
         if (!wait_all(x_empty(s), ph ^ 1u, s_abort, a.status)) {
           ok = false;
           break;
         }
         const uint32_t full = full0 + 8u * s, dst = x0 + s * kXBytes;
-        const int n = boxes * min(per, kbs - ks);
+        const int n = boxes * min(per, t.kb1 - ks);
         if (leader) {
           mbar_arrive_expect_tx(full, n * 4096);
           // every other box is this block's to load
@@ -352,15 +368,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         c0[m] = uniform(nb & 7);
         cw[m] = uniform(min(8, nbs - (nb & ~7)));
         cb[m] = uniform(max(0, min(4, nbs - nb)));
-        csrc[m] = a.codes[mat] + ec + (int64_t)(nb & ~7) * kbs * kW4Tile;
-        ssrc[m] = a.scales[mat] + es + (int64_t)(nb & ~7) * steps * 16 * GPS;
+        csrc[m] = a.codes[mat] + ec + ((int64_t)(nb & ~7) * kbs + t.kb0 * cw[m]) * kW4Tile;
+        ssrc[m] =
+            a.scales[mat] + es + ((int64_t)(nb & ~7) * steps + t.kb0 / 2 * cw[m]) * 16 * GPS;
       }
-      for (int ks = 0; ks < kbs; ks += kCSteps) {
+      for (int ks = t.kb0; ks < t.kb1; ks += kCSteps) {
         if (!wait_all(c_empty(s), ph ^ 1u, s_abort, a.status)) {
           ok = false;
           break;
         }
-        const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
+        const int n = t.kb1 - ks < kCSteps ? t.kb1 - ks : kCSteps;
         const uint32_t cbytes = n * kW4Tile, sbytes = (n + 1) / 2 * 32 * GPS;
         const uint32_t full = full0 + 8u * s;
         if (leader) {
@@ -417,9 +434,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // are fewer, some warps decode what lies there; no product reads it.)
       auto stages = [&](auto P) {
         constexpr bool PLAIN = decltype(P)::value;
-        for (int ks = 0; ks < kbs; ks += kCSteps) {
+        for (int ks = t.kb0; ks < t.kb1; ks += kCSteps) {
           if (!wait_all(c_full(cs), cph, s_abort, a.status)) return false;
-          const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
+          const int n = t.kb1 - ks < kCSteps ? t.kb1 - ks : kCSteps;
           const uint8_t* cp = codes0 + cs * kCBytes + q * n * kW4Tile;
           const uint8_t* sp = scales0 + cs * kSBytes + q * ((n + 1) / 2) * 32 * GPS;
 #pragma unroll
@@ -494,12 +511,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       if (!wait_all(acc_empty + 8 * h, (used >> h & 1u) ^ 1u, s_abort, a.status)) break;
       used ^= 1u << h;
       const uint32_t idesc = idesc_bf16(128, N, 0, 0), d = td + 128 * h;
-      for (int ks = 0; ks < kbs; ks += kCSteps) {
+      for (int ks = t.kb0; ks < t.kb1; ks += kCSteps) {
         if (!wait_all(a_full(s), ph, s_abort, a.status)) {
           ok = false;
           break;
         }
-        const int n = kbs - ks < kCSteps ? kbs - ks : kCSteps;
+        const int n = t.kb1 - ks < kCSteps ? t.kb1 - ks : kCSteps;
         for (int k2 = 0; k2 < n; k2 += per) {
           if (!wait_all(x_full(xs), xph, s_abort, a.status)) {
             ok = false;
@@ -513,7 +530,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 umma_tmem_a(d, at + 8 * kk, ((uint64_t)b_hi << 32) | (b + kk * (32 >> 4)), idesc,
-                            ks + k2 + j > 0 || kk > 0);
+                            ks + k2 + j > t.kb0 || kk > 0);
             }
             umma_commit_both(bars_u + 8u * (kXStages + xs));             // x_empty
           }
@@ -556,7 +573,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t v[16];
         tmem_ld16(at + 128 * h + c0, v);
         tmem_ld_wait();
-        const int64_t first_at = (t.m0 + c0) * a.out_stride + n;
+        const int64_t stride = M == TileMode::Linear && a.splits > 1 ? a.N : a.out_stride;
+        const int64_t first_at = (t.m0 + c0) * stride + n;
         const int here = n < a.N ? t.rows - c0 : 0;          // rows of these sixteen
         if (M == TileMode::GateUp) {
           // of two rows the lower lanes, which hold gates, take the first, the upper ones,
@@ -574,9 +592,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const float f = __uint_as_float(v[c]) * unit;
-            const int64_t o = first_at + c * a.out_stride;
+            const int64_t o = first_at + c * stride;
             if (c < here) {
-              if (M == TileMode::Down || a.out_fp32)
+              if (M == TileMode::Linear && a.splits > 1)
+                a.part[t.sp * a.T * a.N + o] = f;
+              else if (M == TileMode::Down || a.out_fp32)
                 static_cast<float*>(a.out)[o] = f;
               else
                 static_cast<moe_bf16*>(a.out)[o] = __bfloat16_as_ushort(__float2bfloat16_rn(f));
@@ -669,8 +689,45 @@ static cudaError_t tiles(const TileArgs& a, const moe_w4& w, const moe_bf16* x, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// y = the splits' partial sums in order
+__global__ void __launch_bounds__(256) w4_join_kernel(const float* __restrict__ part, int splits,
+                                                      int64_t T, int N, void* __restrict__ y,
+                                                      int64_t stride, int fp32) {
+  pdl_enter();
+  const int64_t n4 = T * N / 4;               // N is a multiple of 8
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n4) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int j = 0; j < splits; ++j) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(part) + j * n4 + i);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+  }
+  const int64_t t = 4 * i / N, n = 4 * i - t * N;
+  if (fp32) {
+    float* o = static_cast<float*>(y) + t * stride + n;
+    o[0] = s.x; o[1] = s.y; o[2] = s.z; o[3] = s.w;
+  } else {
+    const uint32_t a = pack_bf16(s.x, s.y), b = pack_bf16(s.z, s.w);
+    moe_bf16* o = static_cast<moe_bf16*>(y) + t * stride + n;
+    o[0] = (moe_bf16)a; o[1] = (moe_bf16)(a >> 16); o[2] = (moe_bf16)b; o[3] = (moe_bf16)(b >> 16);
+  }
+}
+
+// Runs of K: as many as fill the device once, of at least two stages each (4096 x 2880, 40
+// rows: 12 pairs of tiles for 76 clusters, 14.5 us in one run, 11.2 in six; 8192 x 8192, 256
+// rows: 32 pairs, 44 us and 30 in two).
+int w4_linear_splits(int64_t T, int K, int N) {
+  const int64_t pairs = (int64_t)((N + 255) / 256) * ((T + kTileRows - 1) / kTileRows);
+  const int64_t stages = (w4_kblocks(K) + kCSteps - 1) / kCSteps;
+  int64_t s = num_sms() / 2 / pairs;
+  if (s > stages / 2) s = stages / 2;
+  if (s > 8) s = 8;
+  return s < 2 ? 1 : (int)s;
+}
+
 cudaError_t launch_w4_linear_tiles(const moe_w4& w, const moe_bf16* x, int64_t x_stride, int64_t T,
-                                   void* y, int64_t y_stride, int y_fp32, int* status,
+                                   void* y, int64_t y_stride, int y_fp32, float* part, int* status,
                                    cudaStream_t s) {
   TileArgs a{};
   a.codes[0] = w.codes;
@@ -682,8 +739,16 @@ cudaError_t launch_w4_linear_tiles(const moe_w4& w, const moe_bf16* x, int64_t x
   a.out = y;
   a.out_stride = y_stride;
   a.out_fp32 = y_fp32;
+  a.splits = w4_linear_splits(T, w.K, w.N);
+  a.part = part;
   a.status = status;
-  return tiles<TileMode::Linear>(a, w, x, T, x_stride, pdl_for_tokens(T), s);
+  cudaError_t e = tiles<TileMode::Linear>(a, w, x, T, x_stride, pdl_for_tokens(T), s);
+  if (e == cudaSuccess && a.splits > 1) {
+    e = launch_pdl(pdl_for_tokens(T), w4_join_kernel, dim3((unsigned)((T * w.N / 4 + 255) / 256)),
+                   dim3(256), 0, s, part, a.splits, T, w.N, y, y_stride, y_fp32);
+    note_launches(1);
+  }
+  return e;
 }
 
 cudaError_t launch_w4_experts_tiles(const W4Experts& q, const moe_bf16* xp, const int64_t* offsets,
@@ -702,6 +767,7 @@ cudaError_t launch_w4_experts_tiles(const W4Experts& q, const moe_bf16* xp, cons
   a.act = q.act;
   a.out = A;
   a.out_stride = q.f;
+  a.splits = 1;
   a.status = status;
   cudaError_t e = tiles<TileMode::GateUp>(a, *q.gate, xp, R_cap, q.d, pdl, s);
   a.codes[0] = q.down->codes;

@@ -116,6 +116,46 @@ def test_linear(kind, group, T, K, N):
     assert _status(q.lib) == 0
 
 
+@pytest.mark.parametrize("kind,group", [("int4", 32), ("int4", 128), ("fp4", 64)])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("T,K,N", [(9, 8200, 4808), (40, 4096, 2880), (257, 1288, 1096),
+                                   (300, 1032, 1128), (700, 8, 65536), (1900, 136, 1400)])
+def test_linear_many_rows(kind, group, wide, T, K, N):
+    """Work enough for tensor memory: K in one run and in several, whose sums meet."""
+    from mixture_experts_routed_softmax_gb300.w4 import Linear4
+    rng = np.random.default_rng(T + K + N)
+    codes, scales = _codes(rng, 1, K, N, kind, group, wide)
+    q = _weights4(codes, scales, kind, group)
+    x = torch.tensor(rng.standard_normal((T, K))).to(BF16)
+    x[T // 2, K - 1] = float("nan")
+    clean = torch.nan_to_num(x).double().numpy()
+    Wd = W.weights(codes, scales.double().numpy(), kind, group)[0]
+    for dtype in (BF16, torch.float32):
+        lin = Linear4(q, out_dtype=dtype)
+        ref, bound = W.linear_bound(clean, Wd, dtype is BF16)
+        if wide:                       # code * scale rounded to bf16
+            bound = bound + W.U_BF16 * (np.abs(clean) @ np.abs(Wd))
+        xs = torch.full((T, K + 24), float("nan"), dtype=BF16, device="cuda")
+        xs[:, 8:8 + K] = x.cuda()
+        ys = torch.full((T, N + 5), 7.0, dtype=dtype, device="cuda")
+        b = lin.buffers(T)
+        b.ws.fill_(255)
+        lin.apply(xs[:, 8:8 + K], b, out=ys[:, 2:2 + N])
+        got = ys[:, 2:2 + N]
+        keep = [t for t in range(T) if t != T // 2]
+        W.assert_within("y", _np(got[keep]), ref[keep], bound[keep])
+        assert bool(torch.isnan(got[T // 2]).all())
+        assert bool((ys[:, :2] == 7).all()) and bool((ys[:, 2 + N:] == 7).all())
+        y = lin.apply(x.cuda(), b)
+        assert torch.equal(y[keep], got[keep])           # the same bits
+        short = lin.buffers(T)
+        if short.ws.numel() > 256:
+            short.ws = short.ws[:-256]
+            with pytest.raises(RuntimeError):
+                lin.apply(x.cuda(), short)
+    assert _status(q.lib) == 0
+
+
 def test_linear_any_scales_and_rows():
     """Scales of eight bits; infinities and NaN stay in their rows; no rows at all."""
     from mixture_experts_routed_softmax_gb300.w4 import Linear4
