@@ -45,7 +45,7 @@ constexpr int kCStages = 3;                 // of codes: 256 k
 constexpr int kCSteps = 4;                  // (in 64 k)
 constexpr int kCBytes = 8 * kCSteps * kW4Tile;
 constexpr int kSBytes = 2048;               // and their scales, at most
-constexpr int kDecWarp0 = 4, kDecWarps = 16, kOutWarp0 = 20, kOutWarps = 8;
+constexpr int kDecWarp0 = 4, kDecWarps = 8, kOutWarp0 = 12, kOutWarps = 8;
 constexpr int kTileThreads = 32 * (kOutWarp0 + kOutWarps);
 constexpr int kAccCols = 256;               // accumulators: two halves of 128 columns
 constexpr int kTileSmem = 1024 + kXStages * kXBytes + kCStages * (kCBytes + kSBytes) +
@@ -409,12 +409,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ------------------------------------------------------- codes into bf16 --
     // A stage's stores to tensor memory are waited for when the first values of the next
     // are ready, so that their latency is not the warp's own.
-    const int q = warp & 3, i4 = (warp - kDecWarp0) >> 2, half = i4 & 1, odd = i4 >> 1;
+    const int q = warp & 3, half = (warp - kDecWarp0) >> 2;
     const int g = lane >> 2;
-    const uint32_t dst0 = tmem + ((uint32_t)(32 * q + 16 * half) << 16) + kAccCols + 32 * odd;
-    const uint8_t* codes0 = s_codes + half * (kCBytes / 2) + 16 * lane + odd * kW4Tile;
+    const uint32_t dst0 = tmem + ((uint32_t)(32 * q + 16 * half) << 16) + kAccCols;
+    const uint8_t* codes0 = s_codes + half * (kCBytes / 2) + 16 * lane;
     const uint8_t* scales0 =
-        s_scales + half * (kSBytes / 2) + g * 4 * GPS + odd * (GPS == 4 ? 8 : GPS == 2 ? 4 : 0);
+        s_scales + half * (kSBytes / 2) + g * 4 * GPS;
     const uint32_t full0 = a_full(0), empty0 = a_empty(0);
     const W4Decoder<FP4> decode;
     int s = 0, cs = 0;
@@ -440,15 +440,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           const uint8_t* cp = codes0 + cs * kCBytes + q * n * kW4Tile;
           const uint8_t* sp = scales0 + cs * kSBytes + q * ((n + 1) / 2) * 32 * GPS;
 #pragma unroll
-          for (int sub = 0; sub < 2; ++sub) {
-            const uint4 c = *reinterpret_cast<const uint4*>(cp + sub * 2 * kW4Tile);
+          for (int sub = 0; sub < 4; ++sub) {
+            const uint4 c = *reinterpret_cast<const uint4*>(cp + sub * kW4Tile);
             uint32_t sw[2];                       // of the 64 rows' runs of 32
+            const uint8_t* at = sp + (sub >> 1) * 32 * GPS + (sub & 1) * GPS * 2;
             if (GPS == 4) {
-              const uint2 v = *reinterpret_cast<const uint2*>(sp + sub * 32 * GPS);
+              const uint2 v = *reinterpret_cast<const uint2*>(at);
               sw[0] = v.x;
               sw[1] = v.y;
             } else {
-              sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(sp + sub * 32 * GPS);
+              sw[0] = sw[1] = *reinterpret_cast<const uint32_t*>(GPS == 2 ? at : sp + (sub >> 1) * 32);
             }
             uint32_t r[16];
             const uint32_t word[4] = {c.x, c.y, c.z, c.w};
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
               if (!wait_all(empty0 + 8u * s, ph ^ 1u, s_abort, a.status)) return false;
               tc_fence_after();
             }
-            tmem_st_16x256b_x4(dst0 + 128 * s + 64 * sub, r);
+            tmem_st_16x256b_x4(dst0 + 128 * s + 32 * sub, r);
           }
           before = true;
           s ^= 1;
