@@ -3,28 +3,35 @@
 // products over the padded expert-grouped layout (permute.cu).
 //
 //   D[n, r] += W^T[n, k] x^T[k, r]
-// The weights are the A operand, 128 columns n, 256 k a stage; up to 256 rows of x are the
-// B operand, N = their number rounded up to 16. A lives in tensor memory: sixteen warps take
-// two 512-byte tiles of codes each a stage, turn it into bf16 code * scale in registers
-// (W4Decoder), and store it as the 16x256b shape, whose lanes hold just what a lane's codes are. So
-// the bf16 weights never pass through shared memory, whose bandwidth the products' B operand
-// needs, and the codes are decoded once for 256 rows: that takes 300 cycles of instruction issue
-// a 64 k, the products 2 N. code * scale is rounded to bf16 there; scales of few bits
-// (moe_w4_quantise's) make it exact.
+// Two blocks of a cluster work on 128 columns n each of the same rows of x, by products of both
+// (cta_group::2, M = 256). The weights are the A operand, 256 k a stage; up to 256 rows of x
+// are the B operand, N = their number rounded up to 16, half of them in either block. A
+// lives in tensor memory: eight warps take four 512-byte tiles of codes each a stage, turn them
+// into bf16 code * scale in registers (W4Decoder), and store it as the 16x256b shape, whose
+// lanes hold just what a lane's codes are. So the bf16 weights never pass through shared memory,
+// whose bandwidth the products' B operand needs, and the codes are decoded once for 256
+// rows. code * scale is rounded to bf16 there; scales of few bits (moe_w4_quantise's) make
+// it exact.
+//
+// What bounds it (a stage, cycles): decoding about 1000, most of it on the pipe of the logical
+// operations; the products 8 N, some 500 at least to issue. With few
+// rows decoding and the hand-over of a stage of A between warps and blocks add up: 16 rows of
+// 4096 x 38912 take 26 us, where reading the codes takes 13. With 512 rows 92 us, 92% of the
+// rate of a large bf16 product. Measured on the way there: products of one block each, the
+// rows of x multicast to both: 98 us at 512 rows, 45 at 160 (now 37), the rows came in at 50 bytes a
+// cycle and SM whatever else was left out; sixteen decoding warps of two tiles each: 128 rows 36.6
+// us, eight 35.6.
 //
 // The 128 columns: two runs of 64, of gate and up or of one matrix. Sixteen columns of each
 // make up a warp's 32 lanes of tensor memory, so that gate and up of a column meet by a shuffle.
 //
-// Roles (28 warps): 0 loads rows of x by TMA, 64 k a stage, 128 or 256 where rows are few; 3 streams the codes
-// and scales, contiguous pieces of 64 columns by 256 rows, by bulk copies; 4-19 the sixteen
-// above; 1 issues the products; 20-27 take the finished tile from tensor memory (a thread a
-// column). Tensor memory: 256 columns of accumulators (two tiles of up to 128 rows, so that one
-// is taken out while the next is summed, or one of more), two stages of 128 columns of A. Every wait is
-// bounded.
-//
-// Two blocks of a cluster work on neighbouring columns of the same rows: each loads half of
-// them and hands it to both (TMA multicast). At 144 rows a tile the rows of x came in at a rate that
-// L2 gave out no faster, 50 bytes a cycle and SM; a row loaded once for 256 columns needs half.
+// Roles (20 warps): 0 loads rows of x by TMA, 128 k a stage, 256 where rows are few; 3 streams the
+// codes and scales, contiguous pieces of 64 columns by 256 rows, by bulk copies; 4-11 the eight
+// above; 1 of the first block issues the products; 12-19 take the finished tile from tensor
+// memory (a thread a column). Tensor memory: 256 columns of accumulators (two tiles of up to 128
+// rows, so that one is taken out while the next is summed, or one of more), two stages of 128
+// columns of A. The first block's barriers of x, of A and of emptied accumulators count both
+// blocks' arrivals. Every wait is bounded.
 //
 // An expert's rows are cut into equal chunks of at most 256; tiles of one run of columns
 // follow one another, so that its codes are in L2 for the next chunk.
@@ -38,7 +45,7 @@ namespace moe {
 enum class TileMode { Linear, GateUp, Down };
 
 constexpr int kTileRows = 256;              // rows of x a tile, at most
-constexpr int kXStages = 5;                 // of x: 64 k of 256 rows, 128 of 128, 256 of 64
+constexpr int kXStages = 5;                 // of x: 128 k of 128 rows a block, 256 of 64
 constexpr int kXBytes = kTileRows * 128;
 constexpr int kAStages = 2;                 // of A in tensor memory: 256 k of 128 columns
 constexpr int kCStages = 3;                 // of codes: 256 k
@@ -74,32 +81,31 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]
+// D[tmem] (+)= A[tmem] * B[smem] of both blocks, B's rows half in either
 __device__ __forceinline__ void umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// one box into both blocks of the cluster, counted on the barrier at this offset in each
-__device__ __forceinline__ void tma_load_3d_both(uint32_t dst, const void* map, uint32_t bar,
+// a box into this block, counted on a barrier of either (a shared::cluster address)
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* map, uint32_t bar,
                                                  int c0, int c1, int c2) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "h"((uint16_t)3)
+      ".cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// one arrival at the barrier at this offset in both, when the products so far are done
-__device__ __forceinline__ void umma_commit_both(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
+// An arrival at a barrier of either block (a shared::cluster address) that hands over tensor
+// memory alone: the warp's accesses there are over (tcgen05.wait) and nothing in
+// ordinary memory goes with them, so it needs no release to the cluster, which took 1150 cycles
+// a stage (64 rows of 4096 x 38912 47 us).
+__device__ __forceinline__ void arrive_for_tmem(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -176,9 +182,12 @@ struct Tile {
   int kb0, kb1;               // its steps of 64 k
   int sp;
   int64_t m0;
-  // boxes of 32 rows, and steps of 64 k that fit a stage of x
-  __device__ __forceinline__ int boxes() const { return (rows + 31) / 32; }
-  __device__ __forceinline__ int per_stage() const { return rows <= 64 ? 4 : rows <= 128 ? 2 : 1; }
+  // the products' columns; of the half of them that a block loads: rows, boxes of 32, and
+  // steps of 64 k that fit a stage of x
+  __device__ __forceinline__ int cols() const { return (rows + 15) & ~15; }
+  __device__ __forceinline__ int half() const { return cols() / 2; }
+  __device__ __forceinline__ int boxes() const { return (half() + 31) / 32; }
+  __device__ __forceinline__ int per_stage() const { return boxes() > 2 ? 2 : kCSteps; }
 };
 
 template <TileMode M, bool FP4, int GPS>
@@ -210,10 +219,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXStages; ++s) {
       mbar_init(x_full(s), 1);
-      mbar_init(x_empty(s), 2);            // both blocks' products
+      mbar_init(x_empty(s), 1);
     }
     for (int s = 0; s < kAStages; ++s) {
-      mbar_init(a_full(s), kDecWarps);
+      mbar_init(a_full(s), 2 * kDecWarps);           // of both blocks
       mbar_init(a_empty(s), 1);
     }
     for (int s = 0; s < kCStages; ++s) {
@@ -222,7 +231,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int h = 0; h < 2; ++h) {
       mbar_init(acc_full + 8 * h, 1);
-      mbar_init(acc_empty + 8 * h, kOutWarps);
+      mbar_init(acc_empty + 8 * h, 2 * kOutWarps);
     }
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -230,8 +239,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tma_prefetch_desc(&mapX);
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(s_tmem), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(s_tmem), 512);
+    tmem_relinquish_pair();
   }
   const int nN = (a.N + 2 * kWide - 1) / (2 * kWide);         // pairs of tiles
   const int rank = (int)cluster_ctarank(), first = blockIdx.x >> 1, stride = gridDim.x >> 1;
@@ -305,43 +314,44 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------- rows of x --
     const bool leader = elect_one();
-    const uint32_t x0 = uniform(smem_u32(smem)), full0 = uniform(bar0);
+    const uint32_t x0 = uniform(smem_u32(smem)), full0 = uniform(mapa_shared(bar0, 0));
     int s = 0, fills = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int i = first; i < total && ok; i += stride) {
       const Tile t = tile_at(i);
       const int boxes = uniform(t.boxes()), per = uniform(t.per_stage());
-      const int m0 = uniform((int)t.m0);
+      const int m0 = uniform((int)t.m0 + rank * t.half());
       for (int ks = t.kb0; ks < t.kb1; ks += per) {
         if (!wait_all(x_empty(s), ph ^ 1u, s_abort, a.status)) {
           ok = false;
           break;
         }
-        const uint32_t full = full0 + 8u * s, dst = x0 + s * kXBytes;
-        const int n = boxes * min(per, t.kb1 - ks);
+        const uint32_t full = full0 + 8u * s;
+        uint32_t dst = x0 + s * kXBytes;
+        const int n = min(per, t.kb1 - ks);
         if (leader) {
-          mbar_arrive_expect_tx(full, n * 4096);
-          // every other box is this block's to load
-          int b = rank, k = ks;
-          for (int u = rank; u < n; u += 2) {
-            while (b >= boxes) {
-              b -= boxes;
-              ++k;
-            }
-            tma_load_3d_both(dst + u * 4096, &mapX, full, k * 64, 0, m0 + 32 * b);
-            b += 2;
-          }
+          if (rank == 0) mbar_arrive_expect_tx(x_full(s), 2 * n * boxes * 4096);
+          for (int k = ks; k < ks + n; ++k)
+            for (int b = 0; b < boxes; ++b, dst += 4096)
+              tma_load_3d_pair(dst, &mapX, full, k * 64, 0, m0 + 32 * b);
         }
         ++fills;
         if (++s == kXStages) { s = 0; ph ^= 1u; }
       }
     }
-    // copies already issued land before the block's shared memory goes away
+    // copies already issued land before the block's shared memory goes away; the second
+    // block's are counted in the first, so after a wait that gave up it lets time pass instead
     volatile int never = 0;
-    for (int n = fills < kXStages ? fills : kXStages; n > 0; --n) {
-      if (--s < 0) { s = kXStages - 1; ph ^= 1u; }
-      mbar_wait_bounded(x_full(s), ph, &never, a.status);
+    if (rank == 0) {
+      for (int n = fills < kXStages ? fills : kXStages; n > 0; --n) {
+        if (--s < 0) { s = kXStages - 1; ph ^= 1u; }
+        mbar_wait_bounded(x_full(s), ph, &never, a.status);
+      }
+    } else if (!ok) {
+      const uint64_t t0 = global_ns();
+      while (global_ns() - t0 < 200000ull) {
+      }
     }
   } else if (warp == 3) {
     // ------------------------------------------------------ codes and scales --
@@ -415,7 +425,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint8_t* codes0 = s_codes + half * (kCBytes / 2) + 16 * lane;
     const uint8_t* scales0 =
         s_scales + half * (kSBytes / 2) + g * 4 * GPS;
-    const uint32_t full0 = a_full(0), empty0 = a_empty(0);
+    const uint32_t full0 = mapa_shared(a_full(0), 0), empty0 = a_empty(0);
     const W4Decoder<FP4> decode;
     int s = 0, cs = 0;
     uint32_t ph = 0, cph = 0;
@@ -424,13 +434,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full0 + 8u * (s ^ 1));
+      if (lane == 0) arrive_for_tmem(full0 + 8u * (s ^ 1));
     };
     static_assert(kAStages == 2, "the other stage");
     for (int i = first; i < total && ok; i += stride) {
       const Tile t = tile_at(i);
       const bool plain = plain_of(t.e, half);
-      // All of the tile's stages of 256 rows, two tiles of codes a warp. (Where the last rows
+      // All of the tile's stages of 256 rows, four tiles of codes a warp. (Where the last rows
       // are fewer, some warps decode what lies there; no product reads it.)
       auto stages = [&](auto P) {
         constexpr bool PLAIN = decltype(P)::value;
@@ -488,7 +498,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       ok = plain ? stages(Bool<true>()) : stages(Bool<false>());
     }
     if (before) stored();
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     // -------------------------------------------------------------- products --
     // Addresses and descriptors go through a shuffle once, so that they stay in uniform
     // registers: issued by a lane of a divergent branch, a step's eight products took
@@ -502,7 +512,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bool ok = true;
     for (int i = first; i < total && ok; i += stride) {
       const Tile t = tile_at(i);
-      const int N = uniform((t.rows + 15) & ~15), per = uniform(t.per_stage());
+      const int N = uniform(t.cols()), per = uniform(t.per_stage());
       const uint32_t step_b = uniform(t.boxes() * (4096 >> 4));
       if (N > 128) {                         // both halves, from the first column on
         h = 0;
@@ -511,7 +521,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       if (!wait_all(acc_empty + 8 * h, (used >> h & 1u) ^ 1u, s_abort, a.status)) break;
       used ^= 1u << h;
-      const uint32_t idesc = idesc_bf16(128, N, 0, 0), d = td + 128 * h;
+      const uint32_t idesc = idesc_bf16(256, N, 0, 0), d = td + 128 * h;
       for (int ks = t.kb0; ks < t.kb1; ks += kCSteps) {
         if (!wait_all(a_full(s), ph, s_abort, a.status)) {
           ok = false;
@@ -533,28 +543,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 umma_tmem_a(d, at + 8 * kk, ((uint64_t)b_hi << 32) | (b + kk * (32 >> 4)), idesc,
                             ks + k2 + j > t.kb0 || kk > 0);
             }
-            umma_commit_both(bars_u + 8u * (kXStages + xs));             // x_empty
+            umma_commit_pair(bars_u + 8u * (kXStages + xs), 3);          // x_empty
           }
           if (++xs == kXStages) { xs = 0; xph ^= 1u; }
         }
         if (!ok) break;
-        if (leader) umma_commit(bars_u + 8u * (2 * kXStages + kAStages + s));     // a_empty
+        if (leader) umma_commit_pair(bars_u + 8u * (2 * kXStages + kAStages + s), 3);   // a_empty
         if (++s == kAStages) { s = 0; ph ^= 1u; }
       }
       if (!ok) break;
-      if (leader) umma_commit(acc_full + 8 * h);
+      if (leader) umma_commit_pair(acc_full + 8 * h, 3);
       h = N > 128 ? 0 : h ^ 1;
     }
     // every product has ended before tensor memory is freed
     if (leader) {
-      umma_commit(drain);
+      umma_commit_pair(drain, 3);
       volatile int never = 0;
       mbar_wait_bounded(drain, 0, &never, a.status);
     }
+  } else if (warp == 1) {
+    // the first block's products read and write this one's memory
+    volatile int never = 0;
+    mbar_wait_bounded(drain, 0, &never, a.status);
   } else if (warp >= kOutWarp0) {
     // --------------------------------------------------------------- results --
     const int q = warp & 3, part = (warp - kOutWarp0) >> 2;
     const uint32_t at = tmem + ((uint32_t)(32 * q) << 16);
+    const uint32_t given_back = mapa_shared(acc_empty, 0);
     // this lane's column: of the first run (lanes 0-15) or the second
     const bool second = lane >= 16;
     const int col = 16 * q + (lane & 15) + (M != TileMode::GateUp && second ? 64 : 0);
@@ -608,14 +623,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           half0 = false;
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(acc_empty);
+          if (lane == 0) arrive_for_tmem(given_back);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (half0) mbar_arrive(acc_empty + 8 * h);
-        if (wide) mbar_arrive(acc_empty + 8);
+        if (half0) arrive_for_tmem(given_back + 8 * h);
+        if (wide) arrive_for_tmem(given_back + 8);
       }
       h = wide ? 0 : h ^ 1;
     }
@@ -624,7 +639,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   cluster_sync();                            // no copy or arrival for this block is still to come
   tc_fence_after();
-  if (warp == 2) tmem_dealloc(tmem, 512);
+  if (warp == 2) tmem_dealloc_pair(tmem, 512);
 }
 
 // -------------------------------------------------------------------- host --
@@ -717,7 +732,7 @@ __global__ void __launch_bounds__(256) w4_join_kernel(const float* __restrict__ 
 
 // Runs of K: as many as fill the device once, of at least two stages each (4096 x 2880, 40
 // rows: 12 pairs of tiles for 76 clusters, 14.5 us in one run, 11.2 in six; 8192 x 8192, 256
-// rows: 32 pairs, 44 us and 30 in two).
+// rows: 32 pairs, 44 us and 30 in two; each before the products of two blocks).
 int w4_linear_splits(int64_t T, int K, int N) {
   const int64_t pairs = (int64_t)((N + 255) / 256) * ((T + kTileRows - 1) / kTileRows);
   const int64_t stages = (w4_kblocks(K) + kCSteps - 1) / kCSteps;
