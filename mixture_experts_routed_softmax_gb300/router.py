@@ -47,6 +47,9 @@ class Router:
     renormalise: weights sum to ``scale``; otherwise they are scale * score.
     """
 
+    # the kernels read it at this address: it can be written to, not replaced
+    balance = property(lambda self: self._balance)
+
     def __init__(self, E: int, k: int, score: str = "softmax", n_groups: int = 1,
                  topk_groups: int = 1, group_rank: int = 2, renormalise: bool = True,
                  scale: float = 1.0, balance: Optional[torch.Tensor] = None):
@@ -68,7 +71,7 @@ class Router:
                                     or not balance.is_contiguous()):
             raise ValueError(f"balance: a packed fp32 tensor of {E} values on the device is needed")
         self.E, self.k, self.score, self.scale = int(E), int(k), score, float(scale)
-        self.renormalise, self.balance = bool(renormalise), balance
+        self.renormalise, self._balance = bool(renormalise), balance
         # every expert has a gradient where softmax scores stay as they are
         self.dense = score == "softmax" and not self.renormalise
         self.args = _lib.RouterArgs(None if balance is None else balance.data_ptr(), self.E,

@@ -28,6 +28,10 @@ class Weights4:
     the library's own layout (``codes``, ``scales``: flat arrays to be kept or copied whole).
     """
 
+    # the kernels read them at these addresses: they can be written to, not replaced
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+
     def __init__(self, codes, scales, E: int, K: int, N: int, kind: str, group: int):
         self.lib = _lib.load()
         if kind not in KINDS:
@@ -44,7 +48,7 @@ class Weights4:
         self._dev = codes.get_device()
         _packed("codes", codes, torch.uint8, (nc,), self._dev)
         _packed("scales", scales, BF16, (ns,), self._dev)
-        self.codes, self.scales = codes, scales
+        self._codes, self._scales = codes, scales
         self.E, self.K, self.N, self.kind, self.group = int(E), int(K), int(N), kind, int(group)
         self.args = _lib.W4(_p(codes), _p(scales), self.E, self.K, self.N, self.group,
                             KINDS[kind])

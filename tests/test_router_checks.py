@@ -109,3 +109,9 @@ def test_python_refusals(L):
     r = Router(8, 2)
     with pytest.raises(ValueError):
         r.select(torch.zeros(3, 8), r.buffers(3, device="cpu"))
+
+
+def test_balance_cannot_be_replaced(L):
+    from mixture_experts_routed_softmax_gb300.router import Router
+    with pytest.raises(AttributeError):
+        Router(8, 2).balance = torch.zeros(8)
