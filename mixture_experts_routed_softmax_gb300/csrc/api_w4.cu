@@ -27,14 +27,17 @@ static int check_T(int64_t T) {
 }
 
 // Few rows go through the rows kernel (w4_rows.cu), many through tensor memory
-// (w4_tiles.cu). Measured, rows against tiles: 8192 x 8192, 8 rows 14.5 against 17 us, 16 rows 26
-// against 17; 4096 x 2880, 16 rows 7.6 against 10.5, 32 rows 13.3 against 10.7; 2048 x 2048, 64
-// rows 9.7 against 10.0, 96 rows 13.9 against 10.1. Experts, int4 in groups of 32, by rows an expert on average: 2048 x 768, top-8 of
+// (w4_tiles.cu). The rows kernel takes 32 rows at a time, K over a block's warps; small matrices
+// leave it few blocks. Measured, rows against tiles: 8192 x 8192, 8 rows 14.5 against 16 us, 16
+// rows 26 against 16; 4096 x 2880, 16 rows 7.6 against 10.3, 32 rows 13.3 against 10.3; 2048 x
+// 2048, 64 rows 9.4 against 8.9; 4096 x 512, 32 rows 7.6 against 9.5, 64 rows 14.1 against 10.1;
+// 1024 x 1024, 64 rows 5.6 against 8.0, 128 rows 10.2 against 9.0; 128 x 128, 64 rows 3.2 against
+// 4.8, 128 rows 5.5 against 5.6, 2048 rows 75 against 7.6. Experts, int4 in groups of 32, by rows an expert on average: 2048 x 768, top-8 of
 // 128, 2 rows 90 against 110 us, 4 122 against 127, 8 231 against 139; 2880 x 2880, top-4 of 32, 4
 // rows 130 against 140 us, 8 217 against 157; 2560 x 640, top-10 of 512, 640 pairs 310 against 294,
 // 1280 pairs 439 against 377 (a block of the rows kernel looks through all of them).
 static bool linear_by_tiles(int64_t T, int K, int N) {
-  return T > 8 && (double)T * K * N > 3.4e8;
+  return T > 8 && (T > 96 || T * K > 180000 || (double)T * K * N > 3.4e8);
 }
 static bool experts_by_tiles(int64_t T, int k, int E) {
   return T * k > kRowsMaxPairs || T * k > (int64_t)4 * E;

@@ -156,6 +156,27 @@ def test_linear_many_rows(kind, group, wide, T, K, N):
     assert _status(q.lib) == 0
 
 
+def test_weights_cannot_be_replaced():
+    q = _weights4(*_codes(np.random.default_rng(0), 1, 64, 16, "int4", 32), "int4", 32)
+    for name in ("codes", "scales"):
+        with pytest.raises(AttributeError):
+            setattr(q, name, getattr(q, name).clone())
+
+
+@pytest.mark.parametrize("T,K,N", [(97, 8, 8), (130, 128, 24), (2050, 136, 72), (60, 3200, 16)])
+def test_linear_many_rows_of_small_matrices(T, K, N):
+    from mixture_experts_routed_softmax_gb300.w4 import Linear4
+    rng = np.random.default_rng(T)
+    codes, scales = _codes(rng, 1, K, N, "int4", 64)
+    x = torch.tensor(rng.standard_normal((T, K))).to(BF16)
+    lin = Linear4(_weights4(codes, scales, "int4", 64))
+    b = lin.buffers(T)
+    b.ws.fill_(255)
+    ref, bound = W.linear_bound(x.double().numpy(),
+                                W.weights(codes, scales.double().numpy(), "int4", 64)[0])
+    W.assert_within("y", _np(lin.apply(x.cuda(), b)), ref, bound)
+
+
 def test_linear_any_scales_and_rows():
     """Scales of eight bits; infinities and NaN stay in their rows; no rows at all."""
     from mixture_experts_routed_softmax_gb300.w4 import Linear4
