@@ -11,14 +11,18 @@
 // A group whose a is below 2^-120 becomes zeros (scale 0); one with an infinity
 // or NaN gets scale NaN and stays visible as such.
 //
-// Bound by memory in floor (2 bytes read and 1/2 + 2/group written a weight), by some ten
-// instructions a weight in practice. A block takes 64 columns by 128 rows through shared
-// memory: rows of 128 bytes come in, whole tiles of 512 bytes go out.
+// Bound by memory in floor (2 bytes read and 1/2 + 2/group written a weight). Quantisation: a
+// warp takes 16 columns by 128 rows in registers, a lane two neighbouring columns, so
+// that a word is a load, maxima and conversions work on pairs, and the codes of four rows of both are
+// one word, which goes to the lanes that store it by two shuffles. (32 x 2880 x 2880: 147 us;
+// through shared memory, a weight at a time, 181.) Given codes and the way back: a block takes
+// 64 columns by 128 rows through shared memory, rows on one side, whole tiles of 512 bytes on
+// the other.
 #include "w4.cuh"
 
 namespace moe {
 
-constexpr int kPackN = 64;            // columns of a block: four tiles
+constexpr int kPackN = 64;            // columns of a block: four tiles, a warp each
 constexpr int kPackThreads = 128;
 constexpr int kPackPitch = kPackN + 2;   // bf16 a row: 33 words, so that rows shift banks
 
@@ -61,17 +65,21 @@ __device__ __noinline__ uint32_t nearest_code(float w, float s, bool fp4) {
   return (uint32_t)n | (n && q < 0.f ? 8u : 0u);
 }
 
-// A weight to an int4 code, by r = 1 / scale rounded. w / scale is half a step or at least
+// A weight to an int4 code (the low four bits), by r = 1 / scale rounded. w / scale is half a step or at least
 // 2^-9 away from one (w has eight significant bits, scale five, the quotient is below
 // 7.5), w r is off by 2^-20: rounded to 2^-10 (the first two additions) it is on the right side, or
 // on the half itself, which the third rounds to the even code. The sum's last bits
 // are the code in two's complement.
 __device__ __forceinline__ uint32_t int4_code(float w, float r) {
   const float q = __fadd_rn(__fadd_rn(__fmul_rn(w, r), 12288.0f), -12288.0f);
-  return __float_as_uint(__fadd_rn(q, 12582912.0f)) & 15u;
+  return __float_as_uint(__fadd_rn(q, 12582912.0f));
 }
-// Two weights (w r exact: r is a power of two) to fp4 codes, the first in the low four bits
-__device__ __forceinline__ uint32_t fp4_codes(float w0, float w1, float r0, float r1) {
+// Two neighbouring weights to codes, the first in the low four bits of a byte. (fp4: w r is exact,
+// r is a power of two.)
+template <bool FP4>
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, float r0, float r1) {
+  const float w0 = __uint_as_float(w << 16), w1 = __uint_as_float(w & 0xFFFF0000u);
+  if (!FP4) return (int4_code(w0, r0) & 0xFu) | ((int4_code(w1, r1) << 4) & 0xF0u);
   uint32_t d;
   asm("{\n\t.reg .b8 b;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
@@ -79,6 +87,10 @@ __device__ __forceinline__ uint32_t fp4_codes(float w0, float w1, float r0, floa
       : "=r"(d)
       : "f"(w0 * r0), "f"(w1 * r1));
   return d;
+}
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t a, uint32_t b) {      // NaN stays NaN
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b & 0x7FFF7FFFu));
+  return a;
 }
 // A word of codes side by side (pair i in bits 4i of either half) to the kind's places
 template <bool FP4>
@@ -89,16 +101,105 @@ __device__ __forceinline__ uint32_t w4_arrange(uint32_t x) {
          ((x << 1) & 0x20002000u) | ((x >> 3) & 0x0C000C00u);
 }
 
-// SRC 0: bf16 weights [E, K, N], quantised here; 1: codes [E, K, N] (a byte each) and
-// scales [E, groups, N] of the caller's
-template <int SRC, bool FP4>
-__global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
-    W4View w, const moe_bf16* __restrict__ src, const uint8_t* __restrict__ codes,
-    const moe_bf16* __restrict__ scales) {
+// bf16 weights [E, K, N]
+template <bool FP4>
+__global__ void __launch_bounds__(kPackThreads) w4_quantise_kernel(
+    W4View w, const moe_bf16* __restrict__ src) {
   pdl_enter();
-  __shared__ __align__(16) moe_bf16 tile[128 * kPackPitch];   // weights, or codes
-  __shared__ uint32_t amax[8][kPackN / 2];            // of 16 rows each, two columns a word
-  __shared__ float sc[4][kPackN], rs[4][kPackN];      // the step's groups: scale, its inverse
+  const int lane = threadIdx.x & 31, e = blockIdx.z, step = blockIdx.y;
+  const int nb = blockIdx.x * (kPackN / 16) + threadIdx.x / 32;
+  const int nbs = w4_nblocks(w.N), kbs = w4_kblocks(w.K);
+  if (nb >= nbs) return;
+  // columns n and n + 1 at rows 16j + 4t + q
+  const int p = lane >> 2, t = lane & 3, n = 16 * nb + 2 * p, k0 = 128 * step + 4 * t;
+  const int gps = w4_gps(w.group);
+  const uint32_t* from =
+      reinterpret_cast<const uint32_t*>(src + ((int64_t)e * w.K + k0) * w.N + n);
+  const int left = n < w.N ? w.K - k0 : 0, pitch = w.N / 2;
+  uint32_t v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int k = 16 * (i >> 2) + (i & 3);
+    v[i] = k < left ? __ldcs(from + (int64_t)k * pitch) : 0u;
+  }
+  // magnitudes by 32 rows, then by groups
+  uint32_t m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = max_magnitude(a, v[8 * i + j]);
+    a = max_magnitude(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+    m[i] = max_magnitude(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+  }
+  if (gps < 4) {
+    m[0] = m[1] = max_magnitude(m[0], m[1]);
+    m[2] = m[3] = max_magnitude(m[2], m[3]);
+    if (gps < 2) m[0] = m[1] = m[2] = m[3] = max_magnitude(m[0], m[2]);
+  }
+  // lane t works out the scales of the group that rows 32t lie in
+  const uint32_t a = t == 0 ? m[0] : t == 1 ? m[1] : t == 2 ? m[2] : m[3];
+  const float s0 = group_scale(bf16_lo(a), FP4), s1 = group_scale(bf16_hi(a), FP4);
+  const float r0 = s0 > 0.f ? 1.0f / s0 : 0.f, r1 = s1 > 0.f ? 1.0f / s1 : 0.f;
+  // (scales near the top of bf16's range, which the fast forms do not take)
+  const bool slow = __any_sync(0xFFFFFFFFu, s0 > 1e37f || s1 > 1e37f);
+  if ((t * gps & 3) == 0) {
+    moe_bf16* out = w.scales + (int64_t)e * w4_scales_per_expert(w.K, w.N, w.group) +
+                    w4_scales_at(nb, step, nbs, w4_steps(w.K), gps) +
+                    2 * (((2 * p) & 7) * gps + (t * gps >> 2)) + (p >> 2);
+    const moe_bf16 b0 = __bfloat16_as_ushort(__float2bfloat16_rn(s0));
+    const moe_bf16 b1 = __bfloat16_as_ushort(__float2bfloat16_rn(s1));
+    out[0] = b0;
+    out[2 * gps] = b1;
+    // (or-ed: the order does not matter)
+    if (!plain_scale(b0) || !plain_scale(b1))
+      atomicOr(reinterpret_cast<uint32_t*>(w.scales + w4_flags_at(w.E, w.K, w.N, w.group)) + e, 1u);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(w.codes + (int64_t)e * w4_codes_per_expert(w.K, w.N));
+  float q0 = 0.f, q1 = 0.f;
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    uint32_t word[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int by = (lane & ~3) | (2 * kb + (j >> 1));        // the lane with these rows' scales
+      uint32_t c[4];
+      if (!slow) {
+        if ((j & 1) == 0) {
+          q0 = __shfl_sync(0xFFFFFFFFu, r0, by);
+          q1 = __shfl_sync(0xFFFFFFFFu, r1, by);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) c[q] = two_codes<FP4>(v[16 * kb + 4 * j + q], q0, q1);
+      } else {
+        q0 = __shfl_sync(0xFFFFFFFFu, s0, by);
+        q1 = __shfl_sync(0xFFFFFFFFu, s1, by);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t x = v[16 * kb + 4 * j + q];
+          c[q] = nearest_code(bf16_lo(x), q0, FP4) | (nearest_code(bf16_hi(x), q1, FP4) << 4);
+        }
+      }
+      // bytes of rows 0, 2, 1, 3: both columns of a row; then columns g and g + 8
+      const uint32_t mine = __byte_perm(__byte_perm(c[0], c[2], 0x0040),
+                                        __byte_perm(c[1], c[3], 0x0040), 0x5410);
+      const int g = lane >> 2, at = (g & 1) * 4;
+      const uint32_t lo = __shfl_sync(0xFFFFFFFFu, mine, (g >> 1) * 4 + t) >> at;
+      const uint32_t hi = __shfl_sync(0xFFFFFFFFu, mine, 16 + (g >> 1) * 4 + t) >> at;
+      word[j] = w4_arrange<FP4>((lo & 0x0F0F0F0Fu) | ((hi & 0x0F0F0F0Fu) << 4));
+    }
+    if (2 * step + kb < kbs)
+      dst[w4_tile_at(nb, 2 * step + kb, nbs, kbs) / 16 + lane] =
+          make_uint4(word[0], word[1], word[2], word[3]);
+  }
+}
+
+// The caller's codes [E, K, N] (a byte each) and scales [E, groups, N]
+template <bool FP4>
+__global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
+    W4View w, const uint8_t* __restrict__ codes, const moe_bf16* __restrict__ scales) {
+  pdl_enter();
+  __shared__ __align__(16) uint16_t tile[128 * kPackPitch];
   const int e = blockIdx.z, step = blockIdx.y, n0 = blockIdx.x * kPackN;
   const int tid = threadIdx.x;
   const int gps = w4_gps(w.group), groups = (w.K + w.group - 1) / w.group;
@@ -106,55 +207,16 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
   for (int i = tid; i < 128 * (kPackN / 8); i += kPackThreads) {
     const int r = i / (kPackN / 8), c = (i % (kPackN / 8)) * 8;
     const int k = step * 128 + r;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (k < w.K && n0 + c < w.N) {
-      const int64_t at = ((int64_t)e * w.K + k) * w.N + n0 + c;
-      if (SRC == 0) {
-        v = *reinterpret_cast<const uint4*>(src + at);
-      } else {
-        const uint2 b = *reinterpret_cast<const uint2*>(codes + at);     // a byte to 16 bits
-        v = make_uint4(__byte_perm(b.x, 0, 0x4140), __byte_perm(b.x, 0, 0x4342),
-                       __byte_perm(b.y, 0, 0x4140), __byte_perm(b.y, 0, 0x4342));
-      }
-    }
-    uint32_t* d = reinterpret_cast<uint32_t*>(tile + r * kPackPitch + c);
-    d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+    uint2 b = make_uint2(0u, 0u);
+    if (k < w.K && n0 + c < w.N)
+      b = *reinterpret_cast<const uint2*>(codes + ((int64_t)e * w.K + k) * w.N + n0 + c);
+    uint32_t* d = reinterpret_cast<uint32_t*>(tile + r * kPackPitch + c);      // a byte to 16 bits
+    d[0] = __byte_perm(b.x, 0, 0x4140);
+    d[1] = __byte_perm(b.x, 0, 0x4342);
+    d[2] = __byte_perm(b.y, 0, 0x4140);
+    d[3] = __byte_perm(b.y, 0, 0x4342);
   }
   __syncthreads();
-  bool odd = false;                    // a scale that the fast forms do not take
-  if (SRC == 0) {
-    for (int i = tid; i < 8 * (kPackN / 2); i += kPackThreads) {
-      const int n2 = i % (kPackN / 2), part = i / (kPackN / 2);
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(tile + 16 * part * kPackPitch) + n2;
-      uint32_t a = 0;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        // magnitudes (NaN stays NaN)
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(p[r * (kPackPitch / 2)] & 0x7FFF7FFFu));
-      }
-      amax[part][n2] = a;
-    }
-    __syncthreads();
-    for (int i = tid; i < gps * kPackN; i += kPackThreads) {
-      const int n = i % kPackN, gr = i / kPackN, parts = 8 / gps;
-      uint32_t a = 0;
-      for (int p = 0; p < parts; ++p)
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(amax[gr * parts + p][n / 2]));
-      const float s = group_scale((n & 1) ? bf16_hi(a) : bf16_lo(a), FP4);
-      sc[gr][n] = s;
-      rs[gr][n] = s > 0.f ? 1.0f / s : 0.f;           // (0 codes for scales 0 and NaN)
-      odd |= s > 1e37f;
-    }
-  } else {
-    for (int i = tid; i < gps * kPackN; i += kPackThreads) {
-      const int n = i % kPackN, gr = i / kPackN, g = step * gps + gr;
-      sc[gr][n] = g < groups && n0 + n < w.N
-                      ? __bfloat162float(__ushort_as_bfloat16(
-                            scales[((int64_t)e * groups + g) * w.N + n0 + n]))
-                      : 0.f;
-    }
-  }
-  const bool slow = __syncthreads_or(odd);
   // a warp a tile of 16 columns, its two tiles of 64 rows one after the other
   const int lane = tid & 31, nb = n0 / 16 + tid / 32, g = lane >> 2, t = lane & 3;
   if (nb >= w4_nblocks(w.N)) return;
@@ -164,40 +226,15 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
     uint32_t word[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r0 = 64 * (kb & 1) + 16 * j + 4 * t, gr = (r0 * gps) >> 7;
+      const int r0 = 64 * (kb & 1) + 16 * j + 4 * t;
       uint32_t x = 0;
 #pragma unroll
       for (int hi = 0; hi < 2; ++hi) {                 // column g, column g + 8
-        const int n = c0 + g + 8 * hi;
-        const moe_bf16* p = tile + r0 * kPackPitch + n;
-        uint32_t v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = p[q * kPackPitch];
+        const uint16_t* p = tile + r0 * kPackPitch + c0 + g + 8 * hi;
         // rows 0, 1 are pair hi, rows 2, 3 pair 2 + hi; odd rows in the high half
-        if (SRC == 1) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            x |= (v[q] & 15u) << (4 * hi + 8 * (q >> 1) + 16 * (q & 1));
-        } else if (slow) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            x |= nearest_code(__uint_as_float(v[q] << 16), sc[gr][n], FP4)
-                 << (4 * hi + 8 * (q >> 1) + 16 * (q & 1));
-        } else {
-          const float r = rs[gr][n];
-          if (FP4) {
-            const uint32_t even = fp4_codes(__uint_as_float(v[0] << 16), __uint_as_float(v[2] << 16), r, r);
-            const uint32_t uneven = fp4_codes(__uint_as_float(v[1] << 16), __uint_as_float(v[3] << 16), r, r);
-            // four bits each of rows 0, 2 to bits 0 and 8 of the low half, of 1, 3 of the high
-            const uint32_t b = even | (uneven << 16);
-            x |= ((b & 0x000F000Fu) | ((b & 0x00F000F0u) << 4)) << (4 * hi);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              x |= int4_code(__uint_as_float(v[q] << 16), r)
-                   << (4 * hi + 8 * (q >> 1) + 16 * (q & 1));
-          }
-        }
+        for (int q = 0; q < 4; ++q)
+          x |= (p[q * kPackPitch] & 15u) << (4 * hi + 8 * (q >> 1) + 16 * (q & 1));
       }
       word[j] = w4_arrange<FP4>(x);
     }
@@ -211,8 +248,11 @@ __global__ void __launch_bounds__(kPackThreads) w4_pack_kernel(
   bool plain = true;
   for (int i = lane; i < 16 * gps; i += 32) {
     const int gg = i / (2 * gps), gr = (i / 2) % gps, hi = i & 1;
-    out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(sc[gr][c0 + gg + 8 * hi]));
-    plain = plain && plain_scale(out[i]);
+    const int gk = step * gps + gr, n = n0 + c0 + gg + 8 * hi;
+    const moe_bf16 b =
+        gk < groups && n < w.N ? scales[((int64_t)e * groups + gk) * w.N + n] : (moe_bf16)0;
+    out[i] = b;
+    plain = plain && plain_scale(b);
   }
   // (or-ed: the order does not matter)
   if (!plain)
@@ -276,13 +316,13 @@ cudaError_t launch_w4_pack(const moe_w4& w, const moe_bf16* src, const uint8_t* 
                            const moe_bf16* scales, cudaStream_t s) {
   timer_before(MOE_KERNEL_W4_PACK, s);
   const bool fp4 = w.kind == MOE_W4_FP4;
-  const auto kernel = src ? (fp4 ? w4_pack_kernel<0, true> : w4_pack_kernel<0, false>)
-                          : (fp4 ? w4_pack_kernel<1, true> : w4_pack_kernel<1, false>);
   cudaError_t e = cudaMemsetAsync(w.scales + w4_flags_at(w.E, w.K, w.N, w.group), 0,
                                   (size_t)w.E * 4, s);
   if (e == cudaSuccess)
-    e = launch_pdl(false, kernel, pack_grid(w), dim3(kPackThreads), 0, s, w4_view(w), src, codes,
-                   scales);
+    e = src ? launch_pdl(false, fp4 ? w4_quantise_kernel<true> : w4_quantise_kernel<false>,
+                         pack_grid(w), dim3(kPackThreads), 0, s, w4_view(w), src)
+            : launch_pdl(false, fp4 ? w4_pack_kernel<true> : w4_pack_kernel<false>, pack_grid(w),
+                         dim3(kPackThreads), 0, s, w4_view(w), codes, scales);
   note_launches(1);
   timer_after(MOE_KERNEL_W4_PACK, s);
   return e != cudaSuccess ? e : cudaGetLastError();
