@@ -14,7 +14,7 @@
 // Bound by memory in floor (2 bytes read and 1/2 + 2/group written a weight). Quantisation: a
 // warp takes 16 columns by 128 rows in registers, a lane two neighbouring columns, so
 // that a word is a load, maxima and conversions work on pairs, and the codes of four rows of both are
-// one word, which goes to the lanes that store it by two shuffles. (32 x 2880 x 2880: 147 us;
+// one word, which goes to the lanes that store it by two shuffles. (32 x 2880 x 2880: 129 us;
 // through shared memory, a weight at a time, 181.) Given codes and the way back: a block takes
 // 64 columns by 128 rows through shared memory, rows on one side, whole tiles of 512 bytes on
 // the other.
@@ -74,18 +74,37 @@ __device__ __forceinline__ uint32_t int4_code(float w, float r) {
   const float q = __fadd_rn(__fadd_rn(__fmul_rn(w, r), 12288.0f), -12288.0f);
   return __float_as_uint(__fadd_rn(q, 12582912.0f));
 }
-// Two neighbouring weights to codes, the first in the low four bits of a byte. (fp4: w r is exact,
-// r is a power of two.)
+// Two neighbouring weights of four rows to codes, a byte a row, rows 0, 2, 1, 3, the first weight's
+// in the low four bits. (fp4: w r is exact, r is a power of two.)
 template <bool FP4>
-__device__ __forceinline__ uint32_t two_codes(uint32_t w, float r0, float r1) {
-  const float w0 = __uint_as_float(w << 16), w1 = __uint_as_float(w & 0xFFFF0000u);
-  if (!FP4) return (int4_code(w0, r0) & 0xFu) | ((int4_code(w1, r1) << 4) & 0xF0u);
+__device__ __forceinline__ uint32_t eight_codes(const uint32_t* w, float r0, float r1) {
+  float a[4], b[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    a[q] = __uint_as_float(w[q] << 16);
+    b[q] = __uint_as_float(w[q] & 0xFFFF0000u);
+  }
   uint32_t d;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}\n"
-      : "=r"(d)
-      : "f"(w0 * r0), "f"(w1 * r1));
+  if (FP4) {
+    asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 q, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 r, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\t"
+        "mov.b32 %0, {p, q, r, s};\n\t}\n"
+        : "=r"(d)
+        : "f"(a[0] * r0), "f"(b[0] * r1), "f"(a[1] * r0), "f"(b[1] * r1), "f"(a[2] * r0),
+          "f"(b[2] * r1), "f"(a[3] * r0), "f"(b[3] * r1));
+  } else {
+    // the low bytes together, then their low halves
+    const uint32_t even =
+        __byte_perm(__byte_perm(int4_code(a[0], r0), int4_code(a[2], r0), 0x0040),
+                    __byte_perm(int4_code(a[1], r0), int4_code(a[3], r0), 0x0040), 0x5410);
+    const uint32_t odd =
+        __byte_perm(__byte_perm(int4_code(b[0], r1), int4_code(b[2], r1), 0x0040),
+                    __byte_perm(int4_code(b[1], r1), int4_code(b[3], r1), 0x0040), 0x5410);
+    d = (even & 0x0F0F0F0Fu) | ((odd << 4) & 0xF0F0F0F0u);
+  }
   return d;
 }
 __device__ __forceinline__ uint32_t max_magnitude(uint32_t a, uint32_t b) {      // NaN stays NaN
@@ -117,10 +136,16 @@ __global__ void __launch_bounds__(kPackThreads) w4_quantise_kernel(
       reinterpret_cast<const uint32_t*>(src + ((int64_t)e * w.K + k0) * w.N + n);
   const int left = n < w.N ? w.K - k0 : 0, pitch = w.N / 2;
   uint32_t v[32];
+  if (128 * (step + 1) <= w.K && 16 * (nb + 1) <= w.N) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const int k = 16 * (i >> 2) + (i & 3);
-    v[i] = k < left ? __ldcs(from + (int64_t)k * pitch) : 0u;
+    for (int i = 0; i < 32; ++i)
+      v[i] = __ldcs(from + (int64_t)(16 * (i >> 2) + (i & 3)) * pitch);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int k = 16 * (i >> 2) + (i & 3);
+      v[i] = k < left ? __ldcs(from + (int64_t)k * pitch) : 0u;
+    }
   }
   // magnitudes by 32 rows, then by groups
   uint32_t m[4];
@@ -163,26 +188,24 @@ __global__ void __launch_bounds__(kPackThreads) w4_quantise_kernel(
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int by = (lane & ~3) | (2 * kb + (j >> 1));        // the lane with these rows' scales
-      uint32_t c[4];
+      // columns n and n + 1; columns g and g + 8 after an exchange
+      const uint32_t* x = v + 16 * kb + 4 * j;
+      uint32_t mine;
       if (!slow) {
         if ((j & 1) == 0) {
           q0 = __shfl_sync(0xFFFFFFFFu, r0, by);
           q1 = __shfl_sync(0xFFFFFFFFu, r1, by);
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) c[q] = two_codes<FP4>(v[16 * kb + 4 * j + q], q0, q1);
+        mine = eight_codes<FP4>(x, q0, q1);
       } else {
         q0 = __shfl_sync(0xFFFFFFFFu, s0, by);
         q1 = __shfl_sync(0xFFFFFFFFu, s1, by);
+        mine = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t x = v[16 * kb + 4 * j + q];
-          c[q] = nearest_code(bf16_lo(x), q0, FP4) | (nearest_code(bf16_hi(x), q1, FP4) << 4);
-        }
+        for (int q = 0; q < 4; ++q)
+          mine |= (nearest_code(bf16_lo(x[q]), q0, FP4) | (nearest_code(bf16_hi(x[q]), q1, FP4) << 4))
+                  << (16 * (q & 1) + 8 * (q >> 1));
       }
-      // bytes of rows 0, 2, 1, 3: both columns of a row; then columns g and g + 8
-      const uint32_t mine = __byte_perm(__byte_perm(c[0], c[2], 0x0040),
-                                        __byte_perm(c[1], c[3], 0x0040), 0x5410);
       const int g = lane >> 2, at = (g & 1) * 4;
       const uint32_t lo = __shfl_sync(0xFFFFFFFFu, mine, (g >> 1) * 4 + t) >> at;
       const uint32_t hi = __shfl_sync(0xFFFFFFFFu, mine, 16 + (g >> 1) * 4 + t) >> at;
