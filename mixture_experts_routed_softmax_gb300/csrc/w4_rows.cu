@@ -96,8 +96,16 @@ __device__ __forceinline__ int list_rows(const int32_t* __restrict__ idx, int P,
   return total;
 }
 
+// Blocks an SM that registers are cut for. A linear layer's few blocks want the loads of
+// several steps on their way (one row of 8192 x 8192: 13.8 -> 12.1 us, of 2048 x 2048 3.2 -> 2.5);
+// the experts' many want more of them at a time (the same bound took 16 tokens through
+// 128 experts from 69 to 100 us), as the compiler cuts them.
+constexpr int rows_blocks(RowsMode m, int nt, int rb) {
+  return m == RowsMode::Linear && nt == 1 ? (rb == 2 ? 3 : 1) : 0;
+}
+
 template <RowsMode M, bool FP4, int GPS, int NT, int RB>
-__global__ void __launch_bounds__(kRowThreads) w4_rows_kernel(RowsArgs a) {
+__global__ void __launch_bounds__(kRowThreads, rows_blocks(M, NT, RB)) w4_rows_kernel(RowsArgs a) {
   constexpr int MATS = M == RowsMode::GateUp ? 2 : 1;
   constexpr int R = RB * MATS;                 // 16-column tiles a warp works on
   constexpr int CP = 8 * NT + 2;               // padded columns of the sums in shared memory
@@ -428,7 +436,7 @@ static cudaError_t run_rows_rb(const RowsArgs& a, int units, cudaStream_t s) {
 template <RowsMode M, bool FP4, int GPS>
 static cudaError_t run_rows_nt(const RowsArgs& a, int units, int nt, cudaStream_t s) {
   constexpr int RB = M == RowsMode::GateUp ? 2 : 4;
-  return nt <= 1   ? run_rows_rb<M, FP4, GPS, 1, RB>(a, units, s)
+  return nt <= 1   ? run_rows_rb<M, FP4, GPS, 1, M == RowsMode::Linear ? 2 : RB>(a, units, s)
          : nt <= 2 ? run_rows_rb<M, FP4, GPS, 2, RB>(a, units, s)
                    : run_rows_rb<M, FP4, GPS, 4, RB / 2>(a, units, s);
 }
