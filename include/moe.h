@@ -519,7 +519,8 @@ size_t moe_attn_paged_workspace_size(int Hq, int Hkv, int D);
  *     lower index
  *   w_j = scale * s_j / sum_S s (renormalise), or scale * s_j
  * The choice is that of scores in 64 bits: where fp32 scores lie too near to one
- * another to tell, the token is decided again from doubles. Without a balance, and
+ * another to tell, the token is decided again from doubles (softmax scores are then
+ * exact to 2^-39 of the largest). Without a balance, and
  * with one group or group_rank 1, it goes by the logits themselves.
  * Masked experts: a logit of -inf or NaN has score 0 and is chosen, in index
  * order and with weight 0, only where fewer than k others remain; so is one whose
@@ -644,7 +645,7 @@ size_t moe_w4_linear_workspace_size(const moe_w4* w, int64_t T);
 
 /* moe_expert_fwd_w4 — the whole expert part of the forward (moe_permute, moe_expert_fwd,
  * moe_combine) with 4-bit weights:
- *   A = act(x W_gate[e], x W_up[e]) rounded to bf16,
+ *   A = act(x W_gate[e], x W_up[e]) rounded to bf16 (T * k <= E: to twice its bits),
  *   y[t] = sum_j w[t, j] A W_down[e_j]  + the S shared experts' outputs (weight 1)
  * in fp32 sums in slot order, y rounded once. Weights are exact in the products
  * of few rows; with many rows (the tensor-memory kernel) code * scale is rounded to

@@ -156,8 +156,8 @@ cudaError_t launch_w4_linear_rows(const moe_w4& w, const moe_bf16* x, int64_t x_
                                   void* y, int64_t y_stride, int y_fp32, int* status,
                                   cudaStream_t s);
 // A [T*(k+S), f] and yp [T*(k+S), d] scratch, rows by pair (T*k <= kRowsMaxPairs); y [T, d]
-cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, moe_bf16* y,
-                                   int* status, cudaStream_t s);
+cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, int64_t A_lo, float* yp,
+                                   moe_bf16* y, int* status, cudaStream_t s);
 // w4_tiles.cu: rows in the padded layout (offsets, xp of launch_permute)
 int w4_linear_splits(int64_t T, int K, int N);     // part: that many [T, N], where more than one
 cudaError_t launch_w4_linear_tiles(const moe_w4& w, const moe_bf16* x, int64_t x_stride, int64_t T,

@@ -37,6 +37,7 @@ struct RowsArgs {
   void* out;                  // bf16 A [pairs, N]; fp32 Yp [pairs, N]; y [T, N]
   int64_t out_stride;
   int out_fp32;
+  int64_t lo;                 // 0, or where A's second halves stand behind the first (in elements)
   int* status;
 };
 
@@ -145,6 +146,10 @@ __global__ void __launch_bounds__(kRowThreads, rows_blocks(M, NT, RB)) w4_rows_k
     codes[m] = a.codes[m] + e * w4_codes_per_expert(a.K, a.N) + 16 * lane;
     scales[m] = a.scales[m] + e * w4_scales_per_expert(a.K, a.N, 128 / GPS) + 2 * GPS * g;
   }
+  // Down: a row of A as one or two columns of the product (divided by, not shifted by: the same
+  // with shifts got other registers, and 16 tokens through 128 experts took 87 us instead of 71)
+  const int per = M == RowsMode::Down && a.lo ? 2 : 1;
+  rows *= per;
   for (int64_t r0 = 0; r0 < rows; r0 += 8 * NT) {
     const moe_bf16* xr[NT];
 #pragma unroll
@@ -154,8 +159,9 @@ __global__ void __launch_bounds__(kRowThreads, rows_blocks(M, NT, RB)) w4_rows_k
       if (r < rows) {
         int64_t row = r;
         if (M == RowsMode::GateUp && !shared) row = list[r] / a.k;
-        if (M == RowsMode::Down) row = shared ? shared_base + r : list[r];
+        if (M == RowsMode::Down) row = shared ? shared_base + r / per : list[r / per];
         xr[nt] = a.x + row * a.x_stride;
+        if (M == RowsMode::Down && (r & (per - 1))) xr[nt] += a.lo;
       }
     }
     float acc[R][NT][4];
@@ -245,8 +251,8 @@ __global__ void __launch_bounds__(kRowThreads, rows_blocks(M, NT, RB)) w4_rows_k
       }
     __syncthreads();
     const int here = (int)(rows - r0 < 8 * NT ? rows - r0 : 8 * NT);
-    for (int o = threadIdx.x; o < RB * 16 * here; o += kRowThreads) {
-      const int nl = o % (RB * 16), c = o / (RB * 16);
+    for (int o = threadIdx.x; o < RB * 16 * (here / per); o += kRowThreads) {
+      const int nl = o % (RB * 16), c = o / (RB * 16) * per;
       const int n = nb0 * 16 + nl;
       if (n >= a.N) continue;
       float sum[MATS];
@@ -256,8 +262,13 @@ __global__ void __launch_bounds__(kRowThreads, rows_blocks(M, NT, RB)) w4_rows_k
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w)
           sum[m] += red[((w * R + (nl / 16) * MATS + m) * 16 + nl % 16) * CP + c];
+        if (per == 2) {
+#pragma unroll
+          for (int w = 0; w < kRowWarps; ++w)
+            sum[m] += red[((w * R + (nl / 16) * MATS + m) * 16 + nl % 16) * CP + c + 1];
+        }
       }
-      const int64_t r = r0 + c;
+      const int64_t r = (r0 + c) / per;
       if (M == RowsMode::Linear) {
         const int64_t at = r * a.out_stride + n;
         if (a.out_fp32)
@@ -266,11 +277,19 @@ __global__ void __launch_bounds__(kRowThreads, rows_blocks(M, NT, RB)) w4_rows_k
           static_cast<moe_bf16*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(sum[0]));
       } else {
         const int64_t at = (shared ? shared_base + r : (int64_t)list[r]) * a.N + n;
-        if (M == RowsMode::GateUp)
-          static_cast<moe_bf16*>(a.out)[at] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(gated(sum[0], sum[MATS - 1], a.act)));
-        else
+        if (M == RowsMode::GateUp) {
+          const float v = gated(sum[0], sum[MATS - 1], a.act);
+          const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+          static_cast<moe_bf16*>(a.out)[at] = __bfloat16_as_ushort(hi);
+          // (what is not finite has no rest)
+          if (a.lo) {
+            const float rest = v - __bfloat162float(hi);
+            static_cast<moe_bf16*>(a.out)[at + a.lo] =
+                __bfloat16_as_ushort(__float2bfloat16_rn(rest - rest == 0.f ? rest : 0.f));
+          }
+        } else {
           static_cast<float*>(a.out)[at] = sum[0];
+        }
       }
     }
     __syncthreads();
@@ -330,9 +349,9 @@ __global__ void __launch_bounds__(kRowThreads) w4_token_kernel(RowsArgs a,
       for (int h = 0; h < 8; ++h) {
         const int k = 128 * step + 16 * h + 4 * t;
         xv[i][h] = make_uint2(0u, 0u);
-        // (the other columns of the product's B operand stay zeros)
-        if (id >= 0 && g == 0 && k < a.K)
-          xv[i][h] = *reinterpret_cast<const uint2*>(a.x + slot * a.x_stride + k);
+        // columns 0 and 1 of the product's B operand, the others stay zeros
+        if (id >= 0 && g < 2 && k < a.K)
+          xv[i][h] = *reinterpret_cast<const uint2*>(a.x + slot * a.x_stride + g * a.lo + k);
       }
     }
 #pragma unroll
@@ -349,13 +368,13 @@ __global__ void __launch_bounds__(kRowThreads) w4_token_kernel(RowsArgs a,
         mma16816(part, av, xv[i][2 * h + 1].x, xv[i][2 * h + 1].y);
         if (h % (4 / GPS) == 4 / GPS - 1) {
           const uint32_t s = sw[i][h / (4 / GPS)];
-          acc[0] = fmaf(bf16_lo(s) * f[i], part[0], acc[0]);
-          acc[2] = fmaf(bf16_hi(s) * f[i], part[2], acc[2]);
+          acc[0] = fmaf(bf16_lo(s) * f[i], part[0] + part[1], acc[0]);
+          acc[2] = fmaf(bf16_hi(s) * f[i], part[2] + part[3], acc[2]);
         }
       }
     }
   }
-  if (t == 0) {                              // column 0: this token
+  if (t == 0) {                              // columns 0 and 1: this token
     red[warp][g] = acc[0];
     red[warp][g + 8] = acc[2];
   }
@@ -495,8 +514,8 @@ static cudaError_t launch_w4_combine(const W4Experts& q, const float* yp, moe_bf
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, moe_bf16* y,
-                                   int* status, cudaStream_t s) {
+cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, int64_t A_lo, float* yp,
+                                   moe_bf16* y, int* status, cudaStream_t s) {
   const int64_t P = q.T * q.k;
   RowsArgs a{};
   a.codes[0] = q.gate->codes;
@@ -515,6 +534,7 @@ cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, m
   a.by_pair = P < q.E;
   a.act = q.act;
   a.out = A;
+  a.lo = A_lo;
   a.status = status;
   const int units = (int)(a.by_pair ? P : q.E) + q.S;
   const int nt = tiles_for((double)P / q.E, q.T);
@@ -542,7 +562,8 @@ cudaError_t launch_w4_experts_rows(const W4Experts& q, moe_bf16* A, float* yp, m
     if (e == cudaSuccess)
       e = launch_pdl(true, kernel, dim3(w4_nblocks(q.d)), dim3(kRowThreads), 0, s, a, q.topk_w);
   } else if (e == cudaSuccess) {
-    e = rows<RowsMode::Down>(a, *q.down, units, nt, s);
+    const int per = A_lo ? 2 : 1;
+    e = rows<RowsMode::Down>(a, *q.down, units, tiles_for((double)per * P / q.E, per * q.T), s);
   }
   note_launches(2);
   timer_after(MOE_KERNEL_W4_ROWS, s);

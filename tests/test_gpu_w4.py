@@ -261,6 +261,18 @@ def test_experts(name, wide):
     assert torch.equal(y, first)
 
 
+@pytest.mark.parametrize("name", ["one", "one_k1", "two_shared"])
+def test_experts_of_few_rows_keep_A(name):
+    """T * k <= E: A stands as two bf16 numbers, the second the first's rounding, off by
+    2^-8 of that: 2^-16 in all."""
+    ex, ws, x, idx, w, act, E = _experts_case(name)
+    y = ex.forward(x.cuda(), torch.tensor(idx).cuda(), torch.tensor(w).cuda(),
+                   ex.buffers(x.shape[0]))
+    ref, bound = W.experts(x.double().numpy(), idx, w.astype(np.float64), *ws, E, act,
+                           a_rounded=2.0 ** -16)
+    W.assert_within(name, _np(y), ref, bound)
+
+
 @pytest.mark.parametrize("name", ["eight", "some", "many"])
 def test_experts_odd_choices(name):
     """The same expert twice for a token; ids out of range: reported, their pairs left out."""

@@ -83,9 +83,10 @@ def linear_bound(x, W, out_bf16=True):
     return ref, sums(x.shape[1]) * CUT * (np.abs(x) @ np.abs(W)) + out_bf16 * U_BF16 * np.abs(ref)
 
 
-def experts(x, idx, w, gate, up, down, E, act=None, rounded=0.0):
+def experts(x, idx, w, gate, up, down, E, act=None, rounded=0.0, a_rounded=U_BF16):
     """(y, bound) of the experts' forward; weights [E+S, .., ..] in 64 bits. rounded: how far
-    code * scale may be rounded in the products, relative (2^-8 where scales have many bits)."""
+    code * scale may be rounded in the products, relative (2^-8 where scales have many bits);
+    a_rounded: how far A is."""
     limit, alpha, off = act if act is not None else (np.inf, 1.0, 0.0)
     T, d = x.shape
     S = gate.shape[0] - E
@@ -106,7 +107,7 @@ def experts(x, idx, w, gate, up, down, E, act=None, rounded=0.0):
         A = Gc * sig * (Uc + off)
         # |h'| <= 1.1 for every alpha; exp and quotient: 2^-20 (1 + |alpha G|)
         eA = (1.1 * np.abs(Uc + off) * eG + np.abs(Gc * sig) * eU + 1.1 * eG * eU
-              + np.abs(A) * (U_BF16 + 2.0 ** -20 * (1 + np.abs(alpha * Gc))))
+              + np.abs(A) * (a_rounded + 2.0 ** -20 * (1 + np.abs(alpha * Gc))))
         Y = A @ down[e]
         absY = (np.abs(A) + eA) @ np.abs(down[e])
         eY = eA @ np.abs(down[e]) + (sums(down.shape[1]) * CUT + rounded) * absY
