@@ -305,7 +305,8 @@ __device__ const float2 kExp2_32[32] = {
 // the lane's own entry; every lane of the warp calls exp_pair together
 __device__ __forceinline__ float2 exp_table(int lane) { return kExp2_32[lane]; }
 
-// exp(l - m) for finite l <= m, to 2^-42 of itself, as hi + lo: 2^(k / 32) from the table times
+// exp(l - m) for finite l <= m, to 2^-42 of itself, as hi + lo (a table-driven exponential as in
+// Tang, ACM TOMS 1989, with Cody and Waite's reduction): 2^(k / 32) from the table times
 // 1 + r + r^2 / 2 + .. r^5 / 120 (the rest below 2^-48), r = l - m - k log(2) / 32, |r| <=
 // log(2) / 64. log(2) / 32 is three numbers, k times the first of 12 bits is exact; sums and
 // products keep their roundings' errors (Knuth's two-sum, Dekker's pairs) down to the
