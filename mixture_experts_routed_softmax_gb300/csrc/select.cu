@@ -64,6 +64,18 @@ __device__ __forceinline__ float border_err(float score, float v) {
   return 2.f * score + 2.3841858e-7f * fabsf(v) + 1e-37f;
 }
 
+// A group's rank is a sum of two values, each rounded on its own, whose signs may differ: what it is
+// off by goes by what it is a sum of, not by itself.
+__device__ __forceinline__ float rank_size(const SelArgs& a, float c0, float c1) {
+  return a.group_rank == 2 && c1 > -INFINITY ? fabsf(c0) + fabsf(c1) : 0.f;
+}
+// How far apart two groups' ranks near v have to be: both carry the error of two scores, and half
+// a step each of either value and of their sum, 2 2^-24 of `size` (the largest rank_size); border_err
+// allows it four.
+__device__ __forceinline__ float rank_err(float score, float v, float size) {
+  return 2.f * border_err(score, fmaxf(fabsf(v), size));
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
@@ -525,10 +537,11 @@ __device__ __forceinline__ uint32_t keep_groups(const SelArgs& a, int lane, cons
       }
     }
     if (!direct) {
-      // ranks of two carry two errors
       const float lv = key_value(low);
       const uint32_t high = warp_max_key(rest);
-      const float hv = key_value(high), err = 2.f * border_err(top, hv);
+      const float size = rank_size(a, key_value(b0), key_value(b1));
+      const float hv = key_value(high),
+                  err = rank_err(top, hv, __uint_as_float(warp_max_key(__float_as_uint(size))));
       if (high != 0u && hv > -INFINITY && !(lv - hv > err)) {
         const float v = key_value(rank);
         const bool sure = real && v - hv > err, out = !real || lv - v > err;
@@ -543,6 +556,7 @@ __device__ __forceinline__ uint32_t keep_groups(const SelArgs& a, int lane, cons
   for (int i = 0; i < NV; ++i)
     if (lane * NV + i < a.E) crow[lane * NV + i] = key[i];
   __syncwarp();
+  float size = 0.f;
   for (int g = lane; g < a.n_groups; g += 32) {
     uint32_t b0 = none, b1 = none;
     for (int i = 0; i < gs; ++i) {
@@ -551,6 +565,7 @@ __device__ __forceinline__ uint32_t keep_groups(const SelArgs& a, int lane, cons
       b0 = max(b0, c);
     }
     rank[g] = rank_of(b0, b1);
+    size = fmaxf(size, rank_size(a, key_value(b0), key_value(b1)));
   }
   __syncwarp();
   uint32_t lo = ~0u, hi = 0u, kept = 0u;   // bit i: group lane + 32 i (up to 1024 groups)
@@ -570,7 +585,8 @@ __device__ __forceinline__ uint32_t keep_groups(const SelArgs& a, int lane, cons
   const float lv = key_value(__reduce_min_sync(0xFFFFFFFFu, lo));
   hi = __reduce_max_sync(0xFFFFFFFFu, hi);
   const float hv = key_value(hi);
-  *open = !direct && hi != 0u && hv > -INFINITY && !(lv - hv > 2.f * border_err(top, hv));
+  size = __uint_as_float(warp_max_key(__float_as_uint(size)));
+  *open = !direct && hi != 0u && hv > -INFINITY && !(lv - hv > rank_err(top, hv, size));
   __syncwarp();
   uint32_t bits = 0;
 #pragma unroll

@@ -379,3 +379,76 @@ def test_softmax_router_equals_the_layers_own():
         scored.decode_fwd(x[:1], scored.decode_buffers(1))
     with pytest.raises(ValueError):
         plain.route_bwd(plain.buffers(200), accumulate=True)
+
+
+# Experts of which two a group count, the balances +a and -a on them: a rank is the difference of
+# two rounded values, all of whose bits it may lose.
+CANCEL = {
+    # name: (E, n_groups, topk_groups, k, score, logits around, their spread, sizes of a); k =
+    # 2 topk_groups and no two a alike: nothing near another value but the groups' border
+    "pairs": (8, 4, 2, 4, "sigmoid", -14.0, 0.03, (0.1,)),
+    "whole_lanes": (256, 8, 3, 6, "sigmoid", -13.0, 0.03, (0.1, 0.5, 1.0)),
+    "odd_groups": (96, 16, 5, 10, "sigmoid", -12.0, 0.02, (0.75, 1.0, 4.0)),
+    "softmax_lanes": (256, 8, 3, 6, "softmax", 0.0, 1e-4, (1.0, 4.0)),
+    "softmax_odd": (60, 20, 7, 14, "softmax", 0.0, 2e-5, (1.0, 3.0)),
+    "widest": (1024, 64, 9, 18, "sigmoid", -12.0, 0.02, (0.5, 1.0)),
+}
+
+
+def _cancelling(name, masks, T=200):
+    """Logits, balance and choice arguments; tokens that 64 bits themselves leave open (a
+    border within 1e-14, or 2^-36 of the largest softmax score) are left out."""
+    E, n, tg, k, score, mid, spread, sizes = CANCEL[name]
+    rng = np.random.default_rng(sorted(CANCEL).index(name) + 90)
+    gs = E // n
+    l = (mid + 0.5 * rng.standard_normal((T, 1)) + spread * rng.standard_normal((T, E))).astype(
+        np.float32)
+    bal = np.full((n, gs), -8.0, dtype=np.float32)
+    a = rng.choice(sizes, n) * (1 + np.arange(n) / 256)
+    bal[:, 0], bal[:, 1] = a, -a
+    at = rng.permuted(np.tile(np.arange(gs), (n, 1)), axis=1)
+    bal = np.take_along_axis(bal, at, 1).reshape(E)
+    if masks:
+        rest = np.tile(bal == -8.0, (T, 1))
+        l[rest & (rng.random((T, E)) < 0.5)] = -np.inf
+        l[rest & (rng.random((T, E)) < 0.1)] = np.nan
+        l[np.arange(0, T, 3), :gs] = -np.inf               # a group without anyone
+    kw = dict(score=score, n_groups=n, topk_groups=tg)
+    keep = []
+    for t in range(T):
+        s, live = R.scores(l[t], score)
+        c = np.where(live, s + bal.astype(np.float64), -np.inf).reshape(n, gs)
+        best = np.sort(c, 1)[:, ::-1][:, :2]
+        rank = np.sort(np.where(np.isinf(best[:, 1]), best[:, 0], best.sum(1)))[::-1]
+        if rank[tg - 1] - rank[tg] > max(1e-14, 2.0 ** -36 * s.max() * (score == "softmax")):
+            keep.append(t)
+    return l[keep], bal, k, kw
+
+
+@pytest.mark.parametrize("masks", [False, True])
+@pytest.mark.parametrize("name", sorted(CANCEL))
+def test_ranks_that_nearly_cancel(name, masks):
+    l, bal, k, kw = _cancelling(name, masks)
+    T, E = l.shape
+    assert T > 100
+    r = _router(E, k, kw, bal)
+    b = r.buffers(T)
+    r.select(torch.tensor(l).cuda(), b)
+    got = b.topk_idx.cpu().numpy()
+    for t in range(T):
+        want = R.choose(l[t], k, balance=bal, **kw)
+        np.testing.assert_array_equal(got[t], want, err_msg=f"token {t}")
+
+
+@pytest.mark.parametrize("l,bal,groups,topk,kept", [
+    ([-15.048437, -15.0238905, -14.990487, -14.968859, -14.963728, -14.998065, -14.982132,
+      -14.98184], [0.1, -0.1] * 4, 4, 2, [1, 2]),
+    ([-12.010436, -11.995859, -11.998528, -12.006201], [1.0, -1.0, 0.75, -0.75], 2, 1, [1])])
+def test_ranks_that_nearly_cancel_by_hand(l, bal, groups, topk, kept):
+    l, bal = np.array([l], dtype=np.float32), np.array(bal, dtype=np.float32)
+    k = 2 * topk
+    r = _router(l.shape[1], k, dict(score="sigmoid", n_groups=groups, topk_groups=topk), bal)
+    b = r.buffers(1)
+    r.select(torch.tensor(l).cuda(), b)
+    assert sorted(set(b.topk_idx.cpu()[0].tolist())) == sorted(
+        e for g in kept for e in (2 * g, 2 * g + 1))
