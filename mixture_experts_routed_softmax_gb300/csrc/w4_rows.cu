@@ -312,9 +312,11 @@ __global__ void __launch_bounds__(kRowThreads) w4_token_kernel(RowsArgs a,
   if (threadIdx.x < slots) {
     const int j = threadIdx.x;
     const int id = j < a.k ? a.idx[j] : a.E + j - a.k;
-    // (an id out of range is reported by the gate/up products)
-    expert[j] = j < a.k && (id < 0 || id >= a.E) ? -1 : id;
-    weight[j] = j < a.k ? w[j] : 1.f;
+    // (an id out of range is reported by the gate/up products; its weight, which may be
+    // anything, does not meet the sum)
+    const bool out = j < a.k && (id < 0 || id >= a.E);
+    expert[j] = out ? -1 : id;
+    weight[j] = out ? 0.f : j < a.k ? w[j] : 1.f;
   }
   __syncthreads();
   const W4Decoder<FP4> decode;

@@ -363,3 +363,21 @@ def test_layer(T, scored):
     forced = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda")
     q.forward(x, b, forced_idx=forced)
     assert torch.equal(b.topk_idx, forced)
+
+
+@pytest.mark.parametrize("name", ["one", "one_k1", "two_shared", "eight", "some", "many"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
+def test_experts_out_of_range_whatever_the_weight(name, value):
+    """A pair whose expert is out of range is left out, its weight with it: first and last slots,
+    one token and several."""
+    ex, ws, x, idx, w, act, E = _experts_case(name)
+    T, k = idx.shape
+    bad, wb = idx.copy(), w.copy()
+    for t, j, e in ((0, 0, -1), (T - 1, k - 1, E), (T // 2, k // 2, 2 ** 31 - 1)):
+        bad[t, j], wb[t, j] = e, value
+    y = ex.forward(x.cuda(), torch.tensor(bad).cuda(), torch.tensor(wb).cuda(), ex.buffers(T))
+    assert ex.status() == 5
+    gone = (bad < 0) | (bad >= E)
+    ref, bound = W.experts(x.double().numpy(), np.where(gone, 10 ** 6, bad),
+                           np.where(gone, 0.0, w.astype(np.float64)), *ws, E, act)
+    W.assert_within(name, _np(y), ref, bound)
