@@ -6,7 +6,8 @@
 // Bound by reading the codes (half a byte a weight). Each weight is read once and
 // used for 8 NT rows: the codes are the A operand of m16n8k16 products, 16 columns n
 // by 16 k straight from 16-byte loads without shared memory (w4.cuh), the rows of x are
-// the B operand, eight rows a product. The values go in exactly; a group's partial
+// the B operand, eight rows a product. The values go in exactly (int4's as 2^-13 of them, given
+// back at the end: a scale times 2^13 would leave fp32's range from 2^115 on); a group's partial
 // sum is multiplied by its scale in fp32, so any scale is exact too.
 //
 // A block of eight warps takes RB blocks of 16 columns (of one matrix, or of gate
@@ -100,9 +101,12 @@ __device__ __forceinline__ int list_rows(const int32_t* __restrict__ idx, int P,
 // Blocks an SM that registers are cut for. A linear layer's few blocks want the loads of
 // several steps on their way (one row of 8192 x 8192: 13.8 -> 12.1 us, of 2048 x 2048 3.2 -> 2.5);
 // the experts' many want more of them at a time (the same bound took 16 tokens through
-// 128 experts from 69 to 100 us), as the compiler cuts them.
+// 128 experts from 69 to 100 us), as the compiler cuts them, but two blocks of gate and up at
+// least (one: 16 tokens 78 -> 96 us, 64 tokens 116 -> 144).
 constexpr int rows_blocks(RowsMode m, int nt, int rb) {
-  return m == RowsMode::Linear && nt == 1 ? (rb == 2 ? 3 : 1) : 0;
+  return m == RowsMode::Linear && nt == 1   ? (rb == 2 ? 3 : 1)
+         : m == RowsMode::GateUp && nt == 1 && rb == 2 ? 2
+                                                       : 0;
 }
 
 template <RowsMode M, bool FP4, int GPS, int NT, int RB>
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(kRowThreads, rows_blocks(M, NT, RB)) w4_rows_k
             mma16816(part[nt], av, xv[nt][2 * h + 1].x, xv[nt][2 * h + 1].y);
           if (h % (4 / GPS) == 4 / GPS - 1) {
             const uint32_t s = sw[r][h / (4 / GPS)];
-            const float lo = bf16_lo(s) * decode.kUnit, hi = bf16_hi(s) * decode.kUnit;
+            const float lo = bf16_lo(s), hi = bf16_hi(s);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               acc[r][nt][0] = fmaf(lo, part[nt][0], acc[r][nt][0]);
@@ -267,6 +271,7 @@ __global__ void __launch_bounds__(kRowThreads, rows_blocks(M, NT, RB)) w4_rows_k
           for (int w = 0; w < kRowWarps; ++w)
             sum[m] += red[((w * R + (nl / 16) * MATS + m) * 16 + nl % 16) * CP + c + 1];
         }
+        sum[m] *= decode.kUnit;
       }
       const int64_t r = (r0 + c) / per;
       if (M == RowsMode::Linear) {
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kRowThreads) w4_token_kernel(RowsArgs a,
     for (int i = 0; i < U; ++i) {
       const int slot = min((u0 + i) / steps, slots - 1), step = (u0 + i) - slot * steps;
       const int id = step < steps ? expert[slot] : -1;
-      f[i] = decode.kUnit * weight[slot];
+      f[i] = weight[slot];
       const uint32_t zero = FP4 ? 0u : 0x88888888u;
       cw[i][0] = cw[i][1] = make_uint4(zero, zero, zero, zero);
 #pragma unroll
@@ -370,8 +375,8 @@ __global__ void __launch_bounds__(kRowThreads) w4_token_kernel(RowsArgs a,
         mma16816(part, av, xv[i][2 * h + 1].x, xv[i][2 * h + 1].y);
         if (h % (4 / GPS) == 4 / GPS - 1) {
           const uint32_t s = sw[i][h / (4 / GPS)];
-          acc[0] = fmaf(bf16_lo(s) * f[i], part[0] + part[1], acc[0]);
-          acc[2] = fmaf(bf16_hi(s) * f[i], part[2] + part[3], acc[2]);
+          acc[0] = fmaf(f[i], bf16_lo(s) * (part[0] + part[1]), acc[0]);
+          acc[2] = fmaf(f[i], bf16_hi(s) * (part[2] + part[3]), acc[2]);
         }
       }
     }
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(kRowThreads) w4_token_kernel(RowsArgs a,
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kRowWarps; ++i) sum += red[i][threadIdx.x];
-    static_cast<moe_bf16*>(a.out)[n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
+    static_cast<moe_bf16*>(a.out)[n] = __bfloat16_as_ushort(__float2bfloat16_rn(sum * decode.kUnit));
   }
 }
 

@@ -381,3 +381,67 @@ def test_experts_out_of_range_whatever_the_weight(name, value):
     ref, bound = W.experts(x.double().numpy(), np.where(gone, 10 ** 6, bad),
                            np.where(gone, 0.0, w.astype(np.float64)), *ws, E, act)
     W.assert_within(name, _np(y), ref, bound)
+
+
+# ------------------------------------------------------- scales of any size --
+@pytest.mark.parametrize("kind,group", [("int4", 32), ("int4", 128), ("fp4", 64)])
+@pytest.mark.parametrize("T,K,N", [(1, 520, 72), (5, 1032, 136), (12, 264, 520), (60, 520, 264),
+                                   (300, 1032, 264)])
+@pytest.mark.parametrize("power", [120, 9, -101, -110])
+def test_linear_scales_of_any_size(kind, group, T, K, N, power):
+    """Scales by 2^power: what fp32 holds comes out, however large or small the scales are. x goes
+    the other way, so that nothing leaves fp32's range."""
+    from mixture_experts_routed_softmax_gb300.w4 import Linear4
+    rng = np.random.default_rng(T + K + N)
+    codes, scales = _codes(rng, 1, K, N, kind, group)
+    scales = (scales.double() * 2.0 ** power).to(BF16)
+    # every third column's stay as they are: both kinds in one matrix
+    scales[..., ::3] = (scales[..., ::3].double() * 2.0 ** -power).to(BF16)
+    x = torch.tensor(rng.standard_normal((T, K)) * 2.0 ** (-power // 4)).to(BF16)
+    Wd = W.weights(codes, scales.double().numpy(), kind, group)[0]
+    q = _weights4(codes, scales, kind, group)
+    np.testing.assert_array_equal(_np(q.dequantise())[0], Wd)
+    for dtype in (BF16, torch.float32):
+        lin = Linear4(q, out_dtype=dtype)
+        b = lin.buffers(T)
+        b.ws.fill_(255)
+        y = _np(lin.apply(x.cuda(), b))
+        ref, bound = W.linear_bound(x.double().numpy(), Wd, dtype is BF16)
+        unit = np.where(np.arange(N) % 3 == 0, 1.0, 2.0 ** -power) * 2.0 ** (power // 4)
+        W.assert_within("y", y * unit, ref * unit, bound * unit)
+
+
+@pytest.mark.parametrize("name", ["one", "one_k1", "two_shared", "eight", "few_experts", "many",
+                                  "very_many", "skewed"])
+@pytest.mark.parametrize("which,power", [("gate", 12), ("gate", -104), ("up", 12), ("up", 100),
+                                         ("up", -104), ("down", 120), ("down", -104)])
+def test_experts_scales_of_any_size(name, which, power):
+    """One of the three matrices by 2^power, every other expert of it."""
+    from mixture_experts_routed_softmax_gb300.w4 import Experts4
+    T, d, f, E, k, S, kind, group, act = CASES[name]
+    rng = np.random.default_rng(sorted(CASES).index(name) + 80)
+    ws, qs = [], []
+    for m, (K, N) in (("gate", (d, f)), ("up", (d, f)), ("down", (f, d))):
+        codes, scales = _codes(rng, E + S, K, N, kind, group)
+        if m == which:
+            scales[::2] = (scales[::2].double() * 2.0 ** power).to(BF16)
+        qs.append(_weights4(codes, scales, kind, group))
+        ws.append(W.weights(codes, scales.double().numpy(), kind, group))
+    # a token's experts alike, so that none hides behind the others
+    first = rng.integers(0, 2, (T, 1))
+    rank = np.argsort(rng.standard_normal((T, E)) + 100.0 * (np.arange(E) % 2 == first), axis=1)
+    idx = rank[:, ::-1][:, :k].astype(np.int32)
+    idx = np.where(idx % 2 == first, idx, first % E).astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32)
+    x = torch.tensor(rng.standard_normal((T, d))).to(BF16)
+    ex = Experts4(*qs, k=k, E=E, act=act)
+    b = ex.buffers(T)
+    b.ws.fill_(255)
+    y = _np(ex.forward(x.cuda(), torch.tensor(idx).cuda(), torch.tensor(w).cuda(), b))
+    assert ex.status() == 0
+    ref, bound = W.experts(x.double().numpy(), idx, w.astype(np.float64), *ws, E, act)
+    unit = np.ones((T, 1))
+    if which == "down" or (which == "up" and act is None) or (which == "gate" and power < 0):
+        unit = np.where(first == 0, 2.0 ** -power, 1.0) if not S else unit
+    W.assert_within(name, y * unit, ref * unit, bound * unit)
+
