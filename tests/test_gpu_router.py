@@ -452,3 +452,27 @@ def test_ranks_that_nearly_cancel_by_hand(l, bal, groups, topk, kept):
     r.select(torch.tensor(l).cuda(), b)
     assert sorted(set(b.topk_idx.cpu()[0].tolist())) == sorted(
         e for g in kept for e in (2 * g, 2 * g + 1))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,topk,k", [(32, 1, 1, 4), (64, 1, 1, 4), (256, 1, 1, 8), (256, 8, 4, 8),
+                                             (60, 20, 7, 5), (1000, 1, 1, 31), (1024, 1, 1, 32)])
+def test_balance_of_any_size(score, E, groups, topk, k):
+    """A balance of +inf puts experts first, in index order, -inf or NaN last; the largest finite
+    ones leave no scores to tell apart."""
+    rng = np.random.default_rng(E + groups)
+    l = rng.standard_normal((40, E)).astype(np.float32)
+    l[5:9, rng.random(E) < 0.3] = -np.inf
+    kw = dict(score=score, n_groups=groups, topk_groups=topk)
+    big = float(np.finfo(np.float32).max)
+    for n, value in ((k // 2, np.inf), (k, np.inf), (k + 1, np.inf), (E // 2, np.inf), (E, np.inf),
+                     (E // 2, -np.inf), (E // 2, np.nan), (E, -np.inf), (E, np.nan), (k + 3, big),
+                     (E, big), (E, -big)):
+        bal = (0.01 * rng.standard_normal(E)).astype(np.float32)
+        bal[rng.permutation(E)[:n]] = value
+        r = _router(E, k, kw, bal)
+        b = r.buffers(len(l))
+        r.select(torch.tensor(l).cuda(), b)
+        assert r.lib.moe_status(torch.cuda.current_stream().cuda_stream) == 0
+        with np.errstate(over="ignore"):
+            _check_choice(l, k, kw, bal, b.topk_idx.cpu().numpy(), b.topk_w.cpu().numpy())

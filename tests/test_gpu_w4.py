@@ -445,3 +445,26 @@ def test_experts_scales_of_any_size(name, which, power):
         unit = np.where(first == 0, 2.0 ** -power, 1.0) if not S else unit
     W.assert_within(name, y * unit, ref * unit, bound * unit)
 
+
+
+def test_scales_that_are_not_finite():
+    """An infinite scale or NaN shows in its column and nowhere else, few rows or many."""
+    from mixture_experts_routed_softmax_gb300.w4 import Linear4
+    rng = np.random.default_rng(4)
+    for kind in ("int4", "fp4"):
+        codes, scales = _codes(rng, 1, 264, 136, kind, 64)
+        scales[0, 1, 5], scales[0, 4, 77], scales[0, 0, 130] = float("inf"), float("nan"), -3e38
+        clean = scales.clone()
+        clean[0, :, [5, 77]] = 1.0
+        for T in (1, 6, 200, 600):
+            x = torch.tensor(rng.standard_normal((T, 264)) * 2.0 ** -8).to(BF16)
+            lin = Linear4(_weights4(codes, scales, kind, 64), out_dtype=torch.float32)
+            y = _np(lin.apply(x.cuda(), lin.buffers(T)))
+            bad = np.isin(np.arange(136), [5, 77])
+            assert not np.isfinite(y[:, bad]).any()
+            Wd = W.weights(codes, clean.double().numpy(), kind, 64)[0]
+            ref, bound = W.linear_bound(x.double().numpy(), Wd, False)
+            # 3e38's code * scale rounded to bf16, where it stays below bf16's top
+            bound = bound + W.U_BF16 * (np.abs(x.double().numpy()) @ np.abs(Wd))
+            keep = ~bad & (np.abs(Wd).max(0) < W.BF16_MAX)
+            W.assert_within("y", y[:, keep], ref[:, keep], bound[:, keep])
