@@ -765,8 +765,11 @@ static cudaError_t run_select(const moe_router& r, const float* logits, const in
   const int rd = sel_row_doubles(r);
   const size_t smem = (size_t)kSelWarps * rd * sizeof(double);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        select_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the most that this instance takes, in every call: another thread's call with fewer experts
+    // does not lower it)
+    const cudaError_t e =
+        cudaFuncSetAttribute(select_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSelWarps * 2 * 32 * NV * (int)sizeof(double));
     if (e != cudaSuccess) return e;
   }
   const bool vec = r.E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
