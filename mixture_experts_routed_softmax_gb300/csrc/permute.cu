@@ -309,32 +309,38 @@ cudaError_t launch_permute(const int32_t* topk_idx, int64_t T, int k, int E, int
   int32_t* rank_in_blk =
       reinterpret_cast<int32_t*>(static_cast<char*>(ws) + al256((size_t)nblk * E * 4));
   const size_t hist_smem = (size_t)kHistWarps * E * 4;
+  // (the most it takes, in every call: another thread's call with fewer experts does not lower it)
   cudaError_t err = cudaFuncSetAttribute(permute_hist_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)hist_smem);
+                                         kHistWarps * kMaxExperts * 4);
   if (err != cudaSuccess) return err;
   timer_before(MOE_KERNEL_PERMUTE, s);
-  int launches = 2;
+  int launches = 0;
+  // Each kernel indexes by what the one before wrote, the scan in place: after a launch that
+  // failed nothing more is launched.
+  auto next = [&](auto kernel, dim3 grid, dim3 block, size_t smem, auto... args) {
+    if (err != cudaSuccess) return;
+    err = launch_pdl(pdl_for_tokens(T), kernel, grid, block, smem, s, args...);
+    launches += err == cudaSuccess;
+  };
   if (P > 0 && P <= kSmallPairs) {
-    launch_pdl(pdl_for_tokens(T), permute_small_kernel, dim3(1), dim3(1024), 0, s, topk_idx, P, E,
-               S, T, align, counts, offsets, dst_row, src_pair, status);
+    next(permute_small_kernel, dim3(1), dim3(1024), 0, topk_idx, P, E, S, T, align, counts, offsets,
+         dst_row, src_pair, status);
   } else {
     if (P > 0)
-      launch_pdl(pdl_for_tokens(T), permute_hist_kernel, dim3((unsigned)nblk),
-                 dim3(kHistWarps * 32), hist_smem, s, topk_idx, P, E, blk_count, rank_in_blk,
-                 status);
-    launch_pdl(pdl_for_tokens(T), permute_scan_kernel, dim3(1), dim3(1024), 0, s, blk_count, nblk,
-               E, S, T, align, counts, offsets);
+      next(permute_hist_kernel, dim3((unsigned)nblk), dim3(kHistWarps * 32), hist_smem, topk_idx, P,
+           E, blk_count, rank_in_blk, status);
+    next(permute_scan_kernel, dim3(1), dim3(1024), 0, blk_count, nblk, E, S, T, align, counts,
+         offsets);
     if (P > 0)
-      launch_pdl(pdl_for_tokens(T), permute_scatter_kernel, dim3((unsigned)((P + 255) / 256)),
-                 dim3(256), 0, s, topk_idx, P, E, blk_count, rank_in_blk, dst_row, src_pair);
-    launches = P > 0 ? 4 : 2;
+      next(permute_scatter_kernel, dim3((unsigned)((P + 255) / 256)), dim3(256), 0, topk_idx, P, E,
+           blk_count, rank_in_blk, dst_row, src_pair);
   }
-  launch_pdl(pdl_for_tokens(T), permute_gather_kernel, dim3((unsigned)((R_cap + 7) / 8)), dim3(256),
-             0, s, x, d, k, T, offsets, counts, E, S, R_cap, src_pair, dst_row, xp);
+  next(permute_gather_kernel, dim3((unsigned)((R_cap + 7) / 8)), dim3(256), 0, x, d, k, T, offsets,
+       counts, E, S, R_cap, src_pair, dst_row, xp);
   note_launches(launches);
   timer_after(MOE_KERNEL_PERMUTE, s);
-  return cudaGetLastError();
+  return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace moe

@@ -52,3 +52,30 @@ def test_choices_of_different_E():
     for l, groups, b in checks:
         want = [R.choose(row, 4, n_groups=groups, topk_groups=5) for row in l]
         np.testing.assert_array_equal(b.topk_idx.cpu().numpy(), want)
+
+
+def test_permutes_of_different_E():
+    import workloads
+    from mixture_experts_routed_softmax_gb300.layer import MoELayer
+    jobs, checks = [], []
+    for E in (8, 1024, 64, 512):
+        wl = workloads.Workload("threads", T=5000, d=64, f=64, E=E, k=4, align=16)
+        inp = workloads.generate(wl)
+        layer = MoELayer.from_inputs(inp, 4, 16)
+        x, b, s = inp["x"].cuda(), layer.buffers(5000, backward=False), torch.cuda.Stream()
+        layer.route(x, b)
+        layer.permute(x, b)
+        torch.cuda.synchronize()
+        want = b.dst_row.clone()
+        b.dst_row.fill_(-7)
+
+        def job(layer=layer, x=x, b=b, s=s):
+            for _ in range(1000):
+                layer.permute(x, b, None, s)
+
+        jobs.append(job)
+        checks.append((want, b))
+    torch.cuda.synchronize()
+    _together(jobs)
+    for want, b in checks:
+        assert torch.equal(b.dst_row, want)
