@@ -226,6 +226,11 @@ class MoELayer:
         if self.router is not None:
             dense = self.router.dense or accumulate
             ws = b.ws_logits_bwd
+            # before the first launch: what is added to d_logits would stay there
+            if ws is None or ws.numel() < int(self.lib.moe_logits_bwd_workspace_size(
+                    b.T, self.d, self.E, dense)):
+                raise ValueError("buffers(T, backward=True"
+                                 + (", logits_loss=True" if accumulate else "") + ") are needed")
             _lib.call("moe_select_bwd", self.router._ref, _p(b.d_topk_w), _p(b.logits),
                       _p(b.topk_idx), b.T, int(accumulate), _p(b.d_logits), _stream(stream))
             _lib.call("moe_logits_bwd", _p(b.d_logits), _p(self.w_router), _p(x), b.T, self.d,

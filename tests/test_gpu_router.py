@@ -476,3 +476,24 @@ def test_balance_of_any_size(score, E, groups, topk, k):
         assert r.lib.moe_status(torch.cuda.current_stream().cuda_stream) == 0
         with np.errstate(over="ignore"):
             _check_choice(l, k, kw, bal, b.topk_idx.cpu().numpy(), b.topk_w.cpu().numpy())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_logits_loss_without_room(score):
+    """A backward that is refused for its buffers has added nothing to the logits' gradient."""
+    import workloads
+    from mixture_experts_routed_softmax_gb300.layer import MoELayer
+    wl = workloads.Workload("room", T=40, d=64, f=64, E=16, k=3, align=16)
+    inp = workloads.generate(wl)
+    layer = MoELayer.from_inputs(inp, 3, 16, router=_router(16, 3, dict(score=score), None))
+    b = layer.buffers(40)
+    layer.forward(inp["x"].cuda(), b)
+    layer.expert_bwd(inp["dy"].cuda(), b)
+    b.d_logits.fill_(0.25)
+    with pytest.raises(ValueError):
+        layer.route_bwd(b, accumulate=True)
+    assert bool((b.d_logits == 0.25).all())
+    layer.route_bwd(b)
+    with pytest.raises(ValueError):
+        layer.route_bwd(layer.buffers(40, backward=False), x=b.x)
+    assert layer.status() == 0
