@@ -884,7 +884,7 @@ __global__ void __launch_bounds__(32 * kSelWarps) select_bwd_chosen_kernel(
     my_e = -1;
   }
   const float l = my_e >= 0 ? __ldg(logits + t * a.E + my_e) : -INFINITY;
-  g = masked(l) ? 0.f : g * a.scale;
+  if (masked(l)) g = 0.f;
   auto sum = [](float v) {
 #pragma unroll
     for (int off = SLOTS / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
@@ -896,6 +896,11 @@ __global__ void __launch_bounds__(32 * kSelWarps) select_bwd_chosen_kernel(
 #pragma unroll
     for (int off = SLOTS / 2; off > 0; off >>= 1)
       r = fmaxf(r, __shfl_xor_sync(0xFFFFFFFFu, r, off));
+    // A constant on all of g changes nothing: less the g of the largest score, whose q may be
+    // nearly all of the sum, so that what is left there is not the difference of equal numbers.
+    const uint32_t is_top = __ballot_sync(0xFFFFFFFFu, l == r) >> (seg * SLOTS);
+    g = (g - __shfl_sync(0xFFFFFFFFu, g, seg * SLOTS + ((__ffs(is_top) - 1) & (SLOTS - 1)))) *
+        a.scale;
     if (a.sigmoid) r = fminf(r, 0.f);
     float q = renorm_score(a.sigmoid, l, r);
     const float total = sum(q);
@@ -903,7 +908,7 @@ __global__ void __launch_bounds__(32 * kSelWarps) select_bwd_chosen_kernel(
     dl = q * (g - sum(q * g));
     if (a.sigmoid) dl *= sigmoid_of(-l);                      // 1 - s, without its cancellation
   } else {
-    dl = g * sigmoid_of(l) * sigmoid_of(-l);
+    dl = g * a.scale * sigmoid_of(l) * sigmoid_of(-l);
   }
   if (masked(l)) dl = 0.f;
   // one lane an expert: the first slot that names it takes the others' terms
@@ -925,7 +930,10 @@ __global__ void __launch_bounds__(32 * kSelWarps) select_bwd_chosen_kernel(
 }
 
 // Raw softmax scores: a warp a token, every expert's - p_e (sum_j p_j g_j) written, then the
-// chosen entries with their p g on top.
+// chosen entries with their own, p_e (g_e - sum_j p_j g_j). Where a chosen expert * has more than half
+// of the row these are differences of nearly equal numbers; a constant on every expert's g (0 where
+// it is not chosen) changes nothing, so there they are, less g_*,
+//   p_e ((g_e - g_*) - (sum_{chosen, not *} p_j g_j - g_* sum_{not *} p)).
 template <int NV>
 __global__ void __launch_bounds__(32 * kSelWarps) select_bwd_kernel(
     const __grid_constant__ SelArgs a, const float* __restrict__ d_topk_w,
@@ -939,7 +947,7 @@ __global__ void __launch_bounds__(32 * kSelWarps) select_bwd_kernel(
   float* drow = d_logits + t * a.E;
   const bool slot = lane < a.k;
   int my_e = slot ? topk_idx[t * a.k + lane] : -1;
-  float g = slot ? a.scale * d_topk_w[t * a.k + lane] : 0.f;
+  float g = slot ? d_topk_w[t * a.k + lane] : 0.f;
   if (slot && (my_e < 0 || my_e >= a.E)) {
     raise_status(status, MOE_ERR_DEVICE_INDEX);
     my_e = -1;
@@ -960,18 +968,32 @@ __global__ void __launch_bounds__(32 * kSelWarps) select_bwd_kernel(
   }
   z = warp_sum(z);
   const float p = dead ? 0.f : exp_below(lj, m) / z;
-  const float inner = warp_sum(p * g);
-  const float dl = p * g;                 // the chosen entry's own term; - p_e inner for every e
+  const float inner = a.scale * warp_sum(p * g);
   const uint32_t same = __match_any_sync(0xFFFFFFFFu, my_e);
   const bool first = (same & ((1u << lane) - 1u)) == 0;
-  float add = dl;
+  // the g of all the slots that name this lane's expert
   if (__any_sync(0xFFFFFFFFu, my_e >= 0 && !first)) {
-    add = 0.f;
+    float all = 0.f;
     for (int j = 0; j < a.k; ++j) {
-      const float dj = __shfl_sync(0xFFFFFFFFu, dl, j);
-      if ((same >> j) & 1u) add += dj;
+      const float gj = __shfl_sync(0xFFFFFFFFu, g, j);
+      if ((same >> j) & 1u) all += gj;
     }
+    g = all;
   }
+  float own = a.scale * (p * g) - p * inner;
+  const uint32_t most = __ballot_sync(0xFFFFFFFFu, p > 0.5f);
+  if (most) {
+    const int star = __shfl_sync(0xFFFFFFFFu, my_e, __ffs(most) - 1);
+    const float gs = __shfl_sync(0xFFFFFFFFu, g, __ffs(most) - 1);
+    float others = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) others += lane * NV + i == star ? 0.f : l[i];
+    others = warp_sum(others) / z;
+    const float rest = warp_sum(first && my_e >= 0 && my_e != star ? p * g : 0.f) - gs * others;
+    own = a.scale * (p * ((g - gs) - rest));
+  }
+  const float before = accumulate && my_e >= 0 ? drow[my_e] : 0.f;
+  __syncwarp();
   const float gz = z > 0.f ? inner / z : 0.f;
   if (NV >= 4 && vec) {
 #pragma unroll
@@ -994,13 +1016,7 @@ __global__ void __launch_bounds__(32 * kSelWarps) select_bwd_kernel(
     }
   }
   __syncwarp();
-  if (my_e >= 0 && first) {
-    if (accumulate) {
-      drow[my_e] += add;
-    } else {
-      drow[my_e] = add - p * inner;
-    }
-  }
+  if (my_e >= 0 && first) drow[my_e] = before + own;
 }
 
 // NV: logits a lane, or CHOSEN: lanes a token

@@ -497,3 +497,71 @@ def test_logits_loss_without_room(score):
     with pytest.raises(ValueError):
         layer.route_bwd(layer.buffers(40, backward=False), x=b.x)
     assert layer.status() == 0
+
+
+def _gradient_by_pairs(dw, l, idx, score, renormalise, scale):
+    """One token's gradient as sums over pairs, p_e sum_f p_f (g_e - g_f), in 64 bits, where no
+    difference of nearly equal sums appears; and the magnitudes that fp32 rounds: with * the largest
+    chosen score (renormalised weights), or a chosen expert of more than half of the row,
+    p_e (|g_e - g_*| + sum_{f not *} p_f |g_f - g_*|), each g_f - g_* of f that is not chosen
+    or of raw scores as |g_f| + |g_*|."""
+    s, live = R.scores(l, score)
+    out, mag = np.zeros(len(s)), np.zeros(len(s))
+    if renormalise:
+        q = R.chosen_scores(l, idx, score, True)
+        g = np.where(live[idx], np.asarray(dw, dtype=np.float64), 0.0)
+        top = g[np.argmax(np.where(live[idx], np.asarray(l, dtype=np.float64)[idx], -np.inf))]
+        for j, e in enumerate(idx):
+            f = 1.0 / (1.0 + np.exp(float(l[e]))) if score == "sigmoid" else 1.0
+            if live[e]:
+                out[e] += scale * q[j] * f * (q * (g[j] - g)).sum()
+                mag[e] += abs(scale) * q[j] * f * (abs(g[j] - top) + (q * np.abs(g - top)).sum())
+        return out, mag
+    G = np.zeros(len(s))
+    np.add.at(G, idx[live[idx]], np.asarray(dw, dtype=np.float64)[live[idx]])
+    out = scale * s * (s[None] * (G[:, None] - G[None])).sum(1)
+    chosen = np.zeros(len(s), dtype=bool)
+    chosen[idx] = True
+    mag = s * (np.abs(G) + (s * np.abs(G)).sum())
+    star = int(np.argmax(s))
+    if chosen[star] and s[star] > 0.5:
+        rest = np.delete(s * (np.abs(G) + abs(G[star])), star).sum()
+        mag = np.where(chosen, s * (np.abs(G - G[star]) + rest), mag)
+    return out, abs(scale) * mag
+
+
+@pytest.mark.parametrize("score,renormalise", [("softmax", True), ("sigmoid", True),
+                                               ("softmax", False)])
+@pytest.mark.parametrize("E,k", [(24, 2), (61, 5), (256, 8), (520, 32)])
+def test_gradient_of_peaked_rows(score, renormalise, E, k):
+    """One expert has nearly the whole row, or the g of several are nearly alike: what is left of
+    the differences is the gradient, not rounding."""
+    rng = np.random.default_rng(E + k)
+    T = 60
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l -= np.linspace(0, 3, T, dtype=np.float32)[:, None] * (10 if score == "sigmoid" else 1)
+    at = rng.integers(0, E, T)
+    l[np.arange(T), at] += np.linspace(0, 40, T).astype(np.float32)
+    l[rng.random((T, E)) < 0.05] = -np.inf
+    kw = dict(score=score, renormalise=renormalise, scale=2.5)
+    r = _router(E, k, kw, None)
+    b = r.buffers(T, backward=True)
+    lg = torch.tensor(l).cuda()
+    r.select(lg, b)
+    idx = b.topk_idx.cpu().numpy()
+    idx[::7, k - 1] = idx[::7, 0]                  # an expert twice
+    idx[5::7] = rng.integers(0, E, idx[5::7].shape)    # a caller's choice, without the largest
+    b.topk_idx.copy_(torch.tensor(idx))
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    dw[::2] = (1 + 1e-5 * dw[::2]).astype(np.float32)
+    d = r.select_bwd(torch.tensor(dw).cuda(), lg, b).cpu().numpy().astype(np.float64)
+    base = (1e-6 * rng.standard_normal((T, E))).astype(np.float32)
+    b.d_logits.copy_(torch.tensor(base))
+    added = r.select_bwd(torch.tensor(dw).cuda(), lg, b, accumulate=True).cpu().numpy()
+    for t in range(T):
+        ref, mag = _gradient_by_pairs(dw[t], l[t], idx[t], **kw)
+        tol = (2 * R.half_steps(E, l[t]) + k) * R.EPS32 * mag + 1e-37
+        assert np.all(np.abs(d[t] - ref) <= tol), (t, (np.abs(d[t] - ref) / tol).max())
+        # added to: the rounding of the sum, once
+        assert np.all(np.abs(added[t] - base[t] - d[t]) <=
+                      2 * R.EPS32 * (np.abs(base[t]) + np.abs(d[t])) + 1e-37), t
