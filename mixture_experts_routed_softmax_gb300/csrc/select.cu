@@ -51,12 +51,14 @@ struct SelArgs {
 // largest score where that is over 1/2; below, s (4 + 2.35 |l|) grows with l and is 4 + 2.35 |m|
 // of the largest score at most, m the largest logit (and one more for that score's own
 // rounding): 10 + 2.4 max(0, -m). Softmax, e (1 / Z): the argument's rounding
-// moves e by at most |x| e^x < 0.4 halves of the largest, expf 4 halves, the same again
-// for the terms of Z, Z's NV + 5 additions one half each, its inverse and the product one
-// each. The balance's addition is a half of the value itself (border_err).
+// moves e by at most |x| e^x < 0.4 halves of the largest, expf 4 halves. Z: expf's 4 again, its NV + 5
+// additions one half each, and of the arguments' roundings, which may all go one way, sum |x| e^x / Z:
+// at most f with f e^(f + 1) = E - 1 (one expert far above equal others), 4.5 for 1024 experts. The
+// inverse and the product one each: NV + 20. The balance's addition is a half of the value itself
+// (border_err).
 template <int NV>
 __device__ __forceinline__ float score_err(bool sigmoid, float m) {
-  return (sigmoid ? 10.f + 2.4f * fmaxf(0.f, -m) : (float)(NV + 5 + 11)) * 5.9604645e-8f;
+  return (sigmoid ? 10.f + 2.4f * fmaxf(0.f, -m) : (float)(NV + 20)) * 5.9604645e-8f;
 }
 // how far apart two values near v have to be to be told apart (and scores below
 // fp32's normal range, which have fewer bits, never are)

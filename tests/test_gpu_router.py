@@ -565,3 +565,30 @@ def test_gradient_of_peaked_rows(score, renormalise, E, k):
         # added to: the rounding of the sum, once
         assert np.all(np.abs(added[t] - base[t] - d[t]) <=
                       2 * R.EPS32 * (np.abs(base[t]) + np.abs(d[t])) + 1e-37), t
+
+
+@pytest.mark.parametrize("E", [32, 100, 512, 1024])
+def test_near_ties_below_a_far_maximum(E):
+    """One expert far above equal others, where the arguments' roundings weigh most and all go one
+    way, and a balance that leaves the order to the last half steps of fp32."""
+    rng = np.random.default_rng(E)
+    T = 64
+    far = 1.0 + np.log(E) - np.log(np.log(E))        # about f + 1 of f e^(f + 1) = E - 1
+    open_ = 0
+    for half_steps in range(-24, 25, 3):
+        l = np.full((T, E), -far / 2, dtype=np.float32)
+        l[:, 0] = far / 2 + rng.random() + np.arange(T) * 2.0 ** -22
+        s = np.array([R.scores(row, "softmax")[0] for row in l])
+        bal = np.full(E, -4.0, dtype=np.float32)
+        bal[0], bal[1] = 0.0, (s[:, 0] - s[:, 1]).mean() * (1 + half_steps * R.EPS32)
+        r = _router(E, 1, dict(score="softmax"), bal)
+        b = r.buffers(T)
+        r.select(torch.tensor(l).cuda(), b)
+        c = s[:, :2] + bal[:2].astype(np.float64)
+        sure = np.abs(c[:, 0] - c[:, 1]) > 2.0 ** -36 * s[:, 0]   # 64 bits can tell them apart
+        open_ += (np.abs(c[:, 0] - c[:, 1]) < 2.0 ** -22 * s[:, 0]).sum()
+        got = b.topk_idx.cpu().numpy()[:, 0]
+        np.testing.assert_array_equal(got[sure], (c[:, 1] > c[:, 0]).astype(int)[sure])
+    # the inputs do what they are for: rows lie some 2^-24 of the score apart, so of a call's several are
+    # within 2^-22 of the border
+    assert open_ > 2 * 17
