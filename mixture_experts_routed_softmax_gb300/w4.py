@@ -20,6 +20,18 @@ BF16 = torch.bfloat16
 KINDS = {"int4": _lib.MOE_W4_INT4, "fp4": _lib.MOE_W4_FP4}
 
 
+def _fresh(stream, dev: int, *tensors) -> None:
+    """Tensors just allocated, to be written by a call on ``stream``: their memory may be what work
+    still to come on the current stream uses, so ``stream`` waits for that, and is not given
+    out again before the call has ended."""
+    _stream(dev, stream)
+    current = torch.cuda.current_stream(dev)
+    if stream is not None and stream != current:
+        stream.wait_stream(current)
+        for t in tensors:
+            t.record_stream(stream)
+
+
 class Weights4:
     """Matrices [E, K, N] in 4 bits: value(code) * scale, one scale for ``group``
     (32, 64 or 128) neighbouring rows of a column.
@@ -68,14 +80,18 @@ class Weights4:
     def quantise(cls, w, kind: str = "int4", group: int = 32, stream=None) -> "Weights4":
         """4-bit weights of w [E, K, N] bf16."""
         E, K, N = w.shape
-        return cls.empty(E, K, N, kind, group, w.device).quantise_from(w, stream)
+        q = cls.empty(E, K, N, kind, group, w.device)
+        _fresh(stream, q._dev, q.codes, q.scales)
+        return q.quantise_from(w, stream)
 
     @classmethod
     def from_codes(cls, codes, scales, kind: str = "int4", group: int = 32,
                    stream=None) -> "Weights4":
         """Weights given as codes [E, K, N] uint8 and scales [E, ceil(K/group), N] bf16."""
         E, K, N = codes.shape
-        return cls.empty(E, K, N, kind, group, codes.device).pack_from(codes, scales, stream)
+        q = cls.empty(E, K, N, kind, group, codes.device)
+        _fresh(stream, q._dev, q.codes, q.scales)
+        return q.pack_from(codes, scales, stream)
 
     def quantise_from(self, w, stream=None) -> "Weights4":
         _check("moe_w4_quantise", self.lib.moe_w4_quantise(
@@ -95,6 +111,7 @@ class Weights4:
         shape = (self.E, self.K, self.N)
         if out is None:
             out = torch.empty(shape, dtype=BF16, device=self.codes.device)
+            _fresh(stream, self._dev, out)
         _check("moe_w4_dequantise", self.lib.moe_w4_dequantise(
             self._ref, _packed("out", out, BF16, shape, self._dev), _stream(self._dev, stream)))
         return out

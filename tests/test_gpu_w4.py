@@ -468,3 +468,34 @@ def test_scales_that_are_not_finite():
             bound = bound + W.U_BF16 * (np.abs(x.double().numpy()) @ np.abs(Wd))
             keep = ~bad & (np.abs(Wd).max(0) < W.BF16_MAX)
             W.assert_within("y", y[:, keep], ref[:, keep], bound[:, keep])
+
+
+@pytest.mark.parametrize("what", ["quantise", "from_codes", "dequantise"])
+def test_made_on_another_stream(what):
+    """What a call on another stream allocates is memory that work on the current one, not over yet,
+    may still write to."""
+    from mixture_experts_routed_softmax_gb300.w4 import Weights4
+    rng = np.random.default_rng(6)
+    E, K, N = 4, 1024, 768
+    codes, scales = _codes(rng, E, K, N, "int4", 32)
+    cg, sg = torch.tensor(codes).cuda(), scales.cuda()
+    w = torch.tensor(rng.standard_normal((E, K, N)), dtype=torch.float32).to(BF16).cuda()
+    make = {"quantise": lambda s: Weights4.quantise(w, "int4", 32, stream=s),
+            "from_codes": lambda s: Weights4.from_codes(cg, sg, "int4", 32, stream=s),
+            "dequantise": None}[what]
+    have = Weights4.from_codes(cg, sg, "int4", 32)
+    want = (make(None) if make else have).dequantise()
+    nc, ns = have.codes.numel(), have.scales.numel()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        junk = [torch.empty(nc, dtype=torch.uint8, device="cuda"),
+                torch.empty(ns, dtype=BF16, device="cuda"), torch.empty_like(want)]
+        torch.cuda._sleep(20_000_000)
+        for j in junk:
+            j.fill_(77)
+        del junk, j
+        got = make(side).dequantise(stream=side) if make else have.dequantise(stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del got
