@@ -766,7 +766,7 @@ static cudaError_t run_select(const moe_router& r, const float* logits, const in
                               cudaStream_t s) {
   const int rd = sel_row_doubles(r);
   const size_t smem = (size_t)kSelWarps * rd * sizeof(double);
-  if (smem > 48 * 1024) {
+  if (smem > 40 * 1024) {                   // (with the kernel's own, 48 KB need no leave)
     // (the most that this instance takes, in every call: another thread's call with fewer experts
     // does not lower it)
     const cudaError_t e =

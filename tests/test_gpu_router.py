@@ -592,3 +592,17 @@ def test_near_ties_below_a_far_maximum(E):
     # the inputs do what they are for: rows lie some 2^-24 of the score apart, so of a call's several are
     # within 2^-22 of the border
     assert open_ > 2 * 17
+
+
+@pytest.mark.parametrize("E,groups,topk", [(640, 20, 3), (744, 31, 4), (752, 47, 6), (760, 20, 3),
+                                           (768, 24, 4), (776, 8, 2), (1024, 128, 9)])
+def test_wide_rows_in_groups(E, groups, topk):
+    """Rows around what shared memory takes without being asked (E = 768: 48 KB, and the kernel's
+    own)."""
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((9, E)).astype(np.float32)
+    kw = dict(score="sigmoid", n_groups=groups, topk_groups=topk)
+    r = _router(E, 6, kw, None)
+    b = r.buffers(9)
+    r.select(torch.tensor(l).cuda(), b)
+    _check_choice(l, 6, kw, None, b.topk_idx.cpu().numpy(), b.topk_w.cpu().numpy())
