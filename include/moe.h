@@ -521,7 +521,7 @@ size_t moe_attn_paged_workspace_size(int Hq, int Hkv, int D);
  * The choice is that of scores in 64 bits: where fp32 scores lie too near to one
  * another to tell, the token is decided again from doubles (softmax scores are then
  * exact to 2^-39 of the largest). Without a balance, and
- * with one group or group_rank 1, it goes by the logits themselves.
+ * with one group, groups that all stay or group_rank 1, it goes by the logits themselves.
  * Masked experts: a logit of -inf or NaN has score 0 and is chosen, in index
  * order and with weight 0, only where fewer than k others remain; so is one whose
  * choice value is NaN, with the weight of its score. A token whose chosen scores are all 0

@@ -8,7 +8,7 @@
 //   S   = the k largest c among them, in descending order, ties to the lower index
 //   w_j = scale s_j, or scale s_j / sum_S s  (renormalise)
 //
-// Without a balance (and without sums of two) the order of c is the order of l,
+// Without a balance (and without sums of two that decide) the order of c is the order of l,
 // which needs no score at all: the choice is exact. Otherwise it is made from
 // fp32 scores whose error has a bound (score_err, below); a token where two values
 // that decide lie nearer to one another than that bound is decided again from

@@ -606,3 +606,17 @@ def test_wide_rows_in_groups(E, groups, topk):
     b = r.buffers(9)
     r.select(torch.tensor(l).cuda(), b)
     _check_choice(l, 6, kw, None, b.topk_idx.cpu().numpy(), b.topk_w.cpu().numpy())
+
+
+def test_groups_that_all_stay_are_one():
+    """Sigmoids that 64 bits hold as equal: without a balance the logits decide, as for one group."""
+    rng = np.random.default_rng(12)
+    l = (40 + 5 * rng.standard_normal((30, 64))).astype(np.float32)
+    got = []
+    for groups in (1, 8):
+        r = _router(64, 6, dict(score="sigmoid", n_groups=groups, topk_groups=groups), None)
+        b = r.buffers(30)
+        r.select(torch.tensor(l).cuda(), b)
+        got.append(b.topk_idx.cpu().numpy())
+    np.testing.assert_array_equal(got[0], got[1])
+    np.testing.assert_array_equal(got[0], np.argsort(-l, axis=1, kind="stable")[:, :6])
