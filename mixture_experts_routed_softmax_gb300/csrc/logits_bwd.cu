@@ -9,8 +9,9 @@
 // (renormalised or sigmoid scores: the chosen experts) gather those rows of
 // W_r^T, k d fp32 products a token. Dense rows go through the tensor cores: the
 // first two parts of dl (16 significant bits; dx itself keeps 8) against the three
-// parts of W_r^T. Measured at 8192 tokens of 512 experts, d = 2560: see the table
-// in the design notes.
+// parts of W_r^T. Measured at 8192 tokens of 512 experts, d = 2560: 203 us with 10 entries a
+// row, 395 dense (the bytes alone take 22 us at the copy's rate); 16384 tokens of 256, d = 2048: 192
+// with 8 entries, 385 dense.
 #include <algorithm>
 
 #include "common.cuh"
