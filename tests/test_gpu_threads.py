@@ -79,3 +79,38 @@ def test_permutes_of_different_E():
     _together(jobs)
     for want, b in checks:
         assert torch.equal(b.dst_row, want)
+
+
+def test_4_bit_calls_at_once():
+    """Rows and tile kernels of several streams on the GPU at a time: the bits of calls alone."""
+    from mixture_experts_routed_softmax_gb300.w4 import Experts4, Linear4, Weights4
+    gen = torch.Generator("cuda").manual_seed(3)
+
+    def weights(E, K, N, kind):
+        w = torch.randn(E, K, N, generator=gen, device="cuda") / K ** 0.5
+        return Weights4.quantise(w.to(torch.bfloat16), kind, 64)
+
+    jobs, checks = [], []
+    for T, kind in ((1, "int4"), (30, "fp4"), (400, "int4"), (900, "fp4")):
+        ex = Experts4(weights(12, 520, 264, kind), weights(12, 520, 264, kind),
+                      weights(12, 264, 520, kind), k=3)
+        lin = Linear4(weights(1, 520, 1032, kind))
+        x = torch.randn(T, 520, generator=gen, device="cuda").to(torch.bfloat16)
+        idx = torch.argsort(torch.rand(T, 12, generator=gen, device="cuda"), 1)[:, :3]
+        idx, w = idx.to(torch.int32).contiguous(), torch.rand(T, 3, generator=gen, device="cuda")
+        be, bl, s = ex.buffers(T), lin.buffers(T), torch.cuda.Stream()
+        want = (ex.forward(x, idx, w, be).clone(), lin.apply(x, bl).clone())
+        be.y.zero_()
+        bl.y.zero_()
+
+        def job(ex=ex, lin=lin, x=x, idx=idx, w=w, be=be, bl=bl, s=s):
+            for _ in range(200):
+                ex.forward(x, idx, w, be, stream=s)
+                lin.apply(x, bl, stream=s)
+
+        jobs.append(job)
+        checks.append((want, be, bl))
+    torch.cuda.synchronize()
+    _together(jobs)
+    for want, be, bl in checks:
+        assert torch.equal(be.y, want[0]) and torch.equal(bl.y, want[1])
